@@ -25,6 +25,9 @@ KT_HEAD_SHARED, KT_HEAD_SEPARATE = 0, 1
 (KT_OP_SCORE_SELECT, KT_OP_SPARSE_ATTN, KT_OP_DENSE_ATTN, KT_OP_SPARSE_STEP,
  KT_OP_DYNAMIC_REPS, KT_OP_PRESELECT) = 0, 1, 2, 3, 4, 5
 KT_LAYER_DENSE, KT_LAYER_SELECT, KT_LAYER_REUSE = 0, 1, 2
+KT_F16, KT_BF16, KT_F32 = 0, 1, 2
+KT_ROPE_HALF, KT_ROPE_PAIRS = 0, 1
+KT_ROPE_PLAIN, KT_ROPE_LINEAR, KT_ROPE_NTK, KT_ROPE_YARN, KT_ROPE_BANDS = 0, 1, 2, 3, 4
 
 # Every symbol declared in include/kt.h.
 EXPORTS = (
@@ -38,6 +41,10 @@ EXPORTS = (
     "kt_decode_layer", "kt_append_kv", "kt_set_max_ctas", "kt_set_phase_stamps",
     "kt_sparse_decode_attn_hostkv", "kt_quantize_kv_q8_0", "kt_sparse_decode_attn_q8_0",
     "kt_noalloc_read_status", "kt_selftest_step_timeout", "kt_sparse_decode_step_q8_0",
+    "kt_rope_init", "kt_apply_rope", "kt_workspace_bytes_f8", "kt_reps_pool_bytes_f8",
+    "kt_build_block_reps_f8", "kt_append_kv_f8", "kt_read_kv_f8", "kt_sparse_decode_attn_f8",
+    "kt_dense_decode_attn_f8", "kt_score_select_blocks_f8", "kt_sparse_decode_step_f8",
+    "kt_decode_layer_f8",
 )
 
 
@@ -73,6 +80,37 @@ class PagedKVQ8(ctypes.Structure):
                 ("batch", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32), ("block_size", ctypes.c_int32),
                 ("max_blocks_per_seq", ctypes.c_int32), ("num_pages", ctypes.c_int32)]
+
+
+class PagedKVF8(ctypes.Structure):
+    """kt_paged_kv_f8: e4m3 code and binary32 scale pools + block table and lengths."""
+    _fields_ = [("k_code", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_code", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("block_table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
+                ("batch", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("block_size", ctypes.c_int32),
+                ("max_blocks_per_seq", ctypes.c_int32), ("num_pages", ctypes.c_int32)]
+
+
+class RopeParams(ctypes.Structure):
+    """kt_rope_params."""
+    _fields_ = [("theta", ctypes.c_double), ("factor", ctypes.c_double),
+                ("beta_fast", ctypes.c_double), ("beta_slow", ctypes.c_double),
+                ("original_len", ctypes.c_int32), ("rotary_dim", ctypes.c_int32),
+                ("layout", ctypes.c_int32), ("scaling", ctypes.c_int32)]
+
+
+class Rope(ctypes.Structure):
+    """kt_rope: frequencies as 64-bit fractions of a turn, as kt_rope_init fills them."""
+    _fields_ = [("phase", ctypes.c_uint64 * 64), ("amplitude", ctypes.c_float),
+                ("rotary_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class Rows(ctypes.Structure):
+    """kt_rows: head rows of a projection (pointer, token stride in elements, heads, type)."""
+    _fields_ = [("data", ctypes.c_void_p), ("stride", ctypes.c_int64), ("heads", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
 
 
 class ReusePolicy(ctypes.Structure):
@@ -137,6 +175,28 @@ def _load():
         "kt_sparse_decode_step_q8_0": (ctypes.c_int, [vp, P(PagedKVQ8), vp, P(SparseParams), vp,
                                                       vp, vp, vp, sz, vp]),
     }
+    sig.update({
+        "kt_rope_init": (ctypes.c_int, [P(RopeParams), P(Rope)]),
+        "kt_apply_rope": (ctypes.c_int, [P(Rope), vp, i32, P(Rows), vp, P(Rows), vp, vp]),
+        "kt_workspace_bytes_f8": (ctypes.c_int, [ctypes.c_int, P(PagedKVF8), P(SparseParams),
+                                                 P(sz)]),
+        "kt_reps_pool_bytes_f8": (sz, [P(PagedKVF8), P(SparseParams)]),
+        "kt_build_block_reps_f8": (ctypes.c_int, [P(PagedKVF8), P(SparseParams), i32, i32, vp,
+                                                  vp]),
+        "kt_append_kv_f8": (ctypes.c_int, [P(PagedKVF8), P(SparseParams), P(Rope), P(Rows), vp,
+                                           P(Rows), P(Rows), vp, i32, vp, vp, vp, sz, vp]),
+        "kt_read_kv_f8": (ctypes.c_int, [P(PagedKVF8), vp, vp, i32, i32, vp, vp, vp, sz, vp]),
+        "kt_sparse_decode_attn_f8": (ctypes.c_int, [vp, P(PagedKVF8), P(SparseParams), vp, vp,
+                                                    vp, vp, sz, vp]),
+        "kt_dense_decode_attn_f8": (ctypes.c_int, [vp, P(PagedKVF8), i32, ctypes.c_float, vp, vp,
+                                                   sz, vp]),
+        "kt_score_select_blocks_f8": (ctypes.c_int, [vp, P(PagedKVF8), vp, P(SparseParams), vp,
+                                                     vp, vp, vp, sz, vp]),
+        "kt_sparse_decode_step_f8": (ctypes.c_int, [vp, P(PagedKVF8), vp, P(SparseParams), vp,
+                                                    vp, vp, vp, sz, vp]),
+        "kt_decode_layer_f8": (ctypes.c_int, [P(ReusePolicy), i32, i32, vp, P(PagedKVF8), vp,
+                                              P(SparseParams), vp, vp, vp, vp, sz, vp]),
+    })
     for name, (res, args) in sig.items():
         f = getattr(L, name)
         f.restype = res
@@ -357,6 +417,160 @@ def kt_sparse_decode_attn_q8_0(q, kvq, params, sel, cnt, out, ws, stream=None):
                                           _ptr(sel), _ptr(cnt), _ptr(out), _ptr(ws), ws.numel(),
                                           _stream(stream)),
            "kt_sparse_decode_attn_q8_0")
+
+
+def rope(rotary_dim=128, *, theta=10000.0, layout=KT_ROPE_HALF, scaling=KT_ROPE_PLAIN, factor=1.0,
+         original_len=0, beta_fast=32.0, beta_slow=1.0) -> Rope:
+    """The kt_rope of these parameters (kt_rope_init)."""
+    rp = RopeParams(theta, factor, beta_fast, beta_slow, original_len, rotary_dim, layout, scaling)
+    r = Rope()
+    _check(lib.kt_rope_init(ctypes.byref(rp), ctypes.byref(r)), "kt_rope_init")
+    return r
+
+
+def _dtype(t, call):
+    import torch
+    d = {torch.float16: KT_F16, torch.bfloat16: KT_BF16, torch.float32: KT_F32}.get(t.dtype)
+    if d is None:
+        raise KtError(KT_ERR_UNSUPPORTED, call)
+    return d
+
+
+def rows(t) -> Rows:
+    """kt_rows of a tensor [tokens][heads][128] (it may be a part of a packed projection); the
+    last two dimensions are contiguous."""
+    if isinstance(t, Rows):
+        return t
+    tokens, heads, d = t.shape
+    s0, s1, s2 = t.stride()
+    if d != 128 or s2 != 1 or (heads > 1 and s1 != 128):
+        raise KtError(KT_ERR_INVALID_ARG, "rows")
+    return Rows(t.data_ptr(), s0 if tokens > 1 else heads * 128, heads, _dtype(t, "rows"))
+
+
+def _rows(t):
+    return None if t is None else ctypes.byref(rows(t))
+
+
+def _check_out(out, shape, call):
+    if out is not None and (tuple(out.shape) != tuple(shape) or not out.is_contiguous()):
+        raise KtError(KT_ERR_INVALID_ARG, call)
+
+
+def kt_apply_rope(rope, positions, q=None, q_out=None, k=None, k_out=None, stream=None):
+    """Rotates q into q_out and k into k_out ([tokens][heads][128]; outputs float16); positions:
+    int32 [tokens]."""
+    tokens = positions.numel()
+    for x, y in ((q, q_out), (k, k_out)):
+        if x is not None:
+            if x.shape[0] != tokens:
+                raise KtError(KT_ERR_INVALID_ARG, "kt_apply_rope")
+            _check_out(y, x.shape, "kt_apply_rope")
+    _check(lib.kt_apply_rope(ctypes.byref(rope), _ptr(positions), tokens, _rows(q), _ptr(q_out),
+                             _rows(k), _ptr(k_out), _stream(stream)),
+           "kt_apply_rope")
+
+
+def paged_kv_f8(k_code, k_scale, v_code, v_scale, block_table, seq_lens) -> PagedKVF8:
+    """k_code/v_code: e4m3 (or uint8) [P][H_kv][128][128]; k_scale/v_scale: float32 [P][H_kv]."""
+    P, H_kv, bs, d = k_code.shape
+    return PagedKVF8(_ptr(k_code), _ptr(k_scale), _ptr(v_code), _ptr(v_scale), _ptr(block_table),
+                     _ptr(seq_lens), int(seq_lens.shape[0]), H_kv, d, bs,
+                     int(block_table.shape[1]), P)
+
+
+def kt_workspace_bytes_f8(op, kv, params) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib.kt_workspace_bytes_f8(op, ctypes.byref(kv), ctypes.byref(params), ctypes.byref(n)),
+           "kt_workspace_bytes_f8")
+    return int(n.value)
+
+
+def workspace_f8(op, kv, params, device="cuda"):
+    """A zero-filled workspace tensor (uint8) for `op` over an 8-bit cache."""
+    import torch
+    ws = torch.empty(kt_workspace_bytes_f8(op, kv, params), dtype=torch.uint8, device=device)
+    kt_workspace_init(ws)
+    return ws
+
+
+def kt_reps_pool_bytes_f8(kv, params) -> int:
+    return int(lib.kt_reps_pool_bytes_f8(ctypes.byref(kv), ctypes.byref(params)))
+
+
+def kt_build_block_reps_f8(kv, params, first_block, num_blocks, reps_pool, stream=None):
+    _check(lib.kt_build_block_reps_f8(ctypes.byref(kv), ctypes.byref(params), first_block,
+                                      num_blocks, _ptr(reps_pool), _stream(stream)),
+           "kt_build_block_reps_f8")
+
+
+def kt_append_kv_f8(kv, params, k, v, ws, *, rope=None, q=None, q_out=None, cu_tokens=None,
+                    new_lens=None, reps_pool=None, stream=None):
+    """Appends the rows k / v ([tokens][H_kv][128]) to the cache.  cu_tokens None: one row per
+    sequence; new_lens None: kv's lengths advance in place."""
+    tokens = k.shape[0]
+    if v.shape[0] != tokens or (q is not None and q.shape[0] != tokens):
+        raise KtError(KT_ERR_INVALID_ARG, "kt_append_kv_f8")
+    if q is not None:
+        _check_out(q_out, q.shape, "kt_append_kv_f8")
+    _check(lib.kt_append_kv_f8(ctypes.byref(kv), ctypes.byref(params),
+                               None if rope is None else ctypes.byref(rope), _rows(q),
+                               _ptr(q_out), _rows(k), _rows(v), _ptr(cu_tokens), tokens,
+                               _ptr(new_lens), _ptr(reps_pool), _ptr(ws), ws.numel(),
+                               _stream(stream)),
+           "kt_append_kv_f8")
+
+
+def kt_read_kv_f8(kv, cu_tokens, k_out, v_out, ws, *, first=None, stream=None):
+    """Tokens first[b] .. of every sequence into the rows of k_out / v_out ([tokens][H_kv][128];
+    either may be None)."""
+    out = k_out if k_out is not None else v_out
+    if out is None or (k_out is not None and v_out is not None and k_out.dtype != v_out.dtype):
+        raise KtError(KT_ERR_INVALID_ARG, "kt_read_kv_f8")
+    shape = (out.shape[0], kv.num_kv_heads, 128)
+    _check_out(k_out, shape, "kt_read_kv_f8")
+    _check_out(v_out, shape, "kt_read_kv_f8")
+    _check(lib.kt_read_kv_f8(ctypes.byref(kv), _ptr(first), _ptr(cu_tokens), out.shape[0],
+                             _dtype(out, "kt_read_kv_f8"), _ptr(k_out), _ptr(v_out), _ptr(ws),
+                             ws.numel(), _stream(stream)),
+           "kt_read_kv_f8")
+
+
+def kt_sparse_decode_attn_f8(q, kv, params, sel, cnt, out, ws, stream=None):
+    _check(lib.kt_sparse_decode_attn_f8(_ptr(q), ctypes.byref(kv), ctypes.byref(params),
+                                        _ptr(sel), _ptr(cnt), _ptr(out), _ptr(ws), ws.numel(),
+                                        _stream(stream)),
+           "kt_sparse_decode_attn_f8")
+
+
+def kt_dense_decode_attn_f8(q, kv, num_q_heads, softmax_scale, out, ws, stream=None):
+    _check(lib.kt_dense_decode_attn_f8(_ptr(q), ctypes.byref(kv), num_q_heads, softmax_scale,
+                                       _ptr(out), _ptr(ws), ws.numel(), _stream(stream)),
+           "kt_dense_decode_attn_f8")
+
+
+def kt_score_select_blocks_f8(q, kv, reps_pool, params, sel, cnt, sel_scores, ws, stream=None):
+    _check(lib.kt_score_select_blocks_f8(_ptr(q), ctypes.byref(kv), _ptr(reps_pool),
+                                         ctypes.byref(params), _ptr(sel), _ptr(cnt),
+                                         _ptr(sel_scores), _ptr(ws), ws.numel(),
+                                         _stream(stream)),
+           "kt_score_select_blocks_f8")
+
+
+def kt_sparse_decode_step_f8(q, kv, reps_pool, params, sel, cnt, out, ws, stream=None):
+    _check(lib.kt_sparse_decode_step_f8(_ptr(q), ctypes.byref(kv), _ptr(reps_pool),
+                                        ctypes.byref(params), _ptr(sel), _ptr(cnt), _ptr(out),
+                                        _ptr(ws), ws.numel(), _stream(stream)),
+           "kt_sparse_decode_step_f8")
+
+
+def kt_decode_layer_f8(pol, token_idx, layer_idx, q, kv, reps_pool, params, hist_sel, hist_cnt,
+                       out, ws, stream=None):
+    _check(lib.kt_decode_layer_f8(ctypes.byref(pol), token_idx, layer_idx, _ptr(q),
+                                  ctypes.byref(kv), _ptr(reps_pool), ctypes.byref(params),
+                                  _ptr(hist_sel), _ptr(hist_cnt), _ptr(out), _ptr(ws),
+                                  ws.numel(), _stream(stream)),
+           "kt_decode_layer_f8")
 
 
 def kt_set_phase_stamps(stamps, max_ctas: int = 0):

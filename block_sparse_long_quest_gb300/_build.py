@@ -2,7 +2,7 @@
 
 Each translation unit is compiled in parallel to an object file under _build/,
 then linked into block_sparse_long_quest_gb300/libkt.so.  Objects are rebuilt
-when their source, the internal header or the public header changed.
+when their source, an internal header or the public header changed.
 """
 from __future__ import annotations
 
@@ -18,7 +18,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libkt.so")
 SOURCES = ["kt_api.cu", "attn.cu", "select.cu", "reps.cu", "dynamic.cu", "preselect.cu",
-           "quant.cu"]
+           "quant.cu", "rope.cu", "kv_f8.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -39,7 +39,8 @@ def _flags(verbose_ptxas: bool):
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    headers = [os.path.join(CSRC, "kt_internal.cuh"), os.path.join(INCLUDE, "kt.h")]
+    headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cuh")]
+    headers.append(os.path.join(INCLUDE, "kt.h"))
     hdr_time = max(os.path.getmtime(h) for h in headers)
     objs, procs = [], []
     for src in SOURCES:

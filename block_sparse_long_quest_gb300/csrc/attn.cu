@@ -83,8 +83,22 @@ static_assert(Q8_RING_OFF + STAGES * Q8_STAGE_BYTES <= STAGES * KV_STAGE_BYTES,
               "Q8_0 stages and the dequantised block fit the ring");
 static_assert(Q8_STAGE_BYTES % 1024 == 0, "128-byte swizzled boxes need 1024-byte alignment");
 
+// e4m3 source: a stage holds the codes of K and V (16 KB each, 128-byte swizzled
+// TMA boxes), so the ring has twice the stages; the two scales of the block land
+// in the stage's info by 4-byte cp.async, which arrive on the stage's barrier
+// beside the TMA copies (nothing waits for them on its own).  The consumers turn
+// codes into binary16 fragments in registers.
+constexpr int F8_STAGE_BYTES = 2 * UNIT * D;
+constexpr int F8_STAGES = STAGES * KV_STAGE_BYTES / F8_STAGE_BYTES;
+constexpr float F8_SCALE_MIN = 0x1.0p-30f, F8_SCALE_MAX = 0x1.0p30f;
+template <int KVM>
+struct Ring {
+  static constexpr int stages = KVM == KVM_F8 ? F8_STAGES : STAGES;
+};
+
 struct StageInfo {
-  int ntok, end, pad0, pad1;
+  int ntok, end;
+  float ks, vs;  // e4m3 source: the block's scales
 };
 
 struct SmemLayout {
@@ -93,8 +107,8 @@ struct SmemLayout {
   static constexpr int scratch = q + Q_BYTES;
   static constexpr int cum = scratch + SCRATCH_FLOATS * 4;  // [MAX_SEGS+1] work prefix
   static constexpr int info = cum + (MAX_SEGS + 1) * 4;
-  static constexpr int bars = (info + STAGES * (int)sizeof(StageInfo) + 15) & ~15;
-  static constexpr int bcast = bars + (2 * STAGES + 6) * 8;
+  static constexpr int bars = (info + F8_STAGES * (int)sizeof(StageInfo) + 15) & ~15;
+  static constexpr int bcast = bars + (2 * F8_STAGES + 6) * 8;
   static constexpr int total = bcast + 64 * 4;
 };
 constexpr int SMEM_BYTES = SmemLayout::total + 1024;  // + alignment slack
@@ -132,8 +146,8 @@ struct Params {
   unsigned long long* stamps;
   const __half* k_src;    // KVM_HOST: fp16 pools in device-accessible host memory
   const __half* v_src;
-  const __half* k_scale;  // KVM_Q8: binary16 scales [P][H_kv][128][4]
-  const __half* v_scale;
+  const void* k_scale;    // KVM_Q8: binary16 scales [P][H_kv][128][4]; KVM_F8: binary32 [P][H_kv]
+  const void* v_scale;
   int skip_publish;                  // fused, failure-path test only: CTA + 1, 0 = none
   int wait_at_entry;  // programmatic dependent: wait for the previous grid before any global access
   int q_mapped;       // q and out in page-locked host memory (plain loads, no bulk copy of q)
@@ -673,9 +687,29 @@ __device__ int fused_pick(const Params& p, uint8_t* scr, unsigned long long* sh_
   return i1 - i0;
 }
 
+// e4m3 source: byte selector from (t0: c0 c1, t1: c0 c1) to (c0: t0 t1, c1: t0 t1),
+// t0 = token `tok`; bytes of tokens from ntok on come from the zero operand.
+__device__ __forceinline__ uint32_t f8_permute(int tok, int ntok) {
+  return (tok < ntok ? 0x0100u : 0x0404u) | (tok + 1 < ntok ? 0x3020u : 0x4040u);
+}
+// e4m3 source, one thread: the loads of stage st (codes by TMA, scales by
+// cp.async), with both of its arrivals.
+__device__ __forceinline__ void issue_f8(const Params& p, uint32_t kv_base, StageInfo* info,
+                                         uint32_t st, int row, uint32_t bar, uint64_t policy) {
+  mbar_arrive_expect_tx(bar, F8_STAGE_BYTES);
+  const uint32_t dst = kv_base + st * F8_STAGE_BYTES;
+  tma_load_2d(dst, &p.kmap, 0, row, bar, policy);
+  tma_load_2d(dst + UNIT * D, &p.vmap, 0, row, bar, policy);
+  const size_t slab = (size_t)row / BS;
+  cp_async_4(smem_u32(&info[st].ks), static_cast<const float*>(p.k_scale) + slab);
+  cp_async_4(smem_u32(&info[st].vs), static_cast<const float*>(p.v_scale) + slab);
+  cp_async_mbar_arrive_noinc(bar);
+}
+
 template <int SK, int KVM = KVM_F16>
 __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const __grid_constant__ Params p) {
   constexpr bool FUSED = SK != SK_NONE;
+  constexpr int NST = Ring<KVM>::stages;
   static_assert(!FUSED || KVM != KVM_HOST, "the one-launch step reads device pools");
   extern __shared__ uint8_t smem_raw[];
   __shared__ unsigned int f_hist[FUSED ? 512 : 1];
@@ -696,8 +730,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const __grid_constant_
   int* bcast = reinterpret_cast<int*>(smem + SmemLayout::bcast);
   float* scratch = reinterpret_cast<float*>(smem + SmemLayout::scratch);
   const uint32_t bar_full = smem_u32(smem + SmemLayout::bars);
-  const uint32_t bar_empty = bar_full + STAGES * 8;
-  const uint32_t bar_q = bar_empty + STAGES * 8;
+  const uint32_t bar_empty = bar_full + NST * 8;
+  const uint32_t bar_q = bar_empty + NST * 8;
   const uint32_t bar_sel = bar_q + 8;      // fused: this CTA's selected pages are ready
   const uint32_t bar_scored = bar_sel + 8;  // fused: this CTA's scoring loads are done
   const uint32_t bar_reps = bar_scored + 8;  // fused: staged reps landed (two, one per ring half)
@@ -705,9 +739,10 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const __grid_constant_
   const uint32_t kv_base = smem_u32(smem + SmemLayout::kv);
   auto bar_c = [] { named_bar_sync(1, NCT); };
   if (tid == 0) {
-    for (int i = 0; i < STAGES; ++i) {
-      // host source: all 32 producer lanes arrive (each once its copies land)
-      mbar_init(bar_full + 8 * i, KVM == KVM_HOST ? 32 : 1);
+    for (int i = 0; i < NST; ++i) {
+      // host source: all 32 producer lanes arrive (each once its copies land);
+      // e4m3: the issuing thread arrives for the TMA copies and for the scales
+      mbar_init(bar_full + 8 * i, KVM == KVM_HOST ? 32 : KVM == KVM_F8 ? 2 : 1);
       mbar_init(bar_empty + 8 * i, CONSUMERS);
     }
     mbar_init(bar_q, 1);
@@ -860,11 +895,11 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const __grid_constant_
         for (int k = 0; k < nbatch; ++k) {
           const int ntok_k = __shfl_sync(0xffffffffu, ntok, k);
           const int row_k = __shfl_sync(0xffffffffu, row, k);
-          const uint32_t st = it % STAGES;
+          const uint32_t st = it % NST;
           int okl = 1;
           if (lane == 0) {
-            if (it >= STAGES &&
-                !mbar_wait(bar_empty + 8 * st, ((it / STAGES) - 1) & 1, p.status))
+            if (it >= NST &&
+                !mbar_wait(bar_empty + 8 * st, ((it / NST) - 1) & 1, p.status))
               okl = 0;
             if (okl) {
               info[st].ntok = ntok_k;
@@ -885,13 +920,17 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const __grid_constant_
                   const uint32_t dst = kv_base + Q8_RING_OFF + st * Q8_STAGE_BYTES;
                   tma_load_2d(dst, &p.kmap, 0, row_k, bar, policy);
                   tma_load_2d(dst + Q8_CODE_BYTES, &p.vmap, 0, row_k, bar, policy);
-                  bulk_load(dst + 2 * Q8_CODE_BYTES, p.k_scale + (size_t)row_k * (D / 32),
+                  const size_t g0 = (size_t)row_k * (D / 32);
+                  bulk_load(dst + 2 * Q8_CODE_BYTES, static_cast<const __half*>(p.k_scale) + g0,
                             Q8_SCALE_BYTES, bar);
                   bulk_load(dst + 2 * Q8_CODE_BYTES + Q8_SCALE_BYTES,
-                            p.v_scale + (size_t)row_k * (D / 32), Q8_SCALE_BYTES, bar);
+                            static_cast<const __half*>(p.v_scale) + g0, Q8_SCALE_BYTES, bar);
+                } else if constexpr (KVM == KVM_F8) {
+                  issue_f8(p, kv_base, info, st, row_k, bar, policy);
                 }
               } else if constexpr (KVM != KVM_HOST) {
                 mbar_arrive(bar);
+                if constexpr (KVM == KVM_F8) mbar_arrive(bar);
               }
             }
           }
@@ -901,7 +940,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const __grid_constant_
             // every lane: its 128 of the block's 4096 16-byte pieces (K and V,
             // each two 64-channel boxes in the 128-byte swizzled layout of the
             // TMA stages), then an arrival that completes once they have landed
-            const uint32_t st = it % STAGES;
+            const uint32_t st = it % NST;
             if (ntok_k > 0) {
               const uint32_t dst = kv_base + st * KV_STAGE_BYTES;
 #pragma unroll 4
@@ -970,17 +1009,18 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const __grid_constant_
       produce(phase, u0, u1);
     }
     if (ok) {
-      const uint32_t st = it % STAGES;
+      const uint32_t st = it % NST;
       int okl = 0;
       if (lane == 0 &&
-          (it < STAGES || mbar_wait(bar_empty + 8 * st, ((it / STAGES) - 1) & 1, p.status))) {
+          (it < NST || mbar_wait(bar_empty + 8 * st, ((it / NST) - 1) & 1, p.status))) {
         info[st].end = 1;
         info[st].ntok = 0;
         okl = 1;
       }
       okl = __shfl_sync(0xffffffffu, okl, 0);
-      // the end marker: one arrival, or one per lane for the host source
+      // the end marker: one arrival (two for e4m3), or one per lane for the host source
       if (okl && (KVM == KVM_HOST || lane == 0)) mbar_arrive(bar_full + 8 * st);
+      if (KVM == KVM_F8 && okl && lane == 0) mbar_arrive(bar_full + 8 * st);
     }
     return;
   }
@@ -1009,7 +1049,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const __grid_constant_
     // handed to the producer warp, whose shared-memory reads would queue
     // behind the consumers' fragment loads once the attention starts.
     const int nil = a1 - a0;
-    const int npre = nil < STAGES ? min(n1, STAGES - nil) : 0;
+    const int npre = nil < NST ? min(n1, NST - nil) : 0;
     if (ctid < npre) {
       const int nsl = p.ncpu * p.kk_f;
       const FusedPickLayout Lp = fused_pick_layout(nsl, min(p.top_k, nsl));
@@ -1035,10 +1075,13 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const __grid_constant_
           const uint32_t dst = kv_base + Q8_RING_OFF + st * Q8_STAGE_BYTES;
           tma_load_2d(dst, &p.kmap, 0, row, bar, policy);
           tma_load_2d(dst + Q8_CODE_BYTES, &p.vmap, 0, row, bar, policy);
-          bulk_load(dst + 2 * Q8_CODE_BYTES, p.k_scale + (size_t)row * (D / 32), Q8_SCALE_BYTES,
-                    bar);
-          bulk_load(dst + 2 * Q8_CODE_BYTES + Q8_SCALE_BYTES, p.v_scale + (size_t)row * (D / 32),
+          const size_t g0 = (size_t)row * (D / 32);
+          bulk_load(dst + 2 * Q8_CODE_BYTES, static_cast<const __half*>(p.k_scale) + g0,
                     Q8_SCALE_BYTES, bar);
+          bulk_load(dst + 2 * Q8_CODE_BYTES + Q8_SCALE_BYTES,
+                    static_cast<const __half*>(p.v_scale) + g0, Q8_SCALE_BYTES, bar);
+        } else if constexpr (KVM == KVM_F8) {
+          issue_f8(p, kv_base, info, st, row, bar, policy);
         } else {
           mbar_arrive_expect_tx(bar, KV_STAGE_BYTES);
           const uint32_t dst = kv_base + st * KV_STAGE_BYTES;
@@ -1049,6 +1092,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const __grid_constant_
         }
       } else {
         mbar_arrive(bar);
+        if constexpr (KVM == KVM_F8) mbar_arrive(bar);
       }
     }
     if (ctid == 0) {
@@ -1065,10 +1109,11 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const __grid_constant_
   float m_run = -INFINITY, l_part = 0.0f;
   uint32_t qa[8][2];
   bool q_loaded = false;
+  float vs_run = 1.0f;  // e4m3: acc holds the output divided by this V scale
 
   for (uint32_t it = 0;; ++it) {
-    const uint32_t st = it % STAGES;
-    if (!mbar_wait(bar_full + 8 * st, (it / STAGES) & 1, p.status)) break;
+    const uint32_t st = it % NST;
+    if (!mbar_wait(bar_full + 8 * st, (it / NST) & 1, p.status)) break;
     const StageInfo in = info[st];
     if (in.end) break;
     if (in.ntok > 0 && !q_loaded) {
@@ -1077,7 +1122,13 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const __grid_constant_
       const __half* qs = reinterpret_cast<const __half*>(smem + SmemLayout::q);
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk) {
-        if (g < p.G) {
+        if (KVM == KVM_F8 && g < p.G) {
+          // a lane's four codes of a 16-channel piece are channels 4t .. 4t+3:
+          // the k order of the product is permuted, and q's alike
+          const uint2 v = *reinterpret_cast<const uint2*>(qs + g * D + kk * 16 + 4 * t);
+          qa[kk][0] = v.x;
+          qa[kk][1] = v.y;
+        } else if (g < p.G) {
           qa[kk][0] = *reinterpret_cast<const uint32_t*>(qs + g * D + kk * 16 + 2 * t);
           qa[kk][1] = *reinterpret_cast<const uint32_t*>(qs + g * D + kk * 16 + 8 + 2 * t);
         } else {
@@ -1086,7 +1137,13 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const __grid_constant_
       }
       q_loaded = true;
     }
-    if (in.ntok > warp * 16) {
+    bool scales_ok = true;
+    if constexpr (KVM == KVM_F8) {
+      scales_ok = in.ntok <= 0 || (in.ks >= F8_SCALE_MIN && in.ks <= F8_SCALE_MAX &&
+                                   in.vs >= F8_SCALE_MIN && in.vs <= F8_SCALE_MAX);
+      if (!scales_ok && ctid == 0) set_status(p.status, KT_ERR_DEVICE_CHECK);
+    }
+    if (in.ntok > warp * 16 && scales_ok) {
       if constexpr (KVM == KVM_Q8) {
         // this warp's 16 token rows of K and V: int8 code * binary16 scale,
         // rounded once to fp16, into the fp16 block at the start of the ring
@@ -1128,8 +1185,10 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const __grid_constant_
         }
         __syncwarp();
       }
-      const uint32_t kb = KVM == KVM_Q8 ? kv_base : kv_base + st * KV_STAGE_BYTES;
-      const uint32_t vb = kb + 2 * BOX_BYTES;
+      const uint32_t kb = KVM == KVM_Q8   ? kv_base
+                          : KVM == KVM_F8 ? kv_base + st * F8_STAGE_BYTES
+                                          : kv_base + st * KV_STAGE_BYTES;
+      const uint32_t vb = kb + (KVM == KVM_F8 ? UNIT * D : 2 * BOX_BYTES);
       const int mi = lane >> 3, r = lane & 7;
       // ---- S = q K^T for this warp's 16 tokens: two n-tiles, each with two
       // independent accumulation chains over the 8 k-steps
@@ -1138,24 +1197,42 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const __grid_constant_
       for (int a = 0; a < 2; ++a)
 #pragma unroll
         for (int c = 0; c < 2; ++c) s[a][c][0] = s[a][c][1] = s[a][c][2] = s[a][c][3] = 0.f;
+      if constexpr (KVM == KVM_F8) {
+        // 16 tokens x 32 channels of codes per load: two 16-channel k-steps
 #pragma unroll
-      for (int kk = 0; kk < 8; ++kk) {
-        const int tok = warp * 16 + (mi >> 1) * 8 + r;
-        const int chunk = kk * 2 + (mi & 1);
-        const uint32_t addr = kb + (chunk >> 3) * BOX_BYTES + tok * 128 +
-                              (((chunk & 7) ^ (tok & 7)) << 4);
-        uint32_t b0, b1, b2, b3;
-        ldsm_x4(b0, b1, b2, b3, addr);
-        mma_16816(s[0][kk & 1], qa[kk][0], 0u, qa[kk][1], 0u, b0, b1);
-        mma_16816(s[1][kk & 1], qa[kk][0], 0u, qa[kk][1], 0u, b2, b3);
+        for (int kk = 0; kk < 4; ++kk) {
+          const int tok = warp * 16 + (mi >> 1) * 8 + r;
+          const uint32_t addr = kb + tok * 128 + (((kk * 2 + (mi & 1)) ^ (tok & 7)) << 4);
+          uint32_t c0, c1, c2, c3;
+          ldsm_x4(c0, c1, c2, c3, addr);
+          const uint32_t* qe = qa[2 * kk];
+          const uint32_t* qo = qa[2 * kk + 1];
+          mma_16816(s[0][0], qe[0], 0u, qe[1], 0u, f8x2_lo(c0), f8x2_hi(c0));
+          mma_16816(s[1][0], qe[0], 0u, qe[1], 0u, f8x2_lo(c2), f8x2_hi(c2));
+          mma_16816(s[0][1], qo[0], 0u, qo[1], 0u, f8x2_lo(c1), f8x2_hi(c1));
+          mma_16816(s[1][1], qo[0], 0u, qo[1], 0u, f8x2_lo(c3), f8x2_hi(c3));
+        }
+      } else {
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const int tok = warp * 16 + (mi >> 1) * 8 + r;
+          const int chunk = kk * 2 + (mi & 1);
+          const uint32_t addr = kb + (chunk >> 3) * BOX_BYTES + tok * 128 +
+                                (((chunk & 7) ^ (tok & 7)) << 4);
+          uint32_t b0, b1, b2, b3;
+          ldsm_x4(b0, b1, b2, b3, addr);
+          mma_16816(s[0][kk & 1], qa[kk][0], 0u, qa[kk][1], 0u, b0, b1);
+          mma_16816(s[1][kk & 1], qa[kk][0], 0u, qa[kk][1], 0u, b2, b3);
+        }
       }
       // ---- online softmax (base 2), rows = query heads
       const int tok0 = warp * 16 + 2 * t;
+      const float scale_log2 = KVM == KVM_F8 ? p.scale_log2 * in.ks : p.scale_log2;
       float x[4];
-      x[0] = (tok0 < in.ntok) ? (s[0][0][0] + s[0][1][0]) * p.scale_log2 : -INFINITY;
-      x[1] = (tok0 + 1 < in.ntok) ? (s[0][0][1] + s[0][1][1]) * p.scale_log2 : -INFINITY;
-      x[2] = (tok0 + 8 < in.ntok) ? (s[1][0][0] + s[1][1][0]) * p.scale_log2 : -INFINITY;
-      x[3] = (tok0 + 9 < in.ntok) ? (s[1][0][1] + s[1][1][1]) * p.scale_log2 : -INFINITY;
+      x[0] = (tok0 < in.ntok) ? (s[0][0][0] + s[0][1][0]) * scale_log2 : -INFINITY;
+      x[1] = (tok0 + 1 < in.ntok) ? (s[0][0][1] + s[0][1][1]) * scale_log2 : -INFINITY;
+      x[2] = (tok0 + 8 < in.ntok) ? (s[1][0][0] + s[1][1][0]) * scale_log2 : -INFINITY;
+      x[3] = (tok0 + 9 < in.ntok) ? (s[1][0][1] + s[1][1][1]) * scale_log2 : -INFINITY;
       float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
@@ -1164,9 +1241,13 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const __grid_constant_
       float pr[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) pr[i] = exp2f(x[i] - m_use);
-      if (__any_sync(0xffffffffu, m_new != m_run)) {
-        const float alpha = exp2f(m_run - m_use);
+      if (__any_sync(0xffffffffu, m_new != m_run) || (KVM == KVM_F8 && in.vs != vs_run)) {
+        float alpha = exp2f(m_run - m_use);
         l_part *= alpha;
+        if constexpr (KVM == KVM_F8) {
+          alpha *= vs_run / in.vs;  // acc goes over to this block's V scale
+          vs_run = in.vs;
+        }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           acc[i][0] *= alpha;
@@ -1189,16 +1270,38 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const __grid_constant_
       const uint32_t pa2 = pack_half2(hi[2], hi[3]);
       const uint32_t pa3 = pack_half2(lo[2], lo[3]);
       // ---- O += P V
+      if constexpr (KVM == KVM_F8) {
+        // a transposed register holds two tokens' pairs of channels (2g, 2g + 1):
+        // the permute makes a pair of tokens per channel, with zeros for tokens
+        // behind the sequence's end (their codes may be anything)
+        const uint32_t p0 = f8_permute(tok0, in.ntok), p1 = f8_permute(tok0 + 8, in.ntok);
 #pragma unroll
-      for (int cp = 0; cp < 8; ++cp) {
-        const int tok = warp * 16 + (mi & 1) * 8 + r;
-        const int chunk = cp * 2 + (mi >> 1);
-        const uint32_t addr = vb + (chunk >> 3) * BOX_BYTES + tok * 128 +
-                              (((chunk & 7) ^ (tok & 7)) << 4);
-        uint32_t b0, b1, b2, b3;
-        ldsm_x4_t(b0, b1, b2, b3, addr);
-        mma_16816(acc[2 * cp], pa0, pa1, pa2, pa3, b0, b1);
-        mma_16816(acc[2 * cp + 1], pa0, pa1, pa2, pa3, b2, b3);
+        for (int cp = 0; cp < 4; ++cp) {
+          const int tok = warp * 16 + (mi & 1) * 8 + r;
+          const uint32_t addr = vb + tok * 128 + (((cp * 2 + (mi >> 1)) ^ (tok & 7)) << 4);
+          uint32_t c0, c1, c2, c3;
+          ldsm_x4_t(c0, c1, c2, c3, addr);
+          c0 = __byte_perm(c0, 0u, p0);
+          c1 = __byte_perm(c1, 0u, p1);
+          c2 = __byte_perm(c2, 0u, p0);
+          c3 = __byte_perm(c3, 0u, p1);
+          mma_16816(acc[4 * cp], pa0, pa1, pa2, pa3, f8x2_lo(c0), f8x2_lo(c1));
+          mma_16816(acc[4 * cp + 1], pa0, pa1, pa2, pa3, f8x2_hi(c0), f8x2_hi(c1));
+          mma_16816(acc[4 * cp + 2], pa0, pa1, pa2, pa3, f8x2_lo(c2), f8x2_lo(c3));
+          mma_16816(acc[4 * cp + 3], pa0, pa1, pa2, pa3, f8x2_hi(c2), f8x2_hi(c3));
+        }
+      } else {
+#pragma unroll
+        for (int cp = 0; cp < 8; ++cp) {
+          const int tok = warp * 16 + (mi & 1) * 8 + r;
+          const int chunk = cp * 2 + (mi >> 1);
+          const uint32_t addr = vb + (chunk >> 3) * BOX_BYTES + tok * 128 +
+                                (((chunk & 7) ^ (tok & 7)) << 4);
+          uint32_t b0, b1, b2, b3;
+          ldsm_x4_t(b0, b1, b2, b3, addr);
+          mma_16816(acc[2 * cp], pa0, pa1, pa2, pa3, b0, b1);
+          mma_16816(acc[2 * cp + 1], pa0, pa1, pa2, pa3, b2, b3);
+        }
       }
     }
     __syncwarp();
@@ -1230,10 +1333,24 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const __grid_constant_
         sw[0] = m_run;
         sw[1] = l_row;
       }
+      if constexpr (KVM == KVM_F8) {
+        // tiles 2c and 2c + 1 hold the even and odd channels of piece c
 #pragma unroll
-      for (int nt = 0; nt < 16; ++nt)
-        *reinterpret_cast<float2*>(sw + 2 + nt * 8 + 2 * t) =
-            make_float2(acc[nt][0] + acc[nt][2], acc[nt][1] + acc[nt][3]);
+        for (int c = 0; c < 8; ++c) {
+          const float* e = acc[2 * c];
+          const float* o = acc[2 * c + 1];
+          float* d = sw + 2 + c * 16 + 4 * t;
+          *reinterpret_cast<float2*>(d) =
+              make_float2((e[0] + e[2]) * vs_run, (o[0] + o[2]) * vs_run);
+          *reinterpret_cast<float2*>(d + 2) =
+              make_float2((e[1] + e[3]) * vs_run, (o[1] + o[3]) * vs_run);
+        }
+      } else {
+#pragma unroll
+        for (int nt = 0; nt < 16; ++nt)
+          *reinterpret_cast<float2*>(sw + 2 + nt * 8 + 2 * t) =
+              make_float2(acc[nt][0] + acc[nt][2], acc[nt][1] + acc[nt][3]);
+      }
     }
   }
   named_bar_sync(1, NCT);
@@ -1447,7 +1564,13 @@ int attn_smem_optin() {
                           (const void*)attn_kernel<SK_LINEAR, KVM_Q8>,
                           (const void*)attn_kernel<SK_MMA, KVM_Q8>,
                           (const void*)attn_kernel<SK_F32, KVM_Q8>,
-                          (const void*)attn_kernel<SK_MULTI, KVM_Q8>})
+                          (const void*)attn_kernel<SK_MULTI, KVM_Q8>,
+                          (const void*)attn_kernel<SK_NONE, KVM_F8>,
+                          (const void*)attn_kernel<SK_COLS, KVM_F8>,
+                          (const void*)attn_kernel<SK_LINEAR, KVM_F8>,
+                          (const void*)attn_kernel<SK_MMA, KVM_F8>,
+                          (const void*)attn_kernel<SK_F32, KVM_F8>,
+                          (const void*)attn_kernel<SK_MULTI, KVM_F8>})
       if (e == cudaSuccess)
         e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
     return (int)e;
@@ -1469,7 +1592,12 @@ int attn_fused_max_ctas_per_sm() {
                           (const void*)attn_kernel<SK_LINEAR, KVM_Q8>,
                           (const void*)attn_kernel<SK_MMA, KVM_Q8>,
                           (const void*)attn_kernel<SK_F32, KVM_Q8>,
-                          (const void*)attn_kernel<SK_MULTI, KVM_Q8>}) {
+                          (const void*)attn_kernel<SK_MULTI, KVM_Q8>,
+                          (const void*)attn_kernel<SK_COLS, KVM_F8>,
+                          (const void*)attn_kernel<SK_LINEAR, KVM_F8>,
+                          (const void*)attn_kernel<SK_MMA, KVM_F8>,
+                          (const void*)attn_kernel<SK_F32, KVM_F8>,
+                          (const void*)attn_kernel<SK_MULTI, KVM_F8>}) {
       if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, f, THREADS, SMEM_BYTES) !=
           cudaSuccess)
         return 0;
@@ -1525,8 +1653,8 @@ cudaError_t launch_attention(const AttnLaunch& a, cudaStream_t stream) {
   p.stamps = a.stamps;
   p.k_src = static_cast<const __half*>(a.k_src);
   p.v_src = static_cast<const __half*>(a.v_src);
-  p.k_scale = static_cast<const __half*>(a.k_scale);
-  p.v_scale = static_cast<const __half*>(a.v_scale);
+  p.k_scale = a.k_scale;
+  p.v_scale = a.v_scale;
   p.skip_publish = a.skip_publish;
   p.poll_limit_ns = a.poll_limit_ns ? a.poll_limit_ns : WAIT_LIMIT_NS;
   p.wait_at_entry = (a.fused || !a.pdl) ? 1 : 0;
@@ -1554,6 +1682,7 @@ cudaError_t launch_attention(const AttnLaunch& a, cudaStream_t stream) {
   if (!a.fused) {
     if (a.kvm == KVM_HOST) return cudaLaunchKernelEx(&cfg, attn_kernel<SK_NONE, KVM_HOST>, p);
     if (a.kvm == KVM_Q8) return cudaLaunchKernelEx(&cfg, attn_kernel<SK_NONE, KVM_Q8>, p);
+    if (a.kvm == KVM_F8) return cudaLaunchKernelEx(&cfg, attn_kernel<SK_NONE, KVM_F8>, p);
     return cudaLaunchKernelEx(&cfg, attn_kernel<SK_NONE>, p);
   }
   if (a.kvm == KVM_Q8) {
@@ -1563,6 +1692,16 @@ cudaError_t launch_attention(const AttnLaunch& a, cudaStream_t stream) {
       case SK_MMA: return cudaLaunchKernelEx(&cfg, attn_kernel<SK_MMA, KVM_Q8>, p);
       case SK_F32: return cudaLaunchKernelEx(&cfg, attn_kernel<SK_F32, KVM_Q8>, p);
       case SK_MULTI: return cudaLaunchKernelEx(&cfg, attn_kernel<SK_MULTI, KVM_Q8>, p);
+    }
+    return cudaErrorInvalidValue;
+  }
+  if (a.kvm == KVM_F8) {
+    switch (a.sk) {
+      case SK_COLS: return cudaLaunchKernelEx(&cfg, attn_kernel<SK_COLS, KVM_F8>, p);
+      case SK_LINEAR: return cudaLaunchKernelEx(&cfg, attn_kernel<SK_LINEAR, KVM_F8>, p);
+      case SK_MMA: return cudaLaunchKernelEx(&cfg, attn_kernel<SK_MMA, KVM_F8>, p);
+      case SK_F32: return cudaLaunchKernelEx(&cfg, attn_kernel<SK_F32, KVM_F8>, p);
+      case SK_MULTI: return cudaLaunchKernelEx(&cfg, attn_kernel<SK_MULTI, KVM_F8>, p);
     }
     return cudaErrorInvalidValue;
   }

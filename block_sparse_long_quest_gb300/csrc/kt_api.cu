@@ -167,7 +167,7 @@ bool encode_pool_map(CUtensorMap* map, const void* pool, const kt_paged_kv* kv) 
   return r == CUDA_SUCCESS;
 }
 
-// [rows][128] int8 Q8_0 codes, boxes of 128 bytes x 128 rows (one block of one
+// [rows][128] 8-bit codes (Q8_0 or e4m3), boxes of 128 bytes x 128 rows (one block of one
 // KV head), 128-byte swizzle.
 bool encode_code_map(CUtensorMap* map, const void* pool, long long rows) {
   auto fn = encode_fn();
@@ -289,7 +289,7 @@ kt_status select_impl(const void* q, const kt_paged_kv* kv, const void* reps,
 // (sel_pages) are used directly, and its counts are min(top_k, C) unless
 // counts_vary (a preselection can leave fewer candidates; cnt is then read).
 // KV source of an attention-only launch (KVM_*): for KVM_HOST the device
-// addresses of the host pools; for KVM_Q8 the code and scale pools.
+// addresses of the host pools; for KVM_Q8 and KVM_F8 the code and scale pools.
 struct KvSource {
   int kvm = KVM_F16;
   const void* k_src = nullptr;
@@ -309,8 +309,8 @@ kt_status attn_impl(const void* q, const kt_paged_kv* kv, int num_q_heads, float
   if (src.kvm == KVM_F16 &&
       (!make_pool_map(&kmap, kv->k_pool, kv) || !make_pool_map(&vmap, kv->v_pool, kv)))
     return KT_ERR_CUDA;
-  if (src.kvm == KVM_Q8 && (!make_pool_map(&kmap, src.k_src, kv, true) ||
-                            !make_pool_map(&vmap, src.v_src, kv, true)))
+  if ((src.kvm == KVM_Q8 || src.kvm == KVM_F8) &&
+      (!make_pool_map(&kmap, src.k_src, kv, true) || !make_pool_map(&vmap, src.v_src, kv, true)))
     return KT_ERR_CUDA;
   const int sms = cta_budget();
   if (sms <= 0) return KT_ERR_CUDA;
@@ -802,7 +802,7 @@ kt_status step_impl(const void* q, const kt_paged_kv* kv, const void* reps_pool,
   if (sms > 0 && fused_plan(kv, p, sms, &ncpu, &chunk, &kk)) {
     // one launch: selection inside the attention kernel
     CUtensorMap kmap, vmap;
-    const bool codes = src.kvm == KVM_Q8;
+    const bool codes = src.kvm == KVM_Q8 || src.kvm == KVM_F8;
     if (!make_pool_map(&kmap, codes ? src.k_src : kv->k_pool, kv, codes) ||
         !make_pool_map(&vmap, codes ? src.v_src : kv->v_pool, kv, codes))
       return KT_ERR_CUDA;
@@ -1057,6 +1057,423 @@ kt_status kt_append_kv(const kt_paged_kv* kv, const kt_sparse_params* p, const v
   r.first_block = -1;
   r.num_blocks = 1;
   return cuda_status(launch_reps(r, (cudaStream_t)stream));
+}
+
+// ---- rotary positions, and the 8-bit cache with a scale per block and head ----
+
+kt_status kt_rope_init(const kt_rope_params* rp, kt_rope* rope) {
+  if (!rp || !rope) return KT_ERR_INVALID_ARG;
+  const int rot = rp->rotary_dim, half = rot / 2;
+  if (rot < 2 || rot > D || rot % 2 != 0) return KT_ERR_INVALID_ARG;
+  if (rp->layout != KT_ROPE_HALF && rp->layout != KT_ROPE_PAIRS) return KT_ERR_INVALID_ARG;
+  if (!(rp->theta > 1.0) || !std::isfinite(rp->theta) || !(rp->factor >= 1.0) ||
+      !std::isfinite(rp->factor))
+    return KT_ERR_INVALID_ARG;
+  const double two_pi = 6.283185307179586;
+  double theta = rp->theta, amplitude = 1.0, lo = 0.0, hi = 0.0;
+  switch (rp->scaling) {
+    case KT_ROPE_PLAIN:
+      if (rp->factor != 1.0) return KT_ERR_INVALID_ARG;
+      break;
+    case KT_ROPE_LINEAR:
+      break;
+    case KT_ROPE_NTK:
+      if (rot == 2) return KT_ERR_INVALID_ARG;
+      theta *= std::pow(rp->factor, (double)rot / (rot - 2));
+      if (!std::isfinite(theta)) return KT_ERR_INVALID_ARG;
+      break;
+    case KT_ROPE_YARN:
+    case KT_ROPE_BANDS:
+      if (rp->original_len < 1 || !(rp->beta_slow > 0.0) || !(rp->beta_fast > rp->beta_slow) ||
+          !std::isfinite(rp->beta_fast))
+        return KT_ERR_INVALID_ARG;
+      if (rp->scaling == KT_ROPE_YARN) {
+        auto edge = [&](double beta) {
+          return rot * std::log(rp->original_len / (beta * two_pi)) / (2.0 * std::log(theta));
+        };
+        lo = std::fmin(std::fmax(std::floor(edge(rp->beta_fast)), 0.0), rot - 1.0);
+        hi = std::fmin(std::fmax(std::ceil(edge(rp->beta_slow)), 0.0), rot - 1.0);
+        amplitude = 0.1 * std::log(rp->factor) + 1.0;
+      }
+      break;
+    default:
+      return KT_ERR_INVALID_ARG;
+  }
+  std::memset(rope, 0, sizeof(*rope));
+  for (int i = 0; i < half; ++i) {
+    double f = std::pow(theta, -2.0 * i / rot);
+    if (rp->scaling == KT_ROPE_LINEAR) f /= rp->factor;
+    if (rp->scaling == KT_ROPE_YARN) {
+      const double r = std::fmin(std::fmax((i - lo) / std::fmax(hi - lo, 0.001), 0.0), 1.0);
+      f = f / rp->factor * r + f * (1.0 - r);
+    }
+    if (rp->scaling == KT_ROPE_BANDS) {
+      const double t = rp->original_len * f / two_pi;
+      const double w = std::fmin(
+          std::fmax((t - rp->beta_slow) / (rp->beta_fast - rp->beta_slow), 0.0), 1.0);
+      f = f * w + f / rp->factor * (1.0 - w);
+    }
+    // f <= 1: the fraction is below 2^62
+    rope->phase[i] = (uint64_t)std::llrint(f / two_pi * 0x1.0p64);
+  }
+  rope->amplitude = (float)amplitude;
+  rope->rotary_dim = rot;
+  rope->layout = rp->layout;
+  return KT_OK;
+}
+
+namespace {
+bool rope_ok(const kt_rope* r) {
+  return r->rotary_dim >= 2 && r->rotary_dim <= D && r->rotary_dim % 2 == 0 &&
+         (r->layout == KT_ROPE_HALF || r->layout == KT_ROPE_PAIRS) &&
+         std::isfinite(r->amplitude);
+}
+
+constexpr int MAX_ROW_HEADS = 4096;
+int dtype_bytes(int dtype) { return dtype == KT_F32 ? 4 : 2; }
+
+kt_status check_rows(const kt_rows* r) {
+  if (!r || !r->data || !aligned16(r->data) || r->heads < 1) return KT_ERR_INVALID_ARG;
+  if (r->dtype != KT_F16 && r->dtype != KT_BF16 && r->dtype != KT_F32) return KT_ERR_INVALID_ARG;
+  if (r->heads > MAX_ROW_HEADS) return KT_ERR_UNSUPPORTED;
+  if (r->stride < (int64_t)r->heads * D || r->stride > ((int64_t)1 << 28) ||
+      r->stride * dtype_bytes(r->dtype) % 16 != 0)
+    return KT_ERR_INVALID_ARG;
+  return KT_OK;
+}
+
+struct Bytes {
+  uintptr_t lo, hi;
+};
+Bytes bytes_of(const void* p, size_t n) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+  return Bytes{a, a + n};
+}
+Bytes rows_bytes(const kt_rows* r, int tokens) {
+  const size_t n = (size_t)(tokens - 1) * r->stride + (size_t)r->heads * D;
+  return bytes_of(r->data, n * dtype_bytes(r->dtype));
+}
+bool overlap(Bytes a, Bytes b) { return a.lo < b.hi && b.lo < a.hi; }
+Bytes out_bytes(const kt_rows* r, const void* out, int tokens) {
+  return bytes_of(out, (size_t)tokens * r->heads * D * 2);
+}
+// whether out may be written while r is read: apart, or exactly in place
+bool out_ok(const kt_rows* r, const void* out, int tokens) {
+  if (!overlap(rows_bytes(r, tokens), out_bytes(r, out, tokens))) return true;
+  return out == r->data && r->dtype == KT_F16 && r->stride == (int64_t)r->heads * D;
+}
+
+kt_paged_kv kv_view_f8(const kt_paged_kv_f8* f) {
+  kt_paged_kv kv;
+  kv.k_pool = f->k_code;
+  kv.v_pool = f->v_code;
+  kv.block_table = f->block_table;
+  kv.seq_lens = f->seq_lens;
+  kv.batch = f->batch;
+  kv.num_kv_heads = f->num_kv_heads;
+  kv.head_dim = f->head_dim;
+  kv.block_size = f->block_size;
+  kv.max_blocks_per_seq = f->max_blocks_per_seq;
+  kv.num_pages = f->num_pages;
+  return kv;
+}
+
+// The cache's shapes as a kt_paged_kv (the code pools stand in for the binary16
+// pools in the checks; they are never read as binary16).
+kt_status check_kv_f8(const kt_paged_kv_f8* f, kt_paged_kv* kv) {
+  if (!f) return KT_ERR_INVALID_ARG;
+  *kv = kv_view_f8(f);
+  const kt_status s = check_kv(kv);
+  if (s != KT_OK) return s;
+  if (!f->k_scale || !f->v_scale || !aligned16(f->k_scale) || !aligned16(f->v_scale))
+    return KT_ERR_INVALID_ARG;
+  return KT_OK;
+}
+
+KvSource source_f8(const kt_paged_kv_f8* f) {
+  KvSource src;
+  src.kvm = KVM_F8;
+  src.k_src = f->k_code;
+  src.v_src = f->v_code;
+  src.k_scale = f->k_scale;
+  src.v_scale = f->v_scale;
+  return src;
+}
+
+constexpr size_t WS_TICKET = 64;  // append ticket, inside the status header
+}  // namespace
+
+kt_status kt_apply_rope(const kt_rope* rope, const int32_t* positions, int32_t tokens,
+                        const kt_rows* q, void* q_out, const kt_rows* k, void* k_out,
+                        kt_stream_t stream) {
+  if (!rope || !rope_ok(rope) || !positions || !aligned16(positions) || tokens < 0)
+    return KT_ERR_INVALID_ARG;
+  if ((!q && !k) || (q && !q_out) || (k && !k_out) || (!q && q_out) || (!k && k_out))
+    return KT_ERR_INVALID_ARG;
+  if ((q_out && !aligned16(q_out)) || (k_out && !aligned16(k_out))) return KT_ERR_INVALID_ARG;
+  for (const kt_rows* r : {q, k}) {
+    if (!r) continue;
+    const kt_status s = check_rows(r);
+    if (s != KT_OK) return s;
+  }
+  if (q && k && q->dtype != k->dtype) return KT_ERR_INVALID_ARG;
+  if (tokens == 0) return KT_OK;
+  if ((q && !out_ok(q, q_out, tokens)) || (k && !out_ok(k, k_out, tokens)))
+    return KT_ERR_INVALID_ARG;
+  if (q && k &&
+      (overlap(out_bytes(q, q_out, tokens), out_bytes(k, k_out, tokens)) ||
+       overlap(out_bytes(q, q_out, tokens), rows_bytes(k, tokens)) ||
+       overlap(out_bytes(k, k_out, tokens), rows_bytes(q, tokens))))
+    return KT_ERR_INVALID_ARG;
+  RopeLaunch a;
+  std::memset(&a, 0, sizeof(a));
+  a.rope = rope;
+  a.positions = positions;
+  a.q = q ? q->data : nullptr;
+  a.k = k ? k->data : nullptr;
+  a.qs = q ? q->stride : 0;
+  a.ks = k ? k->stride : 0;
+  a.q_out = static_cast<__half*>(q_out);
+  a.k_out = static_cast<__half*>(k_out);
+  a.hq = q ? q->heads : 0;
+  a.hk = k ? k->heads : 0;
+  a.tokens = tokens;
+  a.dtype = q ? q->dtype : k->dtype;
+  a.num_sms = num_sms();
+  if (a.num_sms <= 0) return KT_ERR_CUDA;
+  return cuda_status(launch_rope(a, (cudaStream_t)stream));
+}
+
+kt_status kt_workspace_bytes_f8(kt_op op, const kt_paged_kv_f8* kvf, const kt_sparse_params* p,
+                                size_t* bytes) {
+  kt_paged_kv kv;
+  const kt_status s = check_kv_f8(kvf, &kv);
+  if (s != KT_OK) return s;
+  if (op == KT_OP_DYNAMIC_REPS || op == KT_OP_PRESELECT) return KT_ERR_INVALID_ARG;
+  return kt_workspace_bytes(op, &kv, p, 0, bytes);
+}
+
+size_t kt_reps_pool_bytes_f8(const kt_paged_kv_f8* kvf, const kt_sparse_params* p) {
+  if (!kvf || !p || p->rep == KT_REP_DYNAMIC) return 0;
+  const kt_paged_kv kv = kv_view_f8(kvf);
+  return kt_reps_pool_bytes(&kv, p);
+}
+
+kt_status kt_build_block_reps_f8(const kt_paged_kv_f8* kvf, const kt_sparse_params* p,
+                                 int32_t first_block, int32_t num_blocks, void* reps_pool,
+                                 kt_stream_t stream) {
+  kt_paged_kv kv;
+  kt_status s = check_kv_f8(kvf, &kv);
+  if (s != KT_OK) return s;
+  s = check_params(&kv, p);
+  if (s != KT_OK) return s;
+  if (!reps_pool || !aligned16(reps_pool) || first_block < 0 || num_blocks < 0 ||
+      p->rep == KT_REP_DYNAMIC)
+    return KT_ERR_INVALID_ARG;
+  RepsF8Launch a;
+  a.k_code = static_cast<const uint8_t*>(kvf->k_code);
+  a.k_scale = kvf->k_scale;
+  a.table = kv.block_table;
+  a.seq_lens = kv.seq_lens;
+  a.reps = reps_pool;
+  a.B = kv.batch;
+  a.H_kv = kv.num_kv_heads;
+  a.max_blocks = kv.max_blocks_per_seq;
+  a.P = kv.num_pages;
+  a.rep = p->rep;
+  a.R = reps_rows(p);
+  a.fix_stride = p->fix_stride;
+  a.first_block = first_block;
+  const long long last = (long long)first_block + num_blocks;
+  a.num_blocks = (int)((last > a.max_blocks ? a.max_blocks : last) -
+                       (first_block > a.max_blocks ? a.max_blocks : first_block));
+  return cuda_status(launch_reps_f8(a, (cudaStream_t)stream));
+}
+
+kt_status kt_append_kv_f8(const kt_paged_kv_f8* kvf, const kt_sparse_params* p,
+                          const kt_rope* rope, const kt_rows* q, void* q_out, const kt_rows* k,
+                          const kt_rows* v, const int32_t* cu_tokens, int32_t tokens,
+                          int32_t* new_lens, void* reps_pool, void* ws, size_t ws_bytes,
+                          kt_stream_t stream) {
+  kt_paged_kv kv;
+  kt_status s = check_kv_f8(kvf, &kv);
+  if (s != KT_OK) return s;
+  s = check_params(&kv, p);
+  if (s != KT_OK) return s;
+  if (rope && !rope_ok(rope)) return KT_ERR_INVALID_ARG;
+  s = check_rows(k);
+  if (s == KT_OK) s = check_rows(v);
+  if (s == KT_OK && q) s = check_rows(q);
+  if (s != KT_OK) return s;
+  if (k->heads != kv.num_kv_heads || v->heads != kv.num_kv_heads || k->dtype != v->dtype)
+    return KT_ERR_INVALID_ARG;
+  if ((q != nullptr) != (q_out != nullptr)) return KT_ERR_INVALID_ARG;
+  if (q && (q->heads != p->num_q_heads || q->dtype != k->dtype || !aligned16(q_out)))
+    return KT_ERR_INVALID_ARG;
+  if (!ws || ws_bytes < 256 || !aligned16(ws) || (cu_tokens && !aligned16(cu_tokens)) ||
+      (new_lens && !aligned16(new_lens)) || (reps_pool && !aligned16(reps_pool)))
+    return KT_ERR_INVALID_ARG;
+  if (tokens < 0 || (!cu_tokens && tokens != kv.batch)) return KT_ERR_INVALID_ARG;
+  if (new_lens == kv.seq_lens) new_lens = nullptr;  // in place
+  if (new_lens && overlap(bytes_of(new_lens, (size_t)kv.batch * 4),
+                          bytes_of(kv.seq_lens, (size_t)kv.batch * 4)))
+    return KT_ERR_INVALID_ARG;
+  if (q && tokens > 0 &&
+      (!out_ok(q, q_out, tokens) || overlap(out_bytes(q, q_out, tokens), rows_bytes(k, tokens)) ||
+       overlap(out_bytes(q, q_out, tokens), rows_bytes(v, tokens))))
+    return KT_ERR_INVALID_ARG;
+  AppendF8Launch a;
+  a.rope = rope;
+  a.q = q ? q->data : nullptr;
+  a.k = k->data;
+  a.v = v->data;
+  a.qs = q ? q->stride : 0;
+  a.ks = k->stride;
+  a.vs = v->stride;
+  a.q_out = static_cast<__half*>(q_out);
+  a.k_code = static_cast<uint8_t*>(const_cast<void*>(kvf->k_code));
+  a.v_code = static_cast<uint8_t*>(const_cast<void*>(kvf->v_code));
+  a.k_scale = const_cast<float*>(kvf->k_scale);
+  a.v_scale = const_cast<float*>(kvf->v_scale);
+  a.table = kv.block_table;
+  a.cu = cu_tokens;
+  a.seq_lens = const_cast<int32_t*>(kv.seq_lens);
+  a.new_lens = new_lens;
+  a.reps = p->rep == KT_REP_DYNAMIC ? nullptr : reps_pool;
+  a.status = at<int>(ws, 0);
+  a.ticket = at<int>(ws, WS_TICKET);
+  a.B = kv.batch;
+  a.H_kv = kv.num_kv_heads;
+  a.H_q = q ? q->heads : 0;
+  a.max_blocks = kv.max_blocks_per_seq;
+  a.P = kv.num_pages;
+  a.tokens = tokens;
+  a.dtype = k->dtype;
+  a.rep = p->rep;
+  a.R = reps_rows(p);
+  a.fix_stride = p->fix_stride;
+  a.num_sms = num_sms();
+  if (a.num_sms <= 0) return KT_ERR_CUDA;
+  return cuda_status(launch_append_f8(a, (cudaStream_t)stream));
+}
+
+kt_status kt_read_kv_f8(const kt_paged_kv_f8* kvf, const int32_t* first, const int32_t* cu_tokens,
+                        int32_t tokens, int32_t out_dtype, void* k_out, void* v_out, void* ws,
+                        size_t ws_bytes, kt_stream_t stream) {
+  kt_paged_kv kv;
+  const kt_status s = check_kv_f8(kvf, &kv);
+  if (s != KT_OK) return s;
+  if (!cu_tokens || !aligned16(cu_tokens) || (first && !aligned16(first)) || tokens < 0 ||
+      (!k_out && !v_out) || (k_out && !aligned16(k_out)) || (v_out && !aligned16(v_out)) || !ws ||
+      ws_bytes < 256 || !aligned16(ws))
+    return KT_ERR_INVALID_ARG;
+  if (out_dtype != KT_F16 && out_dtype != KT_BF16 && out_dtype != KT_F32)
+    return KT_ERR_INVALID_ARG;
+  const size_t n = (size_t)tokens * kv.num_kv_heads * D * dtype_bytes(out_dtype);
+  if (k_out && v_out && overlap(bytes_of(k_out, n), bytes_of(v_out, n)))
+    return KT_ERR_INVALID_ARG;
+  ReadF8Launch a;
+  a.k_code = static_cast<const uint8_t*>(kvf->k_code);
+  a.v_code = static_cast<const uint8_t*>(kvf->v_code);
+  a.k_scale = kvf->k_scale;
+  a.v_scale = kvf->v_scale;
+  a.k_out = k_out;
+  a.v_out = v_out;
+  a.table = kv.block_table;
+  a.seq_lens = kv.seq_lens;
+  a.first = first;
+  a.cu = cu_tokens;
+  a.status = at<int>(ws, 0);
+  a.B = kv.batch;
+  a.H_kv = kv.num_kv_heads;
+  a.max_blocks = kv.max_blocks_per_seq;
+  a.P = kv.num_pages;
+  a.tokens = tokens;
+  a.dtype = out_dtype;
+  return cuda_status(launch_read_f8(a, (cudaStream_t)stream));
+}
+
+kt_status kt_sparse_decode_attn_f8(const void* q, const kt_paged_kv_f8* kvf,
+                                   const kt_sparse_params* p, const int32_t* sel,
+                                   const int32_t* cnt, float* out, void* ws, size_t ws_bytes,
+                                   kt_stream_t stream) {
+  kt_paged_kv kv;
+  kt_status s = check_kv_f8(kvf, &kv);
+  if (s != KT_OK) return s;
+  s = check_params(&kv, p);
+  if (s != KT_OK) return s;
+  if (!q || !sel || !cnt || !out || !ws || !aligned16(q) || !aligned16(out) || !aligned16(ws))
+    return KT_ERR_INVALID_ARG;
+  const WsLayout L = layout(KT_OP_SPARSE_ATTN, &kv, p, 0);
+  if (ws_bytes < L.total) return KT_ERR_WORKSPACE_TOO_SMALL;
+  return attn_impl(q, &kv, p->num_q_heads, p->softmax_scale, p, sel, cnt, out, ws, L, false,
+                   false, (cudaStream_t)stream, false, false, source_f8(kvf));
+}
+
+kt_status kt_dense_decode_attn_f8(const void* q, const kt_paged_kv_f8* kvf, int32_t num_q_heads,
+                                  float softmax_scale, float* out, void* ws, size_t ws_bytes,
+                                  kt_stream_t stream) {
+  kt_paged_kv kv;
+  kt_status s = check_kv_f8(kvf, &kv);
+  if (s != KT_OK) return s;
+  s = check_heads(&kv, num_q_heads, softmax_scale);
+  if (s != KT_OK) return s;
+  if (!q || !out || !ws || !aligned16(q) || !aligned16(out) || !aligned16(ws))
+    return KT_ERR_INVALID_ARG;
+  kt_sparse_params p;
+  std::memset(&p, 0, sizeof(p));
+  p.num_q_heads = num_q_heads;
+  p.softmax_scale = softmax_scale;
+  p.top_k = 1;
+  p.local_blocks = 1;
+  const WsLayout L = layout(KT_OP_DENSE_ATTN, &kv, &p, 0);
+  if (ws_bytes < L.total) return KT_ERR_WORKSPACE_TOO_SMALL;
+  return attn_impl(q, &kv, num_q_heads, softmax_scale, &p, nullptr, nullptr, out, ws, L, true,
+                   false, (cudaStream_t)stream, false, false, source_f8(kvf));
+}
+
+kt_status kt_score_select_blocks_f8(const void* q, const kt_paged_kv_f8* kvf,
+                                    const void* reps_pool, const kt_sparse_params* p,
+                                    int32_t* sel, int32_t* cnt, float* sel_scores, void* ws,
+                                    size_t ws_bytes, kt_stream_t stream) {
+  kt_paged_kv kv;
+  const kt_status s = check_kv_f8(kvf, &kv);
+  if (s != KT_OK) return s;
+  if (p && p->rep == KT_REP_DYNAMIC) return KT_ERR_INVALID_ARG;
+  return kt_score_select_blocks(q, &kv, reps_pool, p, sel, cnt, sel_scores, ws, ws_bytes, stream);
+}
+
+kt_status kt_sparse_decode_step_f8(const void* q, const kt_paged_kv_f8* kvf,
+                                   const void* reps_pool, const kt_sparse_params* p,
+                                   int32_t* sel, int32_t* cnt, float* out, void* ws,
+                                   size_t ws_bytes, kt_stream_t stream) {
+  kt_paged_kv kv;
+  const kt_status s = check_kv_f8(kvf, &kv);
+  if (s != KT_OK) return s;
+  if (p && p->rep == KT_REP_DYNAMIC) return KT_ERR_INVALID_ARG;
+  return step_impl(q, &kv, reps_pool, p, nullptr, nullptr, sel, cnt, out, ws, ws_bytes, stream, 0,
+                   0, false, false, source_f8(kvf));
+}
+
+kt_status kt_decode_layer_f8(const kt_reuse_policy* pol, int32_t token_idx, int32_t layer_idx,
+                             const void* q, const kt_paged_kv_f8* kv, const void* reps_pool,
+                             const kt_sparse_params* p, int32_t* hist_sel, int32_t* hist_cnt,
+                             float* out, void* ws, size_t ws_bytes, kt_stream_t stream) {
+  int32_t action = 0, slot = 0;
+  const kt_status s = kt_decode_layer_action(pol, token_idx, layer_idx, &action, &slot);
+  if (s != KT_OK) return s;
+  if (!kv || !p) return KT_ERR_INVALID_ARG;
+  if (action == KT_LAYER_DENSE)
+    return kt_dense_decode_attn_f8(q, kv, p->num_q_heads, p->softmax_scale, out, ws, ws_bytes,
+                                   stream);
+  if (!hist_sel || !hist_cnt || p->top_k < 1 || p->top_k > MAX_TOPK) return KT_ERR_INVALID_ARG;
+  const int SEL = p->head_mode == KT_HEAD_SHARED ? 1 : kv->num_kv_heads;
+  const size_t units = (size_t)kv->batch * SEL;
+  int32_t* sel = hist_sel + (size_t)slot * units * p->top_k;
+  int32_t* cnt = hist_cnt + (size_t)slot * units;
+  if (action == KT_LAYER_SELECT)
+    return kt_sparse_decode_step_f8(q, kv, reps_pool, p, sel, cnt, out, ws, ws_bytes, stream);
+  return kt_sparse_decode_attn_f8(q, kv, p, sel, cnt, out, ws, ws_bytes, stream);
 }
 
 kt_status kt_read_device_status(void* ws, size_t ws_bytes, kt_stream_t stream,

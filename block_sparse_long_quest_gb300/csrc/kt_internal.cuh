@@ -45,9 +45,11 @@ constexpr int FUSED_MAX_CHUNK = 8 * ATTN_CONSUMER_THREADS;  // blocks one CTA sc
 enum : int { SK_NONE = 0, SK_COLS = 1, SK_LINEAR = 2, SK_MMA = 3, SK_F32 = 4, SK_MULTI = 5 };
 // Where the attention-only kernel reads K and V: fp16 pools in device memory
 // (2-D TMA), fp16 pools in host memory the GPU reads over NVLink-C2C (16-byte
-// cp.async by the producer warp), or Q8_0 pools in device memory (TMA of the
-// int8 codes and bulk copies of the binary16 scales, dequantised per warp).
-enum : int { KVM_F16 = 0, KVM_HOST = 1, KVM_Q8 = 2 };
+// cp.async by the producer warp), Q8_0 pools in device memory (TMA of the
+// int8 codes and bulk copies of the binary16 scales, dequantised per warp), or
+// e4m3 pools with a scale per block and head (TMA of the codes, turned into
+// binary16 in registers).
+enum : int { KVM_F16 = 0, KVM_HOST = 1, KVM_Q8 = 2, KVM_F8 = 3 };
 // the most fp16 blocks a CTA scores on the CUDA cores in one pass
 __host__ __device__ inline int fused_lin_max(int V) {
   return 8 * (ATTN_CONSUMER_THREADS / 32) / (V <= 32 ? 1 : V <= 64 ? 2 : V <= 128 ? 4 : 8);
@@ -352,6 +354,35 @@ __device__ __forceinline__ void mma_16816_sched(float* d, uint32_t a0, uint32_t 
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// e4m3 codes <-> binary16: the low / high two codes of a word as binary16 (exact),
+// and four binary16 as codes (nearest even, saturating).
+__device__ __forceinline__ uint32_t f8x2_lo(uint32_t v) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}"
+      : "=r"(r)
+      : "r"(v));
+  return r;
+}
+__device__ __forceinline__ uint32_t f8x2_hi(uint32_t v) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}"
+      : "=r"(r)
+      : "r"(v));
+  return r;
+}
+__device__ __forceinline__ uint32_t h4_to_f8(uint32_t lo, uint32_t hi) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tcvt.rn.satfinite.e4m3x2.f16x2 l, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 h, %2;\n\tmov.b32 %0, {l, h};\n\t}"
+      : "=r"(r)
+      : "r"(lo), "r"(hi));
+  return r;
+}
+
+// 4-byte asynchronous copy global -> shared.
+__device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
 // 16-byte asynchronous copy global -> shared (L2 only), 16-byte aligned both.
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -537,7 +568,8 @@ struct AttnLaunch {
   unsigned long long* stamps;   // nullable: [grid][KT_PHASE_STAMPS] global-timer stamps
   // attention-only kernel, KV source (KVM_*): KVM_HOST reads k_src / v_src
   // (device-accessible host pools, fp16); KVM_Q8 reads the int8 codes through
-  // kmap / vmap and the binary16 scales [pages][H_kv][128][4] at k_scale / v_scale
+  // kmap / vmap and the binary16 scales [pages][H_kv][128][4] at k_scale / v_scale;
+  // KVM_F8 the e4m3 codes and the binary32 scales [pages][H_kv]
   int kvm;
   const void* k_src;
   const void* v_src;
@@ -585,6 +617,68 @@ struct QuantLaunch {
   int first_page, num_pages, H_kv;
 };
 cudaError_t launch_quant(const QuantLaunch& a, cudaStream_t stream);
+
+// Rotation of q and k rows (kt_apply_rope).
+struct RopeLaunch {
+  const kt_rope* rope;
+  const int32_t* positions;
+  const void* q;
+  const void* k;
+  long long qs, ks;
+  __half* q_out;
+  __half* k_out;
+  int hq, hk, tokens, dtype, num_sms;
+};
+cudaError_t launch_rope(const RopeLaunch& a, cudaStream_t stream);
+
+// The 8-bit cache: quantising append, representatives, read-back.
+struct AppendF8Launch {
+  const kt_rope* rope;  // nullable
+  const void* q;        // nullable
+  const void* k;
+  const void* v;
+  long long qs, ks, vs;
+  __half* q_out;
+  uint8_t* k_code;
+  uint8_t* v_code;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* table;
+  const int32_t* cu;  // nullable: one row per sequence
+  int32_t* seq_lens;
+  int32_t* new_lens;  // nullable: seq_lens in place
+  void* reps;         // nullable
+  int* status;
+  int* ticket;        // zero between calls
+  int B, H_kv, H_q, max_blocks, P, tokens, dtype, rep, R, fix_stride, num_sms;
+};
+cudaError_t launch_append_f8(const AppendF8Launch& a, cudaStream_t stream);
+
+struct RepsF8Launch {
+  const uint8_t* k_code;
+  const float* k_scale;
+  const int32_t* table;
+  const int32_t* seq_lens;
+  void* reps;
+  int B, H_kv, max_blocks, P, rep, R, fix_stride, first_block, num_blocks;
+};
+cudaError_t launch_reps_f8(const RepsF8Launch& a, cudaStream_t stream);
+
+struct ReadF8Launch {
+  const uint8_t* k_code;
+  const uint8_t* v_code;
+  const float* k_scale;
+  const float* v_scale;
+  void* k_out;  // nullable
+  void* v_out;  // nullable
+  const int32_t* table;
+  const int32_t* seq_lens;
+  const int32_t* first;  // nullable: zeros
+  const int32_t* cu;
+  int* status;
+  int B, H_kv, max_blocks, P, tokens, dtype;
+};
+cudaError_t launch_read_f8(const ReadF8Launch& a, cudaStream_t stream);
 
 struct RepsLaunch {
   const __half* k_pool;

@@ -1,0 +1,690 @@
+// kv_f8.cu — the 8-bit KV cache: e4m3 codes with one binary32 scale per (page,
+// KV head): quantising append, representatives and read-back.
+//
+// Scale of a block and head: 2^e, the least e in [-15, 8] with amax <= 448 2^e.
+// A power of two makes x / s exact, so a code is one rounding of x, and coding
+// an old row again for a grown scale only shifts its exponent (a rounding is
+// left only where it becomes subnormal).  e >= -15 keeps the least code 2^-9 a
+// binary16 value; at e = 8 codes stop at 240 (61440) because 256 * 2^8 is not.
+//
+// Append: one CTA per (block touched, K or V, group of heads), 256 threads over
+// the 128 x 128 tile: lane group (8 lanes) r takes rows r, r + 32, r + 64, r + 96,
+// each lane two 8-channel vectors of a row (the two of a rotation pair).  The
+// tile stays in registers as binary16 between the maximum and the coding, so new
+// rows are read once.  (cos, sin) of the tile's rows are computed once per CTA
+// into shared memory and serve all its heads.  A tile that the call completes
+// has its representatives made from the codes in shared memory.  The rotation
+// of q rides in the same launch on CTAs of its own, and one more CTA writes the
+// lengths (in place: the CTA that finishes last does).
+#include "rope.cuh"
+
+namespace kt {
+namespace {
+
+constexpr int THREADS = 256;
+constexpr int WARPS = THREADS / 32;
+constexpr int ROWS_PER = BS / (THREADS / ROPE_UNITS);  // row steps of a lane: 4
+constexpr int Q_TOK = 4;                               // tokens of a q CTA at most
+constexpr int RED_BYTES = 2 * WARPS * D * 2;           // representatives: partials per warp
+constexpr int TILE_BYTES = BS * D;
+
+struct Params {
+  kt_rope rope;  // rotary_dim 0: no rotation
+  const void* q;
+  const void* k;
+  const void* v;
+  long long qs, ks, vs;
+  __half* q_out;
+  uint8_t* k_code;
+  uint8_t* v_code;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* table;
+  const int32_t* cu;
+  int32_t* seq_lens;
+  int32_t* new_lens;
+  void* reps;
+  int* status;
+  int* ticket;
+  int B, H_kv, H_q, max_blocks, P, tokens, rep, R, fix_stride;
+  int heads_per, groups, cache_ctas, q_ctas, q_per, cs_rows;
+};
+
+struct Span {
+  int n, m, c0, blocks;  // cached tokens, new rows, first row, blocks touched
+};
+
+__device__ __forceinline__ Span seq_span(const Params& p, int s, bool flag) {
+  Span a;
+  a.n = p.seq_lens[s];
+  a.c0 = p.cu ? p.cu[s] : s;
+  a.m = p.cu ? p.cu[s + 1] - a.c0 : 1;
+  if (a.m < 0 || a.c0 < 0 || (long long)a.c0 + a.m > p.tokens || a.n < 0 ||
+      (long long)a.n + a.m > (long long)p.max_blocks * BS) {
+    if (flag) set_status(p.status, KT_ERR_DEVICE_CHECK);
+    a.m = 0;
+  }
+  a.blocks = a.m > 0 ? (a.n + a.m - 1) / BS - a.n / BS + 1 : 0;
+  return a;
+}
+
+__device__ __forceinline__ __half2 as_h2(uint32_t v) { return *reinterpret_cast<__half2*>(&v); }
+__device__ __forceinline__ uint32_t as_u32(__half2 v) { return *reinterpret_cast<uint32_t*>(&v); }
+
+// The scale of values up to amax (a binary16 value or infinity): 448 = 1.75 * 2^8, so
+// e is the exponent of amax less 8, one more where its mantissa exceeds 1.75.
+__device__ __forceinline__ float block_scale(float amax) {
+  const int e = (int)((__float_as_uint(amax) + 0x1FFFFFu) >> 23) - 127 - 8;
+  return __uint_as_float((uint32_t)(min(max(e, -15), 8) + 127) << 23);
+}
+__device__ __forceinline__ bool scale_ok(float s) {
+  const uint32_t u = __float_as_uint(s);
+  return (u & 0x807FFFFFu) == 0u && u >= ((127u - 15u) << 23) && u <= ((127u + 8u) << 23);
+}
+
+// Eight binary16 (four words) / s, as codes.
+__device__ __forceinline__ uint2 code8(const uint32_t (&h)[4], __half2 inv, bool top) {
+  uint32_t y[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    __half2 v = __hmul2(as_h2(h[i]), inv);  // exact where the code is not zero
+    if (top) {
+      const __half2 m = __float2half2_rn(240.0f);
+      v = __hmax2_nan(__hmin2_nan(v, m), __hneg2(m));
+    }
+    y[i] = as_u32(v);
+  }
+  return make_uint2(h4_to_f8(y[0], y[1]), h4_to_f8(y[2], y[3]));
+}
+
+// Codes of an old scale under a new one: round(code * ratio), ratio a power of two.
+__device__ __forceinline__ uint32_t recode4(uint32_t c, float ratio) {
+  uint32_t h[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float2 f = __half22float2(as_h2(i ? f8x2_hi(c) : f8x2_lo(c)));
+    // exact in binary16 from 2^-14 on (a code has 4 significant bits), and what
+    // is smaller lies far below half the least code
+    h[i] = as_u32(__floats2half2_rn(f.x * ratio, f.y * ratio));
+  }
+  return h4_to_f8(h[0], h[1]);
+}
+
+// Representatives of a full tile of codes in shared memory, written at rep row
+// `row0` of the pool.  red: RED_BYTES of shared memory.  Every thread calls it.
+__device__ void tile_reps(const uint8_t* tile, float s, int rep, int R, int fix_stride, void* reps,
+                          size_t row0, uint8_t* red, int tid) {
+  const int warp = tid >> 5, lane = tid & 31;
+  const uint32_t* words = reinterpret_cast<const uint32_t*>(tile);
+  const __half2 s2 = __float2half2_rn(s);  // 2^e is a binary16 value, and so is every product
+  if (rep == KT_REP_FIX) {
+    uint2* out = reinterpret_cast<uint2*>(static_cast<__half*>(reps) + row0 * D);
+    for (int i = tid; i < R * 32; i += THREADS) {
+      const uint32_t c = words[(i >> 5) * fix_stride * 32 + (i & 31)];
+      out[i] = make_uint2(as_u32(__hmul2(as_h2(f8x2_lo(c)), s2)),
+                          as_u32(__hmul2(as_h2(f8x2_hi(c)), s2)));
+    }
+    return;
+  }
+  const int r0 = warp * (BS / WARPS);
+  if (rep == KT_REP_MEAN) {
+    // a code is a whole number of 2^-9, at most 448 * 2^9: 128 of them are below 2^25
+    int acc[4] = {0, 0, 0, 0};
+#pragma unroll 4
+    for (int r = r0; r < r0 + BS / WARPS; ++r) {
+      const uint32_t c = words[r * 32 + lane];
+      const float2 a = __half22float2(as_h2(f8x2_lo(c)));
+      const float2 b = __half22float2(as_h2(f8x2_hi(c)));
+      acc[0] += __float2int_rn(a.x * 512.0f);
+      acc[1] += __float2int_rn(a.y * 512.0f);
+      acc[2] += __float2int_rn(b.x * 512.0f);
+      acc[3] += __float2int_rn(b.y * 512.0f);
+    }
+    int4* part = reinterpret_cast<int4*>(red);
+    part[warp * 32 + lane] = make_int4(acc[0], acc[1], acc[2], acc[3]);
+    __syncthreads();
+    if (tid < D) {
+      int sum = 0;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) sum += reinterpret_cast<const int*>(red)[w * D + tid];
+      // one rounding; the factors are powers of two
+      static_cast<float*>(reps)[row0 * D + tid] = __int2float_rn(sum) * 0x1.0p-16f * s;
+    }
+    return;
+  }
+  __half2 mx[2], mn[2];
+  mx[0] = mx[1] = __float2half2_rn(-INFINITY);
+  mn[0] = mn[1] = __float2half2_rn(INFINITY);
+#pragma unroll 4
+  for (int r = r0; r < r0 + BS / WARPS; ++r) {
+    const uint32_t c = words[r * 32 + lane];
+    const __half2 a = as_h2(f8x2_lo(c)), b = as_h2(f8x2_hi(c));
+    mx[0] = __hmax2(mx[0], a);
+    mx[1] = __hmax2(mx[1], b);
+    mn[0] = __hmin2(mn[0], a);
+    mn[1] = __hmin2(mn[1], b);
+  }
+  uint2* part = reinterpret_cast<uint2*>(red);
+  part[warp * 32 + lane] = make_uint2(as_u32(mx[0]), as_u32(mx[1]));
+  part[(WARPS + warp) * 32 + lane] = make_uint2(as_u32(mn[0]), as_u32(mn[1]));
+  __syncthreads();
+  // warp 0: the maxima, warp 1 (Quest): the minima
+  if (warp == 0 || (warp == 1 && rep == KT_REP_QUEST)) {
+    uint2 v = part[warp * WARPS * 32 + lane];
+    __half2 a = as_h2(v.x), b = as_h2(v.y);
+#pragma unroll
+    for (int w = 1; w < WARPS; ++w) {
+      v = part[(warp * WARPS + w) * 32 + lane];
+      a = warp ? __hmin2(a, as_h2(v.x)) : __hmax2(a, as_h2(v.x));
+      b = warp ? __hmin2(b, as_h2(v.y)) : __hmax2(b, as_h2(v.y));
+    }
+    const size_t row = row0 + (rep == KT_REP_QUEST && warp == 0 ? 1 : 0);
+    reinterpret_cast<uint2*>(static_cast<__half*>(reps) + row * D)[lane] =
+        make_uint2(as_u32(__hmul2(a, s2)), as_u32(__hmul2(b, s2)));
+  }
+}
+static_assert(RED_BYTES >= WARPS * D * 4, "the sums of the means fit the partials");
+
+// The sequence and block of tile `tile` of the call (false: behind the last), by
+// all threads.  sh: WARPS + 8 ints.
+__device__ bool find_tile(const Params& p, int tile, int* sh, int tid, int* b_out, int* j_out,
+                          Span* a_out) {
+  if (!p.cu) {
+    *b_out = tile;
+    *a_out = seq_span(p, tile, true);
+    *j_out = a_out->n / BS;
+    return a_out->blocks > 0;
+  }
+  const int warp = tid >> 5, lane = tid & 31;
+  int before = 0;
+  for (int s0 = 0; s0 < p.B; s0 += THREADS) {
+    const int s = s0 + tid;
+    Span a;
+    a.n = a.m = a.c0 = a.blocks = 0;
+    if (s < p.B) a = seq_span(p, s, true);
+    int incl = a.blocks;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) sh[warp] = incl;
+    if (tid == 0) sh[WARPS] = -1;
+    __syncthreads();
+    int total = 0, off = before;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      if (w < warp) off += sh[w];
+      total += sh[w];
+    }
+    incl += off;
+    if (tile < incl && tile >= incl - a.blocks) {
+      sh[WARPS] = s;
+      sh[WARPS + 1] = a.n / BS + (tile - (incl - a.blocks));
+      sh[WARPS + 2] = a.n;
+      sh[WARPS + 3] = a.m;
+      sh[WARPS + 4] = a.c0;
+    }
+    __syncthreads();
+    const int hit = sh[WARPS];
+    if (hit >= 0) {
+      *b_out = hit;
+      *j_out = sh[WARPS + 1];
+      a_out->n = sh[WARPS + 2];
+      a_out->m = sh[WARPS + 3];
+      a_out->c0 = sh[WARPS + 4];
+      a_out->blocks = 1;
+      return true;
+    }
+    before += total;
+    __syncthreads();
+  }
+  return false;
+}
+
+// The lengths after the call: a warp takes 32 sequences; the pages of a span of
+// many blocks are looked up by the whole warp.
+__device__ void write_lengths(const Params& p, int tid) {
+  const int warp = tid >> 5, lane = tid & 31;
+  int32_t* dst = p.new_lens ? p.new_lens : p.seq_lens;
+  for (int s0 = warp * 32; s0 < p.B; s0 += THREADS) {
+    const int s = s0 + lane;
+    Span a;
+    a.n = a.m = a.c0 = a.blocks = 0;
+    if (s < p.B) a = seq_span(p, s, true);
+    bool ok = true;
+    const int j0 = a.blocks ? a.n / BS : 0;
+    if (a.blocks <= 2)
+      for (int j = j0; j < j0 + a.blocks; ++j)
+        ok = ok && (unsigned)p.table[(size_t)s * p.max_blocks + j] < (unsigned)p.P;
+    unsigned int many = __ballot_sync(0xffffffffu, a.blocks > 2);
+    while (many) {
+      const int src = __ffs(many) - 1;
+      many &= many - 1;
+      const int nb = __shfl_sync(0xffffffffu, a.blocks, src);
+      const int f = __shfl_sync(0xffffffffu, j0, src);
+      const int32_t* row = p.table + (size_t)(s0 + src) * p.max_blocks + f;
+      bool good = true;
+#pragma unroll 4
+      for (int i = lane; i < nb; i += 32) good = good && (unsigned)row[i] < (unsigned)p.P;
+      good = __all_sync(0xffffffffu, good);
+      if (lane == src) ok = good;
+    }
+    if (s < p.B) {
+      if (!ok) set_status(p.status, KT_ERR_DEVICE_CHECK);
+      dst[s] = a.n + (ok ? a.m : 0);
+    }
+  }
+}
+
+template <class T>
+__device__ void append_tile(const Params& p, int cta, uint8_t* smem, int* sh, int tid) {
+  const int warp = tid >> 5, lane = tid & 31;
+  const int per_tile = 2 * p.groups;
+  const int tile = cta / per_tile, rest = cta - tile * per_tile;
+  const bool is_v = rest >= p.groups;
+  const int h0 = (is_v ? rest - p.groups : rest) * p.heads_per;
+  const int h1 = min(h0 + p.heads_per, p.H_kv);
+  int b, j;
+  Span a;
+  if (!find_tile(p, tile, sh, tid, &b, &j, &a)) return;
+  const int r0 = j == a.n / BS ? a.n % BS : 0, r1 = min(BS, a.n + a.m - j * BS);
+  const int page = p.table[(size_t)b * p.max_blocks + j];
+  if ((unsigned)page >= (unsigned)p.P) {
+    if (tid == 0) set_status(p.status, KT_ERR_DEVICE_CHECK);
+    return;
+  }
+  float2* cs = reinterpret_cast<float2*>(smem);
+  uint8_t* codes = smem + p.cs_rows * 64 * sizeof(float2);
+  uint8_t* red = codes + TILE_BYTES;
+  const bool turn = !is_v && p.rope.rotary_dim > 0;
+  int va, vb;
+  row_vectors(p.rope, tid & (ROPE_UNITS - 1), &va, &vb);
+  if (turn) {
+    const int half = p.rope.rotary_dim >> 1;
+    for (int i = tid; i < (r1 - r0) * 64; i += THREADS)
+      if ((i & 63) < half) cs[i] = rope_cos_sin(p.rope, i & 63, j * BS + r0 + (i >> 6));
+    __syncthreads();
+  }
+  const T* src = static_cast<const T*>(is_v ? p.v : p.k);
+  const long long stride = is_v ? p.vs : p.ks;
+  const long long tok0 = (long long)a.c0 + ((long long)j * BS + r0 - a.n);
+  const bool complete = !is_v && p.reps && r1 == BS;
+  float* red_max = reinterpret_cast<float*>(sh);
+  for (int h = h0; h < h1; ++h) {
+    const size_t slab = (size_t)page * p.H_kv + h;
+    float* scale = (is_v ? p.v_scale : p.k_scale) + slab;
+    uint8_t* dst = (is_v ? p.v_code : p.k_code) + slab * TILE_BYTES;
+    const float old = r0 > 0 ? *scale : 0.0f;
+    uint32_t xa[ROWS_PER][4], xb[ROWS_PER][4];
+    __half2 mx = __float2half2_rn(0.0f);
+#pragma unroll
+    for (int i = 0; i < ROWS_PER; ++i) {
+      const int r = (tid >> 3) + i * (THREADS / ROPE_UNITS);
+      if (r >= r0 && r < r1) {
+        const T* row = src + (tok0 + (r - r0)) * stride + h * D;
+        float x[8], y[8];
+        load8(row + 8 * va, x);
+        load8(row + 8 * vb, y);
+        if (turn) rope_rotate(p.rope, cs + (r - r0) * 64, row, va, vb, x, y);
+        pack8(x, xa[i]);
+        pack8(y, xb[i]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          mx = __hmax2(mx, __habs2(as_h2(xa[i][e])));
+          mx = __hmax2(mx, __habs2(as_h2(xb[i][e])));
+        }
+      }
+    }
+    float am = fmaxf(__low2float(mx), __high2float(mx));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+    __syncthreads();  // the readers of sh, and the previous head's of codes, are done
+    if (lane == 0) red_max[warp] = am;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) am = fmaxf(am, red_max[w]);
+    float s = block_scale(am);
+    bool again = false;
+    if (r0 > 0) {
+      if (!scale_ok(old)) {
+        if (tid == 0) set_status(p.status, KT_ERR_DEVICE_CHECK);
+      } else {
+        s = fmaxf(s, old);
+        again = s > old;
+      }
+    }
+    const float ratio = again ? old / s : 1.0f;
+    const __half2 inv = __float2half2_rn(1.0f / s);
+    const bool top = s == 256.0f;
+#pragma unroll
+    for (int i = 0; i < ROWS_PER; ++i) {
+      const int r = (tid >> 3) + i * (THREADS / ROPE_UNITS);
+      uint2* da = reinterpret_cast<uint2*>(dst + r * D + 8 * va);
+      uint2* db = reinterpret_cast<uint2*>(dst + r * D + 8 * vb);
+      uint2 ca, cb;
+      if (r >= r0 && r < r1) {
+        ca = code8(xa[i], inv, top);
+        cb = code8(xb[i], inv, top);
+        *da = ca;
+        *db = cb;
+      } else if (r < r0 && (again || complete)) {
+        ca = *da;
+        cb = *db;
+        if (again) {
+          ca = make_uint2(recode4(ca.x, ratio), recode4(ca.y, ratio));
+          cb = make_uint2(recode4(cb.x, ratio), recode4(cb.y, ratio));
+          *da = ca;
+          *db = cb;
+        }
+      } else {
+        continue;
+      }
+      if (complete) {
+        *reinterpret_cast<uint2*>(codes + r * D + 8 * va) = ca;
+        *reinterpret_cast<uint2*>(codes + r * D + 8 * vb) = cb;
+      }
+    }
+    // every thread has read the old scale before the barriers above
+    if (tid == 0) *scale = s;
+    if (complete) {
+      __syncthreads();
+      tile_reps(codes, s, p.rep, p.R, p.fix_stride, p.reps, slab * p.R, red, tid);
+    }
+  }
+}
+
+template <class T>
+__device__ void append_q(const Params& p, int cta, uint8_t* smem, int* sh, int tid) {
+  const int t0 = cta * p.q_per, ntok = min(p.q_per, p.tokens - t0);
+  float2* cs = reinterpret_cast<float2*>(smem);
+  if (p.rope.rotary_dim > 0) {
+    if (tid < ntok) {
+      const int t = t0 + tid;
+      int s = t, first = t;
+      if (p.cu) {  // the last sequence that begins at or before row t
+        int lo = 0, hi = p.B - 1;
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) >> 1;
+          if (p.cu[mid] <= t) lo = mid; else hi = mid - 1;
+        }
+        s = lo;
+        first = p.cu[s];
+      }
+      sh[tid] = p.seq_lens[s] + (t - first);
+    }
+    __syncthreads();
+    for (int i = tid; i < ntok * 64; i += THREADS)
+      if ((i & 63) < p.rope.rotary_dim / 2) cs[i] = rope_cos_sin(p.rope, i & 63, sh[i >> 6]);
+    __syncthreads();
+  }
+  rope_tokens(p.rope, cs, t0, ntok, static_cast<const T*>(p.q), p.qs, p.H_q, p.q_out,
+              static_cast<const T*>(nullptr), 0, 0, nullptr, tid, THREADS);
+}
+
+template <class T>
+__global__ void __launch_bounds__(THREADS, 2) append_f8_kernel(const __grid_constant__ Params p) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ int sh[WARPS + 8];
+  static_assert(Q_TOK <= WARPS + 8, "positions of a q CTA");
+  griddep_wait();
+  griddep_launch_dependents();
+  const int tid = threadIdx.x, cta = blockIdx.x;
+  if (cta < p.cache_ctas)
+    append_tile<T>(p, cta, smem, sh, tid);
+  else if (cta < p.cache_ctas + p.q_ctas)
+    append_q<T>(p, cta - p.cache_ctas, smem, sh, tid);
+  else if (p.new_lens)
+    write_lengths(p, tid);
+  if (!p.new_lens) {
+    // in place: once every CTA has read the lengths
+    __syncthreads();
+    if (tid == 0) {
+      const int before = atom_acq_rel_gpu_add(p.ticket, 1);
+      sh[0] = before + 1 == (int)gridDim.x;
+      if (sh[0]) *p.ticket = 0;
+    }
+    __syncthreads();
+    if (sh[0]) write_lengths(p, tid);
+  }
+}
+
+struct RepsParams {
+  const uint8_t* k_code;
+  const float* k_scale;
+  const int32_t* table;
+  const int32_t* seq_lens;
+  void* reps;
+  int H_kv, max_blocks, P, rep, R, fix_stride, first_block;
+};
+
+// One CTA per (logical block, KV head, sequence): the tile of codes through
+// shared memory, read once.
+__global__ void __launch_bounds__(THREADS) reps_f8_kernel(const __grid_constant__ RepsParams p) {
+  __shared__ __align__(16) uint8_t tile[TILE_BYTES];
+  __shared__ __align__(16) uint8_t red[RED_BYTES];
+  const int j = p.first_block + (int)(blockIdx.x / (unsigned)p.H_kv);
+  const int h = (int)(blockIdx.x % (unsigned)p.H_kv), b = blockIdx.y, tid = threadIdx.x;
+  if (j >= p.max_blocks || (long long)(j + 1) * BS > p.seq_lens[b]) return;
+  const int page = p.table[(size_t)b * p.max_blocks + j];
+  if ((unsigned)page >= (unsigned)p.P) return;
+  const size_t slab = (size_t)page * p.H_kv + h;
+  const uint4* src = reinterpret_cast<const uint4*>(p.k_code + slab * TILE_BYTES);
+#pragma unroll
+  for (int i = 0; i < TILE_BYTES / 16 / THREADS; ++i)
+    reinterpret_cast<uint4*>(tile)[tid + i * THREADS] = __ldg(src + tid + i * THREADS);
+  __syncthreads();
+  tile_reps(tile, p.k_scale[slab], p.rep, p.R, p.fix_stride, p.reps, slab * p.R, red, tid);
+}
+
+struct ReadParams {
+  const uint8_t* code[2];
+  const float* scale[2];
+  void* out[2];
+  const int32_t* table;
+  const int32_t* seq_lens;
+  const int32_t* first;
+  const int32_t* cu;
+  int* status;
+  int B, H_kv, max_blocks, P, tokens;
+};
+
+__device__ __forceinline__ void store4(__half* p, float2 a, float2 b) {
+  *reinterpret_cast<uint2*>(p) =
+      make_uint2(as_u32(__floats2half2_rn(a.x, a.y)), as_u32(__floats2half2_rn(b.x, b.y)));
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float2 a, float2 b) {
+  const __nv_bfloat162 x = __floats2bfloat162_rn(a.x, a.y), y = __floats2bfloat162_rn(b.x, b.y);
+  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&x),
+                                            *reinterpret_cast<const uint32_t*>(&y));
+}
+__device__ __forceinline__ void store4(float* p, float2 a, float2 b) {
+  *reinterpret_cast<float4*>(p) = make_float4(a.x, a.y, b.x, b.y);
+}
+
+constexpr int READ_ROWS = 16;
+
+// A CTA takes 16 rows: one thread each finds the row's sequence, page and place;
+// then lanes read 4 codes and write 4 values, a warp one head row.
+template <class O>
+__global__ void __launch_bounds__(THREADS) read_f8_kernel(const __grid_constant__ ReadParams p) {
+  __shared__ int sh_page[READ_ROWS], sh_row[READ_ROWS];
+  const int tid = threadIdx.x, t0 = (int)blockIdx.x * READ_ROWS;
+  if (tid < READ_ROWS) {
+    const int t = t0 + tid;
+    int page = -1, row = 0;
+    if (t < p.tokens) {
+      int lo = 0, hi = p.B - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (p.cu[mid] <= t) lo = mid; else hi = mid - 1;
+      }
+      const int c0 = p.cu[lo], c1 = p.cu[lo + 1];
+      const long long pos = (p.first ? (long long)p.first[lo] : 0ll) + (t - c0);
+      if (t >= c0 && t < c1 && pos >= 0 && pos < p.seq_lens[lo] &&
+          pos < (long long)p.max_blocks * BS) {
+        page = p.table[(size_t)lo * p.max_blocks + pos / BS];
+        row = (int)(pos % BS);
+        if ((unsigned)page >= (unsigned)p.P) page = -1;
+      }
+      if (page < 0) set_status(p.status, KT_ERR_DEVICE_CHECK);
+    }
+    sh_page[tid] = page;
+    sh_row[tid] = row;
+  }
+  __syncthreads();
+  const int warp = tid >> 5, lane = tid & 31;
+#pragma unroll
+  for (int side = 0; side < 2; ++side) {
+    if (!p.out[side]) continue;
+    for (int i = warp; i < READ_ROWS * p.H_kv; i += WARPS) {
+      const int r = i / p.H_kv, h = i - r * p.H_kv;
+      const int page = sh_page[r];
+      if (page < 0) continue;
+      const size_t slab = (size_t)page * p.H_kv + h;
+      const float s = p.scale[side][slab];
+      const uint32_t c = reinterpret_cast<const uint32_t*>(p.code[side] + slab * TILE_BYTES +
+                                                           sh_row[r] * D)[lane];
+      const float2 x = __half22float2(as_h2(f8x2_lo(c)));
+      const float2 y = __half22float2(as_h2(f8x2_hi(c)));
+      store4(static_cast<O*>(p.out[side]) + ((size_t)(t0 + r) * p.H_kv + h) * D + 4 * lane,
+             make_float2(x.x * s, x.y * s), make_float2(y.x * s, y.y * s));
+    }
+  }
+}
+
+template <class T>
+cudaError_t launch_append_t(const Params& p, unsigned grid, size_t smem, cudaStream_t stream) {
+  static std::atomic<int> slot[KT_MAX_DEVICES];
+  const cudaError_t e = (cudaError_t)per_device_cached(slot, [] {
+    return (int)cudaFuncSetAttribute((const void*)append_f8_kernel<T>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     BS * 64 * (int)sizeof(float2) + TILE_BYTES + RED_BYTES);
+  });
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, append_f8_kernel<T>, p);
+}
+
+}  // namespace
+
+cudaError_t launch_append_f8(const AppendF8Launch& a, cudaStream_t stream) {
+  Params p;
+  if (a.rope) {
+    p.rope = *a.rope;
+  } else {
+    p.rope.rotary_dim = 0;
+    p.rope.layout = KT_ROPE_PAIRS;
+    p.rope.amplitude = 1.0f;
+  }
+  p.q = a.q;
+  p.k = a.k;
+  p.v = a.v;
+  p.qs = a.qs;
+  p.ks = a.ks;
+  p.vs = a.vs;
+  p.q_out = a.q_out;
+  p.k_code = a.k_code;
+  p.v_code = a.v_code;
+  p.k_scale = a.k_scale;
+  p.v_scale = a.v_scale;
+  p.table = a.table;
+  p.cu = a.cu;
+  p.seq_lens = a.seq_lens;
+  p.new_lens = a.new_lens;
+  p.reps = a.reps;
+  p.status = a.status;
+  p.ticket = a.ticket;
+  p.B = a.B;
+  p.H_kv = a.H_kv;
+  p.H_q = a.H_q;
+  p.max_blocks = a.max_blocks;
+  p.P = a.P;
+  p.tokens = a.tokens;
+  p.rep = a.rep;
+  p.R = a.R;
+  p.fix_stride = a.fix_stride;
+  // a sequence with m new rows touches at most m / 128 + 2 blocks, and at most m
+  const long long seqs = a.B < a.tokens ? a.B : a.tokens;
+  long long tiles = a.tokens / BS + 2 * seqs;
+  if (tiles > a.tokens) tiles = a.tokens;
+  // heads of a CTA: as many as leave two CTAs an SM, so that few angles are computed twice
+  long long per = tiles * a.H_kv / a.num_sms;
+  per = per < 1 ? 1 : per > a.H_kv ? a.H_kv : per;
+  p.groups = (int)((a.H_kv + per - 1) / per);
+  p.heads_per = (a.H_kv + p.groups - 1) / p.groups;
+  const long long cache = tiles * 2 * p.groups;
+  p.q_per = a.tokens >= 4 * a.num_sms ? Q_TOK : 1;
+  const long long qn = a.q ? ((long long)a.tokens + p.q_per - 1) / p.q_per : 0;
+  if (cache + qn + 1 > 0x7FFFFFFFll) return cudaErrorInvalidValue;
+  p.cache_ctas = (int)cache;
+  p.q_ctas = (int)qn;
+  p.cs_rows = a.cu ? BS : Q_TOK;  // a decoded token needs one row, a q CTA up to four
+  const size_t smem = (size_t)p.cs_rows * 64 * sizeof(float2) + TILE_BYTES + RED_BYTES;
+  const unsigned grid = (unsigned)(cache + qn + 1);
+  switch (a.dtype) {
+    case KT_F16: return launch_append_t<__half>(p, grid, smem, stream);
+    case KT_BF16: return launch_append_t<__nv_bfloat16>(p, grid, smem, stream);
+    case KT_F32: return launch_append_t<float>(p, grid, smem, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_reps_f8(const RepsF8Launch& a, cudaStream_t stream) {
+  if (a.num_blocks <= 0) return cudaSuccess;
+  RepsParams p;
+  p.k_code = a.k_code;
+  p.k_scale = a.k_scale;
+  p.table = a.table;
+  p.seq_lens = a.seq_lens;
+  p.reps = a.reps;
+  p.H_kv = a.H_kv;
+  p.max_blocks = a.max_blocks;
+  p.P = a.P;
+  p.rep = a.rep;
+  p.R = a.R;
+  p.fix_stride = a.fix_stride;
+  p.first_block = a.first_block;
+  reps_f8_kernel<<<dim3((unsigned)a.num_blocks * (unsigned)a.H_kv, a.B), THREADS, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_read_f8(const ReadF8Launch& a, cudaStream_t stream) {
+  if (a.tokens <= 0) return cudaSuccess;
+  ReadParams p;
+  p.code[0] = a.k_code;
+  p.code[1] = a.v_code;
+  p.scale[0] = a.k_scale;
+  p.scale[1] = a.v_scale;
+  p.out[0] = a.k_out;
+  p.out[1] = a.v_out;
+  p.table = a.table;
+  p.seq_lens = a.seq_lens;
+  p.first = a.first;
+  p.cu = a.cu;
+  p.status = a.status;
+  p.B = a.B;
+  p.H_kv = a.H_kv;
+  p.max_blocks = a.max_blocks;
+  p.P = a.P;
+  p.tokens = a.tokens;
+  const unsigned grid = (unsigned)(((long long)a.tokens + READ_ROWS - 1) / READ_ROWS);
+  switch (a.dtype) {
+    case KT_F16: read_f8_kernel<__half><<<grid, THREADS, 0, stream>>>(p); break;
+    case KT_BF16: read_f8_kernel<__nv_bfloat16><<<grid, THREADS, 0, stream>>>(p); break;
+    case KT_F32: read_f8_kernel<float><<<grid, THREADS, 0, stream>>>(p); break;
+    default: return cudaErrorInvalidValue;
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace kt

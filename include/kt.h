@@ -508,6 +508,207 @@ kt_status kt_append_kv(const kt_paged_kv* kv, const kt_sparse_params* p, const v
                        kt_stream_t stream);
 
 /*
+ * ---- rotary positions ---------------------------------------------------------
+ * The queries and keys that every call here takes carry their positions as
+ * rotations: at position pos the pair i (i < rotary_dim/2) of a head's first
+ * rotary_dim channels turns by the angle pos * f_i,
+ *   (x, y) -> amplitude * (x cos - y sin, y cos + x sin),
+ * and the channels from rotary_dim on pass through unchanged.  Pairs are
+ * (i, i + rotary_dim/2) (HALF) or (2i, 2i + 1) (PAIRS).  With
+ * f_i = theta^(-2i/rotary_dim), the scaling for contexts longer than the one a
+ * model was trained on is one of
+ *   PLAIN   f_i
+ *   LINEAR  f_i / factor (position interpolation)
+ *   NTK     theta replaced by theta * factor^(rotary_dim/(rotary_dim - 2))
+ *   YARN    r f_i / factor + (1 - r) f_i, r = clamp((i - lo) / (hi - lo), 0, 1),
+ *           lo = floor(e(beta_fast)), hi = ceil(e(beta_slow)), clamped to
+ *           [0, rotary_dim - 1], e(beta) = rotary_dim ln(original_len / (2 pi
+ *           beta)) / (2 ln theta), hi - lo at least 0.001; amplitude
+ *           0.1 ln(factor) + 1
+ *   BANDS   with t = original_len * f_i / (2 pi) turns over the trained length:
+ *           f_i where t > beta_fast, f_i / factor where t < beta_slow, and
+ *           between them w f_i + (1 - w) f_i / factor,
+ *           w = (t - beta_slow) / (beta_fast - beta_slow)
+ */
+typedef enum { KT_F16 = 0, KT_BF16 = 1, KT_F32 = 2 } kt_dtype;
+
+typedef enum { KT_ROPE_HALF = 0, KT_ROPE_PAIRS = 1 } kt_rope_layout;
+
+typedef enum {
+  KT_ROPE_PLAIN = 0,
+  KT_ROPE_LINEAR = 1,
+  KT_ROPE_NTK = 2,
+  KT_ROPE_YARN = 3,
+  KT_ROPE_BANDS = 4
+} kt_rope_scaling;
+
+typedef struct {
+  double theta;          /* base, > 1 */
+  double factor;         /* context extension, >= 1 (1 for PLAIN) */
+  double beta_fast;      /* YARN (usually 32) and BANDS (usually 4), > beta_slow */
+  double beta_slow;      /* YARN and BANDS (usually 1), > 0 */
+  int32_t original_len;  /* YARN, BANDS: the trained context length, >= 1 */
+  int32_t rotary_dim;    /* even, 2..128 (NTK: from 4) */
+  int32_t layout;        /* kt_rope_layout */
+  int32_t scaling;       /* kt_rope_scaling */
+} kt_rope_params;
+
+/*
+ * What the kernels take, filled by kt_rope_init and passed by value at the
+ * launch (host memory, no device buffer).  phase[i] is f_i in turns per position
+ * as a 64-bit fixed-point fraction, round(f_i / (2 pi) * 2^64): the product with
+ * a position wraps modulo one turn, so far positions lose nothing.  amplitude
+ * may be changed by the caller afterwards.
+ */
+typedef struct {
+  uint64_t phase[64];
+  float amplitude;
+  int32_t rotary_dim;
+  int32_t layout;
+  int32_t reserved;      /* 0 */
+} kt_rope;
+
+/* Fills *rope (host only).  INVALID_ARG for values outside the ranges above. */
+kt_status kt_rope_init(const kt_rope_params* rp, kt_rope* rope);
+
+/*
+ * Rows of heads as a projection leaves them: element (token t, head h, channel
+ * c) at data[t * stride + h * 128 + c], so q, k and v may be parts of one packed
+ * row.  data is 16-byte aligned, stride (in elements) is a multiple of 16 bytes
+ * and at least heads * 128; at most 4096 heads (UNSUPPORTED beyond).
+ */
+typedef struct {
+  const void* data;
+  int64_t stride;
+  int32_t heads;
+  int32_t dtype;         /* kt_dtype */
+} kt_rows;
+
+/*
+ * Rotates the rows of `tokens` tokens: q into q_out and k into k_out, binary16
+ * [tokens][heads][128] contiguous, each value computed in binary32 and rounded
+ * once.  positions: int32 [tokens] (device).  Either of q / k may be NULL (with
+ * its output); both have one type.  An output may be its own binary16 input
+ * where that is contiguous (stride = heads * 128); any other overlap of an
+ * output with an input or with the other output is INVALID_ARG.  tokens = 0 does
+ * nothing.
+ */
+kt_status kt_apply_rope(const kt_rope* rope, const int32_t* positions, int32_t tokens,
+                        const kt_rows* q, void* q_out, const kt_rows* k, void* k_out,
+                        kt_stream_t stream);
+
+/*
+ * ---- 8-bit KV cache with one scale per block and head -------------------------
+ * Each value is an e4m3 code (1 sign, 4 exponent, 3 mantissa bits; at most 448)
+ * times the binary32 scale of its (page, KV head) of K or V: 32 KB per block and
+ * head for K+V instead of the 64 KB of binary16 or the 34 KB of Q8_0.
+ * kt_append_kv_f8 keeps every scale a power of two 2^e, e in [-15, 8], the least
+ * with amax <= 448 * 2^e over the values the block has held since it was begun,
+ * so every value read back is a finite binary16.
+ */
+typedef struct {
+  const void* k_code;    /* e4m3 [num_pages][num_kv_heads][128][128] */
+  const float* k_scale;  /* [num_pages][num_kv_heads] */
+  const void* v_code;    /* as k_code */
+  const float* v_scale;  /* as k_scale */
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  int32_t batch, num_kv_heads, head_dim, block_size, max_blocks_per_seq, num_pages;
+} kt_paged_kv_f8;
+
+/* kt_workspace_bytes, kt_reps_pool_bytes and kt_build_block_reps for this cache.
+ * Reps are those of the values read back (Max / Mean / Quest / Fix; no ops or
+ * reps of the Dynamic method or the preselection: INVALID_ARG, 0 bytes). */
+kt_status kt_workspace_bytes_f8(kt_op op, const kt_paged_kv_f8* kv, const kt_sparse_params* p,
+                                size_t* bytes);
+size_t kt_reps_pool_bytes_f8(const kt_paged_kv_f8* kv, const kt_sparse_params* p);
+kt_status kt_build_block_reps_f8(const kt_paged_kv_f8* kv, const kt_sparse_params* p,
+                                 int32_t first_block, int32_t num_blocks, void* reps_pool,
+                                 kt_stream_t stream);
+
+/*
+ * Appends tokens to the sequences, quantising them as they are written, in one
+ * launch: row cu_tokens[b] + t of k and v becomes token seq_lens[b] + t of
+ * sequence b.
+ *   rope      : nullable; rotates the K rows (and q) by their token positions.
+ *   q, q_out  : nullable; q's rows (p->num_q_heads heads) are rotated (with rope
+ *               NULL: only rounded) into q_out, binary16 [tokens][heads][128],
+ *               as kt_apply_rope does.
+ *   k, v      : kv->num_kv_heads heads each; q, k and v have one type.
+ *   cu_tokens : int32 [batch + 1] (device), first row of each sequence and their
+ *               total, not decreasing; NULL: one row per sequence (tokens =
+ *               batch).
+ *   tokens    : rows of q / k / v.  Sequences may get none.
+ *   new_lens  : int32 [batch] receives the new lengths and kv->seq_lens stays;
+ *               NULL or kv->seq_lens itself: that is advanced (through its const
+ *               pointer) once the whole call has read it.
+ *   reps_pool : nullable; the reps of every block that the call completes are
+ *               built too (Dynamic: none).
+ *   ws        : any zero-initialised workspace of at least 256 bytes (its header
+ *               is used).
+ * Every value is first rounded to binary16 (the type of the other caches).  A
+ * block that the call begins (at row 0) takes the scale of its new rows; in a
+ * block already begun the scale can only grow, and then the rows before the new
+ * ones are coded again, round(code * old / new).  A code is x / scale rounded to
+ * the nearest (ties to even), at most 240 in magnitude where e is 8; infinities
+ * become the largest code, NaN stays NaN and does not count for the scale.  Rows
+ * of a block behind the appended ones stay as they were.
+ * A sequence with a negative length, no room in its table or rows outside
+ * [0, tokens) records KT_ERR_DEVICE_CHECK and is left unchanged; a page outside
+ * the pool records it, its block is skipped and the sequence keeps its length,
+ * and a scale of a begun block that is no such power of two records it and is
+ * replaced.  Two sequences must not append into the same page, and two calls
+ * that share a workspace or a cache must not overlap.
+ */
+kt_status kt_append_kv_f8(const kt_paged_kv_f8* kv, const kt_sparse_params* p,
+                          const kt_rope* rope, const kt_rows* q, void* q_out, const kt_rows* k,
+                          const kt_rows* v, const int32_t* cu_tokens, int32_t tokens,
+                          int32_t* new_lens, void* reps_pool, void* ws, size_t ws_bytes,
+                          kt_stream_t stream);
+
+/*
+ * Reads tokens back: row cu_tokens[b] + t of k_out / v_out ([tokens]
+ * [num_kv_heads][128] of out_dtype, either may be NULL) becomes token first[b] + t
+ * of sequence b (first NULL: from token 0).  Values are exact in all three types
+ * with the scales that kt_append_kv_f8 writes.  A row outside its sequence, or
+ * whose page is outside the pool, records KT_ERR_DEVICE_CHECK and is left as it
+ * was.  ws as kt_append_kv_f8.
+ */
+kt_status kt_read_kv_f8(const kt_paged_kv_f8* kv, const int32_t* first, const int32_t* cu_tokens,
+                        int32_t tokens, int32_t out_dtype, void* k_out, void* v_out, void* ws,
+                        size_t ws_bytes, kt_stream_t stream);
+
+/*
+ * kt_sparse_decode_attn, kt_dense_decode_attn, kt_score_select_blocks,
+ * kt_sparse_decode_step and kt_decode_layer over this cache: the codes become
+ * binary16 in registers (exactly), the K scale of a block multiplies its scores
+ * and the V scale its share of the output, both in binary32, so the attention is
+ * that over the values read back.  Scales may be any value in [2^-30, 2^30];
+ * others record KT_ERR_DEVICE_CHECK and their block is skipped.  Codes behind
+ * seq_lens[b] in the last page may be anything.  Arguments, workspaces (of
+ * kt_workspace_bytes_f8) and errors as the calls named; no Dynamic reps.
+ */
+kt_status kt_sparse_decode_attn_f8(const void* q, const kt_paged_kv_f8* kv,
+                                   const kt_sparse_params* p, const int32_t* sel,
+                                   const int32_t* cnt, float* out, void* ws, size_t ws_bytes,
+                                   kt_stream_t stream);
+kt_status kt_dense_decode_attn_f8(const void* q, const kt_paged_kv_f8* kv, int32_t num_q_heads,
+                                  float softmax_scale, float* out, void* ws, size_t ws_bytes,
+                                  kt_stream_t stream);
+kt_status kt_score_select_blocks_f8(const void* q, const kt_paged_kv_f8* kv,
+                                    const void* reps_pool, const kt_sparse_params* p,
+                                    int32_t* sel, int32_t* cnt, float* sel_scores, void* ws,
+                                    size_t ws_bytes, kt_stream_t stream);
+kt_status kt_sparse_decode_step_f8(const void* q, const kt_paged_kv_f8* kv,
+                                   const void* reps_pool, const kt_sparse_params* p,
+                                   int32_t* sel, int32_t* cnt, float* out, void* ws,
+                                   size_t ws_bytes, kt_stream_t stream);
+kt_status kt_decode_layer_f8(const kt_reuse_policy* pol, int32_t token_idx, int32_t layer_idx,
+                             const void* q, const kt_paged_kv_f8* kv, const void* reps_pool,
+                             const kt_sparse_params* p, int32_t* hist_sel, int32_t* hist_cnt,
+                             float* out, void* ws, size_t ws_bytes, kt_stream_t stream);
+
+/*
  * kt_sparse_decode_attn without a workspace, for callers that cannot allocate
  * device memory: for example a kernel plugged into an engine or framework
  * that hands it only its input and output buffers and owns every other byte
