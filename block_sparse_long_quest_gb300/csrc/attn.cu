@@ -1110,6 +1110,11 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const __grid_constant_
   uint32_t qa[8][2];
   bool q_loaded = false;
   float vs_run = 1.0f;  // e4m3: acc holds the output divided by this V scale
+  // e4m3: V blocks of very different scale meet in one output, so P is held as
+  // 2^15 P (at most 32768, binary16's largest power): its binary16 parts then end
+  // at 2^-39 of the largest P instead of 2^-24.  Numerator and denominator carry
+  // the factor alike.
+  constexpr float P_SHIFT = KVM == KVM_F8 ? 15.0f : 0.0f;
 
   for (uint32_t it = 0;; ++it) {
     const uint32_t st = it % NST;
@@ -1240,7 +1245,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const __grid_constant_
       const float m_use = (m_new == -INFINITY) ? 0.0f : m_new;
       float pr[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) pr[i] = exp2f(x[i] - m_use);
+      for (int i = 0; i < 4; ++i) pr[i] = exp2f(x[i] - (m_use - P_SHIFT));
       if (__any_sync(0xffffffffu, m_new != m_run) || (KVM == KVM_F8 && in.vs != vs_run)) {
         float alpha = exp2f(m_run - m_use);
         l_part *= alpha;

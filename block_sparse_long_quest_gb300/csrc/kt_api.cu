@@ -1132,8 +1132,10 @@ bool rope_ok(const kt_rope* r) {
 constexpr int MAX_ROW_HEADS = 4096;
 int dtype_bytes(int dtype) { return dtype == KT_F32 ? 4 : 2; }
 
-kt_status check_rows(const kt_rows* r) {
-  if (!r || !r->data || !aligned16(r->data) || r->heads < 1) return KT_ERR_INVALID_ARG;
+// rows of no tokens may have no address
+kt_status check_rows(const kt_rows* r, int tokens) {
+  if (!r || (!r->data && tokens > 0) || !aligned16(r->data) || r->heads < 1)
+    return KT_ERR_INVALID_ARG;
   if (r->dtype != KT_F16 && r->dtype != KT_BF16 && r->dtype != KT_F32) return KT_ERR_INVALID_ARG;
   if (r->heads > MAX_ROW_HEADS) return KT_ERR_UNSUPPORTED;
   if (r->stride < (int64_t)r->heads * D || r->stride > ((int64_t)1 << 28) ||
@@ -1206,18 +1208,18 @@ constexpr size_t WS_TICKET = 64;  // append ticket, inside the status header
 kt_status kt_apply_rope(const kt_rope* rope, const int32_t* positions, int32_t tokens,
                         const kt_rows* q, void* q_out, const kt_rows* k, void* k_out,
                         kt_stream_t stream) {
-  if (!rope || !rope_ok(rope) || !positions || !aligned16(positions) || tokens < 0)
-    return KT_ERR_INVALID_ARG;
+  if (!rope || !rope_ok(rope) || tokens < 0) return KT_ERR_INVALID_ARG;
+  if (tokens == 0) return KT_OK;
+  if (!positions || !aligned16(positions)) return KT_ERR_INVALID_ARG;
   if ((!q && !k) || (q && !q_out) || (k && !k_out) || (!q && q_out) || (!k && k_out))
     return KT_ERR_INVALID_ARG;
   if ((q_out && !aligned16(q_out)) || (k_out && !aligned16(k_out))) return KT_ERR_INVALID_ARG;
   for (const kt_rows* r : {q, k}) {
     if (!r) continue;
-    const kt_status s = check_rows(r);
+    const kt_status s = check_rows(r, tokens);
     if (s != KT_OK) return s;
   }
   if (q && k && q->dtype != k->dtype) return KT_ERR_INVALID_ARG;
-  if (tokens == 0) return KT_OK;
   if ((q && !out_ok(q, q_out, tokens)) || (k && !out_ok(k, k_out, tokens)))
     return KT_ERR_INVALID_ARG;
   if (q && k &&
@@ -1301,19 +1303,19 @@ kt_status kt_append_kv_f8(const kt_paged_kv_f8* kvf, const kt_sparse_params* p,
   s = check_params(&kv, p);
   if (s != KT_OK) return s;
   if (rope && !rope_ok(rope)) return KT_ERR_INVALID_ARG;
-  s = check_rows(k);
-  if (s == KT_OK) s = check_rows(v);
-  if (s == KT_OK && q) s = check_rows(q);
+  if (tokens < 0 || (!cu_tokens && tokens != kv.batch)) return KT_ERR_INVALID_ARG;
+  s = check_rows(k, tokens);
+  if (s == KT_OK) s = check_rows(v, tokens);
+  if (s == KT_OK && q) s = check_rows(q, tokens);
   if (s != KT_OK) return s;
   if (k->heads != kv.num_kv_heads || v->heads != kv.num_kv_heads || k->dtype != v->dtype)
     return KT_ERR_INVALID_ARG;
-  if ((q != nullptr) != (q_out != nullptr)) return KT_ERR_INVALID_ARG;
+  if (tokens > 0 && (q != nullptr) != (q_out != nullptr)) return KT_ERR_INVALID_ARG;
   if (q && (q->heads != p->num_q_heads || q->dtype != k->dtype || !aligned16(q_out)))
     return KT_ERR_INVALID_ARG;
   if (!ws || ws_bytes < 256 || !aligned16(ws) || (cu_tokens && !aligned16(cu_tokens)) ||
       (new_lens && !aligned16(new_lens)) || (reps_pool && !aligned16(reps_pool)))
     return KT_ERR_INVALID_ARG;
-  if (tokens < 0 || (!cu_tokens && tokens != kv.batch)) return KT_ERR_INVALID_ARG;
   if (new_lens == kv.seq_lens) new_lens = nullptr;  // in place
   if (new_lens && overlap(bytes_of(new_lens, (size_t)kv.batch * 4),
                           bytes_of(kv.seq_lens, (size_t)kv.batch * 4)))
@@ -1324,7 +1326,7 @@ kt_status kt_append_kv_f8(const kt_paged_kv_f8* kvf, const kt_sparse_params* p,
     return KT_ERR_INVALID_ARG;
   AppendF8Launch a;
   a.rope = rope;
-  a.q = q ? q->data : nullptr;
+  a.q = q && tokens > 0 ? q->data : nullptr;
   a.k = k->data;
   a.v = v->data;
   a.qs = q ? q->stride : 0;
@@ -1363,6 +1365,7 @@ kt_status kt_read_kv_f8(const kt_paged_kv_f8* kvf, const int32_t* first, const i
   kt_paged_kv kv;
   const kt_status s = check_kv_f8(kvf, &kv);
   if (s != KT_OK) return s;
+  if (tokens == 0) return KT_OK;
   if (!cu_tokens || !aligned16(cu_tokens) || (first && !aligned16(first)) || tokens < 0 ||
       (!k_out && !v_out) || (k_out && !aligned16(k_out)) || (v_out && !aligned16(v_out)) || !ws ||
       ws_bytes < 256 || !aligned16(ws))

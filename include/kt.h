@@ -575,7 +575,8 @@ kt_status kt_rope_init(const kt_rope_params* rp, kt_rope* rope);
  * Rows of heads as a projection leaves them: element (token t, head h, channel
  * c) at data[t * stride + h * 128 + c], so q, k and v may be parts of one packed
  * row.  data is 16-byte aligned, stride (in elements) is a multiple of 16 bytes
- * and at least heads * 128; at most 4096 heads (UNSUPPORTED beyond).
+ * and at least heads * 128; at most 4096 heads (UNSUPPORTED beyond).  Rows of a
+ * call with no tokens may have a NULL address.
  */
 typedef struct {
   const void* data;

@@ -492,7 +492,10 @@ def test_read_outside_is_left_alone(kt):
     touched = read([0, 120])
     assert touched.tolist() == [True] * 10 + [False] * 8 + [True] * 2
     assert_status(kt, ws, kt.KT_ERR_DEVICE_CHECK)
-    read([0, 128])
+    touched = read([0, 128])  # the second sequence ends after two of its rows
+    assert touched.tolist() == [True] * 12 + [False] * 8
+    assert_status(kt, ws, kt.KT_ERR_DEVICE_CHECK)
+    read([190, 128], torch.tensor([0, 10, 12], dtype=torch.int32, device="cuda"), 12)
     assert_status(kt, ws)
 
 
