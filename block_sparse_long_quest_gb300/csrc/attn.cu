@@ -86,8 +86,10 @@ static_assert(Q8_STAGE_BYTES % 1024 == 0, "128-byte swizzled boxes need 1024-byt
 // e4m3 source: a stage holds the codes of K and V (16 KB each, 128-byte swizzled
 // TMA boxes), so the ring has twice the stages; the two scales of the block land
 // in the stage's info by 4-byte cp.async, which arrive on the stage's barrier
-// beside the TMA copies (nothing waits for them on its own).  The consumers turn
-// codes into binary16 fragments in registers.
+// beside the TMA copies (nothing waits for them on its own).  The consumers are
+// two groups of four warps that take the stages in turn (consume_f8).
+constexpr int F8_GROUP = 4;
+constexpr int F8_GROUPS = CONSUMERS / F8_GROUP;
 constexpr int F8_STAGE_BYTES = 2 * UNIT * D;
 constexpr int F8_STAGES = STAGES * KV_STAGE_BYTES / F8_STAGE_BYTES;
 constexpr float F8_SCALE_MIN = 0x1.0p-30f, F8_SCALE_MAX = 0x1.0p30f;
@@ -687,11 +689,6 @@ __device__ int fused_pick(const Params& p, uint8_t* scr, unsigned long long* sh_
   return i1 - i0;
 }
 
-// e4m3 source: byte selector from (t0: c0 c1, t1: c0 c1) to (c0: t0 t1, c1: t0 t1),
-// t0 = token `tok`; bytes of tokens from ntok on come from the zero operand.
-__device__ __forceinline__ uint32_t f8_permute(int tok, int ntok) {
-  return (tok < ntok ? 0x0100u : 0x0404u) | (tok + 1 < ntok ? 0x3020u : 0x4040u);
-}
 // e4m3 source, one thread: the loads of stage st (codes by TMA, scales by
 // cp.async), with both of its arrivals.
 __device__ __forceinline__ void issue_f8(const Params& p, uint32_t kv_base, StageInfo* info,
@@ -704,6 +701,248 @@ __device__ __forceinline__ void issue_f8(const Params& p, uint32_t kv_base, Stag
   cp_async_4(smem_u32(&info[st].ks), static_cast<const float*>(p.k_scale) + slab);
   cp_async_4(smem_u32(&info[st].vs), static_cast<const float*>(p.v_scale) + slab);
   cp_async_mbar_arrive_noinc(bar);
+}
+
+// ---- e4m3 consumers -----------------------------------------------------------
+// Half the bytes of binary16 arrive per block, so a block has half the time; the
+// work per block is cut instead:
+//   - a warp takes 32 tokens of a block, and the four warps of a group a block:
+//     barriers, scales and the softmax's reductions serve twice the tokens, and
+//     the two groups work on neighbouring blocks at once;
+//   - K and V are the A operand (16 tokens or 16 channels by 16), the heads the 8
+//     columns of B: each fragment of 256 codes is one MMA.  With G <= 4 the
+//     columns 4..7 are the heads again and hold the low part of P (P = P_hi +
+//     P_lo in binary16), so one MMA does both; with G > 4 there are two;
+//   - codes become binary16 in registers: the four codes that ldmatrix gives a
+//     lane are channels 4t .. 4t+3 of a token; the MMA's k order is permuted to
+//     match (q's alike).  A transposed load of V gives two tokens' channel pairs
+//     (2g, 2g+1), one byte permute makes them (2g: two tokens, 2g+1: two tokens),
+//     rows g and g + 8 of the A fragment.
+// The K scale multiplies the scores; acc is held in units of the V scale of the
+// last block, and rescaled with the running maximum.  V blocks of very different
+// scale meet in one output, so P is held as 2^15 P (at most 32768, binary16's
+// largest power of two): its binary16 parts then end at 2^-39 of the largest P
+// instead of 2^-24.  Numerator and denominator carry the factor alike.
+constexpr float F8_P_SHIFT = 15.0f;
+
+struct F8State {
+  float acc[8][4];  // 16-channel piece c: channel 16c + 2g (heads 2t, 2t+1), 16c + 2g+1
+  float m[2], l[2]; // of heads 2t, 2t + 1 (l: this lane's tokens)
+  float vs;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// 8x8 transpose of binary16 across a warp (row lane/4, columns 2(lane%4), +1).
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+// Byte selector from (t0: c0 c1, t1: c0 c1) to (c0: t0 t1, c1: t0 t1), t0 = token
+// `tok`; bytes of tokens from ntok on come from the zero operand (their codes may
+// be anything).
+__device__ __forceinline__ uint32_t f8_permute(int tok, int ntok) {
+  return (tok < ntok ? 0x0100u : 0x0404u) | (tok + 1 < ntok ? 0x3020u : 0x4040u);
+}
+
+// The attention of this warp's share of the CTA's blocks; whether q was loaded.
+__device__ __forceinline__ bool consume_f8(const Params& p, F8State& z, const uint8_t* smem,
+                                           const StageInfo* info, uint32_t kv_base,
+                                           uint32_t bar_full, uint32_t bar_empty, uint32_t bar_q,
+                                           int warp, int lane) {
+  constexpr uint32_t NST = F8_STAGES;
+  const int g = lane >> 2, t = lane & 3, mi = lane >> 3, r = lane & 7;
+  const int w0 = (warp % F8_GROUP) * 32;  // first of the warp's tokens in a block
+  const bool dup = p.G <= 4;
+  const bool low = dup && t >= 2;  // this lane's columns carry P_lo
+#pragma unroll
+  for (int i = 0; i < 8; ++i) z.acc[i][0] = z.acc[i][1] = z.acc[i][2] = z.acc[i][3] = 0.0f;
+  z.m[0] = z.m[1] = -INFINITY;
+  z.l[0] = z.l[1] = 0.0f;
+  z.vs = 1.0f;
+  uint32_t qb[8][2];
+  bool q_loaded = false;
+  // ldmatrix rows of this lane: matrices 0, 1 are tokens 0-7 and 8-15 of a 16-token
+  // half, matrices 2, 3 the same tokens' next 16 channels
+  const int lrow = w0 + (mi & 1) * 8 + r;
+  const uint32_t lswz = (uint32_t)(lrow & 7), lhi = (uint32_t)(mi >> 1);
+#pragma unroll 1
+  for (uint32_t it = warp / F8_GROUP;; it += F8_GROUPS) {
+    const uint32_t st = it % NST;
+    if (!mbar_wait(bar_full + 8 * st, (it / NST) & 1, p.status)) break;
+    const StageInfo in = info[st];
+    if (in.end) break;
+    if (in.ntok > 0 && !q_loaded) {
+      if (!mbar_wait(bar_q, 0, p.status)) break;
+      const __half* qs = reinterpret_cast<const __half*>(smem + SmemLayout::q);
+      const int hd = dup ? g & 3 : g;
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk) {
+        uint2 v = make_uint2(0u, 0u);
+        if (hd < p.G) v = *reinterpret_cast<const uint2*>(qs + hd * D + kk * 16 + 4 * t);
+        qb[kk][0] = v.x;
+        qb[kk][1] = v.y;
+      }
+      q_loaded = true;
+    }
+    const bool scales_ok = in.ks >= F8_SCALE_MIN && in.ks <= F8_SCALE_MAX &&
+                           in.vs >= F8_SCALE_MIN && in.vs <= F8_SCALE_MAX;
+    if (in.ntok > w0) {
+      if (scales_ok) {
+        const uint32_t kb = kv_base + st * F8_STAGE_BYTES + (uint32_t)lrow * 128;
+        const uint32_t vb = kb + UNIT * D;
+        // ---- S = K q^T: two 16-token halves, two accumulation chains each
+        float s[2][2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) s[h][c][0] = s[h][c][1] = s[h][c][2] = s[h][c][3] = 0.0f;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t c0, c1, c2, c3;
+            ldsm_x4(c0, c1, c2, c3, kb + h * 2048 + (((kk * 2 + lhi) ^ lswz) << 4));
+            mma_16816_sched(s[h][0], f8x2_lo(c0), f8x2_lo(c1), f8x2_hi(c0), f8x2_hi(c1), qb[2 * kk][0],
+                      qb[2 * kk][1]);
+            mma_16816_sched(s[h][1], f8x2_lo(c2), f8x2_lo(c3), f8x2_hi(c2), f8x2_hi(c3),
+                      qb[2 * kk + 1][0], qb[2 * kk + 1][1]);
+          }
+        // ---- online softmax (base 2) of heads 2t, 2t + 1 over the warp's tokens
+        float x[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[h][i] = s[h][0][i] + s[h][1][i];
+        uint32_t perm[2][2] = {{0x3120u, 0x3120u}, {0x3120u, 0x3120u}};
+        if (in.ntok < w0 + 32) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              if (w0 + h * 16 + i * 8 + g >= in.ntok) x[h][2 * i] = x[h][2 * i + 1] = -INFINITY;
+              perm[h][i] = f8_permute(w0 + h * 16 + i * 8 + 2 * t, in.ntok);
+            }
+        }
+        const float sc = p.scale_log2 * in.ks;
+        float mu[2];
+        bool moved = false;
+        float m_new[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float mx = fmaxf(fmaxf(x[0][i], x[0][2 + i]), fmaxf(x[1][i], x[1][2 + i]));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+          m_new[i] = fmaxf(z.m[i], mx * sc);
+          mu[i] = m_new[i] == -INFINITY ? 0.0f : m_new[i];
+          moved = moved || m_new[i] != z.m[i];
+        }
+        float pr[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            pr[h][i] = ex2(fmaf(x[h][i], sc, F8_P_SHIFT - mu[i & 1]));
+        if (__any_sync(0xffffffffu, moved) || in.vs != z.vs) {
+          // acc goes over to this block's V scale as well
+          const float a0 = ex2(z.m[0] - mu[0]), a1 = ex2(z.m[1] - mu[1]);
+          const float rv = z.vs / in.vs;
+          z.l[0] *= a0;
+          z.l[1] *= a1;
+          const float b0 = a0 * rv, b1 = a1 * rv;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            z.acc[i][0] *= b0;
+            z.acc[i][1] *= b1;
+            z.acc[i][2] *= b0;
+            z.acc[i][3] *= b1;
+          }
+          z.vs = in.vs;
+          z.m[0] = m_new[0];
+          z.m[1] = m_new[1];
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          z.l[i] += (pr[0][i] + pr[0][2 + i]) + (pr[1][i] + pr[1][2 + i]);
+        // ---- O^T += V^T P^T, a 16-token half at a time
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t hi[2], lo[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const __half2 a = __floats2half2_rn(pr[h][2 * i], pr[h][2 * i + 1]);
+            const float2 f = __half22float2(a);
+            const __half2 b = __floats2half2_rn(pr[h][2 * i] - f.x, pr[h][2 * i + 1] - f.y);
+            hi[i] = *reinterpret_cast<const uint32_t*>(&a);
+            lo[i] = *reinterpret_cast<const uint32_t*>(&b);
+            hi[i] = transpose8x8(low ? lo[i] : hi[i]);
+          }
+          if (!dup) {
+            lo[0] = transpose8x8(lo[0]);
+            lo[1] = transpose8x8(lo[1]);
+          }
+#pragma unroll
+          for (int cp = 0; cp < 4; ++cp) {
+            uint32_t c0, c1, c2, c3;
+            ldsm_x4_t(c0, c1, c2, c3, vb + h * 2048 + (((cp * 2 + lhi) ^ lswz) << 4));
+            c0 = __byte_perm(c0, 0u, perm[h][0]);
+            c1 = __byte_perm(c1, 0u, perm[h][1]);
+            c2 = __byte_perm(c2, 0u, perm[h][0]);
+            c3 = __byte_perm(c3, 0u, perm[h][1]);
+            const uint32_t e0 = f8x2_lo(c0), e1 = f8x2_hi(c0), e2 = f8x2_lo(c1), e3 = f8x2_hi(c1);
+            const uint32_t o0 = f8x2_lo(c2), o1 = f8x2_hi(c2), o2 = f8x2_lo(c3), o3 = f8x2_hi(c3);
+            mma_16816_sched(z.acc[2 * cp], e0, e1, e2, e3, hi[0], hi[1]);
+            mma_16816_sched(z.acc[2 * cp + 1], o0, o1, o2, o3, hi[0], hi[1]);
+            if (!dup) {
+              mma_16816_sched(z.acc[2 * cp], e0, e1, e2, e3, lo[0], lo[1]);
+              mma_16816_sched(z.acc[2 * cp + 1], o0, o1, o2, o3, lo[0], lo[1]);
+            }
+          }
+        }
+      } else if (w0 == 0 && lane == 0) {
+        set_status(p.status, KT_ERR_DEVICE_CHECK);  // the block is left out
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar_empty + 8 * st);
+  }
+  return q_loaded;
+}
+
+// The warp's state as m, l and O[128] of each head (rows of `stride` floats).
+__device__ __forceinline__ void f8_store(F8State& z, float* rows, int stride, int G, int lane) {
+  const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    z.l[i] += __shfl_xor_sync(0xffffffffu, z.l[i], 4);
+    z.l[i] += __shfl_xor_sync(0xffffffffu, z.l[i], 8);
+    z.l[i] += __shfl_xor_sync(0xffffffffu, z.l[i], 16);
+  }
+  if (G <= 4) {  // columns 4..7: the products with the low part of P
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) z.acc[c][i] += __shfl_xor_sync(0xffffffffu, z.acc[c][i], 2);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int hd = 2 * t + i;
+    if (hd >= G) continue;
+    float* sw = rows + (size_t)hd * stride;
+    if (g == 0) {
+      sw[0] = z.m[i];
+      sw[1] = z.l[i];
+    }
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      *reinterpret_cast<float2*>(sw + 2 + c * 16 + 2 * g) =
+          make_float2(z.acc[c][i] * z.vs, z.acc[c][2 + i] * z.vs);
+  }
 }
 
 template <int SK, int KVM = KVM_F16>
@@ -743,7 +982,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const __grid_constant_
       // host source: all 32 producer lanes arrive (each once its copies land);
       // e4m3: the issuing thread arrives for the TMA copies and for the scales
       mbar_init(bar_full + 8 * i, KVM == KVM_HOST ? 32 : KVM == KVM_F8 ? 2 : 1);
-      mbar_init(bar_empty + 8 * i, CONSUMERS);
+      mbar_init(bar_empty + 8 * i, KVM == KVM_F8 ? F8_GROUP : CONSUMERS);
     }
     mbar_init(bar_q, 1);
     mbar_init(bar_sel, 1);
@@ -1008,7 +1247,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const __grid_constant_
       }
       produce(phase, u0, u1);
     }
-    if (ok) {
+    // the end marker (e4m3: one for each of the consumer groups)
+    for (int e = 0; e < (KVM == KVM_F8 ? F8_GROUPS : 1) && ok; ++e, ++it) {
       const uint32_t st = it % NST;
       int okl = 0;
       if (lane == 0 &&
@@ -1018,9 +1258,10 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const __grid_constant_
         okl = 1;
       }
       okl = __shfl_sync(0xffffffffu, okl, 0);
-      // the end marker: one arrival (two for e4m3), or one per lane for the host source
+      // one arrival (two for e4m3), or one per lane for the host source
       if (okl && (KVM == KVM_HOST || lane == 0)) mbar_arrive(bar_full + 8 * st);
       if (KVM == KVM_F8 && okl && lane == 0) mbar_arrive(bar_full + 8 * st);
+      ok = okl != 0;
     }
     return;
   }
@@ -1109,13 +1350,11 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const __grid_constant_
   float m_run = -INFINITY, l_part = 0.0f;
   uint32_t qa[8][2];
   bool q_loaded = false;
-  float vs_run = 1.0f;  // e4m3: acc holds the output divided by this V scale
-  // e4m3: V blocks of very different scale meet in one output, so P is held as
-  // 2^15 P (at most 32768, binary16's largest power): its binary16 parts then end
-  // at 2^-39 of the largest P instead of 2^-24.  Numerator and denominator carry
-  // the factor alike.
-  constexpr float P_SHIFT = KVM == KVM_F8 ? 15.0f : 0.0f;
 
+  F8State f8;
+  if constexpr (KVM == KVM_F8)
+    q_loaded = consume_f8(p, f8, smem, info, kv_base, bar_full, bar_empty, bar_q, warp, lane);
+  if constexpr (KVM != KVM_F8)
   for (uint32_t it = 0;; ++it) {
     const uint32_t st = it % NST;
     if (!mbar_wait(bar_full + 8 * st, (it / NST) & 1, p.status)) break;
@@ -1127,13 +1366,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const __grid_constant_
       const __half* qs = reinterpret_cast<const __half*>(smem + SmemLayout::q);
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk) {
-        if (KVM == KVM_F8 && g < p.G) {
-          // a lane's four codes of a 16-channel piece are channels 4t .. 4t+3:
-          // the k order of the product is permuted, and q's alike
-          const uint2 v = *reinterpret_cast<const uint2*>(qs + g * D + kk * 16 + 4 * t);
-          qa[kk][0] = v.x;
-          qa[kk][1] = v.y;
-        } else if (g < p.G) {
+        if (g < p.G) {
           qa[kk][0] = *reinterpret_cast<const uint32_t*>(qs + g * D + kk * 16 + 2 * t);
           qa[kk][1] = *reinterpret_cast<const uint32_t*>(qs + g * D + kk * 16 + 8 + 2 * t);
         } else {
@@ -1142,13 +1375,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const __grid_constant_
       }
       q_loaded = true;
     }
-    bool scales_ok = true;
-    if constexpr (KVM == KVM_F8) {
-      scales_ok = in.ntok <= 0 || (in.ks >= F8_SCALE_MIN && in.ks <= F8_SCALE_MAX &&
-                                   in.vs >= F8_SCALE_MIN && in.vs <= F8_SCALE_MAX);
-      if (!scales_ok && ctid == 0) set_status(p.status, KT_ERR_DEVICE_CHECK);
-    }
-    if (in.ntok > warp * 16 && scales_ok) {
+    if (in.ntok > warp * 16) {
       if constexpr (KVM == KVM_Q8) {
         // this warp's 16 token rows of K and V: int8 code * binary16 scale,
         // rounded once to fp16, into the fp16 block at the start of the ring
@@ -1190,10 +1417,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const __grid_constant_
         }
         __syncwarp();
       }
-      const uint32_t kb = KVM == KVM_Q8   ? kv_base
-                          : KVM == KVM_F8 ? kv_base + st * F8_STAGE_BYTES
-                                          : kv_base + st * KV_STAGE_BYTES;
-      const uint32_t vb = kb + (KVM == KVM_F8 ? UNIT * D : 2 * BOX_BYTES);
+      const uint32_t kb = KVM == KVM_Q8 ? kv_base : kv_base + st * KV_STAGE_BYTES;
+      const uint32_t vb = kb + 2 * BOX_BYTES;
       const int mi = lane >> 3, r = lane & 7;
       // ---- S = q K^T for this warp's 16 tokens: two n-tiles, each with two
       // independent accumulation chains over the 8 k-steps
@@ -1202,42 +1427,24 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const __grid_constant_
       for (int a = 0; a < 2; ++a)
 #pragma unroll
         for (int c = 0; c < 2; ++c) s[a][c][0] = s[a][c][1] = s[a][c][2] = s[a][c][3] = 0.f;
-      if constexpr (KVM == KVM_F8) {
-        // 16 tokens x 32 channels of codes per load: two 16-channel k-steps
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          const int tok = warp * 16 + (mi >> 1) * 8 + r;
-          const uint32_t addr = kb + tok * 128 + (((kk * 2 + (mi & 1)) ^ (tok & 7)) << 4);
-          uint32_t c0, c1, c2, c3;
-          ldsm_x4(c0, c1, c2, c3, addr);
-          const uint32_t* qe = qa[2 * kk];
-          const uint32_t* qo = qa[2 * kk + 1];
-          mma_16816(s[0][0], qe[0], 0u, qe[1], 0u, f8x2_lo(c0), f8x2_hi(c0));
-          mma_16816(s[1][0], qe[0], 0u, qe[1], 0u, f8x2_lo(c2), f8x2_hi(c2));
-          mma_16816(s[0][1], qo[0], 0u, qo[1], 0u, f8x2_lo(c1), f8x2_hi(c1));
-          mma_16816(s[1][1], qo[0], 0u, qo[1], 0u, f8x2_lo(c3), f8x2_hi(c3));
-        }
-      } else {
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          const int tok = warp * 16 + (mi >> 1) * 8 + r;
-          const int chunk = kk * 2 + (mi & 1);
-          const uint32_t addr = kb + (chunk >> 3) * BOX_BYTES + tok * 128 +
-                                (((chunk & 7) ^ (tok & 7)) << 4);
-          uint32_t b0, b1, b2, b3;
-          ldsm_x4(b0, b1, b2, b3, addr);
-          mma_16816(s[0][kk & 1], qa[kk][0], 0u, qa[kk][1], 0u, b0, b1);
-          mma_16816(s[1][kk & 1], qa[kk][0], 0u, qa[kk][1], 0u, b2, b3);
-        }
+      for (int kk = 0; kk < 8; ++kk) {
+        const int tok = warp * 16 + (mi >> 1) * 8 + r;
+        const int chunk = kk * 2 + (mi & 1);
+        const uint32_t addr = kb + (chunk >> 3) * BOX_BYTES + tok * 128 +
+                              (((chunk & 7) ^ (tok & 7)) << 4);
+        uint32_t b0, b1, b2, b3;
+        ldsm_x4(b0, b1, b2, b3, addr);
+        mma_16816(s[0][kk & 1], qa[kk][0], 0u, qa[kk][1], 0u, b0, b1);
+        mma_16816(s[1][kk & 1], qa[kk][0], 0u, qa[kk][1], 0u, b2, b3);
       }
       // ---- online softmax (base 2), rows = query heads
       const int tok0 = warp * 16 + 2 * t;
-      const float scale_log2 = KVM == KVM_F8 ? p.scale_log2 * in.ks : p.scale_log2;
       float x[4];
-      x[0] = (tok0 < in.ntok) ? (s[0][0][0] + s[0][1][0]) * scale_log2 : -INFINITY;
-      x[1] = (tok0 + 1 < in.ntok) ? (s[0][0][1] + s[0][1][1]) * scale_log2 : -INFINITY;
-      x[2] = (tok0 + 8 < in.ntok) ? (s[1][0][0] + s[1][1][0]) * scale_log2 : -INFINITY;
-      x[3] = (tok0 + 9 < in.ntok) ? (s[1][0][1] + s[1][1][1]) * scale_log2 : -INFINITY;
+      x[0] = (tok0 < in.ntok) ? (s[0][0][0] + s[0][1][0]) * p.scale_log2 : -INFINITY;
+      x[1] = (tok0 + 1 < in.ntok) ? (s[0][0][1] + s[0][1][1]) * p.scale_log2 : -INFINITY;
+      x[2] = (tok0 + 8 < in.ntok) ? (s[1][0][0] + s[1][1][0]) * p.scale_log2 : -INFINITY;
+      x[3] = (tok0 + 9 < in.ntok) ? (s[1][0][1] + s[1][1][1]) * p.scale_log2 : -INFINITY;
       float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
@@ -1245,14 +1452,10 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const __grid_constant_
       const float m_use = (m_new == -INFINITY) ? 0.0f : m_new;
       float pr[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) pr[i] = exp2f(x[i] - (m_use - P_SHIFT));
-      if (__any_sync(0xffffffffu, m_new != m_run) || (KVM == KVM_F8 && in.vs != vs_run)) {
-        float alpha = exp2f(m_run - m_use);
+      for (int i = 0; i < 4; ++i) pr[i] = exp2f(x[i] - m_use);
+      if (__any_sync(0xffffffffu, m_new != m_run)) {
+        const float alpha = exp2f(m_run - m_use);
         l_part *= alpha;
-        if constexpr (KVM == KVM_F8) {
-          alpha *= vs_run / in.vs;  // acc goes over to this block's V scale
-          vs_run = in.vs;
-        }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           acc[i][0] *= alpha;
@@ -1275,38 +1478,16 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const __grid_constant_
       const uint32_t pa2 = pack_half2(hi[2], hi[3]);
       const uint32_t pa3 = pack_half2(lo[2], lo[3]);
       // ---- O += P V
-      if constexpr (KVM == KVM_F8) {
-        // a transposed register holds two tokens' pairs of channels (2g, 2g + 1):
-        // the permute makes a pair of tokens per channel, with zeros for tokens
-        // behind the sequence's end (their codes may be anything)
-        const uint32_t p0 = f8_permute(tok0, in.ntok), p1 = f8_permute(tok0 + 8, in.ntok);
 #pragma unroll
-        for (int cp = 0; cp < 4; ++cp) {
-          const int tok = warp * 16 + (mi & 1) * 8 + r;
-          const uint32_t addr = vb + tok * 128 + (((cp * 2 + (mi >> 1)) ^ (tok & 7)) << 4);
-          uint32_t c0, c1, c2, c3;
-          ldsm_x4_t(c0, c1, c2, c3, addr);
-          c0 = __byte_perm(c0, 0u, p0);
-          c1 = __byte_perm(c1, 0u, p1);
-          c2 = __byte_perm(c2, 0u, p0);
-          c3 = __byte_perm(c3, 0u, p1);
-          mma_16816(acc[4 * cp], pa0, pa1, pa2, pa3, f8x2_lo(c0), f8x2_lo(c1));
-          mma_16816(acc[4 * cp + 1], pa0, pa1, pa2, pa3, f8x2_hi(c0), f8x2_hi(c1));
-          mma_16816(acc[4 * cp + 2], pa0, pa1, pa2, pa3, f8x2_lo(c2), f8x2_lo(c3));
-          mma_16816(acc[4 * cp + 3], pa0, pa1, pa2, pa3, f8x2_hi(c2), f8x2_hi(c3));
-        }
-      } else {
-#pragma unroll
-        for (int cp = 0; cp < 8; ++cp) {
-          const int tok = warp * 16 + (mi & 1) * 8 + r;
-          const int chunk = cp * 2 + (mi >> 1);
-          const uint32_t addr = vb + (chunk >> 3) * BOX_BYTES + tok * 128 +
-                                (((chunk & 7) ^ (tok & 7)) << 4);
-          uint32_t b0, b1, b2, b3;
-          ldsm_x4_t(b0, b1, b2, b3, addr);
-          mma_16816(acc[2 * cp], pa0, pa1, pa2, pa3, b0, b1);
-          mma_16816(acc[2 * cp + 1], pa0, pa1, pa2, pa3, b2, b3);
-        }
+      for (int cp = 0; cp < 8; ++cp) {
+        const int tok = warp * 16 + (mi & 1) * 8 + r;
+        const int chunk = cp * 2 + (mi >> 1);
+        const uint32_t addr = vb + (chunk >> 3) * BOX_BYTES + tok * 128 +
+                              (((chunk & 7) ^ (tok & 7)) << 4);
+        uint32_t b0, b1, b2, b3;
+        ldsm_x4_t(b0, b1, b2, b3, addr);
+        mma_16816(acc[2 * cp], pa0, pa1, pa2, pa3, b0, b1);
+        mma_16816(acc[2 * cp + 1], pa0, pa1, pa2, pa3, b2, b3);
       }
     }
     __syncwarp();
@@ -1328,7 +1509,9 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const __grid_constant_
     wst = reinterpret_cast<float*>(smem + SmemLayout::kv);
     named_bar_sync(1, NCT);
   }
-  {
+  if constexpr (KVM == KVM_F8) {
+    f8_store(f8, wst + (size_t)warp * p.G * WST, WST, p.G, lane);
+  } else {
     float l_row = l_part;
     l_row += __shfl_xor_sync(0xffffffffu, l_row, 1);
     l_row += __shfl_xor_sync(0xffffffffu, l_row, 2);
@@ -1338,24 +1521,10 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const __grid_constant_
         sw[0] = m_run;
         sw[1] = l_row;
       }
-      if constexpr (KVM == KVM_F8) {
-        // tiles 2c and 2c + 1 hold the even and odd channels of piece c
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const float* e = acc[2 * c];
-          const float* o = acc[2 * c + 1];
-          float* d = sw + 2 + c * 16 + 4 * t;
-          *reinterpret_cast<float2*>(d) =
-              make_float2((e[0] + e[2]) * vs_run, (o[0] + o[2]) * vs_run);
-          *reinterpret_cast<float2*>(d + 2) =
-              make_float2((e[1] + e[3]) * vs_run, (o[1] + o[3]) * vs_run);
-        }
-      } else {
-#pragma unroll
-        for (int nt = 0; nt < 16; ++nt)
-          *reinterpret_cast<float2*>(sw + 2 + nt * 8 + 2 * t) =
-              make_float2(acc[nt][0] + acc[nt][2], acc[nt][1] + acc[nt][3]);
-      }
+      for (int nt = 0; nt < 16; ++nt)
+        *reinterpret_cast<float2*>(sw + 2 + nt * 8 + 2 * t) =
+            make_float2(acc[nt][0] + acc[nt][2], acc[nt][1] + acc[nt][3]);
     }
   }
   named_bar_sync(1, NCT);
