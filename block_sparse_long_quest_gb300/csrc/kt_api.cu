@@ -1393,6 +1393,8 @@ kt_status kt_read_kv_f8(const kt_paged_kv_f8* kvf, const int32_t* first, const i
   a.P = kv.num_pages;
   a.tokens = tokens;
   a.dtype = out_dtype;
+  a.num_sms = num_sms();
+  if (a.num_sms <= 0) return KT_ERR_CUDA;
   return cuda_status(launch_read_f8(a, (cudaStream_t)stream));
 }
 

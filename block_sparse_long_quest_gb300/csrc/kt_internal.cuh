@@ -676,7 +676,7 @@ struct ReadF8Launch {
   const int32_t* first;  // nullable: zeros
   const int32_t* cu;
   int* status;
-  int B, H_kv, max_blocks, P, tokens, dtype;
+  int B, H_kv, max_blocks, P, tokens, dtype, num_sms;
 };
 cudaError_t launch_read_f8(const ReadF8Launch& a, cudaStream_t stream);
 

@@ -486,39 +486,62 @@ struct ReadParams {
   const int32_t* first;
   const int32_t* cu;
   int* status;
-  int B, H_kv, max_blocks, P, tokens;
+  int B, H_kv, max_blocks, P, tokens, heads_per, row_steps;
 };
 
-__device__ __forceinline__ void store4(__half* p, float2 a, float2 b) {
-  *reinterpret_cast<uint2*>(p) =
-      make_uint2(as_u32(__floats2half2_rn(a.x, a.y)), as_u32(__floats2half2_rn(b.x, b.y)));
+// eight values as the output's type, 16-byte stores
+__device__ __forceinline__ void store8(__half* p, const float2 (&v)[4]) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(
+      as_u32(__floats2half2_rn(v[0].x, v[0].y)), as_u32(__floats2half2_rn(v[1].x, v[1].y)),
+      as_u32(__floats2half2_rn(v[2].x, v[2].y)), as_u32(__floats2half2_rn(v[3].x, v[3].y)));
 }
-__device__ __forceinline__ void store4(__nv_bfloat16* p, float2 a, float2 b) {
-  const __nv_bfloat162 x = __floats2bfloat162_rn(a.x, a.y), y = __floats2bfloat162_rn(b.x, b.y);
-  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&x),
-                                            *reinterpret_cast<const uint32_t*>(&y));
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float2 (&v)[4]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(v[i].x, v[i].y);
+    w[i] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
-__device__ __forceinline__ void store4(float* p, float2 a, float2 b) {
-  *reinterpret_cast<float4*>(p) = make_float4(a.x, a.y, b.x, b.y);
+__device__ __forceinline__ void store8(float* p, const float2 (&v)[4]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
 }
 
-constexpr int READ_ROWS = 16;
+constexpr int READ_LANES = 16;                      // lanes of a head row, 8 codes each
+constexpr int READ_GROUPS = THREADS / READ_LANES;   // 16 rows at a time
+constexpr int READ_MAX_ROWS = 4 * READ_GROUPS;
 
-// A CTA takes 16 rows: one thread each finds the row's sequence, page and place;
-// then lanes read 4 codes and write 4 values, a warp one head row.
+// Read-back: a CTA takes up to 64 rows of a group of heads; its first warps find
+// each row's sequence, page and place, then 16 lanes read a head row (8 codes, 128
+// bytes together) and write it (16 bytes each of binary16).  A lane has up to
+// eight loads in flight (four heads or rows, K and V) before its first store.
+// Bound by HBM: one byte in, two out for each value.
 template <class O>
 __global__ void __launch_bounds__(THREADS) read_f8_kernel(const __grid_constant__ ReadParams p) {
-  __shared__ int sh_page[READ_ROWS], sh_row[READ_ROWS];
-  const int tid = threadIdx.x, t0 = (int)blockIdx.x * READ_ROWS;
-  if (tid < READ_ROWS) {
-    const int t = t0 + tid;
+  __shared__ int sh_page[READ_MAX_ROWS], sh_row[READ_MAX_ROWS];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int tid = threadIdx.x, rows = READ_GROUPS * p.row_steps;
+  const int t0 = (int)blockIdx.x * rows;
+  if (tid < ((rows + 31) & ~31)) {  // whole warps
+    const int lane = tid & 31, t = t0 + tid;
+    // the last sequence that begins at or before row t0 + 32 * warp, 32 at a time
+    const int tw = t0 + (tid & ~31);
+    int lo = 0, n = p.B;
+    while (n > 1) {
+      const int step = (n + 31) / 32;
+      const int s = lo + lane * step;
+      const bool le = lane * step < n && p.cu[s] <= tw;
+      const unsigned int at = __ballot_sync(0xffffffffu, le) | 1u;
+      const int k = 31 - __clz(at);
+      lo += k * step;
+      n = min(step, n - k * step);
+    }
     int page = -1, row = 0;
-    if (t < p.tokens) {
-      int lo = 0, hi = p.B - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (p.cu[mid] <= t) lo = mid; else hi = mid - 1;
-      }
+    if (tid < rows && t < p.tokens) {
+      while (lo + 1 < p.B && p.cu[lo + 1] <= t) ++lo;
       const int c0 = p.cu[lo], c1 = p.cu[lo + 1];
       const long long pos = (p.first ? (long long)p.first[lo] : 0ll) + (t - c0);
       if (t >= c0 && t < c1 && pos >= 0 && pos < p.seq_lens[lo] &&
@@ -527,28 +550,57 @@ __global__ void __launch_bounds__(THREADS) read_f8_kernel(const __grid_constant_
         row = (int)(pos % BS);
         if ((unsigned)page >= (unsigned)p.P) page = -1;
       }
-      if (page < 0) set_status(p.status, KT_ERR_DEVICE_CHECK);
+      if (page < 0 && blockIdx.y == 0) set_status(p.status, KT_ERR_DEVICE_CHECK);
     }
-    sh_page[tid] = page;
-    sh_row[tid] = row;
+    if (tid < rows) {
+      sh_page[tid] = page;
+      sh_row[tid] = row;
+    }
   }
   __syncthreads();
-  const int warp = tid >> 5, lane = tid & 31;
+  const int grp = tid / READ_LANES, c8 = (tid & (READ_LANES - 1)) * 8;
+  const int h0 = (int)blockIdx.y * p.heads_per, h1 = min(h0 + p.heads_per, p.H_kv);
+  // items of a lane group: rows grp, grp + 16, .. and the heads of each
+  const int nh = h1 - h0, items = p.row_steps * nh;
+  for (int i0 = 0; i0 < items; i0 += 4) {
+    uint2 c[4][2];
+    float s[4][2];
+    size_t at[4];
+    bool ok[4];
 #pragma unroll
-  for (int side = 0; side < 2; ++side) {
-    if (!p.out[side]) continue;
-    for (int i = warp; i < READ_ROWS * p.H_kv; i += WARPS) {
-      const int r = i / p.H_kv, h = i - r * p.H_kv;
-      const int page = sh_page[r];
-      if (page < 0) continue;
-      const size_t slab = (size_t)page * p.H_kv + h;
-      const float s = p.scale[side][slab];
-      const uint32_t c = reinterpret_cast<const uint32_t*>(p.code[side] + slab * TILE_BYTES +
-                                                           sh_row[r] * D)[lane];
-      const float2 x = __half22float2(as_h2(f8x2_lo(c)));
-      const float2 y = __half22float2(as_h2(f8x2_hi(c)));
-      store4(static_cast<O*>(p.out[side]) + ((size_t)(t0 + r) * p.H_kv + h) * D + 4 * lane,
-             make_float2(x.x * s, x.y * s), make_float2(y.x * s, y.y * s));
+    for (int i = 0; i < 4; ++i) {
+      const int it = i0 + i;
+      const int q = it / nh, rr = grp + q * READ_GROUPS, h = h0 + it - q * nh;
+      ok[i] = it < items && sh_page[rr] >= 0;
+      if (ok[i]) {
+        const size_t slab = (size_t)sh_page[rr] * p.H_kv + h;
+        at[i] = ((size_t)(t0 + rr) * p.H_kv + h) * D + c8;
+#pragma unroll
+        for (int side = 0; side < 2; ++side)
+          if (p.out[side]) {
+            c[i][side] = __ldcs(reinterpret_cast<const uint2*>(
+                p.code[side] + slab * TILE_BYTES + sh_row[rr] * D + c8));
+            s[i][side] = __ldg(p.scale[side] + slab);
+          }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (!ok[i]) continue;
+#pragma unroll
+      for (int side = 0; side < 2; ++side)
+        if (p.out[side]) {
+          const uint32_t w[4] = {f8x2_lo(c[i][side].x), f8x2_hi(c[i][side].x),
+                                 f8x2_lo(c[i][side].y), f8x2_hi(c[i][side].y)};
+          float2 v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            v[e] = __half22float2(as_h2(w[e]));
+            v[e].x *= s[i][side];
+            v[e].y *= s[i][side];
+          }
+          store8(static_cast<O*>(p.out[side]) + at[i], v);
+        }
     }
   }
 }
@@ -677,14 +729,33 @@ cudaError_t launch_read_f8(const ReadF8Launch& a, cudaStream_t stream) {
   p.max_blocks = a.max_blocks;
   p.P = a.P;
   p.tokens = a.tokens;
-  const unsigned grid = (unsigned)(((long long)a.tokens + READ_ROWS - 1) / READ_ROWS);
+  // four items a lane group where that leaves four CTAs an SM; fewer for short
+  // calls, where the rows and heads are spread instead
+  const long long groups = ((long long)a.tokens + READ_GROUPS - 1) / READ_GROUPS;
+  const long long want = 4ll * a.num_sms;
+  p.heads_per = a.H_kv;
+  while (p.heads_per > 1 && groups * ((a.H_kv + p.heads_per - 1) / p.heads_per) < want)
+    p.heads_per = (p.heads_per + 1) / 2;
+  p.row_steps = 1;
+  while (p.row_steps < 4 && p.row_steps * 2 * p.heads_per <= 4 && groups / (p.row_steps * 2) >= want)
+    p.row_steps *= 2;
+  const int rows = READ_GROUPS * p.row_steps;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(((long long)a.tokens + rows - 1) / rows),
+                     (unsigned)((a.H_kv + p.heads_per - 1) / p.heads_per));
+  cfg.blockDim = dim3(THREADS);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
   switch (a.dtype) {
-    case KT_F16: read_f8_kernel<__half><<<grid, THREADS, 0, stream>>>(p); break;
-    case KT_BF16: read_f8_kernel<__nv_bfloat16><<<grid, THREADS, 0, stream>>>(p); break;
-    case KT_F32: read_f8_kernel<float><<<grid, THREADS, 0, stream>>>(p); break;
-    default: return cudaErrorInvalidValue;
+    case KT_F16: return cudaLaunchKernelEx(&cfg, read_f8_kernel<__half>, p);
+    case KT_BF16: return cudaLaunchKernelEx(&cfg, read_f8_kernel<__nv_bfloat16>, p);
+    case KT_F32: return cudaLaunchKernelEx(&cfg, read_f8_kernel<float>, p);
   }
-  return cudaGetLastError();
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace kt
