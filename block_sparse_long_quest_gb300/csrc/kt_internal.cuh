@@ -618,10 +618,13 @@ struct QuantLaunch {
 };
 cudaError_t launch_quant(const QuantLaunch& a, cudaStream_t stream);
 
-// Rotation of q and k rows (kt_apply_rope).
+// Rotation of q and k rows (kt_apply_rope; the q rows of a long append).
 struct RopeLaunch {
-  const kt_rope* rope;
-  const int32_t* positions;
+  const kt_rope* rope;       // nullable: the rows are only rounded
+  const int32_t* positions;  // nullable: row t is token seq_lens[s] + t - cu[s] of its sequence s
+  const int32_t* cu;
+  const int32_t* seq_lens;
+  int B;
   const void* q;
   const void* k;
   long long qs, ks;

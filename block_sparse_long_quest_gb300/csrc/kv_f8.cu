@@ -16,6 +16,8 @@
 // has its representatives made from the codes in shared memory.  The rotation
 // of q rides in the same launch on CTAs of its own, and one more CTA writes the
 // lengths (in place: the CTA that finishes last does).
+#include <cstring>
+
 #include "rope.cuh"
 
 namespace kt {
@@ -24,9 +26,9 @@ namespace {
 constexpr int THREADS = 256;
 constexpr int WARPS = THREADS / 32;
 constexpr int ROWS_PER = BS / (THREADS / ROPE_UNITS);  // row steps of a lane: 4
-constexpr int Q_TOK = 4;                               // tokens of a q CTA at most
 constexpr int RED_BYTES = 2 * WARPS * D * 2;           // representatives: partials per warp
 constexpr int TILE_BYTES = BS * D;
+constexpr int APPEND_HEADS = 2;                        // heads of an append CTA at most
 
 struct Params {
   kt_rope rope;  // rotary_dim 0: no rotation
@@ -47,7 +49,8 @@ struct Params {
   int* status;
   int* ticket;
   int B, H_kv, H_q, max_blocks, P, tokens, rep, R, fix_stride;
-  int heads_per, groups, cache_ctas, q_ctas, q_per, cs_rows;
+  int heads_per, groups, cache_ctas, q_ctas, q_heads, cs_rows;
+  int late_wait;  // the launch before is this call's rotation of q: wait for it at the end
 };
 
 struct Span {
@@ -277,8 +280,30 @@ __device__ void write_lengths(const Params& p, int tid) {
   }
 }
 
+// A lane's part of a tile's new rows as loaded.
 template <class T>
+struct TileRaw {
+  Raw8<T> a[ROWS_PER], b[ROWS_PER];
+};
+template <class T>
+__device__ __forceinline__ void load_tile(TileRaw<T>& x, const T* src, long long stride, int r0,
+                                          int r1, int tid, int va, int vb) {
+#pragma unroll
+  for (int i = 0; i < ROWS_PER; ++i) {
+    const int r = (tid >> 3) + i * (THREADS / ROPE_UNITS);
+    if (r >= r0 && r < r1) {
+      const T* row = src + (r - r0) * stride;
+      x.a[i] = load8(row + 8 * va);
+      x.b[i] = load8(row + 8 * vb);
+    }
+  }
+}
+
+template <class T, int M>
 __device__ void append_tile(const Params& p, int cta, uint8_t* smem, int* sh, int tid) {
+  // 16-bit rows of the next head are loaded while a head is coded; the registers
+  // do not hold two of binary32
+  constexpr bool AHEAD = M != ROPE_M_NONE && sizeof(T) == 2;
   const int warp = tid >> 5, lane = tid & 31;
   const int per_tile = 2 * p.groups;
   const int tile = cta / per_tile, rest = cta - tile * per_tile;
@@ -290,6 +315,13 @@ __device__ void append_tile(const Params& p, int cta, uint8_t* smem, int* sh, in
   if (!find_tile(p, tile, sh, tid, &b, &j, &a)) return;
   const int r0 = j == a.n / BS ? a.n % BS : 0, r1 = min(BS, a.n + a.m - j * BS);
   const int page = p.table[(size_t)b * p.max_blocks + j];
+  int va, vb;
+  row_vectors<M>(p.rope, tid & (ROPE_UNITS - 1), &va, &vb);
+  const long long stride = is_v ? p.vs : p.ks;
+  const T* src = static_cast<const T*>(is_v ? p.v : p.k) +
+                 ((long long)a.c0 + ((long long)j * BS + r0 - a.n)) * stride;
+  TileRaw<T> raw;
+  load_tile(raw, src + h0 * D, stride, r0, r1, tid, va, vb);
   if ((unsigned)page >= (unsigned)p.P) {
     if (tid == 0) set_status(p.status, KT_ERR_DEVICE_CHECK);
     return;
@@ -297,36 +329,38 @@ __device__ void append_tile(const Params& p, int cta, uint8_t* smem, int* sh, in
   float2* cs = reinterpret_cast<float2*>(smem);
   uint8_t* codes = smem + p.cs_rows * 64 * sizeof(float2);
   uint8_t* red = codes + TILE_BYTES;
-  const bool turn = !is_v && p.rope.rotary_dim > 0;
-  int va, vb;
-  row_vectors(p.rope, tid & (ROPE_UNITS - 1), &va, &vb);
+  const bool turn = M != ROPE_M_NONE && !is_v;
   if (turn) {
     const int half = p.rope.rotary_dim >> 1;
     for (int i = tid; i < (r1 - r0) * 64; i += THREADS)
-      if ((i & 63) < half) cs[i] = rope_cos_sin(p.rope, i & 63, j * BS + r0 + (i >> 6));
+      if ((i & 63) < half)
+        cs[(i & ~63) + cs_at(i & 63)] = rope_cos_sin(p.rope, i & 63, j * BS + r0 + (i >> 6));
     __syncthreads();
   }
-  const T* src = static_cast<const T*>(is_v ? p.v : p.k);
-  const long long stride = is_v ? p.vs : p.ks;
-  const long long tok0 = (long long)a.c0 + ((long long)j * BS + r0 - a.n);
   const bool complete = !is_v && p.reps && r1 == BS;
   float* red_max = reinterpret_cast<float*>(sh);
+#pragma unroll 1
   for (int h = h0; h < h1; ++h) {
     const size_t slab = (size_t)page * p.H_kv + h;
     float* scale = (is_v ? p.v_scale : p.k_scale) + slab;
     uint8_t* dst = (is_v ? p.v_code : p.k_code) + slab * TILE_BYTES;
     const float old = r0 > 0 ? *scale : 0.0f;
+    if (!AHEAD && h > h0) load_tile(raw, src + h * D, stride, r0, r1, tid, va, vb);
     uint32_t xa[ROWS_PER][4], xb[ROWS_PER][4];
     __half2 mx = __float2half2_rn(0.0f);
 #pragma unroll
     for (int i = 0; i < ROWS_PER; ++i) {
       const int r = (tid >> 3) + i * (THREADS / ROPE_UNITS);
       if (r >= r0 && r < r1) {
-        const T* row = src + (tok0 + (r - r0)) * stride + h * D;
         float x[8], y[8];
-        load8(row + 8 * va, x);
-        load8(row + 8 * vb, y);
-        if (turn) rope_rotate(p.rope, cs + (r - r0) * 64, row, va, vb, x, y);
+        unpack8(raw.a[i], x);
+        unpack8(raw.b[i], y);
+        if (turn) {
+          float2 w[8];
+          const float2* row_cs = cs + (r - r0) * 64;
+          rope_weights<M>(row_cs, va, vb, w);
+          rope_rotate<M>(p.rope, w, row_cs, src + (r - r0) * stride + h * D, va, vb, x, y);
+        }
         pack8(x, xa[i]);
         pack8(y, xb[i]);
 #pragma unroll
@@ -336,6 +370,7 @@ __device__ void append_tile(const Params& p, int cta, uint8_t* smem, int* sh, in
         }
       }
     }
+    if (AHEAD && h + 1 < h1) load_tile(raw, src + (h + 1) * D, stride, r0, r1, tid, va, vb);
     float am = fmaxf(__low2float(mx), __high2float(mx));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
@@ -354,35 +389,32 @@ __device__ void append_tile(const Params& p, int cta, uint8_t* smem, int* sh, in
         again = s > old;
       }
     }
-    const float ratio = again ? old / s : 1.0f;
     const __half2 inv = __float2half2_rn(1.0f / s);
     const bool top = s == 256.0f;
 #pragma unroll
     for (int i = 0; i < ROWS_PER; ++i) {
       const int r = (tid >> 3) + i * (THREADS / ROPE_UNITS);
-      uint2* da = reinterpret_cast<uint2*>(dst + r * D + 8 * va);
-      uint2* db = reinterpret_cast<uint2*>(dst + r * D + 8 * vb);
-      uint2 ca, cb;
       if (r >= r0 && r < r1) {
-        ca = code8(xa[i], inv, top);
-        cb = code8(xb[i], inv, top);
-        *da = ca;
-        *db = cb;
-      } else if (r < r0 && (again || complete)) {
-        ca = *da;
-        cb = *db;
-        if (again) {
-          ca = make_uint2(recode4(ca.x, ratio), recode4(ca.y, ratio));
-          cb = make_uint2(recode4(cb.x, ratio), recode4(cb.y, ratio));
-          *da = ca;
-          *db = cb;
+        const uint2 ca = code8(xa[i], inv, top), cb = code8(xb[i], inv, top);
+        *reinterpret_cast<uint2*>(dst + r * D + 8 * va) = ca;
+        *reinterpret_cast<uint2*>(dst + r * D + 8 * vb) = cb;
+        if (complete) {
+          *reinterpret_cast<uint2*>(codes + r * D + 8 * va) = ca;
+          *reinterpret_cast<uint2*>(codes + r * D + 8 * vb) = cb;
         }
-      } else {
-        continue;
       }
-      if (complete) {
-        *reinterpret_cast<uint2*>(codes + r * D + 8 * va) = ca;
-        *reinterpret_cast<uint2*>(codes + r * D + 8 * vb) = cb;
+    }
+    if (again || (complete && r0 > 0)) {  // the block's rows before the new ones
+      const float ratio = again ? old / s : 1.0f;
+#pragma unroll 1
+      for (int i = tid; i < r0 * (D / 16); i += THREADS) {
+        uint4 c = reinterpret_cast<const uint4*>(dst)[i];
+        if (again) {
+          c = make_uint4(recode4(c.x, ratio), recode4(c.y, ratio), recode4(c.z, ratio),
+                         recode4(c.w, ratio));
+          reinterpret_cast<uint4*>(dst)[i] = c;
+        }
+        if (complete) reinterpret_cast<uint4*>(codes)[i] = c;
       }
     }
     // every thread has read the old scale before the barriers above
@@ -394,48 +426,41 @@ __device__ void append_tile(const Params& p, int cta, uint8_t* smem, int* sh, in
   }
 }
 
-template <class T>
-__device__ void append_q(const Params& p, int cta, uint8_t* smem, int* sh, int tid) {
-  const int t0 = cta * p.q_per, ntok = min(p.q_per, p.tokens - t0);
-  float2* cs = reinterpret_cast<float2*>(smem);
-  if (p.rope.rotary_dim > 0) {
-    if (tid < ntok) {
-      const int t = t0 + tid;
-      int s = t, first = t;
-      if (p.cu) {  // the last sequence that begins at or before row t
-        int lo = 0, hi = p.B - 1;
-        while (lo < hi) {
-          const int mid = (lo + hi + 1) >> 1;
-          if (p.cu[mid] <= t) lo = mid; else hi = mid - 1;
-        }
-        s = lo;
-        first = p.cu[s];
-      }
-      sh[tid] = p.seq_lens[s] + (t - first);
-    }
-    __syncthreads();
-    for (int i = tid; i < ntok * 64; i += THREADS)
-      if ((i & 63) < p.rope.rotary_dim / 2) cs[i] = rope_cos_sin(p.rope, i & 63, sh[i >> 6]);
-    __syncthreads();
+// One warp a token (or a slice of its heads).
+template <class T, int M>
+__device__ void append_q(const Params& p, int unit, uint8_t* smem, int tid) {
+  const int warp = tid >> 5, lane = tid & 31;
+  unit = unit * WARPS + warp;
+  const int slices = (p.H_q + p.q_heads - 1) / p.q_heads;
+  const int t = unit / slices, h0 = (unit - t * slices) * p.q_heads;
+  if (t >= p.tokens) return;
+  int pos = 0;
+  if (M != ROPE_M_NONE) {
+    const int s = p.cu ? row_sequence(p.cu, p.B, t, lane) : t;
+    pos = p.seq_lens[s] + (t - (p.cu ? p.cu[s] : t));
   }
-  rope_tokens(p.rope, cs, t0, ntok, static_cast<const T*>(p.q), p.qs, p.H_q, p.q_out,
-              static_cast<const T*>(nullptr), 0, 0, nullptr, tid, THREADS);
+  rope_token<M, 1>(p.rope, reinterpret_cast<float2*>(smem) + warp * 64, pos, t, h0,
+                min(h0 + p.q_heads, p.H_q), static_cast<const T*>(p.q), p.qs, p.H_q, p.q_out,
+                static_cast<const T*>(nullptr), 0, 0, static_cast<__half*>(nullptr), lane);
 }
 
-template <class T>
-__global__ void __launch_bounds__(THREADS, 2) append_f8_kernel(const __grid_constant__ Params p) {
+template <class T, int M>
+__global__ void __launch_bounds__(THREADS, M == ROPE_M_NONE && sizeof(T) == 2 ? 3 : 2)
+    append_f8_kernel(const __grid_constant__ Params p) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ int sh[WARPS + 8];
-  static_assert(Q_TOK <= WARPS + 8, "positions of a q CTA");
-  griddep_wait();
+  if (!p.late_wait) griddep_wait();
   griddep_launch_dependents();
   const int tid = threadIdx.x, cta = blockIdx.x;
   if (cta < p.cache_ctas)
-    append_tile<T>(p, cta, smem, sh, tid);
+    append_tile<T, M>(p, cta, smem, sh, tid);
   else if (cta < p.cache_ctas + p.q_ctas)
-    append_q<T>(p, cta - p.cache_ctas, smem, sh, tid);
+    append_q<T, M>(p, cta - p.cache_ctas, smem, tid);
   else if (p.new_lens)
     write_lengths(p, tid);
+  // behind the rotation of q (which waited for everything before it), this launch
+  // may not end, nor change the lengths that it reads, before that one has
+  if (p.late_wait) griddep_wait();
   if (!p.new_lens) {
     // in place: once every CTA has read the lengths
     __syncthreads();
@@ -527,18 +552,7 @@ __global__ void __launch_bounds__(THREADS) read_f8_kernel(const __grid_constant_
   const int t0 = (int)blockIdx.x * rows;
   if (tid < ((rows + 31) & ~31)) {  // whole warps
     const int lane = tid & 31, t = t0 + tid;
-    // the last sequence that begins at or before row t0 + 32 * warp, 32 at a time
-    const int tw = t0 + (tid & ~31);
-    int lo = 0, n = p.B;
-    while (n > 1) {
-      const int step = (n + 31) / 32;
-      const int s = lo + lane * step;
-      const bool le = lane * step < n && p.cu[s] <= tw;
-      const unsigned int at = __ballot_sync(0xffffffffu, le) | 1u;
-      const int k = 31 - __clz(at);
-      lo += k * step;
-      n = min(step, n - k * step);
-    }
+    int lo = row_sequence(p.cu, p.B, t0 + (tid & ~31), lane);
     int page = -1, row = 0;
     if (tid < rows && t < p.tokens) {
       while (lo + 1 < p.B && p.cu[lo + 1] <= t) ++lo;
@@ -605,11 +619,11 @@ __global__ void __launch_bounds__(THREADS) read_f8_kernel(const __grid_constant_
   }
 }
 
-template <class T>
+template <class T, int M>
 cudaError_t launch_append_t(const Params& p, unsigned grid, size_t smem, cudaStream_t stream) {
   static std::atomic<int> slot[KT_MAX_DEVICES];
   const cudaError_t e = (cudaError_t)per_device_cached(slot, [] {
-    return (int)cudaFuncSetAttribute((const void*)append_f8_kernel<T>,
+    return (int)cudaFuncSetAttribute((const void*)append_f8_kernel<T, M>,
                                      cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      BS * 64 * (int)sizeof(float2) + TILE_BYTES + RED_BYTES);
   });
@@ -624,20 +638,27 @@ cudaError_t launch_append_t(const Params& p, unsigned grid, size_t smem, cudaStr
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, append_f8_kernel<T>, p);
+  return cudaLaunchKernelEx(&cfg, append_f8_kernel<T, M>, p);
+}
+
+template <class T>
+cudaError_t launch_append_m(const Params& p, int mode, unsigned grid, size_t smem,
+                            cudaStream_t stream) {
+  switch (mode) {
+    case ROPE_M_NONE: return launch_append_t<T, ROPE_M_NONE>(p, grid, smem, stream);
+    case ROPE_M_VECTORS: return launch_append_t<T, ROPE_M_VECTORS>(p, grid, smem, stream);
+    case ROPE_M_PAIRS: return launch_append_t<T, ROPE_M_PAIRS>(p, grid, smem, stream);
+    case ROPE_M_ANY: return launch_append_t<T, ROPE_M_ANY>(p, grid, smem, stream);
+  }
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
 cudaError_t launch_append_f8(const AppendF8Launch& a, cudaStream_t stream) {
   Params p;
-  if (a.rope) {
-    p.rope = *a.rope;
-  } else {
-    p.rope.rotary_dim = 0;
-    p.rope.layout = KT_ROPE_PAIRS;
-    p.rope.amplitude = 1.0f;
-  }
+  std::memset(&p, 0, sizeof(p));
+  if (a.rope) p.rope = *a.rope;
   p.q = a.q;
   p.k = a.k;
   p.v = a.v;
@@ -669,24 +690,53 @@ cudaError_t launch_append_f8(const AppendF8Launch& a, cudaStream_t stream) {
   const long long seqs = a.B < a.tokens ? a.B : a.tokens;
   long long tiles = a.tokens / BS + 2 * seqs;
   if (tiles > a.tokens) tiles = a.tokens;
-  // heads of a CTA: as many as leave two CTAs an SM, so that few angles are computed twice
-  long long per = tiles * a.H_kv / a.num_sms;
-  per = per < 1 ? 1 : per > a.H_kv ? a.H_kv : per;
+  // a head a CTA; with a rotation two where that leaves four CTAs an SM, so that
+  // fewer angles are computed twice and the next head's rows are on their way
+  long long per = a.rope ? tiles * a.H_kv / (2ll * a.num_sms) : 1;
+  per = per < 1 ? 1 : per > APPEND_HEADS ? APPEND_HEADS : per;
   p.groups = (int)((a.H_kv + per - 1) / per);
   p.heads_per = (a.H_kv + p.groups - 1) / p.groups;
   const long long cache = tiles * 2 * p.groups;
-  p.q_per = a.tokens >= 4 * a.num_sms ? Q_TOK : 1;
-  const long long qn = a.q ? ((long long)a.tokens + p.q_per - 1) / p.q_per : 0;
+  // many q rows go ahead in a launch of their own, which has the shared memory
+  // for more warps an SM than the tiles leave; few ride along
+  if (a.q && a.cu && a.tokens >= 16 * a.num_sms) {
+    RopeLaunch q;
+    std::memset(&q, 0, sizeof(q));
+    q.rope = a.rope;
+    q.cu = a.cu;
+    q.seq_lens = a.seq_lens;
+    q.B = a.B;
+    q.q = a.q;
+    q.qs = a.qs;
+    q.q_out = a.q_out;
+    q.hq = a.H_q;
+    q.tokens = a.tokens;
+    q.dtype = a.dtype;
+    q.num_sms = a.num_sms;
+    const cudaError_t e = launch_rope(q, stream);
+    if (e != cudaSuccess) return e;
+    p.q = nullptr;
+    p.late_wait = 1;
+  }
+  p.q_heads = a.H_q > 0 ? a.H_q : 1;
+  while (p.q_heads > 4 &&
+         (long long)a.tokens * ((a.H_q + p.q_heads - 1) / p.q_heads) < 16ll * a.num_sms)
+    p.q_heads = (((p.q_heads + 1) / 2) + 3) & ~3;
+  const long long qn =
+      p.q ? ((long long)a.tokens * ((a.H_q + p.q_heads - 1) / p.q_heads) + WARPS - 1) / WARPS : 0;
   if (cache + qn + 1 > 0x7FFFFFFFll) return cudaErrorInvalidValue;
   p.cache_ctas = (int)cache;
   p.q_ctas = (int)qn;
-  p.cs_rows = a.cu ? BS : Q_TOK;  // a decoded token needs one row, a q CTA up to four
-  const size_t smem = (size_t)p.cs_rows * 64 * sizeof(float2) + TILE_BYTES + RED_BYTES;
+  // angles: of a tile's rows, or of a decoded token and the q rows (one a warp)
+  p.cs_rows = a.rope ? (a.cu ? BS : WARPS) : 0;
+  const size_t smem = (size_t)p.cs_rows * 64 * sizeof(float2) +
+                      (p.reps ? (size_t)TILE_BYTES + RED_BYTES : 0);
   const unsigned grid = (unsigned)(cache + qn + 1);
+  const int mode = rope_mode(a.rope);
   switch (a.dtype) {
-    case KT_F16: return launch_append_t<__half>(p, grid, smem, stream);
-    case KT_BF16: return launch_append_t<__nv_bfloat16>(p, grid, smem, stream);
-    case KT_F32: return launch_append_t<float>(p, grid, smem, stream);
+    case KT_F16: return launch_append_m<__half>(p, mode, grid, smem, stream);
+    case KT_BF16: return launch_append_m<__nv_bfloat16>(p, mode, grid, smem, stream);
+    case KT_F32: return launch_append_m<float>(p, mode, grid, smem, stream);
   }
   return cudaErrorInvalidValue;
 }

@@ -21,9 +21,31 @@ namespace kt {
 
 constexpr int ROPE_UNITS = 8;  // lanes of a head row, two 8-channel vectors each
 
-__device__ __forceinline__ void load8(const __half* p, float (&x)[8]) {
-  const uint4 v = *reinterpret_cast<const uint4*>(p);
-  const __half2* h = reinterpret_cast<const __half2*>(&v);
+// How channels are paired, one kernel instantiation each (one that branches over
+// them needs twice the registers): no rotation, HALF by whole vectors (rotary_dim
+// a multiple of 16), PAIRS, any other HALF.
+enum : int { ROPE_M_NONE = 0, ROPE_M_VECTORS = 1, ROPE_M_PAIRS = 2, ROPE_M_ANY = 3 };
+inline int rope_mode(const kt_rope* r) {
+  return !r                              ? ROPE_M_NONE
+         : r->layout == KT_ROPE_PAIRS    ? ROPE_M_PAIRS
+         : (r->rotary_dim & 15) == 0     ? ROPE_M_VECTORS
+                                         : ROPE_M_ANY;
+}
+
+// Eight values of a row as loaded, and in binary32.
+template <class T>
+struct Raw8 {
+  uint4 v[sizeof(T) / 2];
+};
+template <class T>
+__device__ __forceinline__ Raw8<T> load8(const T* p) {
+  Raw8<T> r;
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(T) / 2); ++i) r.v[i] = reinterpret_cast<const uint4*>(p)[i];
+  return r;
+}
+__device__ __forceinline__ void unpack8(const Raw8<__half>& r, float (&x)[8]) {
+  const __half2* h = reinterpret_cast<const __half2*>(&r.v[0]);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 f = __half22float2(h[i]);
@@ -31,9 +53,8 @@ __device__ __forceinline__ void load8(const __half* p, float (&x)[8]) {
     x[2 * i + 1] = f.y;
   }
 }
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
-  const uint4 v = *reinterpret_cast<const uint4*>(p);
-  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&v);
+__device__ __forceinline__ void unpack8(const Raw8<__nv_bfloat16>& r, float (&x)[8]) {
+  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&r.v[0]);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 f = __bfloat1622float2(h[i]);
@@ -41,10 +62,14 @@ __device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
     x[2 * i + 1] = f.y;
   }
 }
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-  x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+__device__ __forceinline__ void unpack8(const Raw8<float>& r, float (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    x[4 * i] = __uint_as_float(r.v[i].x);
+    x[4 * i + 1] = __uint_as_float(r.v[i].y);
+    x[4 * i + 2] = __uint_as_float(r.v[i].z);
+    x[4 * i + 3] = __uint_as_float(r.v[i].w);
+  }
 }
 __device__ __forceinline__ float load1(const __half* p) { return __half2float(*p); }
 __device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
@@ -62,52 +87,67 @@ __device__ __forceinline__ float2 rope_cos_sin(const kt_rope& r, int i, int pos)
 }
 
 // The two vectors (8 channels each) of lane j of a head row.
+template <int M>
 __device__ __forceinline__ void row_vectors(const kt_rope& r, int j, int* va, int* vb) {
-  const int nv = r.layout == KT_ROPE_HALF && (r.rotary_dim & 15) == 0 ? r.rotary_dim >> 4 : 0;
-  if (nv) {
-    *va = j < nv ? j : 2 * j;  // behind the pairs: 2 nv + 2 (j - nv)
-    *vb = j < nv ? j + nv : 2 * j + 1;
-  } else {
-    *va = j;
-    *vb = j + 8;
+  const int nv = M == ROPE_M_VECTORS ? r.rotary_dim >> 4 : 8;
+  *va = j < nv ? j : 2 * j;  // behind the pairs: 2 nv + 2 (j - nv)
+  *vb = j < nv ? j + nv : 2 * j + 1;
+}
+
+// Place of pair i in a row's table of 64 (cos, sin): the 16-byte words that the 8
+// lanes of a row read together (pairs 8j + e, e fixed, of a HALF rotation) lie side
+// by side, so a read has no bank conflicts.
+__device__ __forceinline__ int cs_at(int i) { return (i & 6) * 8 + (i >> 3) * 2 + (i & 1); }
+
+// The (cos, sin) of the eight pairs in a lane's vectors (M_VECTORS, M_PAIRS); cs:
+// the row's table.
+template <int M>
+__device__ __forceinline__ void rope_weights(const float2* cs, int va, int vb, float2 (&w)[8]) {
+  if constexpr (M == ROPE_M_VECTORS || M == ROPE_M_PAIRS) {
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+      const int i = M == ROPE_M_PAIRS ? 4 * (e < 4 ? va : vb) + (e & 3) : 8 * va + e;
+      // a lane without pairs reads any entry of the table
+      const float4 v = *reinterpret_cast<const float4*>(cs + cs_at(i & 63));
+      w[e] = make_float2(v.x, v.y);
+      w[e + 1] = make_float2(v.z, v.w);
+    }
   }
 }
 
-// Rotates vectors va and vb (values a, b) of the row at `row`; cs: the row's
-// (cos, sin) by pair.  Channels from rotary_dim on are left as they are.
-template <class T>
-__device__ __forceinline__ void rope_rotate(const kt_rope& r, const float2* cs, const T* row,
-                                            int va, int vb, float (&a)[8], float (&b)[8]) {
+// Rotates vectors va and vb (values a, b) of the row at `row`; w: rope_weights,
+// cs: the row's table.  Channels from rotary_dim on are left as they are.
+template <int M, class T>
+__device__ __forceinline__ void rope_rotate(const kt_rope& r, const float2 (&w)[8],
+                                            const float2* cs, const T* row, int va, int vb,
+                                            float (&a)[8], float (&b)[8]) {
   const int rot = r.rotary_dim;
-  if (r.layout == KT_ROPE_PAIRS) {
+  if constexpr (M == ROPE_M_PAIRS) {
 #pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      float* x = v ? b : a;
-      const int c0 = 8 * (v ? vb : va);
-#pragma unroll
-      for (int e = 0; e < 8; e += 2) {
-        if (c0 + e < rot) {
-          const float2 w = cs[(c0 + e) >> 1];
-          const float p = x[e], q = x[e + 1];
-          x[e] = p * w.x - q * w.y;
-          x[e + 1] = q * w.x + p * w.y;
-        }
+    for (int e = 0; e < 4; ++e) {
+      if (8 * va + 2 * e < rot) {
+        const float x = a[2 * e], y = a[2 * e + 1];
+        a[2 * e] = x * w[e].x - y * w[e].y;
+        a[2 * e + 1] = y * w[e].x + x * w[e].y;
+      }
+      if (8 * vb + 2 * e < rot) {
+        const float x = b[2 * e], y = b[2 * e + 1];
+        b[2 * e] = x * w[4 + e].x - y * w[4 + e].y;
+        b[2 * e + 1] = y * w[4 + e].x + x * w[4 + e].y;
       }
     }
-  } else if ((rot & 15) == 0) {
-    if (8 * va < (rot >> 1)) {
-      const float4* w4 = reinterpret_cast<const float4*>(cs + 8 * va);
+  }
+  if constexpr (M == ROPE_M_VECTORS) {
+    if (16 * va < rot) {
 #pragma unroll
-      for (int e = 0; e < 8; e += 2) {
-        const float4 w = w4[e >> 1];
-        const float p = a[e], q = b[e], p1 = a[e + 1], q1 = b[e + 1];
-        a[e] = p * w.x - q * w.y;
-        b[e] = q * w.x + p * w.y;
-        a[e + 1] = p1 * w.z - q1 * w.w;
-        b[e + 1] = q1 * w.z + p1 * w.w;
+      for (int e = 0; e < 8; ++e) {
+        const float x = a[e], y = b[e];
+        a[e] = x * w[e].x - y * w[e].y;
+        b[e] = y * w[e].x + x * w[e].y;
       }
     }
-  } else {
+  }
+  if constexpr (M == ROPE_M_ANY) {
     const int half = rot >> 1;
 #pragma unroll
     for (int v = 0; v < 2; ++v) {
@@ -117,15 +157,29 @@ __device__ __forceinline__ void rope_rotate(const kt_rope& r, const float2* cs, 
       for (int e = 0; e < 8; ++e) {
         const int c = c0 + e;
         if (c < half) {
-          const float2 w = cs[c];
-          x[e] = x[e] * w.x - load1(row + c + half) * w.y;
+          const float2 u = cs[cs_at(c)];
+          x[e] = x[e] * u.x - load1(row + c + half) * u.y;
         } else if (c < rot) {
-          const float2 w = cs[c - half];
-          x[e] = x[e] * w.x + load1(row + c - half) * w.y;
+          const float2 u = cs[cs_at(c - half)];
+          x[e] = x[e] * u.x + load1(row + c - half) * u.y;
         }
       }
     }
   }
+}
+
+// The last sequence that begins at or before row t (cu: first rows, not
+// decreasing), by a whole warp, 32 candidates at a time.
+__device__ __forceinline__ int row_sequence(const int32_t* cu, int B, int t, int lane) {
+  int lo = 0, n = B;
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const bool le = lane * step < n && cu[lo + lane * step] <= t;
+    const int k = 31 - __clz(__ballot_sync(0xffffffffu, le) | 1u);
+    lo += k * step;
+    n = min(step, n - k * step);
+  }
+  return lo;
 }
 
 __device__ __forceinline__ void pack8(const float (&x)[8], uint32_t (&h)[4]) {
@@ -136,43 +190,67 @@ __device__ __forceinline__ void pack8(const float (&x)[8], uint32_t (&h)[4]) {
   }
 }
 
-// Rotates the head rows of `ntok` tokens (rows t0 .. of q and k) by a CTA of
-// `threads` threads; cs: [ntok][64] (cos, sin) in shared memory.
-template <class T>
-__device__ __forceinline__ void rope_tokens(const kt_rope& r, const float2* cs, int t0, int ntok,
-                                            const T* q, long long qs, int hq, __half* q_out,
-                                            const T* k, long long ks, int hk, __half* k_out,
-                                            int tid, int threads) {
-  const int j = tid & (ROPE_UNITS - 1), H = hq + hk, items = ntok * H;
+// Rotates heads h0 .. h1 - 1 (q's, then k's) of one token by one warp: four head
+// rows at a time, NB times four loaded before the first is stored; cs: 64 (cos,
+// sin) of shared memory of the warp's own, written behind the first loads and held
+// in registers over the heads.
+template <int M, int NB, class T>
+__device__ __forceinline__ void rope_token(const kt_rope& r, float2* cs, int pos, long long t,
+                                           int h0, int h1, const T* q, long long qs, int hq,
+                                           __half* q_out, const T* k, long long ks, int hk,
+                                           __half* k_out, int lane) {
+  const int j = lane & (ROPE_UNITS - 1), hl = lane / ROPE_UNITS, half = r.rotary_dim >> 1;
   int va, vb;
-  row_vectors(r, j, &va, &vb);
-  // items differ by lane group, and a group's 8 lanes pass together
-  for (int base = 0; base < items; base += threads / ROPE_UNITS) {
-    const int it = base + tid / ROPE_UNITS;
-    const bool live = it < items;
-    uint32_t ha[4], hb[4];
-    __half* dst = nullptr;
-    if (live) {
-      const int tok = it / H, h = it - tok * H;
-      const T* row;
-      if (h < hq) {
-        row = q + (long long)(t0 + tok) * qs + h * D;
-        dst = q_out + ((long long)(t0 + tok) * hq + h) * D;
-      } else {
-        row = k + (long long)(t0 + tok) * ks + (h - hq) * D;
-        dst = k_out + ((long long)(t0 + tok) * hk + (h - hq)) * D;
+  row_vectors<M>(r, j, &va, &vb);
+  const T* qr = q + t * qs;
+  const T* kr = k + t * ks - (long long)hq * D;
+  __half* qo = q_out + t * hq * D;
+  __half* ko = k_out + (t * hk - hq) * D;
+  float2 w[8];
+  bool first = true;
+  for (int h = h0; h < h1; h += 4 * NB) {
+    Raw8<T> ra[NB], rb[NB];
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      const int hh = h + 4 * i + hl;
+      if (hh < h1) {
+        const T* row = (hh < hq ? qr : kr) + hh * D;
+        ra[i] = load8(row + 8 * va);
+        rb[i] = load8(row + 8 * vb);
       }
-      float a[8], b[8];
-      load8(row + 8 * va, a);
-      load8(row + 8 * vb, b);
-      if (r.rotary_dim) rope_rotate(r, cs + tok * 64, row, va, vb, a, b);
-      pack8(a, ha);
-      pack8(b, hb);
+    }
+    if (M != ROPE_M_NONE && first) {
+#pragma unroll
+      for (int i = lane; i < 64; i += 32)
+        if (i < half) cs[cs_at(i)] = rope_cos_sin(r, i, pos);
+      __syncwarp();
+      rope_weights<M>(cs, va, vb, w);
+    }
+    first = false;
+    uint32_t ha[NB][4], hb[NB][4];
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      const int hh = h + 4 * i + hl;
+      if (hh < h1) {
+        float a[8], b[8];
+        unpack8(ra[i], a);
+        unpack8(rb[i], b);
+        rope_rotate<M>(r, w, cs, (hh < hq ? qr : kr) + hh * D, va, vb, a, b);
+        pack8(a, ha[i]);
+        pack8(b, hb[i]);
+      }
     }
     __syncwarp();  // in place: a row's lanes have all read it
-    if (live) {
-      *reinterpret_cast<uint4*>(dst + 8 * va) = make_uint4(ha[0], ha[1], ha[2], ha[3]);
-      *reinterpret_cast<uint4*>(dst + 8 * vb) = make_uint4(hb[0], hb[1], hb[2], hb[3]);
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      const int hh = h + 4 * i + hl;
+      if (hh < h1) {
+        __half* dst = (hh < hq ? qo : ko) + hh * D;
+        *reinterpret_cast<uint4*>(dst + 8 * va) =
+            make_uint4(ha[i][0], ha[i][1], ha[i][2], ha[i][3]);
+        *reinterpret_cast<uint4*>(dst + 8 * vb) =
+            make_uint4(hb[i][0], hb[i][1], hb[i][2], hb[i][3]);
+      }
     }
   }
 }
