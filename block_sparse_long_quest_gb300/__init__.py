@@ -219,11 +219,26 @@ def _ptr(t):
     return t.data_ptr()
 
 
+_current_stream = None  # set on first use: the raw handle of torch's current stream
+
+
+def _find_current_stream():
+    import torch
+    torch.cuda.current_stream()  # initialises CUDA
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    dev = getattr(torch._C, "_cuda_getDevice", None)
+    if raw is None or dev is None:
+        return lambda: torch.cuda.current_stream().cuda_stream
+    return lambda: raw(dev())  # no Stream object per call
+
+
 def _stream(stream):
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
-    import torch
-    return torch.cuda.current_stream().cuda_stream
+    global _current_stream
+    if _current_stream is None:
+        _current_stream = _find_current_stream()
+    return _current_stream()
 
 
 def _check(status, call):
@@ -428,9 +443,14 @@ def rope(rotary_dim=128, *, theta=10000.0, layout=KT_ROPE_HALF, scaling=KT_ROPE_
     return r
 
 
+_DTYPES = {}
+
+
 def _dtype(t, call):
-    import torch
-    d = {torch.float16: KT_F16, torch.bfloat16: KT_BF16, torch.float32: KT_F32}.get(t.dtype)
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.float16: KT_F16, torch.bfloat16: KT_BF16, torch.float32: KT_F32})
+    d = _DTYPES.get(t.dtype)
     if d is None:
         raise KtError(KT_ERR_UNSUPPORTED, call)
     return d
@@ -439,11 +459,11 @@ def _dtype(t, call):
 def rows(t) -> Rows:
     """kt_rows of a tensor [tokens][heads][128] (it may be a part of a packed projection); the
     last two dimensions are contiguous."""
-    if isinstance(t, Rows):
+    if type(t) is Rows:
         return t
     tokens, heads, d = t.shape
     s0, s1, s2 = t.stride()
-    if d != 128 or s2 != 1 or (heads > 1 and s1 != 128):
+    if d != 128 or s2 != 1 or (s1 != 128 and heads > 1):
         raise KtError(KT_ERR_INVALID_ARG, "rows")
     return Rows(t.data_ptr(), s0 if tokens > 1 else heads * 128, heads, _dtype(t, "rows"))
 
@@ -453,7 +473,7 @@ def _rows(t):
 
 
 def _check_out(out, shape, call):
-    if out is not None and (tuple(out.shape) != tuple(shape) or not out.is_contiguous()):
+    if out is not None and (out.shape != shape or not out.is_contiguous()):
         raise KtError(KT_ERR_INVALID_ARG, call)
 
 

@@ -28,7 +28,10 @@ constexpr int WARPS = THREADS / 32;
 constexpr int ROWS_PER = BS / (THREADS / ROPE_UNITS);  // row steps of a lane: 4
 constexpr int RED_BYTES = 2 * WARPS * D * 2;           // representatives: partials per warp
 constexpr int TILE_BYTES = BS * D;
-constexpr int APPEND_HEADS = 2;                        // heads of an append CTA at most
+// K heads of an append CTA at most: a 16K-token chunk of 32 + 8 heads takes 77.3 us
+// with one (the angles are computed for each head), 71.4 with two, 68.6 with four,
+// 72.5 with eight (130 CTAs of K are fewer than the SMs)
+constexpr int APPEND_HEADS = 4;
 
 struct Params {
   kt_rope rope;  // rotary_dim 0: no rotation
@@ -49,7 +52,7 @@ struct Params {
   int* status;
   int* ticket;
   int B, H_kv, H_q, max_blocks, P, tokens, rep, R, fix_stride;
-  int heads_per, groups, cache_ctas, q_ctas, q_heads, cs_rows;
+  int heads_per, groups, k_ctas, cache_ctas, q_ctas, q_heads, cs_rows;
   int late_wait;  // the launch before is this call's rotation of q: wait for it at the end
 };
 
@@ -113,6 +116,11 @@ __device__ __forceinline__ uint32_t recode4(uint32_t c, float ratio) {
   return h4_to_f8(h[0], h[1]);
 }
 
+// A tile of codes in shared memory: word w (four channels) of row r.  Odd rows
+// have their 64-byte halves exchanged, so that the 8-byte stores of a warp (four
+// rows, half a row each) meet every bank twice and not four times.
+__device__ __forceinline__ int tile_word(int r, int w) { return r * 32 + (w ^ ((r & 1) << 4)); }
+
 // Representatives of a full tile of codes in shared memory, written at rep row
 // `row0` of the pool.  red: RED_BYTES of shared memory.  Every thread calls it.
 __device__ void tile_reps(const uint8_t* tile, float s, int rep, int R, int fix_stride, void* reps,
@@ -123,7 +131,7 @@ __device__ void tile_reps(const uint8_t* tile, float s, int rep, int R, int fix_
   if (rep == KT_REP_FIX) {
     uint2* out = reinterpret_cast<uint2*>(static_cast<__half*>(reps) + row0 * D);
     for (int i = tid; i < R * 32; i += THREADS) {
-      const uint32_t c = words[(i >> 5) * fix_stride * 32 + (i & 31)];
+      const uint32_t c = words[tile_word((i >> 5) * fix_stride, i & 31)];
       out[i] = make_uint2(as_u32(__hmul2(as_h2(f8x2_lo(c)), s2)),
                           as_u32(__hmul2(as_h2(f8x2_hi(c)), s2)));
     }
@@ -131,20 +139,23 @@ __device__ void tile_reps(const uint8_t* tile, float s, int rep, int R, int fix_
   }
   const int r0 = warp * (BS / WARPS);
   if (rep == KT_REP_MEAN) {
-    // a code is a whole number of 2^-9, at most 448 * 2^9: 128 of them are below 2^25
-    int acc[4] = {0, 0, 0, 0};
+    // a code is a whole number of 2^-9, at most 448 * 2^9: the sums of a warp's 16
+    // rows stay below 2^22 of them (exact in binary32), all 128 below 2^25
+    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 4
     for (int r = r0; r < r0 + BS / WARPS; ++r) {
-      const uint32_t c = words[r * 32 + lane];
+      const uint32_t c = words[tile_word(r, lane)];
       const float2 a = __half22float2(as_h2(f8x2_lo(c)));
       const float2 b = __half22float2(as_h2(f8x2_hi(c)));
-      acc[0] += __float2int_rn(a.x * 512.0f);
-      acc[1] += __float2int_rn(a.y * 512.0f);
-      acc[2] += __float2int_rn(b.x * 512.0f);
-      acc[3] += __float2int_rn(b.y * 512.0f);
+      acc[0] += a.x;
+      acc[1] += a.y;
+      acc[2] += b.x;
+      acc[3] += b.y;
     }
     int4* part = reinterpret_cast<int4*>(red);
-    part[warp * 32 + lane] = make_int4(acc[0], acc[1], acc[2], acc[3]);
+    part[warp * 32 + lane] = make_int4(
+        __float2int_rn(acc[0] * 512.0f), __float2int_rn(acc[1] * 512.0f),
+        __float2int_rn(acc[2] * 512.0f), __float2int_rn(acc[3] * 512.0f));
     __syncthreads();
     if (tid < D) {
       int sum = 0;
@@ -160,7 +171,7 @@ __device__ void tile_reps(const uint8_t* tile, float s, int rep, int R, int fix_
   mn[0] = mn[1] = __float2half2_rn(INFINITY);
 #pragma unroll 4
   for (int r = r0; r < r0 + BS / WARPS; ++r) {
-    const uint32_t c = words[r * 32 + lane];
+    const uint32_t c = words[tile_word(r, lane)];
     const __half2 a = as_h2(f8x2_lo(c)), b = as_h2(f8x2_hi(c));
     mx[0] = __hmax2(mx[0], a);
     mx[1] = __hmax2(mx[1], b);
@@ -300,16 +311,18 @@ __device__ __forceinline__ void load_tile(TileRaw<T>& x, const T* src, long long
 }
 
 template <class T, int M>
-__device__ void append_tile(const Params& p, int cta, uint8_t* smem, int* sh, int tid) {
+__device__ void append_tile(const Params& p, int cta, const unsigned long long* ph, uint8_t* smem,
+                            int* sh, int tid) {
   // 16-bit rows of the next head are loaded while a head is coded; the registers
   // do not hold two of binary32
   constexpr bool AHEAD = M != ROPE_M_NONE && sizeof(T) == 2;
   const int warp = tid >> 5, lane = tid & 31;
-  const int per_tile = 2 * p.groups;
-  const int tile = cta / per_tile, rest = cta - tile * per_tile;
-  const bool is_v = rest >= p.groups;
-  const int h0 = (is_v ? rest - p.groups : rest) * p.heads_per;
-  const int h1 = min(h0 + p.heads_per, p.H_kv);
+  // the tiles of K (heads_per heads a CTA) come first, those of V (a head a CTA)
+  // fill the SMs up behind them
+  const bool is_v = cta >= p.k_ctas;
+  const int groups = is_v ? p.H_kv : p.groups, per = is_v ? 1 : p.heads_per;
+  const int unit = is_v ? cta - p.k_ctas : cta, tile = unit / groups;
+  const int h0 = (unit - tile * groups) * per, h1 = min(h0 + per, p.H_kv);
   int b, j;
   Span a;
   if (!find_tile(p, tile, sh, tid, &b, &j, &a)) return;
@@ -331,10 +344,10 @@ __device__ void append_tile(const Params& p, int cta, uint8_t* smem, int* sh, in
   uint8_t* red = codes + TILE_BYTES;
   const bool turn = M != ROPE_M_NONE && !is_v;
   if (turn) {
-    const int half = p.rope.rotary_dim >> 1;
-    for (int i = tid; i < (r1 - r0) * 64; i += THREADS)
-      if ((i & 63) < half)
-        cs[(i & ~63) + cs_at(i & 63)] = rope_cos_sin(p.rope, i & 63, j * BS + r0 + (i >> 6));
+    const int i = tid & 63;
+    if (i < p.rope.rotary_dim >> 1)
+      for (int r = tid >> 6; r < r1 - r0; r += THREADS / 64)
+        cs[r * 64 + cs_at(i)] = rope_cos_sin(ph[i], p.rope.amplitude, j * BS + r0 + r);
     __syncthreads();
   }
   const bool complete = !is_v && p.reps && r1 == BS;
@@ -352,17 +365,20 @@ __device__ void append_tile(const Params& p, int cta, uint8_t* smem, int* sh, in
     for (int i = 0; i < ROWS_PER; ++i) {
       const int r = (tid >> 3) + i * (THREADS / ROPE_UNITS);
       if (r >= r0 && r < r1) {
-        float x[8], y[8];
-        unpack8(raw.a[i], x);
-        unpack8(raw.b[i], y);
         if (turn) {
+          float x[8], y[8];
+          unpack8(raw.a[i], x);
+          unpack8(raw.b[i], y);
           float2 w[8];
           const float2* row_cs = cs + (r - r0) * 64;
           rope_weights<M>(row_cs, va, vb, w);
           rope_rotate<M>(p.rope, w, row_cs, src + (r - r0) * stride + h * D, va, vb, x, y);
+          pack8(x, xa[i]);
+          pack8(y, xb[i]);
+        } else {
+          halves8(raw.a[i], xa[i]);
+          halves8(raw.b[i], xb[i]);
         }
-        pack8(x, xa[i]);
-        pack8(y, xb[i]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           mx = __hmax2(mx, __habs2(as_h2(xa[i][e])));
@@ -399,8 +415,8 @@ __device__ void append_tile(const Params& p, int cta, uint8_t* smem, int* sh, in
         *reinterpret_cast<uint2*>(dst + r * D + 8 * va) = ca;
         *reinterpret_cast<uint2*>(dst + r * D + 8 * vb) = cb;
         if (complete) {
-          *reinterpret_cast<uint2*>(codes + r * D + 8 * va) = ca;
-          *reinterpret_cast<uint2*>(codes + r * D + 8 * vb) = cb;
+          *reinterpret_cast<uint2*>(codes + 4 * tile_word(r, 2 * va)) = ca;
+          *reinterpret_cast<uint2*>(codes + 4 * tile_word(r, 2 * vb)) = cb;
         }
       }
     }
@@ -414,7 +430,8 @@ __device__ void append_tile(const Params& p, int cta, uint8_t* smem, int* sh, in
                          recode4(c.w, ratio));
           reinterpret_cast<uint4*>(dst)[i] = c;
         }
-        if (complete) reinterpret_cast<uint4*>(codes)[i] = c;
+        if (complete)
+          *reinterpret_cast<uint4*>(codes + 4 * tile_word(i >> 3, 4 * (i & 7))) = c;
       }
     }
     // every thread has read the old scale before the barriers above
@@ -428,7 +445,8 @@ __device__ void append_tile(const Params& p, int cta, uint8_t* smem, int* sh, in
 
 // One warp a token (or a slice of its heads).
 template <class T, int M>
-__device__ void append_q(const Params& p, int unit, uint8_t* smem, int tid) {
+__device__ void append_q(const Params& p, int unit, const unsigned long long* ph, uint8_t* smem,
+                         int tid) {
   const int warp = tid >> 5, lane = tid & 31;
   unit = unit * WARPS + warp;
   const int slices = (p.H_q + p.q_heads - 1) / p.q_heads;
@@ -439,7 +457,7 @@ __device__ void append_q(const Params& p, int unit, uint8_t* smem, int tid) {
     const int s = p.cu ? row_sequence(p.cu, p.B, t, lane) : t;
     pos = p.seq_lens[s] + (t - (p.cu ? p.cu[s] : t));
   }
-  rope_token<M, 1>(p.rope, reinterpret_cast<float2*>(smem) + warp * 64, pos, t, h0,
+  rope_token<M, 1>(p.rope, ph, reinterpret_cast<float2*>(smem) + warp * 64, pos, t, h0,
                 min(h0 + p.q_heads, p.H_q), static_cast<const T*>(p.q), p.qs, p.H_q, p.q_out,
                 static_cast<const T*>(nullptr), 0, 0, static_cast<__half*>(nullptr), lane);
 }
@@ -449,13 +467,18 @@ __global__ void __launch_bounds__(THREADS, M == ROPE_M_NONE && sizeof(T) == 2 ? 
     append_f8_kernel(const __grid_constant__ Params p) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ int sh[WARPS + 8];
+  __shared__ unsigned long long ph[64];
+  const int tid = threadIdx.x, cta = blockIdx.x;
+  if (M != ROPE_M_NONE) {
+    rope_phases(p.rope, ph, tid);
+    __syncthreads();
+  }
   if (!p.late_wait) griddep_wait();
   griddep_launch_dependents();
-  const int tid = threadIdx.x, cta = blockIdx.x;
   if (cta < p.cache_ctas)
-    append_tile<T, M>(p, cta, smem, sh, tid);
+    append_tile<T, M>(p, cta, ph, smem, sh, tid);
   else if (cta < p.cache_ctas + p.q_ctas)
-    append_q<T, M>(p, cta - p.cache_ctas, smem, tid);
+    append_q<T, M>(p, cta - p.cache_ctas, ph, smem, tid);
   else if (p.new_lens)
     write_lengths(p, tid);
   // behind the rotation of q (which waited for everything before it), this launch
@@ -496,8 +519,8 @@ __global__ void __launch_bounds__(THREADS) reps_f8_kernel(const __grid_constant_
   const size_t slab = (size_t)page * p.H_kv + h;
   const uint4* src = reinterpret_cast<const uint4*>(p.k_code + slab * TILE_BYTES);
 #pragma unroll
-  for (int i = 0; i < TILE_BYTES / 16 / THREADS; ++i)
-    reinterpret_cast<uint4*>(tile)[tid + i * THREADS] = __ldg(src + tid + i * THREADS);
+  for (int i = tid; i < TILE_BYTES / 16; i += THREADS)
+    *reinterpret_cast<uint4*>(tile + 4 * tile_word(i >> 3, 4 * (i & 7))) = __ldg(src + i);
   __syncthreads();
   tile_reps(tile, p.k_scale[slab], p.rep, p.R, p.fix_stride, p.reps, slab * p.R, red, tid);
 }
@@ -690,13 +713,13 @@ cudaError_t launch_append_f8(const AppendF8Launch& a, cudaStream_t stream) {
   const long long seqs = a.B < a.tokens ? a.B : a.tokens;
   long long tiles = a.tokens / BS + 2 * seqs;
   if (tiles > a.tokens) tiles = a.tokens;
-  // a head a CTA; with a rotation two where that leaves four CTAs an SM, so that
-  // fewer angles are computed twice and the next head's rows are on their way
-  long long per = a.rope ? tiles * a.H_kv / (2ll * a.num_sms) : 1;
+  // with a rotation up to APPEND_HEADS heads of K a CTA where that leaves every
+  // SM one, so that few angles are computed twice
+  long long per = a.rope ? tiles * a.H_kv / a.num_sms : 1;
   per = per < 1 ? 1 : per > APPEND_HEADS ? APPEND_HEADS : per;
   p.groups = (int)((a.H_kv + per - 1) / per);
   p.heads_per = (a.H_kv + p.groups - 1) / p.groups;
-  const long long cache = tiles * 2 * p.groups;
+  const long long cache = tiles * (p.groups + a.H_kv);
   // many q rows go ahead in a launch of their own, which has the shared memory
   // for more warps an SM than the tiles leave; few ride along
   if (a.q && a.cu && a.tokens >= 16 * a.num_sms) {
@@ -725,6 +748,7 @@ cudaError_t launch_append_f8(const AppendF8Launch& a, cudaStream_t stream) {
   const long long qn =
       p.q ? ((long long)a.tokens * ((a.H_q + p.q_heads - 1) / p.q_heads) + WARPS - 1) / WARPS : 0;
   if (cache + qn + 1 > 0x7FFFFFFFll) return cudaErrorInvalidValue;
+  p.k_ctas = (int)(tiles * p.groups);
   p.cache_ctas = (int)cache;
   p.q_ctas = (int)qn;
   // angles: of a tile's rows, or of a decoded token and the q rows (one a warp)

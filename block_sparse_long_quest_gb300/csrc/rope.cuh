@@ -3,8 +3,8 @@
 //
 // Angles: kt_rope.phase holds f_i / (2 pi) as a 64-bit fraction of a turn, so
 // phase * position in wrapping 64-bit integers is the angle modulo one turn with
-// an error below position * 2^-53 turns (the host's binary64 frequency); its top
-// 32 bits go to sincospif.  No binary64 arithmetic and no range reduction.
+// an error below position * 2^-53 turns (the host's binary64 frequency).  No
+// binary64 arithmetic, and the reduction to a quadrant is two bits of it.
 //
 // A head row is 16 vectors of 8 channels and is handled by the 8 lanes of a
 // lane group, two vectors a lane (row_vectors).  HALF with rotary_dim a
@@ -71,19 +71,57 @@ __device__ __forceinline__ void unpack8(const Raw8<float>& r, float (&x)[8]) {
     x[4 * i + 3] = __uint_as_float(r.v[i].w);
   }
 }
+// Eight values as binary16 (rounded once).
+__device__ __forceinline__ void halves8(const Raw8<__half>& r, uint32_t (&h)[4]) {
+  h[0] = r.v[0].x, h[1] = r.v[0].y, h[2] = r.v[0].z, h[3] = r.v[0].w;
+}
+template <class T>
+__device__ __forceinline__ void halves8(const Raw8<T>& r, uint32_t (&h)[4]) {
+  float x[8];
+  unpack8(r, x);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 v = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+    h[i] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+}
+
 __device__ __forceinline__ float load1(const __half* p) { return __half2float(*p); }
 __device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 __device__ __forceinline__ float load1(const float* p) { return *p; }
 
-// amplitude * (cos, sin) of pair i at position pos.
-__device__ __forceinline__ float2 rope_cos_sin(const kt_rope& r, int i, int pos) {
+// The phases in shared memory, by the first 64 threads of a CTA: lanes that index
+// the parameters' constant bank apart are served one by one.
+__device__ __forceinline__ void rope_phases(const kt_rope& r, unsigned long long* ph, int tid) {
+  if (tid < 64) ph[tid] = r.phase[tid];
+}
+
+// amplitude * (cos, sin) of a pair at position pos: the top 32 bits of the turn
+// are a quadrant and a signed rest of at most an eighth of a turn, whose sine and
+// cosine are their Taylor polynomials (|x| <= pi/4: the first terms left out are
+// x^11/11! < 1.8e-9 and x^10/10! < 2.5e-8, below half an ulp of either).
+__device__ __forceinline__ float2 rope_cos_sin(unsigned long long phase, float amplitude,
+                                               int pos) {
   const unsigned long long turns =
-      r.phase[i] * static_cast<unsigned long long>(static_cast<long long>(pos));
-  // signed 32-bit fraction of a turn, in half turns [-1, 1) for sincospif
-  const int frac = static_cast<int>((turns + 0x80000000ull) >> 32);
-  float s, c;
-  sincospif(static_cast<float>(frac) * 0x1.0p-31f, &s, &c);
-  return make_float2(c * r.amplitude, s * r.amplitude);
+      phase * static_cast<unsigned long long>(static_cast<long long>(pos));
+  const uint32_t frac = static_cast<uint32_t>((turns + 0x80000000ull) >> 32);
+  const uint32_t quad = (frac + 0x20000000u) >> 30;
+  const float x = static_cast<float>(static_cast<int>(frac - (quad << 30))) *
+                  1.4629180792671596e-9f;  // 2 pi / 2^32
+  const float z = x * x;
+  float s = fmaf(z, 1.0f / 362880.0f, -1.0f / 5040.0f);
+  s = fmaf(z, s, 1.0f / 120.0f);
+  s = fmaf(z, s, -1.0f / 6.0f);
+  s = fmaf(x * z, s, x);
+  float c = fmaf(z, 1.0f / 40320.0f, -1.0f / 720.0f);
+  c = fmaf(z, c, 1.0f / 24.0f);
+  c = fmaf(z, c, -0.5f);
+  c = fmaf(z, c, 1.0f);
+  // a quarter turn takes (cos, sin) to (-sin, cos)
+  float re = (quad & 1u) ? s : c, im = (quad & 1u) ? c : s;
+  re = __uint_as_float(__float_as_uint(re) ^ (((quad + 1u) & 2u) << 30));
+  im = __uint_as_float(__float_as_uint(im) ^ ((quad & 2u) << 30));
+  return make_float2(re * amplitude, im * amplitude);
 }
 
 // The two vectors (8 channels each) of lane j of a head row.
@@ -191,11 +229,12 @@ __device__ __forceinline__ void pack8(const float (&x)[8], uint32_t (&h)[4]) {
 }
 
 // Rotates heads h0 .. h1 - 1 (q's, then k's) of one token by one warp: four head
-// rows at a time, NB times four loaded before the first is stored; cs: 64 (cos,
+// rows at a time, NB times four loaded before the first is stored; ph: rope_phases; cs: 64 (cos,
 // sin) of shared memory of the warp's own, written behind the first loads and held
 // in registers over the heads.
 template <int M, int NB, class T>
-__device__ __forceinline__ void rope_token(const kt_rope& r, float2* cs, int pos, long long t,
+__device__ __forceinline__ void rope_token(const kt_rope& r, const unsigned long long* ph,
+                                           float2* cs, int pos, long long t,
                                            int h0, int h1, const T* q, long long qs, int hq,
                                            __half* q_out, const T* k, long long ks, int hk,
                                            __half* k_out, int lane) {
@@ -222,7 +261,7 @@ __device__ __forceinline__ void rope_token(const kt_rope& r, float2* cs, int pos
     if (M != ROPE_M_NONE && first) {
 #pragma unroll
       for (int i = lane; i < 64; i += 32)
-        if (i < half) cs[cs_at(i)] = rope_cos_sin(r, i, pos);
+        if (i < half) cs[cs_at(i)] = rope_cos_sin(ph[i], r.amplitude, pos);
       __syncwarp();
       rope_weights<M>(cs, va, vb, w);
     }
@@ -232,12 +271,17 @@ __device__ __forceinline__ void rope_token(const kt_rope& r, float2* cs, int pos
     for (int i = 0; i < NB; ++i) {
       const int hh = h + 4 * i + hl;
       if (hh < h1) {
-        float a[8], b[8];
-        unpack8(ra[i], a);
-        unpack8(rb[i], b);
-        rope_rotate<M>(r, w, cs, (hh < hq ? qr : kr) + hh * D, va, vb, a, b);
-        pack8(a, ha[i]);
-        pack8(b, hb[i]);
+        if constexpr (M == ROPE_M_NONE) {
+          halves8(ra[i], ha[i]);
+          halves8(rb[i], hb[i]);
+        } else {
+          float a[8], b[8];
+          unpack8(ra[i], a);
+          unpack8(rb[i], b);
+          rope_rotate<M>(r, w, cs, (hh < hq ? qr : kr) + hh * D, va, vb, a, b);
+          pack8(a, ha[i]);
+          pack8(b, hb[i]);
+        }
       }
     }
     __syncwarp();  // in place: a row's lanes have all read it
