@@ -68,6 +68,7 @@ constexpr int Q_BYTES = MAX_G * D * 2;
 constexpr int HALF_WARPS = CONSUMERS / 2;
 constexpr int SCRATCH_FLOATS = HALF_WARPS * MAX_G * (D + 2);
 static_assert(SCRATCH_FLOATS * 4 == ATTN_SCRATCH_BYTES, "scratch size shared with the host");
+static_assert(NCT * 2 == 4 * D, "a thread combines two channels of four heads");
 static_assert(NCT == ATTN_CONSUMER_THREADS, "consumer threads shared with the host");
 static_assert(STAGES * KV_STAGE_BYTES == ATTN_RING_BYTES, "ring size shared with the host");
 
@@ -199,9 +200,13 @@ __device__ void warp_prefix(int* pref, int S, F count, int lane) {
   const int per = (S + 31) / 32;
   const int lo = min(S, lane * per), hi = min(S, lo + per);
   int sum = 0;
-  for (int s = lo; s < hi; ++s) {
-    sum += count(s);
-    pref[s + 1] = sum;
+  for (int i = 0; i < per; ++i) {  // the whole warp calls count
+    const int s = lo + i;
+    const int n = count(min(s, S - 1), s < hi);
+    if (s < hi) {
+      sum += n;
+      pref[s + 1] = sum;
+    }
   }
   int incl = sum;
   for (int o = 1; o < 32; o <<= 1) {
@@ -749,27 +754,178 @@ __device__ __forceinline__ uint32_t f8_permute(int tok, int ntok) {
   return (tok < ntok ? 0x0100u : 0x0404u) | (tok + 1 < ntok ? 0x3020u : 0x4040u);
 }
 
-// The attention of this warp's share of the CTA's blocks; whether q was loaded.
-__device__ __forceinline__ bool consume_f8(const Params& p, F8State& z, const uint8_t* smem,
-                                           const StageInfo* info, uint32_t kv_base,
-                                           uint32_t bar_full, uint32_t bar_empty, uint32_t bar_q,
-                                           int warp, int lane) {
-  constexpr uint32_t NST = F8_STAGES;
-  const int g = lane >> 2, t = lane & 3, mi = lane >> 3, r = lane & 7;
-  const int w0 = (warp % F8_GROUP) * 32;  // first of the warp's tokens in a block
-  const bool dup = p.G <= 4;
-  const bool low = dup && t >= 2;  // this lane's columns carry P_lo
+// What a lane of an e4m3 consumer warp keeps through the kernel.
+struct F8Lane {
+  int w0;               // first of the warp's 32 tokens in a block
+  int g, t;             // lane / 4, lane % 4
+  bool dup, low;        // G <= 4; this lane's columns carry P_lo
+  int lrow;             // ldmatrix row of this lane (token of a 16-token half),
+  uint32_t lswz, lhi;   // its swizzle, and which of two 16-channel pieces
+};
+__device__ __forceinline__ F8Lane f8_lane(int G, int warp, int lane) {
+  F8Lane c;
+  const int mi = lane >> 3, r = lane & 7;
+  c.w0 = (warp % F8_GROUP) * 32;
+  c.g = lane >> 2;
+  c.t = lane & 3;
+  c.dup = G <= 4;
+  c.low = c.dup && c.t >= 2;
+  // matrices 0, 1 are tokens 0-7 and 8-15 of a half, 2, 3 their next 16 channels
+  c.lrow = c.w0 + (mi & 1) * 8 + r;
+  c.lswz = (uint32_t)(c.lrow & 7);
+  c.lhi = (uint32_t)(mi >> 1);
+  return c;
+}
+__device__ __forceinline__ void f8_reset(F8State& z) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) z.acc[i][0] = z.acc[i][1] = z.acc[i][2] = z.acc[i][3] = 0.0f;
   z.m[0] = z.m[1] = -INFINITY;
   z.l[0] = z.l[1] = 0.0f;
   z.vs = 1.0f;
+}
+// The heads' q rows (at q, in shared or global memory) as B fragments.
+__device__ __forceinline__ void f8_load_q(const F8Lane& c, const __half* q, int G,
+                                          uint32_t (&qb)[8][2]) {
+  const int hd = c.dup ? c.g & 3 : c.g;
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk) {
+    uint2 v = make_uint2(0u, 0u);
+    if (hd < G) v = *reinterpret_cast<const uint2*>(q + hd * D + kk * 16 + 4 * c.t);
+    qb[kk][0] = v.x;
+    qb[kk][1] = v.y;
+  }
+}
+__device__ __forceinline__ bool f8_scales_ok(const StageInfo& in) {
+  return in.ks >= F8_SCALE_MIN && in.ks <= F8_SCALE_MAX && in.vs >= F8_SCALE_MIN &&
+         in.vs <= F8_SCALE_MAX;
+}
+
+// One block (codes at `stage`) into this warp's state.
+__device__ __forceinline__ void f8_block(const F8Lane& cx, F8State& z, const uint32_t (&qb)[8][2],
+                                         const StageInfo& in, uint32_t stage, float q_scale_log2) {
+  const uint32_t kb = stage + (uint32_t)cx.lrow * 128;
+  const uint32_t vb = kb + UNIT * D;
+  // ---- S = K q^T: two 16-token halves, two accumulation chains each
+  float s[2][2][4];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) s[h][c][0] = s[h][c][1] = s[h][c][2] = s[h][c][3] = 0.0f;
+#pragma unroll
+  for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t c0, c1, c2, c3;
+      ldsm_x4(c0, c1, c2, c3, kb + h * 2048 + (((kk * 2 + cx.lhi) ^ cx.lswz) << 4));
+      mma_16816_sched(s[h][0], f8x2_lo(c0), f8x2_lo(c1), f8x2_hi(c0), f8x2_hi(c1), qb[2 * kk][0],
+                qb[2 * kk][1]);
+      mma_16816_sched(s[h][1], f8x2_lo(c2), f8x2_lo(c3), f8x2_hi(c2), f8x2_hi(c3),
+                qb[2 * kk + 1][0], qb[2 * kk + 1][1]);
+    }
+  // ---- online softmax (base 2) of heads 2t, 2t + 1 over the warp's tokens
+  float x[2][4];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[h][i] = s[h][0][i] + s[h][1][i];
+  uint32_t perm[2][2] = {{0x3120u, 0x3120u}, {0x3120u, 0x3120u}};
+  if (in.ntok < cx.w0 + 32) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (cx.w0 + h * 16 + i * 8 + cx.g >= in.ntok) x[h][2 * i] = x[h][2 * i + 1] = -INFINITY;
+        perm[h][i] = f8_permute(cx.w0 + h * 16 + i * 8 + 2 * cx.t, in.ntok);
+      }
+  }
+  const float sc = q_scale_log2 * in.ks;
+  float mu[2];
+  bool moved = false;
+  float m_new[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float mx = fmaxf(fmaxf(x[0][i], x[0][2 + i]), fmaxf(x[1][i], x[1][2 + i]));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+    m_new[i] = fmaxf(z.m[i], mx * sc);
+    mu[i] = m_new[i] == -INFINITY ? 0.0f : m_new[i];
+    moved = moved || m_new[i] != z.m[i];
+  }
+  float pr[2][4];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      pr[h][i] = ex2(fmaf(x[h][i], sc, F8_P_SHIFT - mu[i & 1]));
+  if (__any_sync(0xffffffffu, moved) || in.vs != z.vs) {
+    // acc goes over to this block's V scale as well
+    const float a0 = ex2(z.m[0] - mu[0]), a1 = ex2(z.m[1] - mu[1]);
+    const float rv = z.vs / in.vs;
+    z.l[0] *= a0;
+    z.l[1] *= a1;
+    const float b0 = a0 * rv, b1 = a1 * rv;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      z.acc[i][0] *= b0;
+      z.acc[i][1] *= b1;
+      z.acc[i][2] *= b0;
+      z.acc[i][3] *= b1;
+    }
+    z.vs = in.vs;
+    z.m[0] = m_new[0];
+    z.m[1] = m_new[1];
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    z.l[i] += (pr[0][i] + pr[0][2 + i]) + (pr[1][i] + pr[1][2 + i]);
+  // ---- O^T += V^T P^T, a 16-token half at a time
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t hi[2], lo[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const __half2 a = __floats2half2_rn(pr[h][2 * i], pr[h][2 * i + 1]);
+      const float2 f = __half22float2(a);
+      const __half2 b = __floats2half2_rn(pr[h][2 * i] - f.x, pr[h][2 * i + 1] - f.y);
+      hi[i] = *reinterpret_cast<const uint32_t*>(&a);
+      lo[i] = *reinterpret_cast<const uint32_t*>(&b);
+      hi[i] = transpose8x8(cx.low ? lo[i] : hi[i]);
+    }
+    if (!cx.dup) {
+      lo[0] = transpose8x8(lo[0]);
+      lo[1] = transpose8x8(lo[1]);
+    }
+#pragma unroll
+    for (int cp = 0; cp < 4; ++cp) {
+      uint32_t c0, c1, c2, c3;
+      ldsm_x4_t(c0, c1, c2, c3, vb + h * 2048 + (((cp * 2 + cx.lhi) ^ cx.lswz) << 4));
+      c0 = __byte_perm(c0, 0u, perm[h][0]);
+      c1 = __byte_perm(c1, 0u, perm[h][1]);
+      c2 = __byte_perm(c2, 0u, perm[h][0]);
+      c3 = __byte_perm(c3, 0u, perm[h][1]);
+      const uint32_t e0 = f8x2_lo(c0), e1 = f8x2_hi(c0), e2 = f8x2_lo(c1), e3 = f8x2_hi(c1);
+      const uint32_t o0 = f8x2_lo(c2), o1 = f8x2_hi(c2), o2 = f8x2_lo(c3), o3 = f8x2_hi(c3);
+      mma_16816_sched(z.acc[2 * cp], e0, e1, e2, e3, hi[0], hi[1]);
+      mma_16816_sched(z.acc[2 * cp + 1], o0, o1, o2, o3, hi[0], hi[1]);
+      if (!cx.dup) {
+        mma_16816_sched(z.acc[2 * cp], e0, e1, e2, e3, lo[0], lo[1]);
+        mma_16816_sched(z.acc[2 * cp + 1], o0, o1, o2, o3, lo[0], lo[1]);
+      }
+    }
+  }
+}
+
+// The one-launch step: this warp's share of the CTA's blocks; whether q was loaded.
+__device__ __forceinline__ bool consume_f8(const Params& p, F8State& z, const uint8_t* smem,
+                                           const StageInfo* info, uint32_t kv_base,
+                                           uint32_t bar_full, uint32_t bar_empty, uint32_t bar_q,
+                                           int warp, int lane) {
+  constexpr uint32_t NST = F8_STAGES;
+  const F8Lane cx = f8_lane(p.G, warp, lane);
+  f8_reset(z);
   uint32_t qb[8][2];
   bool q_loaded = false;
-  // ldmatrix rows of this lane: matrices 0, 1 are tokens 0-7 and 8-15 of a 16-token
-  // half, matrices 2, 3 the same tokens' next 16 channels
-  const int lrow = w0 + (mi & 1) * 8 + r;
-  const uint32_t lswz = (uint32_t)(lrow & 7), lhi = (uint32_t)(mi >> 1);
 #pragma unroll 1
   for (uint32_t it = warp / F8_GROUP;; it += F8_GROUPS) {
     const uint32_t st = it % NST;
@@ -778,135 +934,14 @@ __device__ __forceinline__ bool consume_f8(const Params& p, F8State& z, const ui
     if (in.end) break;
     if (in.ntok > 0 && !q_loaded) {
       if (!mbar_wait(bar_q, 0, p.status)) break;
-      const __half* qs = reinterpret_cast<const __half*>(smem + SmemLayout::q);
-      const int hd = dup ? g & 3 : g;
-#pragma unroll
-      for (int kk = 0; kk < 8; ++kk) {
-        uint2 v = make_uint2(0u, 0u);
-        if (hd < p.G) v = *reinterpret_cast<const uint2*>(qs + hd * D + kk * 16 + 4 * t);
-        qb[kk][0] = v.x;
-        qb[kk][1] = v.y;
-      }
+      f8_load_q(cx, reinterpret_cast<const __half*>(smem + SmemLayout::q), p.G, qb);
       q_loaded = true;
     }
-    const bool scales_ok = in.ks >= F8_SCALE_MIN && in.ks <= F8_SCALE_MAX &&
-                           in.vs >= F8_SCALE_MIN && in.vs <= F8_SCALE_MAX;
-    if (in.ntok > w0) {
-      if (scales_ok) {
-        const uint32_t kb = kv_base + st * F8_STAGE_BYTES + (uint32_t)lrow * 128;
-        const uint32_t vb = kb + UNIT * D;
-        // ---- S = K q^T: two 16-token halves, two accumulation chains each
-        float s[2][2][4];
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) s[h][c][0] = s[h][c][1] = s[h][c][2] = s[h][c][3] = 0.0f;
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t c0, c1, c2, c3;
-            ldsm_x4(c0, c1, c2, c3, kb + h * 2048 + (((kk * 2 + lhi) ^ lswz) << 4));
-            mma_16816_sched(s[h][0], f8x2_lo(c0), f8x2_lo(c1), f8x2_hi(c0), f8x2_hi(c1), qb[2 * kk][0],
-                      qb[2 * kk][1]);
-            mma_16816_sched(s[h][1], f8x2_lo(c2), f8x2_lo(c3), f8x2_hi(c2), f8x2_hi(c3),
-                      qb[2 * kk + 1][0], qb[2 * kk + 1][1]);
-          }
-        // ---- online softmax (base 2) of heads 2t, 2t + 1 over the warp's tokens
-        float x[2][4];
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) x[h][i] = s[h][0][i] + s[h][1][i];
-        uint32_t perm[2][2] = {{0x3120u, 0x3120u}, {0x3120u, 0x3120u}};
-        if (in.ntok < w0 + 32) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              if (w0 + h * 16 + i * 8 + g >= in.ntok) x[h][2 * i] = x[h][2 * i + 1] = -INFINITY;
-              perm[h][i] = f8_permute(w0 + h * 16 + i * 8 + 2 * t, in.ntok);
-            }
-        }
-        const float sc = p.scale_log2 * in.ks;
-        float mu[2];
-        bool moved = false;
-        float m_new[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float mx = fmaxf(fmaxf(x[0][i], x[0][2 + i]), fmaxf(x[1][i], x[1][2 + i]));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          m_new[i] = fmaxf(z.m[i], mx * sc);
-          mu[i] = m_new[i] == -INFINITY ? 0.0f : m_new[i];
-          moved = moved || m_new[i] != z.m[i];
-        }
-        float pr[2][4];
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            pr[h][i] = ex2(fmaf(x[h][i], sc, F8_P_SHIFT - mu[i & 1]));
-        if (__any_sync(0xffffffffu, moved) || in.vs != z.vs) {
-          // acc goes over to this block's V scale as well
-          const float a0 = ex2(z.m[0] - mu[0]), a1 = ex2(z.m[1] - mu[1]);
-          const float rv = z.vs / in.vs;
-          z.l[0] *= a0;
-          z.l[1] *= a1;
-          const float b0 = a0 * rv, b1 = a1 * rv;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            z.acc[i][0] *= b0;
-            z.acc[i][1] *= b1;
-            z.acc[i][2] *= b0;
-            z.acc[i][3] *= b1;
-          }
-          z.vs = in.vs;
-          z.m[0] = m_new[0];
-          z.m[1] = m_new[1];
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          z.l[i] += (pr[0][i] + pr[0][2 + i]) + (pr[1][i] + pr[1][2 + i]);
-        // ---- O^T += V^T P^T, a 16-token half at a time
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t hi[2], lo[2];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const __half2 a = __floats2half2_rn(pr[h][2 * i], pr[h][2 * i + 1]);
-            const float2 f = __half22float2(a);
-            const __half2 b = __floats2half2_rn(pr[h][2 * i] - f.x, pr[h][2 * i + 1] - f.y);
-            hi[i] = *reinterpret_cast<const uint32_t*>(&a);
-            lo[i] = *reinterpret_cast<const uint32_t*>(&b);
-            hi[i] = transpose8x8(low ? lo[i] : hi[i]);
-          }
-          if (!dup) {
-            lo[0] = transpose8x8(lo[0]);
-            lo[1] = transpose8x8(lo[1]);
-          }
-#pragma unroll
-          for (int cp = 0; cp < 4; ++cp) {
-            uint32_t c0, c1, c2, c3;
-            ldsm_x4_t(c0, c1, c2, c3, vb + h * 2048 + (((cp * 2 + lhi) ^ lswz) << 4));
-            c0 = __byte_perm(c0, 0u, perm[h][0]);
-            c1 = __byte_perm(c1, 0u, perm[h][1]);
-            c2 = __byte_perm(c2, 0u, perm[h][0]);
-            c3 = __byte_perm(c3, 0u, perm[h][1]);
-            const uint32_t e0 = f8x2_lo(c0), e1 = f8x2_hi(c0), e2 = f8x2_lo(c1), e3 = f8x2_hi(c1);
-            const uint32_t o0 = f8x2_lo(c2), o1 = f8x2_hi(c2), o2 = f8x2_lo(c3), o3 = f8x2_hi(c3);
-            mma_16816_sched(z.acc[2 * cp], e0, e1, e2, e3, hi[0], hi[1]);
-            mma_16816_sched(z.acc[2 * cp + 1], o0, o1, o2, o3, hi[0], hi[1]);
-            if (!dup) {
-              mma_16816_sched(z.acc[2 * cp], e0, e1, e2, e3, lo[0], lo[1]);
-              mma_16816_sched(z.acc[2 * cp + 1], o0, o1, o2, o3, lo[0], lo[1]);
-            }
-          }
-        }
-      } else if (w0 == 0 && lane == 0) {
+    if (in.ntok > cx.w0) {
+      if (f8_scales_ok(in))
+        f8_block(cx, z, qb, in, kv_base + st * F8_STAGE_BYTES, p.scale_log2);
+      else if (cx.w0 == 0 && lane == 0)
         set_status(p.status, KT_ERR_DEVICE_CHECK);  // the block is left out
-      }
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(bar_empty + 8 * st);
@@ -914,9 +949,8 @@ __device__ __forceinline__ bool consume_f8(const Params& p, F8State& z, const ui
   return q_loaded;
 }
 
-// The warp's state as m, l and O[128] of each head (rows of `stride` floats).
-__device__ __forceinline__ void f8_store(F8State& z, float* rows, int stride, int G, int lane) {
-  const int g = lane >> 2, t = lane & 3;
+// Sums of a warp's state over its lanes: l over the tokens, acc over the parts of P.
+__device__ __forceinline__ void f8_reduce(F8State& z, int G) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     z.l[i] += __shfl_xor_sync(0xffffffffu, z.l[i], 4);
@@ -929,11 +963,16 @@ __device__ __forceinline__ void f8_store(F8State& z, float* rows, int stride, in
 #pragma unroll
       for (int i = 0; i < 4; ++i) z.acc[c][i] += __shfl_xor_sync(0xffffffffu, z.acc[c][i], 2);
   }
+}
+// A reduced state as m, l and O[128] of heads h0 .. h1 - 1 (rows of `stride` floats).
+__device__ __forceinline__ void f8_store(const F8State& z, float* rows, int stride, int h0, int h1,
+                                         int lane) {
+  const int g = lane >> 2, t = lane & 3;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int hd = 2 * t + i;
-    if (hd >= G) continue;
-    float* sw = rows + (size_t)hd * stride;
+    if (hd < h0 || hd >= h1) continue;
+    float* sw = rows + (size_t)(hd - h0) * stride;
     if (g == 0) {
       sw[0] = z.m[i];
       sw[1] = z.l[i];
@@ -1003,14 +1042,23 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const __grid_constant_
       prefetch_tensormap(&p.vmap);
     }
     // weight of a segment: its phase-A blocks + the most phase-B blocks + 1
-    warp_prefix(cum, S, [&](int s) {
-      const Part pt = partition(seq_len(p, s / p.H_kv), p.I_b, p.L_b);
+    // one load gives a warp the lengths of up to 32 sequences
+    const int n_lane = p.B <= 32 && lane < p.B ? seq_len(p, lane) : 0;
+    warp_prefix(cum, S, [&](int s, bool live) {
+      const int bs = s / p.H_kv;
+      int n = __shfl_sync(0xffffffffu, n_lane, bs & 31);
+      if (p.B > 32 && live) n = seq_len(p, bs);
+      const Part pt = partition(n, p.I_b, p.L_b);
       return blocks_a(pt, p.dense) + blocks_b_max(pt, p.dense, p.top_k) + 1;
     }, lane);
     // in place: cum[s] -> first CTA of segment s = s + floor(extra * cum[s] / W)
     const long long extra = grid - S, W = cum[S];
     __syncwarp();
-    for (int s = lane; s <= S; s += 32) cum[s] = s + (int)(extra * cum[s] / W);
+    if (W <= (0xFFFFFFFFll >> 10))  // extra < 2^10 CTAs: 32-bit division
+      for (int s = lane; s <= S; s += 32)
+        cum[s] = s + (int)((uint32_t)extra * (uint32_t)cum[s] / (uint32_t)W);
+    else
+      for (int s = lane; s <= S; s += 32) cum[s] = s + (int)(extra * cum[s] / W);
     __syncwarp();
   } else if (FUSED) {
     fused_score<SK>(p, reinterpret_cast<uint8_t*>(scratch), f_hist, f_sh_u64, f_sh_int, tid, warp,
@@ -1510,7 +1558,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const __grid_constant_
     named_bar_sync(1, NCT);
   }
   if constexpr (KVM == KVM_F8) {
-    f8_store(f8, wst + (size_t)warp * p.G * WST, WST, p.G, lane);
+    f8_reduce(f8, p.G);
+    f8_store(f8, wst + (size_t)warp * p.G * WST, WST, 0, p.G, lane);
   } else {
     float l_row = l_part;
     l_row += __shfl_xor_sync(0xffffffffu, l_row, 1);
@@ -1721,6 +1770,567 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const __grid_constant_
   }
 }
 
+
+// ---- e4m3 attention over a given block list (dense, sparse) -------------------
+// Two ways to share the blocks of all segments (units) out over the CTAs:
+//   - CTAs of its own for every segment, one for each F8_SPLIT of its blocks where
+//     there are enough (two CTAs of a segment meet through global memory, which
+//     takes as long as about eight blocks);
+//   - one list: CTA c takes the units [c W / n, (c + 1) W / n), whatever segments
+//     they belong to, which costs a CTA a combination of its warps' states wherever
+//     a segment ends in its range (a piece).
+// The list is taken where there are more segments than CTAs, and where the longest
+// share of the first way exceeds the mean by more than a quarter and three blocks.
+// 16 x 8 segments of 8..63 blocks: 40.4 us with CTAs of their own, 35.1 with the
+// list; 16 x 8 of 33: 26.8 and 29.8; 3 x 8 of 126: 21.2 and 24.4.
+// A piece that is a whole segment is written out; else its part and, at the CTA's
+// end, a ticket: the CTA that takes a segment's last ticket merges its parts in
+// CTA order.
+constexpr int F8K_STAGES = 6;
+// a stage always belongs to the same consumer group: a group that ran ahead to a
+// stage's next phase while its present one, another group's, had not landed would
+// pass the wait by parity
+static_assert(F8K_STAGES % F8_GROUPS == 0 && F8_STAGES % F8_GROUPS == 0, "stages of a group");
+constexpr int F8_SPLIT = 8;
+constexpr int F8_PIECE = 2;    // blocks that the end of a segment costs, about
+constexpr int F8_WST = D + 2;  // m, l, O[128] of a head
+struct F8Smem {
+  static constexpr int kv = 0;
+  static constexpr int wst = kv + F8K_STAGES * F8_STAGE_BYTES;
+  static constexpr int cum = wst + CONSUMERS * 4 * F8_WST * 4;  // units before segment s
+  static constexpr int own = cum + (MAX_SEGS + 1) * 4;              // F8_SPLITs of them, prefix
+  static constexpr int info = (own + (MAX_SEGS + 1) * 4 + 15) & ~15;
+  static constexpr int bars = info + F8K_STAGES * (int)sizeof(StageInfo);
+  static constexpr int bcast = bars + 2 * F8K_STAGES * 8;
+  static constexpr int total = bcast + 32 * 4;
+};
+constexpr int F8_SMEM_BYTES = F8Smem::total + 1024;
+static_assert(F8_SMEM_BYTES <= 232448, "e4m3 attention shared memory exceeds the per-CTA limit");
+
+// A CTA's units of one segment.
+struct F8Piece {  // units 0: none
+  int seg, lo, hi, units;  // units [lo, hi) of the segment's `units`
+  int first, n;            // CTAs that hold units of it: first .. first + n - 1
+};
+
+struct F8Range {
+  const int* cum;
+  long long x0, x1, W;
+  int n, own_first, own_n;  // n: CTAs that share the list (0: segments have their own)
+
+  // the CTA that holds unit x: the last c with c W / n <= x
+  __device__ __forceinline__ int owner(long long x) const {
+    if (W < (1 << 21))  // n < 2^11: 32-bit division
+      return (int)((((uint32_t)x + 1u) * (uint32_t)n + (uint32_t)W - 1u) / (uint32_t)W) - 1;
+    return (int)(((x + 1) * n + W - 1) / W) - 1;
+  }
+  // the first piece at or behind unit x of this CTA's range (x moves to it), from
+  // segment s on; the last F8_PIECE units of a segment stand for its end
+  __device__ __forceinline__ F8Piece piece(long long& x, int s) const {
+    F8Piece q;
+    q.seg = s;
+    q.lo = q.hi = q.units = q.first = q.n = 0;
+    while (x < x1) {
+      while (cum[s + 1] <= x) ++s;
+      const int units = cum[s + 1] - cum[s] - F8_PIECE;
+      if (x - cum[s] < units) {
+        q.seg = s;
+        q.units = units;
+        q.lo = (int)(x - cum[s]);
+        q.hi = (int)min(x1 - cum[s], (long long)units);
+        if (n) {
+          q.first = owner(cum[s]);
+          q.n = owner((long long)cum[s] + units - 1) - q.first + 1;
+        } else {
+          q.first = own_first;
+          q.n = own_n;
+        }
+        return q;
+      }
+      x = cum[s + 1];
+    }
+    return q;
+  }
+};
+
+// Eight states of up to four heads in wst (rows of F8_WST floats, head gg of warp w
+// at 4 w + gg), combined: O / L to `out`, or O, M and L to the part `part` of G
+// heads.  All consumer threads; wst is free at the end.  One copy of the code: it
+// runs a few times a launch, and fetching it costs as much as running it.
+__device__ __noinline__ void f8_combine(float* wst, int nh, float* out, float* part, int G, int h0,
+                                        int ctid) {
+  named_bar_sync(1, NCT);
+  const int gg = 2 * ctid / D, c = 2 * ctid % D;
+  if (gg < nh) {
+    const float* sw = wst + gg * F8_WST;
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < CONSUMERS; ++w) M = fmaxf(M, sw[w * 4 * F8_WST]);
+    const float base = M == -INFINITY ? 0.0f : M;  // then every weight is 0 (or l NaN)
+    float L = 0.0f, o0 = 0.0f, o1 = 0.0f;
+#pragma unroll
+    for (int w = 0; w < CONSUMERS; ++w) {
+      const float wt = ex2(sw[w * 4 * F8_WST] - base);
+      const float2 ov = *reinterpret_cast<const float2*>(sw + w * 4 * F8_WST + 2 + c);
+      L = fmaf(sw[w * 4 * F8_WST + 1], wt, L);
+      o0 = fmaf(ov.x, wt, o0);
+      o1 = fmaf(ov.y, wt, o1);
+    }
+    if (out) {
+      const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+      *reinterpret_cast<float2*>(out + (h0 + gg) * D + c) = make_float2(o0 * inv, o1 * inv);
+    } else {
+      *reinterpret_cast<float2*>(part + (h0 + gg) * D + c) = make_float2(o0, o1);
+      if (c == 0) {
+        part[G * D + h0 + gg] = M;
+        part[G * D + G + h0 + gg] = L;
+      }
+    }
+  }
+  named_bar_sync(1, NCT);
+}
+
+// The eight warps' states of a piece, combined and written: the output if the piece
+// is the whole segment, else this CTA's part.  All consumer threads.
+__device__ __forceinline__ void f8_flush(const Params& p, F8State& z, const F8Piece& q, float* wst,
+                                         int ctid, int warp, int lane) {
+  const bool whole = q.hi - q.lo == q.units;
+  // segments are (sequence, KV head): their query heads follow one another
+  float* out = whole ? p.out + (size_t)q.seg * p.G * D : nullptr;
+  // a segment's first CTA holds its part behind any earlier segment's: slot 1
+  float* part = p.parts + (size_t)(2 * blockIdx.x + (q.lo == 0 ? 1 : 0)) * p.slot_floats;
+  f8_reduce(z, p.G);
+#pragma unroll 1
+  for (int h0 = 0; h0 < p.G; h0 += 4) {
+    const int nh = min(4, p.G - h0);
+    f8_store(z, wst + (size_t)warp * 4 * F8_WST, F8_WST, h0, h0 + nh, lane);
+    f8_combine(wst, nh, out, part, p.G, h0, ctid);
+  }
+}
+
+// The parts of a segment merged in CTA order (warp w takes parts w, w + 8, ..), by
+// all consumer threads of one CTA: as warp states, through f8_combine.
+__device__ __forceinline__ void f8_merge(const Params& p, const F8Piece& q, float* wst, int ctid,
+                                         int warp, int lane) {
+  const int hl = lane >> 3, c0 = (lane & 7) * 16;  // this lane's head of four, and channels
+#pragma unroll 1
+  for (int h0 = 0; h0 < p.G; h0 += 4) {
+    const int nh = min(4, p.G - h0), hd = h0 + min(hl, nh - 1);
+    float M = -INFINITY, L = 0.0f, o[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[i] = 0.0f;
+#pragma unroll 1
+    for (int k0 = warp; k0 < q.n; k0 += 3 * CONSUMERS) {
+      float m[3], l[3];
+      float4 v[3][4];
+#pragma unroll
+      for (int e = 0; e < 3; ++e) {
+        const int k = k0 + e * CONSUMERS;
+        m[e] = -INFINITY;
+        l[e] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[e][i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (k < q.n) {
+          // slot 1 of the segment's first CTA, slot 0 of the others
+          const float* src = p.parts + (size_t)(2 * (q.first + k) + (k == 0)) * p.slot_floats;
+          m[e] = __ldcg(src + p.G * D + hd);
+          l[e] = __ldcg(src + p.G * D + p.G + hd);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            v[e][i] = __ldcg(reinterpret_cast<const float4*>(src + hd * D + c0) + i);
+        }
+      }
+      const float Mn = fmaxf(fmaxf(M, m[0]), fmaxf(m[1], m[2]));
+      const float base = Mn == -INFINITY ? 0.0f : Mn;
+      const float a = ex2(M - base);
+      L *= a;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[i] *= a;
+#pragma unroll
+      for (int e = 0; e < 3; ++e) {
+        const float w = ex2(m[e] - base);
+        L = fmaf(l[e], w, L);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          o[4 * i] = fmaf(v[e][i].x, w, o[4 * i]);
+          o[4 * i + 1] = fmaf(v[e][i].y, w, o[4 * i + 1]);
+          o[4 * i + 2] = fmaf(v[e][i].z, w, o[4 * i + 2]);
+          o[4 * i + 3] = fmaf(v[e][i].w, w, o[4 * i + 3]);
+        }
+      }
+      M = Mn;
+    }
+    if (hl < nh) {
+      float* sw = wst + (size_t)(warp * 4 + hl) * F8_WST;
+      if (c0 == 0) {
+        sw[0] = M;
+        sw[1] = L;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        *reinterpret_cast<float2*>(sw + 2 + c0 + 2 * i) = make_float2(o[2 * i], o[2 * i + 1]);
+    }
+    f8_combine(wst, nh, p.out + (size_t)q.seg * p.G * D, nullptr, p.G, h0, ctid);
+  }
+}
+
+__global__ void __launch_bounds__(THREADS, 1) attn_f8_kernel(const __grid_constant__ Params p) {
+  constexpr uint32_t NST = F8K_STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int grid = gridDim.x, cta = blockIdx.x, S = p.B * p.H_kv, H_q = p.H_kv * p.G;
+  int* cum = reinterpret_cast<int*>(smem + F8Smem::cum);
+  int* own = reinterpret_cast<int*>(smem + F8Smem::own);
+  StageInfo* info = reinterpret_cast<StageInfo*>(smem + F8Smem::info);
+  float* wst = reinterpret_cast<float*>(smem + F8Smem::wst);
+  int* bcast = reinterpret_cast<int*>(smem + F8Smem::bcast);
+  const uint32_t bar_full = smem_u32(smem + F8Smem::bars), bar_empty = bar_full + NST * 8;
+  const uint32_t kv_base = smem_u32(smem + F8Smem::kv);
+  if (tid == 0) {
+    for (uint32_t i = 0; i < NST; ++i) {
+      mbar_init(bar_full + 8 * i, 2);  // the TMA copies and the scales
+      mbar_init(bar_empty + 8 * i, F8_GROUP);
+    }
+    fence_mbar_init();
+    prefetch_tensormap(&p.kmap);
+    prefetch_tensormap(&p.vmap);
+  }
+  // a launch behind the selection kernel waits later, before its selected blocks
+  if (p.wait_at_entry) griddep_wait();
+  if (tid == 0) KT_STAMP(p, 0);
+  // ---- units of every segment, their prefix, and this CTA's share: a thread a
+  // segment (256 at a time), scanned by warps
+  int* tot = bcast;  // [0..7] and [8..15] warp totals, [16] longest share, [17..19] this CTA's
+  int carry_u = 0, carry_v = 0;
+  if (tid == 0) {
+    cum[0] = own[0] = 0;
+    tot[16] = 0;
+    tot[17] = S;
+  }
+  for (int s0 = 0; s0 < S; s0 += NCT) {
+    const int s = s0 + tid;
+    int u = 0;
+    if (tid < NCT && s < S) {
+      const Part pt = partition(seq_len(p, s / p.H_kv), p.I_b, p.L_b);
+      u = blocks_a(pt, p.dense) + blocks_b_max(pt, p.dense, p.top_k);
+    }
+    int iu = u > 0 ? u + F8_PIECE : 0, iv = u / F8_SPLIT;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int a = __shfl_up_sync(0xffffffffu, iu, o), v = __shfl_up_sync(0xffffffffu, iv, o);
+      if (lane >= o) {
+        iu += a;
+        iv += v;
+      }
+    }
+    if (lane == 31 && warp < CONSUMERS) {
+      tot[warp] = iu;
+      tot[8 + warp] = iv;
+    }
+    __syncthreads();
+    int du = carry_u, dv = carry_v;
+#pragma unroll
+    for (int w = 0; w < CONSUMERS; ++w) {
+      if (w < warp) {
+        du += tot[w];
+        dv += tot[8 + w];
+      }
+      carry_u += tot[w];
+      carry_v += tot[8 + w];
+    }
+    if (tid < NCT && s < S) {
+      cum[s + 1] = iu + du;
+      own[s + 1] = iv + dv;
+    }
+    __syncthreads();
+  }
+  F8Range rg;
+  rg.cum = cum;
+  rg.W = carry_u;
+  rg.n = 0;
+  rg.x0 = rg.x1 = 0;
+  rg.own_first = rg.own_n = 0;
+  int seg0 = 0;  // a segment at or before the range
+  bool list = S > grid;
+  if (!list) {
+    if (carry_v == 0) {  // no segment to split
+      if (tid == 0 && cta < S) {
+        tot[17] = cta;
+        tot[18] = cta;
+        tot[19] = 1;
+      }
+    } else {
+      // first CTA of segment s: s and its share of the CTAs that the segments'
+      // F8_SPLITs can use (at most 2^10)
+      const int extra = min(grid - S, carry_v);
+      auto first = [&](int s) {
+        return s + (carry_v < (1 << 21)
+                        ? (int)((uint32_t)extra * (uint32_t)own[s] / (uint32_t)carry_v)
+                        : (int)((long long)extra * own[s] / carry_v));
+      };
+      int most = 0;
+      for (int s = tid; s < S; s += THREADS) {
+        const int f = first(s), n = first(s + 1) - f;
+        most = max(most, (cum[s + 1] - cum[s] + n - 1) / n);
+        if (f <= cta && cta < f + n) {
+          tot[17] = s;
+          tot[18] = f;
+          tot[19] = n;
+        }
+      }
+      most = __reduce_max_sync(0xffffffffu, most);
+      if (lane == 0) atomicMax(&tot[16], most);
+    }
+    __syncthreads();
+    list = carry_u >= grid * F8_SPLIT && 4ll * tot[16] * grid > 5ll * carry_u + 12ll * grid;
+  }
+  if (!list) {
+    seg0 = tot[17];
+    if (seg0 < S) {
+      rg.own_first = tot[18];
+      rg.own_n = tot[19];
+      const long long u = max(0, cum[seg0 + 1] - cum[seg0] - F8_PIECE), i = cta - rg.own_first;
+      rg.x0 = rg.x1 = cum[seg0];
+      if (rg.own_n == 1) {
+        rg.x1 += u;
+      } else if (u < (1 << 21)) {
+        rg.x0 += (uint32_t)(i * u) / (uint32_t)rg.own_n;
+        rg.x1 += (uint32_t)((i + 1) * u) / (uint32_t)rg.own_n;
+      } else {
+        rg.x0 += i * u / rg.own_n;
+        rg.x1 += (i + 1) * u / rg.own_n;
+      }
+    }
+  } else {
+    rg.n = grid;
+    rg.x0 = cta * rg.W / grid;
+    rg.x1 = (cta + 1) * rg.W / grid;
+    int lo = 0, hi = S - 1;  // the last s with cum[s] <= x0
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (cum[mid] <= rg.x0) lo = mid; else hi = mid - 1;
+    }
+    seg0 = lo;
+  }
+
+  if (warp == CONSUMERS) {
+    // =========================== producer warp ===============================
+    const uint64_t policy = l2_evict_first_policy();
+    uint32_t it = 0;
+    bool ok = true, waited = p.wait_at_entry != 0;
+    // up to 32 units at a time, one a lane, whatever segments they belong to:
+    // Initial / Local / dense blocks need the table entry alone (row), selected ones
+    // first their id: their pages are not waited for before the first is issued
+    struct Batch {
+      int n, ntok, row, page, head, piece;
+      unsigned int sel, real;  // lanes with a selected block, with any
+    };
+    int k0 = 0, s_from = seg0;  // pieces before, segment of the last unit
+    auto look_up = [&](long long x) {
+      Batch t;
+      t.n = (int)min(32ll, rg.x1 - x);
+      const bool live = lane < t.n;
+      int s = s_from;
+      if (live)
+        while (cum[s + 1] <= x + lane) ++s;
+      const int units = live ? cum[s + 1] - cum[s] - F8_PIECE : 0;
+      const int i = live ? (int)(x + lane - cum[s]) : 0;
+      const bool real = live && i < units;
+      t.real = __ballot_sync(0xffffffffu, real);
+      // ordinal of the unit's piece: pieces begun so far
+      const unsigned int bm =
+          __ballot_sync(0xffffffffu, real && (i == 0 || x + lane == rg.x0));
+      t.piece = k0 + __popc(bm & (0xFFFFFFFFu >> (31 - lane))) - 1;
+      k0 += __popc(bm);
+      s_from = __shfl_sync(0xffffffffu, s, t.n - 1);
+      const int b = s / p.H_kv, h = s - b * p.H_kv, unit = b * p.SEL + (p.SEL == 1 ? 0 : h);
+      const Part pt = partition(seq_len(p, b), p.I_b, p.L_b);
+      const int nA = blocks_a(pt, p.dense);
+      const bool is_b = real && i >= nA;
+      t.sel = __ballot_sync(0xffffffffu, is_b);
+      if (t.sel && !waited) {  // selected blocks: behind the selection kernel
+        griddep_wait();
+        waited = true;
+      }
+      t.ntok = 0;
+      t.row = 0;
+      t.page = -1;
+      t.head = h;
+      const int nB = units - nA;
+      if (is_b) {
+        const size_t at = (size_t)unit * p.top_k + (i - nA);
+        int c = nB;
+        if (p.cnt) c = p.cnt[unit];
+        if (p.sel_pages) {
+          t.page = p.sel_pages[at];
+        } else {
+          const int id = p.sel[at];
+          if (id >= pt.c0 && id < pt.c1) t.page = p.table[(size_t)b * p.max_blocks + id];
+        }
+        if (c < 0 || c > nB) set_status(p.status, KT_ERR_DEVICE_CHECK);
+        if (i - nA < c) t.ntok = UNIT;  // a Context block is full
+      } else if (real) {
+        const int j = (p.dense || i < pt.c0) ? i : pt.c1 + (i - pt.c0);
+        const int page = p.table[(size_t)b * p.max_blocks + j];
+        if (page < 0 || page >= p.P) {
+          set_status(p.status, KT_ERR_DEVICE_CHECK);  // the block is left out
+        } else {
+          t.ntok = min(UNIT, pt.n - j * BS);
+          t.row = (page * p.H_kv + h) * BS;
+        }
+      }
+      return t;
+    };
+    auto issue = [&](const Batch& t, int e0, int e1) {
+      for (int e = e0; e < e1 && ok; ++e) {
+        if (!((t.real >> e) & 1u)) continue;
+        int ntok = __shfl_sync(0xffffffffu, t.ntok, e);
+        const int k = __shfl_sync(0xffffffffu, t.piece, e);
+        int row = __shfl_sync(0xffffffffu, t.row, e);
+        if ((t.sel >> e) & 1u) {
+          const int page = __shfl_sync(0xffffffffu, t.page, e);
+          row = (page * p.H_kv + __shfl_sync(0xffffffffu, t.head, e)) * BS;
+          if (ntok > 0 && (page < 0 || page >= p.P)) {
+            if (lane == 0) set_status(p.status, KT_ERR_DEVICE_CHECK);
+            ntok = 0;
+          }
+        }
+        const uint32_t st = it % NST;
+        int okl = 1;
+        if (lane == 0) {
+          okl = it < NST || mbar_wait(bar_empty + 8 * st, ((it / NST) - 1) & 1, p.status);
+          if (okl) {
+            info[st].ntok = ntok;
+            info[st].end = k;
+            const uint32_t bar = bar_full + 8 * st;
+            if (ntok > 0) {
+              if (it == 0) KT_STAMP(p, 7);
+              issue_f8(p, kv_base, info, st, row, bar, policy);
+            } else {
+              mbar_arrive(bar);
+              mbar_arrive(bar);
+            }
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, okl, 0) != 0;
+        ++it;
+      }
+    };
+    if (rg.x0 < rg.x1) {
+      Batch t = look_up(rg.x0);
+      for (long long x = rg.x0; ok;) {
+        // the next units are looked up with a ring of loads in flight
+        const int first = min(t.n, (int)NST);
+        issue(t, 0, first);
+        x += t.n;
+        const bool more = x < rg.x1;
+        Batch u = t;
+        if (more && ok) u = look_up(x);
+        issue(t, first, t.n);
+        if (!more) break;
+        t = u;
+      }
+    }
+    // an end marker for each consumer group
+    for (int e = 0; e < F8_GROUPS && ok; ++e, ++it) {
+      const uint32_t st = it % NST;
+      int okl = 1;
+      if (lane == 0) {
+        okl = it < NST || mbar_wait(bar_empty + 8 * st, ((it / NST) - 1) & 1, p.status);
+        if (okl) {
+          info[st].ntok = 0;
+          info[st].end = -1;
+          mbar_arrive(bar_full + 8 * st);
+          mbar_arrive(bar_full + 8 * st);
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, okl, 0) != 0;
+    }
+    if (!waited) griddep_wait();  // nothing of this launch outlives the selection
+    return;
+  }
+
+  // ============================ consumer warps ===============================
+  // segments without a block
+  if (rg.n) {
+    for (int s = cta; s < S; s += grid)
+      if (cum[s + 1] == cum[s])
+        for (int i = tid; i < p.G * D; i += NCT) p.out[(size_t)s * p.G * D + i] = 0.0f;
+  } else if (seg0 < S && cum[seg0 + 1] == cum[seg0]) {
+    for (int i = tid; i < p.G * D; i += NCT) p.out[(size_t)seg0 * p.G * D + i] = 0.0f;
+  }
+  long long x = rg.x0;
+  F8Piece q = rg.piece(x, seg0);
+  if (q.units == 0) return;
+  const F8Lane cx = f8_lane(p.G, warp, lane);
+  F8State z;
+  f8_reset(z);
+  uint32_t qb[8][2];
+  int k = 0;
+  // segments that other CTAs have parts of: the first piece's and the last's
+  F8Piece open0 = q, open1 = q;
+  open0.n = open1.n = 0;
+  auto load_q = [&] {
+    const int b = q.seg / p.H_kv, h = q.seg - b * p.H_kv;
+    f8_load_q(cx, p.q + ((size_t)b * H_q + (size_t)h * p.G) * D, p.G, qb);
+  };
+  // every warp passes every piece once, whatever its waits gave: the barriers of
+  // the flushes match
+  auto next = [&] {
+    const F8Piece done = q;
+    x += q.hi - q.lo;
+    q = rg.piece(x, q.seg);
+    const bool more = q.units > 0;
+    if (more) load_q();  // on its way during the flush
+    f8_flush(p, z, done, wst, tid, warp, lane);
+    if (done.hi - done.lo < done.units) {
+      if (k == 0) open0 = done; else open1 = done;
+    }
+    ++k;
+    f8_reset(z);
+    return more;
+  };
+  load_q();
+#pragma unroll 1
+  for (uint32_t it = warp / F8_GROUP;; it += F8_GROUPS) {
+    const uint32_t st = it % NST;
+    StageInfo in;
+    in.end = -1;  // the end marker, and a wait that ran out
+    if (mbar_wait(bar_full + 8 * st, (it / NST) & 1, p.status)) in = info[st];
+    if (in.end < 0 && tid == 0) {
+      KT_STAMP(p, 9);
+      griddep_launch_dependents();  // the next launch may be scheduled
+    }
+    bool more = true;
+    while (more && k != in.end) more = next();  // to the end where it is the marker
+    if (!more) break;
+    if (in.ntok > cx.w0) {
+      if (f8_scales_ok(in))
+        f8_block(cx, z, qb, in, kv_base + st * F8_STAGE_BYTES, p.scale_log2);
+      else if (cx.w0 == 0 && lane == 0)
+        set_status(p.status, KT_ERR_DEVICE_CHECK);  // the block is left out
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar_empty + 8 * st);
+  }
+  if (tid == 0) KT_STAMP(p, 10);
+  // the barrier at the end of the last flush stands between the parts and the tickets
+  if (tid < 2) {
+    const int seg = tid ? open1.seg : open0.seg, n = tid ? open1.n : open0.n;
+    bcast[20 + tid] = n > 0 && atom_acq_rel_gpu_add(p.counters + seg, 1) + 1 == n;
+  }
+  named_bar_sync(1, NCT);
+#pragma unroll 1
+  for (int i = 0; i < 2; ++i) {
+    if (!bcast[20 + i]) continue;
+    const F8Piece o = i ? open1 : open0;
+    f8_merge(p, o, wst, tid, warp, lane);
+    if (tid == 0) p.counters[o.seg] = 0;
+  }
+  if (tid == 0) KT_STAMP(p, 12);
+}
+
 }  // namespace
 
 // Per device: the shared-memory opt-in of both variants (0 = done, else the
@@ -1739,7 +2349,6 @@ int attn_smem_optin() {
                           (const void*)attn_kernel<SK_MMA, KVM_Q8>,
                           (const void*)attn_kernel<SK_F32, KVM_Q8>,
                           (const void*)attn_kernel<SK_MULTI, KVM_Q8>,
-                          (const void*)attn_kernel<SK_NONE, KVM_F8>,
                           (const void*)attn_kernel<SK_COLS, KVM_F8>,
                           (const void*)attn_kernel<SK_LINEAR, KVM_F8>,
                           (const void*)attn_kernel<SK_MMA, KVM_F8>,
@@ -1747,6 +2356,9 @@ int attn_smem_optin() {
                           (const void*)attn_kernel<SK_MULTI, KVM_F8>})
       if (e == cudaSuccess)
         e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute((const void*)attn_f8_kernel,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, F8_SMEM_BYTES);
     return (int)e;
   });
 }
@@ -1856,7 +2468,11 @@ cudaError_t launch_attention(const AttnLaunch& a, cudaStream_t stream) {
   if (!a.fused) {
     if (a.kvm == KVM_HOST) return cudaLaunchKernelEx(&cfg, attn_kernel<SK_NONE, KVM_HOST>, p);
     if (a.kvm == KVM_Q8) return cudaLaunchKernelEx(&cfg, attn_kernel<SK_NONE, KVM_Q8>, p);
-    if (a.kvm == KVM_F8) return cudaLaunchKernelEx(&cfg, attn_kernel<SK_NONE, KVM_F8>, p);
+    if (a.kvm == KVM_F8) {
+      cfg.gridDim = dim3(a.ctas);
+      cfg.dynamicSmemBytes = F8_SMEM_BYTES;
+      return cudaLaunchKernelEx(&cfg, attn_f8_kernel, p);
+    }
     return cudaLaunchKernelEx(&cfg, attn_kernel<SK_NONE>, p);
   }
   if (a.kvm == KVM_Q8) {

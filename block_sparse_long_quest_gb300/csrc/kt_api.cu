@@ -344,6 +344,7 @@ kt_status attn_impl(const void* q, const kt_paged_kv* kv, int num_q_heads, float
   const int nseg = kv->batch * kv->num_kv_heads;
   const int base = sms < MAX_ATTN_CTAS ? sms : MAX_ATTN_CTAS;
   a.grid = base > nseg ? base : nseg;
+  a.ctas = base;
   a.pdl = pdl;
   a.stamps = stamps_for(a.grid);
   a.kvm = src.kvm;

@@ -546,6 +546,7 @@ struct AttnLaunch {
   int B, H_kv, G, max_blocks, P, I_b, L_b, top_k, SEL, dense, slot_floats;
   float scale_log2;
   int grid;
+  int ctas;  // KVM_F8: CTAs whatever the segments (each may take several)
   bool pdl;  // launched as a programmatic dependent of the previous kernel
   bool q_mapped;  // q and out are page-locked host memory read and written over the link
   // fused step (selection inside the attention kernel, cooperative launch)

@@ -114,7 +114,8 @@ class Cache:
         return x[::stride]
 
     def attend(self, q, b, h, blocks, scale):
-        """softmax(scale q K^T) V over `blocks` of sequence b, and sum p |v|; q [G][128]."""
+        """softmax(scale q K^T) V over `blocks` of sequence b, sum p |v|, the largest
+        scale sum |q k| of a score, and sum |v| / sum exp(s - max s); q [G][128]."""
         n = int(self.lens[b])
         k = np.concatenate([self.values("k", int(self.table[b, j]), h)[:max(0, n - j * 128)]
                             for j in blocks])
@@ -122,8 +123,10 @@ class Cache:
                             for j in blocks])
         s = q.astype(np.float64) @ k.T * scale
         p = np.exp(s - s.max(-1, keepdims=True))
-        p /= p.sum(-1, keepdims=True)
-        return p @ v, p @ np.abs(v)
+        total = p.sum(-1, keepdims=True)
+        p /= total
+        return (p @ v, p @ np.abs(v), (np.abs(q.astype(np.float64)) @ np.abs(k).T).max() * scale,
+                np.abs(v).sum(0)[None] / total)
 
 
 def frequencies(rot, theta, scaling="plain", factor=1.0, original_len=0, fast=32.0, slow=1.0):

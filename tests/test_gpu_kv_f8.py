@@ -22,13 +22,23 @@ def kt():
 
 DTYPES = {"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32}
 SCALE = 128 ** -0.5
-# Attention: |got - want| <= ATTN_TOL * sum p |v| + 2^-22 |want|.  A score of the inputs below is a
-# sum of 128 products of magnitude at most 2^8 in all, accumulated in binary32 over 8 tensor-core
-# steps of which each may truncate (2^-23 of the running magnitude): 8 * 2^-23 * 2^8 * SCALE
-# = 2.2e-5; base-2 exponent and its argument 2^-22 * 32; P is split into two binary16 (2^-22); the
-# sums over a warp's tokens and over warps add up to 2^-24 for each of fewer than 2^9 steps = 3e-5.
-# Numerator and denominator both carry these: twice the sum of 6.0e-5.
-ATTN_TOL = 1.2e-4
+def attention_tolerance(mag, want, score, all_v):
+    """Bound of |got - want|; mag: sum p |v|, score: the largest SCALE * sum |q k|, all_v: sum |v| /
+    sum exp(s - max s).  A score is
+    accumulated in binary32 over 8 tensor-core steps, each of which may truncate 2^-23 of the
+    running magnitude; the base-2 exponent and its argument (at most 2 * 1.45 * score, or 32) err by
+    2^-22 of it; P is split into two binary16 (2^-22); the sums over a warp's tokens and over warps
+    add 2^-24 for each of fewer than 2^9 steps; 2^15 P / max P in binary16 parts ends at 2^-24, half
+    a step of which is 2^-40 of the largest P for every token, however small its own.  Numerator and denominator both carry these.  Inputs
+    of unit size have score < 22.6 (2^8 * SCALE), which gives 1.2e-4."""
+    score = max(score, 22.6)
+    p = 8 * 2.0 ** -23 * score + 2.0 ** -22 * max(32.0, 2.9 * score) + 2.0 ** -22 + 2.0 ** -15
+    return 2 * p * mag + 2.0 ** -22 * np.abs(want) + 2.0 ** -40 * all_v
+
+
+@pytest.fixture(autouse=True)
+def _seed():
+    torch.manual_seed(1234)
 
 
 def host16(t):
@@ -510,9 +520,9 @@ def check_attention(pg, q, out, blocks_of, G):
             if pg.host.lens[b] == 0 or not len(blocks):
                 assert (out[b, sl] == 0).all()
                 continue
-            want, mag = pg.host.attend(q[b, sl], b, h, blocks, SCALE)
+            want, mag, score, all_v = pg.host.attend(q[b, sl], b, h, blocks, SCALE)
             err = np.abs(out[b, sl] - want)
-            tol = ATTN_TOL * mag + 2.0 ** -22 * np.abs(want)
+            tol = attention_tolerance(mag, want, score, all_v)
             assert (err <= tol).all(), (b, h, (err / tol).max())
 
 
@@ -537,6 +547,33 @@ def test_dense_attention(kt, G, H, lens):
         check_attention(pg, q, out, lambda b, h: range(-(-int(pg.host.lens[b]) // 128)), G)
     kt.kt_dense_decode_attn_f8(q, pg.kv, H * G, SCALE, out, ws)
     assert torch.equal(out, first)
+
+
+@pytest.mark.parametrize("G,H,lens", [
+    (4, 8, [20000, 3, 0, 9000, 129, 12345, 128 * 11]),  # one list of blocks over all SMs
+    (8, 2, [70000, 128, 60001]),
+    (2, 1, [(37 * b) % 300 for b in range(400)]),       # more segments than SMs, empty ones too
+    (1, 1, [0] * 200),
+])
+def test_dense_attention_shares_the_blocks_out(kt, G, H, lens):
+    """Enough blocks for every CTA to take an equal part of all segments' blocks: pieces of a
+    segment in several CTAs, several segments in a CTA."""
+    pg = filled(kt, lens, H, 37)
+    q = torch.randn(len(lens), H * G, 128).half().cuda()
+    p = kt.sparse_params(H * G, 0, 1, 1, kt.KT_REP_QUEST, kt.KT_HEAD_SHARED)
+    ws = kt.workspace_f8(kt.KT_OP_DENSE_ATTN, pg.kv, p)
+    first = None
+    for ctas in (0, 0, 0, 3, 50):
+        out = torch.full((len(lens), H * G, 128), float("nan"), device="cuda")
+        kt.kt_set_max_ctas(ctas)
+        kt.kt_dense_decode_attn_f8(q, pg.kv, H * G, SCALE, out, ws)
+        kt.kt_set_max_ctas(0)
+        if first is None or ctas:
+            check_attention(pg, q, out, lambda b, h: range(-(-int(pg.host.lens[b]) // 128)), G)
+            first = out if first is None else first
+        else:
+            assert torch.equal(out, first)  # the order of the sums is the CTAs', not their timing
+    assert_status(kt, ws)
 
 
 def chosen(kt, pg, sel, cnt, p, b, h):
