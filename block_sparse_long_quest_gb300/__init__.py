@@ -443,7 +443,8 @@ def rope(rotary_dim=128, *, theta=10000.0, layout=KT_ROPE_HALF, scaling=KT_ROPE_
     return r
 
 
-_DTYPES = {}
+_byref = ctypes.byref
+_DTYPES = {}  # of torch's types, filled on first use
 
 
 def _dtype(t, call):
@@ -465,29 +466,33 @@ def rows(t) -> Rows:
     s0, s1, s2 = t.stride()
     if d != 128 or s2 != 1 or (s1 != 128 and heads > 1):
         raise KtError(KT_ERR_INVALID_ARG, "rows")
-    return Rows(t.data_ptr(), s0 if tokens > 1 else heads * 128, heads, _dtype(t, "rows"))
+    dtype = _DTYPES.get(t.dtype)
+    if dtype is None:
+        dtype = _dtype(t, "rows")
+    return Rows(t.data_ptr(), s0 if tokens > 1 else heads * 128, heads, dtype)
 
 
-def _rows(t):
-    return None if t is None else ctypes.byref(rows(t))
-
-
-def _check_out(out, shape, call):
-    if out is not None and (out.shape != shape or not out.is_contiguous()):
+def _check_rows(t, tokens, out, call):
+    """The rows t of a call of `tokens` tokens, rotated into out (contiguous, of t's shape)."""
+    shape = t.shape
+    if shape[0] != tokens or (out is not None and (out.shape != shape or
+                                                   not out.is_contiguous())):
         raise KtError(KT_ERR_INVALID_ARG, call)
 
 
 def kt_apply_rope(rope, positions, q=None, q_out=None, k=None, k_out=None, stream=None):
     """Rotates q into q_out and k into k_out ([tokens][heads][128]; outputs float16); positions:
     int32 [tokens]."""
-    tokens = positions.numel()
-    for x, y in ((q, q_out), (k, k_out)):
-        if x is not None:
-            if x.shape[0] != tokens:
-                raise KtError(KT_ERR_INVALID_ARG, "kt_apply_rope")
-            _check_out(y, x.shape, "kt_apply_rope")
-    _check(lib.kt_apply_rope(ctypes.byref(rope), _ptr(positions), tokens, _rows(q), _ptr(q_out),
-                             _rows(k), _ptr(k_out), _stream(stream)),
+    tokens = positions.shape[0]
+    qr = kr = None
+    if q is not None:
+        _check_rows(q, tokens, q_out, "kt_apply_rope")
+        qr = _byref(rows(q))
+    if k is not None:
+        _check_rows(k, tokens, k_out, "kt_apply_rope")
+        kr = _byref(rows(k))
+    _check(lib.kt_apply_rope(_byref(rope), _ptr(positions), tokens, qr, _ptr(q_out), kr,
+                             _ptr(k_out), _stream(stream)),
            "kt_apply_rope")
 
 
@@ -529,16 +534,21 @@ def kt_append_kv_f8(kv, params, k, v, ws, *, rope=None, q=None, q_out=None, cu_t
     """Appends the rows k / v ([tokens][H_kv][128]) to the cache.  cu_tokens None: one row per
     sequence; new_lens None: kv's lengths advance in place."""
     tokens = k.shape[0]
-    if v.shape[0] != tokens or (q is not None and q.shape[0] != tokens):
-        raise KtError(KT_ERR_INVALID_ARG, "kt_append_kv_f8")
+    _check_rows(v, tokens, None, "kt_append_kv_f8")
+    qr = None
     if q is not None:
-        _check_out(q_out, q.shape, "kt_append_kv_f8")
-    _check(lib.kt_append_kv_f8(ctypes.byref(kv), ctypes.byref(params),
-                               None if rope is None else ctypes.byref(rope), _rows(q),
-                               _ptr(q_out), _rows(k), _rows(v), _ptr(cu_tokens), tokens,
-                               _ptr(new_lens), _ptr(reps_pool), _ptr(ws), ws.numel(),
-                               _stream(stream)),
+        _check_rows(q, tokens, q_out, "kt_append_kv_f8")
+        qr = _byref(rows(q))
+    _check(lib.kt_append_kv_f8(_byref(kv), _byref(params), None if rope is None else _byref(rope),
+                               qr, _ptr(q_out), _byref(rows(k)), _byref(rows(v)),
+                               _ptr(cu_tokens), tokens, _ptr(new_lens), _ptr(reps_pool), _ptr(ws),
+                               ws.numel(), _stream(stream)),
            "kt_append_kv_f8")
+
+
+def _check_out(out, shape, call):
+    if out is not None and (out.shape != shape or not out.is_contiguous()):
+        raise KtError(KT_ERR_INVALID_ARG, call)
 
 
 def kt_read_kv_f8(kv, cu_tokens, k_out, v_out, ws, *, first=None, stream=None):

@@ -1193,6 +1193,11 @@ kt_status check_kv_f8(const kt_paged_kv_f8* f, kt_paged_kv* kv) {
   return KT_OK;
 }
 
+// The kernel counts the blocks of all segments together in 32 bits.
+bool units_ok(const kt_paged_kv& kv) {
+  return (long long)kv.batch * kv.num_kv_heads * (kv.max_blocks_per_seq + 2ll) <= 0x3FFFFFFFll;
+}
+
 KvSource source_f8(const kt_paged_kv_f8* f) {
   KvSource src;
   src.kvm = KVM_F8;
@@ -1410,6 +1415,7 @@ kt_status kt_sparse_decode_attn_f8(const void* q, const kt_paged_kv_f8* kvf,
   if (s != KT_OK) return s;
   if (!q || !sel || !cnt || !out || !ws || !aligned16(q) || !aligned16(out) || !aligned16(ws))
     return KT_ERR_INVALID_ARG;
+  if (!units_ok(kv)) return KT_ERR_UNSUPPORTED;
   const WsLayout L = layout(KT_OP_SPARSE_ATTN, &kv, p, 0);
   if (ws_bytes < L.total) return KT_ERR_WORKSPACE_TOO_SMALL;
   return attn_impl(q, &kv, p->num_q_heads, p->softmax_scale, p, sel, cnt, out, ws, L, false,
@@ -1426,6 +1432,7 @@ kt_status kt_dense_decode_attn_f8(const void* q, const kt_paged_kv_f8* kvf, int3
   if (s != KT_OK) return s;
   if (!q || !out || !ws || !aligned16(q) || !aligned16(out) || !aligned16(ws))
     return KT_ERR_INVALID_ARG;
+  if (!units_ok(kv)) return KT_ERR_UNSUPPORTED;
   kt_sparse_params p;
   std::memset(&p, 0, sizeof(p));
   p.num_q_heads = num_q_heads;
@@ -1457,6 +1464,7 @@ kt_status kt_sparse_decode_step_f8(const void* q, const kt_paged_kv_f8* kvf,
   const kt_status s = check_kv_f8(kvf, &kv);
   if (s != KT_OK) return s;
   if (p && p->rep == KT_REP_DYNAMIC) return KT_ERR_INVALID_ARG;
+  if (!units_ok(kv)) return KT_ERR_UNSUPPORTED;
   return step_impl(q, &kv, reps_pool, p, nullptr, nullptr, sel, cnt, out, ws, ws_bytes, stream, 0,
                    0, false, false, source_f8(kvf));
 }

@@ -257,7 +257,9 @@ int32_t kt_sparse_decode_step_kernels(const kt_paged_kv* kv, const kt_sparse_par
  * Caps the CTAs that the attention calls (kt_sparse_decode_attn,
  * kt_sparse_decode_step, kt_decode_layer, kt_dense_decode_attn) launch from
  * the calling host thread: at most max_ctas, and never fewer than one per
- * (sequence, KV head) segment; 0 restores the default of one per SM.  A
+ * (sequence, KV head) segment (kt_sparse_decode_attn_f8 and
+ * kt_dense_decode_attn_f8 share the segments out over max_ctas even where there
+ * are more); 0 restores the default of one per SM.  A
  * caller that runs other work beside the decode step can leave SMs to it.
  * The split-K partition of each segment, and in the one-launch step the
  * scoring slices, follow from the CTA count; outputs agree within rounding
@@ -687,7 +689,8 @@ kt_status kt_read_kv_f8(const kt_paged_kv_f8* kv, const int32_t* first, const in
  * that over the values read back.  Scales may be any value in [2^-30, 2^30];
  * others record KT_ERR_DEVICE_CHECK and their block is skipped.  Codes behind
  * seq_lens[b] in the last page may be anything.  Arguments, workspaces (of
- * kt_workspace_bytes_f8) and errors as the calls named; no Dynamic reps.
+ * kt_workspace_bytes_f8) and errors as the calls named; no Dynamic reps, and
+ * batch * num_kv_heads * (max_blocks_per_seq + 2) below 2^30 (UNSUPPORTED beyond).
  */
 kt_status kt_sparse_decode_attn_f8(const void* q, const kt_paged_kv_f8* kv,
                                    const kt_sparse_params* p, const int32_t* sel,

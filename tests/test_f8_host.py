@@ -289,6 +289,13 @@ def test_attention_refuses():
     assert L.kt_build_block_reps_f8(c, p, 64, 5, FAKE, None) == kt.KT_OK  # behind the table
 
 
+def test_attention_refuses_more_blocks_than_it_counts():
+    wide = cache(batch=16, H_kv=8, max_blocks=(1 << 23))
+    calls = every_call(wide, params())
+    for name in ("sparse", "dense", "step"):
+        assert calls[name]() == kt.KT_ERR_UNSUPPORTED, name
+
+
 def test_sizes_are_those_of_the_binary16_cache():
     c, p = cache(), params()
     same = kt.PagedKV(FAKE, FAKE, FAKE, FAKE, 2, 8, 128, 128, 64, 128)

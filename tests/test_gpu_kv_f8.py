@@ -24,13 +24,15 @@ DTYPES = {"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32}
 SCALE = 128 ** -0.5
 def attention_tolerance(mag, want, score, all_v):
     """Bound of |got - want|; mag: sum p |v|, score: the largest SCALE * sum |q k|, all_v: sum |v| /
-    sum exp(s - max s).  A score is
-    accumulated in binary32 over 8 tensor-core steps, each of which may truncate 2^-23 of the
-    running magnitude; the base-2 exponent and its argument (at most 2 * 1.45 * score, or 32) err by
-    2^-22 of it; P is split into two binary16 (2^-22); the sums over a warp's tokens and over warps
-    add 2^-24 for each of fewer than 2^9 steps; 2^15 P / max P in binary16 parts ends at 2^-24, half
-    a step of which is 2^-40 of the largest P for every token, however small its own.  Numerator and denominator both carry these.  Inputs
-    of unit size have score < 22.6 (2^8 * SCALE), which gives 1.2e-4."""
+    sum exp(s - max s).
+
+    A score is accumulated in binary32 over 8 tensor-core steps, each of which may truncate 2^-23
+    of the running magnitude; the base-2 exponent and its argument (at most 2 * 1.45 * score, or 32)
+    err by 2^-22 of it; P is split into two binary16 (2^-22); the sums over a warp's tokens and over
+    warps add 2^-24 for each of fewer than 2^9 steps.  Numerator and denominator both carry these.
+    2^15 P / max P in binary16 parts ends at 2^-24, half a step of which is 2^-40 of the largest P
+    for every token, however small its own.  Inputs of unit size have score < 22.6 (2^8 * SCALE),
+    which gives 1.2e-4."""
     score = max(score, 22.6)
     p = 8 * 2.0 ** -23 * score + 2.0 ** -22 * max(32.0, 2.9 * score) + 2.0 ** -22 + 2.0 ** -15
     return 2 * p * mag + 2.0 ** -22 * np.abs(want) + 2.0 ** -40 * all_v
@@ -425,6 +427,62 @@ def test_long_spans_of_pages_are_checked(kt):
         kt.kt_append_kv_f8(pg.kv, p, x, x, ws, cu_tokens=cu)
         assert pg.lens.tolist() == [0 if bad else n, 3]
         assert_status(kt, ws, kt.KT_ERR_DEVICE_CHECK if bad else kt.KT_OK)
+
+
+@pytest.mark.parametrize("B", [33, 257, 1500])
+def test_many_sequences(kt, B):
+    """Ragged rows of many sequences, most of them short or empty: appended, then read back."""
+    rng = np.random.default_rng(B)
+    counts = [int(c) for c in rng.choice([0, 0, 1, 2, 130], B, p=[.3, .1, .4, .17, .03])]
+    m = sum(counts)
+    gen = torch.Generator().manual_seed(B)
+    pg = Paged(kt, [0] * B, 1, 2, B)
+    p = kt.sparse_params(1, 1, 1, 2, kt.KT_REP_QUEST, kt.KT_HEAD_SHARED)
+    ws = kt.workspace_f8(kt.KT_OP_SPARSE_STEP, pg.kv, p)
+    k, v = rows_of(gen, m, 1, "f16"), rows_of(gen, m, 1, "f16")
+    q = rows_of(gen, m, 1, "f16")
+    q_out, want = torch.empty_like(q), torch.empty_like(q)
+    cu = torch.tensor(np.cumsum([0] + counts), dtype=torch.int32, device="cuda")
+    r = kt.rope(128)
+    pos = torch.cat([torch.arange(c) for c in counts]).to(torch.int32).cuda()
+    kr = torch.empty_like(k)
+    kt.kt_apply_rope(r, pos, q, want, k, kr)
+    kt.kt_append_kv_f8(pg.kv, p, k, v, ws, rope=r, q=q, q_out=q_out, cu_tokens=cu)
+    pg.host.append(host16(kr), host16(v), counts)
+    pg.check()
+    assert torch.equal(q_out, want)
+    back = torch.empty_like(k)
+    kt.kt_read_kv_f8(pg.kv, cu, back, None, ws)
+    exact = np.concatenate([pg.host.values("k", int(pg.host.table[b, t // 128]), 0)[t % 128][None]
+                            for b in range(B) for t in range(counts[b])])
+    assert np.array_equal(back[:, 0].double().cpu().numpy(), exact)
+    assert_status(kt, ws)
+
+
+def test_long_append_rotates_q_ahead(kt):
+    """More rows than ride along with the tiles: q in a launch of its own, lengths in place."""
+    counts, H, G = [1700, 0, 900, 1], 2, 2
+    gen = torch.Generator().manual_seed(5)
+    qkv = rows_of(gen, sum(counts), H * G + 2 * H, "bf16")
+    q, k, v = qkv[:, :H * G], qkv[:, H * G:H * G + H], qkv[:, H * G + H:]
+    cu = torch.tensor(np.cumsum([0] + counts), dtype=torch.int32, device="cuda")
+    p = kt.sparse_params(H * G, 1, 1, 2, kt.KT_REP_QUEST, kt.KT_HEAD_SHARED)
+    r = kt.rope(128)
+    pos = torch.cat([torch.arange(c) for c in counts]).to(torch.int32).cuda()
+    want, kr = (torch.empty(sum(counts), h, 128, dtype=torch.float16, device="cuda")
+                for h in (H * G, H))
+    kt.kt_apply_rope(r, pos, q, want, k, kr)
+    for rope in (r, None):
+        pg = Paged(kt, [0] * 4, H, 14, 5)
+        ws = kt.workspace_f8(kt.KT_OP_SPARSE_STEP, pg.kv, p)
+        q_out = torch.empty_like(want)
+        for _ in range(3):  # back to back: each call reads the lengths the one before left
+            pg.lens.zero_()
+            kt.kt_append_kv_f8(pg.kv, p, k, v, ws, rope=rope, q=q, q_out=q_out, cu_tokens=cu)
+        pg.host.append(host16(kr if rope else k), host16(v), counts)
+        pg.check()
+        assert torch.equal(q_out, want if rope else q.half())
+        assert_status(kt, ws)
 
 
 # ---- reading back -----------------------------------------------------------------------
