@@ -46,6 +46,10 @@
 // that anyone waits on is left: the tags come from a launch counter that each
 // CTA advances by its share without waiting.  SK selects the scoring path at
 // compile time, so a launch carries only the code it runs.
+//
+// Over an e4m3 cache (KVM_F8) the step runs the same kernel with consumers of its
+// own (consume_f8), and the attention over a given block list is a kernel of its
+// own (attn_f8_kernel).
 #include "select_common.cuh"
 
 namespace kt {
