@@ -444,17 +444,21 @@ def rope(rotary_dim=128, *, theta=10000.0, layout=KT_ROPE_HALF, scaling=KT_ROPE_
 
 
 _byref = ctypes.byref
-_DTYPES = {}  # of torch's types, filled on first use
+_INT32 = -1
+_DTYPES = {}  # kt_dtype (or _INT32) of torch's types, filled on first use
 
 
-def _dtype(t, call):
+def _dtype(t):
     if not _DTYPES:
         import torch
-        _DTYPES.update({torch.float16: KT_F16, torch.bfloat16: KT_BF16, torch.float32: KT_F32})
-    d = _DTYPES.get(t.dtype)
-    if d is None:
-        raise KtError(KT_ERR_UNSUPPORTED, call)
-    return d
+        _DTYPES.update({torch.float16: KT_F16, torch.bfloat16: KT_BF16, torch.float32: KT_F32,
+                        torch.int32: _INT32})
+    return _DTYPES.get(t.dtype)
+
+
+def _check_int32(t, call):
+    if t is not None and _dtype(t) != _INT32:
+        raise KtError(KT_ERR_INVALID_ARG, call)
 
 
 def rows(t) -> Rows:
@@ -464,26 +468,29 @@ def rows(t) -> Rows:
         return t
     tokens, heads, d = t.shape
     s0, s1, s2 = t.stride()
+    dtype = _dtype(t)
     if d != 128 or s2 != 1 or (s1 != 128 and heads > 1):
         raise KtError(KT_ERR_INVALID_ARG, "rows")
-    dtype = _DTYPES.get(t.dtype)
-    if dtype is None:
-        dtype = _dtype(t, "rows")
+    if dtype is None or dtype < 0:
+        raise KtError(KT_ERR_UNSUPPORTED, "rows")
     return Rows(t.data_ptr(), s0 if tokens > 1 else heads * 128, heads, dtype)
 
 
 def _check_rows(t, tokens, out, call):
-    """The rows t of a call of `tokens` tokens, rotated into out (contiguous, of t's shape)."""
+    """The rows t of a call of `tokens` tokens, rotated into out (binary16, contiguous, of t's
+    shape)."""
     shape = t.shape
     if shape[0] != tokens or (out is not None and (out.shape != shape or
-                                                   not out.is_contiguous())):
+                                                   not out.is_contiguous() or
+                                                   _dtype(out) != KT_F16)):
         raise KtError(KT_ERR_INVALID_ARG, call)
 
 
 def kt_apply_rope(rope, positions, q=None, q_out=None, k=None, k_out=None, stream=None):
     """Rotates q into q_out and k into k_out ([tokens][heads][128]; outputs float16); positions:
     int32 [tokens]."""
-    tokens = positions.shape[0]
+    _check_int32(positions, "kt_apply_rope")
+    tokens = positions.numel()
     qr = kr = None
     if q is not None:
         _check_rows(q, tokens, q_out, "kt_apply_rope")
@@ -534,6 +541,8 @@ def kt_append_kv_f8(kv, params, k, v, ws, *, rope=None, q=None, q_out=None, cu_t
     """Appends the rows k / v ([tokens][H_kv][128]) to the cache.  cu_tokens None: one row per
     sequence; new_lens None: kv's lengths advance in place."""
     tokens = k.shape[0]
+    _check_int32(cu_tokens, "kt_append_kv_f8")
+    _check_int32(new_lens, "kt_append_kv_f8")
     _check_rows(v, tokens, None, "kt_append_kv_f8")
     qr = None
     if q is not None:
@@ -557,11 +566,16 @@ def kt_read_kv_f8(kv, cu_tokens, k_out, v_out, ws, *, first=None, stream=None):
     out = k_out if k_out is not None else v_out
     if out is None or (k_out is not None and v_out is not None and k_out.dtype != v_out.dtype):
         raise KtError(KT_ERR_INVALID_ARG, "kt_read_kv_f8")
+    dtype = _dtype(out)
+    if dtype is None or dtype < 0:
+        raise KtError(KT_ERR_UNSUPPORTED, "kt_read_kv_f8")
+    _check_int32(cu_tokens, "kt_read_kv_f8")
+    _check_int32(first, "kt_read_kv_f8")
     shape = (out.shape[0], kv.num_kv_heads, 128)
     _check_out(k_out, shape, "kt_read_kv_f8")
     _check_out(v_out, shape, "kt_read_kv_f8")
     _check(lib.kt_read_kv_f8(ctypes.byref(kv), _ptr(first), _ptr(cu_tokens), out.shape[0],
-                             _dtype(out, "kt_read_kv_f8"), _ptr(k_out), _ptr(v_out), _ptr(ws),
+                             dtype, _ptr(k_out), _ptr(v_out), _ptr(ws),
                              ws.numel(), _stream(stream)),
            "kt_read_kv_f8")
 

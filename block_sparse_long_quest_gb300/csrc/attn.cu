@@ -204,13 +204,9 @@ __device__ void warp_prefix(int* pref, int S, F count, int lane) {
   const int per = (S + 31) / 32;
   const int lo = min(S, lane * per), hi = min(S, lo + per);
   int sum = 0;
-  for (int i = 0; i < per; ++i) {  // the whole warp calls count
-    const int s = lo + i;
-    const int n = count(min(s, S - 1), s < hi);
-    if (s < hi) {
-      sum += n;
-      pref[s + 1] = sum;
-    }
+  for (int s = lo; s < hi; ++s) {
+    sum += count(s);
+    pref[s + 1] = sum;
   }
   int incl = sum;
   for (int o = 1; o < 32; o <<= 1) {
@@ -1046,23 +1042,14 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const __grid_constant_
       prefetch_tensormap(&p.vmap);
     }
     // weight of a segment: its phase-A blocks + the most phase-B blocks + 1
-    // one load gives a warp the lengths of up to 32 sequences
-    const int n_lane = p.B <= 32 && lane < p.B ? seq_len(p, lane) : 0;
-    warp_prefix(cum, S, [&](int s, bool live) {
-      const int bs = s / p.H_kv;
-      int n = __shfl_sync(0xffffffffu, n_lane, bs & 31);
-      if (p.B > 32 && live) n = seq_len(p, bs);
-      const Part pt = partition(n, p.I_b, p.L_b);
+    warp_prefix(cum, S, [&](int s) {
+      const Part pt = partition(seq_len(p, s / p.H_kv), p.I_b, p.L_b);
       return blocks_a(pt, p.dense) + blocks_b_max(pt, p.dense, p.top_k) + 1;
     }, lane);
     // in place: cum[s] -> first CTA of segment s = s + floor(extra * cum[s] / W)
     const long long extra = grid - S, W = cum[S];
     __syncwarp();
-    if (W <= (0xFFFFFFFFll >> 10))  // extra < 2^10 CTAs: 32-bit division
-      for (int s = lane; s <= S; s += 32)
-        cum[s] = s + (int)((uint32_t)extra * (uint32_t)cum[s] / (uint32_t)W);
-    else
-      for (int s = lane; s <= S; s += 32) cum[s] = s + (int)(extra * cum[s] / W);
+    for (int s = lane; s <= S; s += 32) cum[s] = s + (int)(extra * cum[s] / W);
     __syncwarp();
   } else if (FUSED) {
     fused_score<SK>(p, reinterpret_cast<uint8_t*>(scratch), f_hist, f_sh_u64, f_sh_int, tid, warp,
@@ -1785,8 +1772,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const __grid_constant_
 //     a segment ends in its range (a piece).
 // The list is taken where there are more segments than CTAs, and where the longest
 // share of the first way exceeds the mean by more than a quarter and three blocks.
-// 16 x 8 segments of 8..63 blocks: 40.4 us with CTAs of their own, 35.1 with the
-// list; 16 x 8 of 33: 26.8 and 29.8; 3 x 8 of 126: 21.2 and 24.4.
+// 16 x 8 segments of 8..63 blocks take 40.4 us with CTAs of their own and 30.9 with
+// the list; 16 x 8 of 33 blocks 26.8 and 27.9 (the list's CTAs combine twice).
 // A piece that is a whole segment is written out; else its part and, at the CTA's
 // end, a ticket: the CTA that takes a segment's last ticket merges its parts in
 // CTA order.
@@ -1802,7 +1789,7 @@ struct F8Smem {
   static constexpr int kv = 0;
   static constexpr int wst = kv + F8K_STAGES * F8_STAGE_BYTES;
   static constexpr int cum = wst + CONSUMERS * 4 * F8_WST * 4;  // units before segment s
-  static constexpr int own = cum + (MAX_SEGS + 1) * 4;              // F8_SPLITs of them, prefix
+  static constexpr int own = cum + (MAX_SEGS + 1) * 4;          // F8_SPLITs of them, prefix
   static constexpr int info = (own + (MAX_SEGS + 1) * 4 + 15) & ~15;
   static constexpr int bars = info + F8K_STAGES * (int)sizeof(StageInfo);
   static constexpr int bcast = bars + 2 * F8K_STAGES * 8;

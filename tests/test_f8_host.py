@@ -317,6 +317,18 @@ def test_binding_refuses_other_tensors():
     with pytest.raises(kt.KtError):
         kt.kt_apply_rope(r, pos, x.double(), x, stream=0)
     with pytest.raises(kt.KtError):
+        kt.kt_apply_rope(r, pos.long(), x, x, stream=0)
+    with pytest.raises(kt.KtError):
+        kt.kt_apply_rope(r, pos, x, x.bfloat16(), stream=0)
+    with pytest.raises(kt.KtError):
+        kt.kt_append_kv_f8(cache(), params(), x, x, x, cu_tokens=pos.long(), stream=0)
+    with pytest.raises(kt.KtError):
+        kt.kt_append_kv_f8(cache(), params(), x, x, x, new_lens=pos.float(), stream=0)
+    with pytest.raises(kt.KtError):
+        kt.kt_read_kv_f8(cache(), pos, x, None, x, first=pos.long(), stream=0)
+    with pytest.raises(kt.KtError):
+        kt.kt_read_kv_f8(cache(), pos, x.double(), None, x, stream=0)
+    with pytest.raises(kt.KtError):
         kt.kt_append_kv_f8(cache(), params(), x, x[:3], x, stream=0)
     with pytest.raises(kt.KtError):
         kt.kt_read_kv_f8(cache(), pos, None, None, x, stream=0)

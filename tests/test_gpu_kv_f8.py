@@ -482,6 +482,21 @@ def test_long_append_rotates_q_ahead(kt):
         pg.host.append(host16(kr if rope else k), host16(v), counts)
         pg.check()
         assert torch.equal(q_out, want if rope else q.half())
+        # captured: the two launches of a call keep their order with what surrounds them
+        again = Paged(kt, [0] * 4, H, 14, 5)
+        side, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side), torch.cuda.graph(g, stream=side):
+            for _ in range(3):
+                again.lens.zero_()
+                q_out.zero_()
+                kt.kt_append_kv_f8(again.kv, p, k, v, ws, rope=rope, q=q, q_out=q_out,
+                                   cu_tokens=cu)
+        torch.cuda.current_stream().wait_stream(side)
+        for _ in range(3):
+            g.replay()
+        assert torch.equal(again.lens, pg.lens) and torch.equal(again.k_code, pg.k_code)
+        assert torch.equal(q_out, want if rope else q.half())
         assert_status(kt, ws)
 
 
