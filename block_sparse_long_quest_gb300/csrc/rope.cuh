@@ -99,24 +99,31 @@ __device__ __forceinline__ void rope_phases(const kt_rope& r, unsigned long long
 // amplitude * (cos, sin) of a pair at position pos: the top 32 bits of the turn
 // are a quadrant and a signed rest of at most an eighth of a turn, whose sine and
 // cosine are their Taylor polynomials (|x| <= pi/4: the first terms left out are
-// x^11/11! < 1.8e-9 and x^10/10! < 2.5e-8, below half an ulp of either).
+// x^11/11! < 1.8e-9 and x^10/10! < 2.5e-8, below half an ulp of either).  The angle
+// is kept in two parts x + lo, and lo joins the small terms before the one large
+// sum, so that both come out within about an ulp.
 __device__ __forceinline__ float2 rope_cos_sin(unsigned long long phase, float amplitude,
                                                int pos) {
+  constexpr double UNIT = 6.283185307179586 / 4294967296.0;  // 2 pi / 2^32
+  constexpr float C = (float)UNIT, CH = (float)(64.0 * UNIT),
+                  CL = (float)(64.0 * UNIT - (double)CH);
   const unsigned long long turns =
       phase * static_cast<unsigned long long>(static_cast<long long>(pos));
   const uint32_t frac = static_cast<uint32_t>((turns + 0x80000000ull) >> 32);
   const uint32_t quad = (frac + 0x20000000u) >> 30;
-  const float x = static_cast<float>(static_cast<int>(frac - (quad << 30))) *
-                  1.4629180792671596e-9f;  // 2 pi / 2^32
+  const int rest = static_cast<int>(frac - (quad << 30));  // at most 2^29: both parts exact
+  const float fh = static_cast<float>(rest >> 6), fl = static_cast<float>(rest & 63);
+  const float x = fh * CH;
+  const float lo = fmaf(fh, CL, fmaf(fl, C, fmaf(fh, CH, -x)));
   const float z = x * x;
   float s = fmaf(z, 1.0f / 362880.0f, -1.0f / 5040.0f);
   s = fmaf(z, s, 1.0f / 120.0f);
   s = fmaf(z, s, -1.0f / 6.0f);
-  s = fmaf(x * z, s, x);
   float c = fmaf(z, 1.0f / 40320.0f, -1.0f / 720.0f);
   c = fmaf(z, c, 1.0f / 24.0f);
   c = fmaf(z, c, -0.5f);
-  c = fmaf(z, c, 1.0f);
+  s = x + fmaf(x * z, s, lo);
+  c = 1.0f + fmaf(z, c, -lo * x);
   // a quarter turn takes (cos, sin) to (-sin, cos)
   float re = (quad & 1u) ? s : c, im = (quad & 1u) ? c : s;
   re = __uint_as_float(__float_as_uint(re) ^ (((quad + 1u) & 2u) << 30));
