@@ -1770,8 +1770,9 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const __grid_constant_
 //     a segment ends in its range (a piece).
 // The list is taken where there are more segments than CTAs, and where the longest
 // share of the first way exceeds the mean by more than a quarter and three blocks.
-// 16 x 8 segments of 8..63 blocks take 40.4 us with CTAs of their own and 30.9 with
-// the list; 16 x 8 of 33 blocks 26.8 and 27.9 (the list's CTAs combine twice).
+// Own CTAs and list, us: 16 x 8 segments of 8..63 blocks 43.0 and 31.4, 7 x 8 of 71
+// blocks 31.3 and 28.2, 16 x 8 of 33 blocks 28.2 and 31.0, 3 x 8 of 126 blocks 22.7
+// and 24.1.
 // A piece that is a whole segment is written out; else its part and, at the CTA's
 // end, a ticket: the CTA that takes a segment's last ticket merges its parts in
 // CTA order.

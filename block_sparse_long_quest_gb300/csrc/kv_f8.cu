@@ -17,8 +17,8 @@
 // representatives made from the codes in shared memory.  Few q rows ride in the
 // same launch on CTAs of their own (a warp a token), many go ahead in the rotation
 // kernel; one more CTA writes the lengths (in place: the CTA that finishes last
-// does).  A chunk of 16384 tokens of 32 + 8 heads takes 68.6 us, 79% of what its
-// bytes take at the measured copy rate: the q rows run at 6.2 TB/s, and the tiles
+// does).  A chunk of 16384 tokens of 32 + 8 heads takes 69.3 us, its bytes at the
+// measured copy rate 54.6: the q rows run at 6.2 TB/s, and the tiles
 // are bound by their instructions (angles, conversions, representatives).  16
 // decoded tokens take 3.4 us, a chain of dependent loads (length, page, scale).
 #include <cstring>
@@ -33,9 +33,8 @@ constexpr int WARPS = THREADS / 32;
 constexpr int ROWS_PER = BS / (THREADS / ROPE_UNITS);  // row steps of a lane: 4
 constexpr int RED_BYTES = 2 * WARPS * D * 2;           // representatives: partials per warp
 constexpr int TILE_BYTES = BS * D;
-// K heads of an append CTA at most: a 16K-token chunk of 32 + 8 heads takes 77.3 us
-// with one (the angles are computed for each head), 71.4 with two, 68.6 with four,
-// 72.5 with eight (130 CTAs of K are fewer than the SMs)
+// K heads of an append CTA at most: a 16K-token chunk of 32 + 8 heads takes 79.6 us
+// with one (the angles are computed for each head), 72.4 with two, 69.3 with four
 constexpr int APPEND_HEADS = 4;
 
 struct Params {
