@@ -455,7 +455,7 @@ __device__ void append_q(const Params& p, int unit, const unsigned long long* ph
   unit = unit * WARPS + warp;
   const int slices = (p.H_q + p.q_heads - 1) / p.q_heads;
   const int t = unit / slices, h0 = (unit - t * slices) * p.q_heads;
-  if (t >= p.tokens) return;
+  if (t >= p.tokens || (p.cu && (t < p.cu[0] || t >= p.cu[p.B]))) return;
   int pos = 0;
   if (M != ROPE_M_NONE) {
     const int s = p.cu ? row_sequence(p.cu, p.B, t, lane) : t;
@@ -591,7 +591,9 @@ __global__ void __launch_bounds__(THREADS) read_f8_kernel(const __grid_constant_
         row = (int)(pos % BS);
         if ((unsigned)page >= (unsigned)p.P) page = -1;
       }
-      if (page < 0 && blockIdx.y == 0) set_status(p.status, KT_ERR_DEVICE_CHECK);
+      // rows of no sequence (a padded batch) are no error
+      if (page < 0 && t >= c0 && t < c1 && blockIdx.y == 0)
+        set_status(p.status, KT_ERR_DEVICE_CHECK);
     }
     if (tid < rows) {
       sh_page[tid] = page;

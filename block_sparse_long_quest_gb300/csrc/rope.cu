@@ -45,6 +45,7 @@ __global__ void __launch_bounds__(THREADS, 3) rope_kernel(const __grid_constant_
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t = (int)blockIdx.x * WARPS + warp;
   if (t >= p.tokens) return;
+  if (p.cu && (t < p.cu[0] || t >= p.cu[p.B])) return;  // rows of no sequence
   const int h0 = (int)blockIdx.y * p.heads_per, h1 = min(h0 + p.heads_per, p.hq + p.hk);
   int pos = 0;
   if (p.positions) {

@@ -631,8 +631,8 @@ kt_status kt_build_block_reps_f8(const kt_paged_kv_f8* kv, const kt_sparse_param
 
 /*
  * Appends tokens to the sequences, quantising them as they are written, in one
- * launch: row cu_tokens[b] + t of k and v becomes token seq_lens[b] + t of
- * sequence b.
+ * launch (two where many q rows are rotated too): row cu_tokens[b] + t of k and v
+ * becomes token seq_lens[b] + t of sequence b.
  *   rope      : nullable; rotates the K rows (and q) by their token positions.
  *   q, q_out  : nullable; q's rows (p->num_q_heads heads) are rotated (with rope
  *               NULL: only rounded) into q_out, binary16 [tokens][heads][128],
@@ -641,7 +641,10 @@ kt_status kt_build_block_reps_f8(const kt_paged_kv_f8* kv, const kt_sparse_param
  *   cu_tokens : int32 [batch + 1] (device), first row of each sequence and their
  *               total, not decreasing; NULL: one row per sequence (tokens =
  *               batch).
- *   tokens    : rows of q / k / v.  Sequences may get none.
+ *   tokens    : rows of q / k / v.  Sequences may get none.  Rows in front of
+ *               cu_tokens[0] or from cu_tokens[batch] on (a padded batch) belong to
+ *               no sequence: they are not appended, and q_out's are left as they
+ *               were.
  *   new_lens  : int32 [batch] receives the new lengths and kv->seq_lens stays;
  *               NULL or kv->seq_lens itself: that is advanced (through its const
  *               pointer) once the whole call has read it.
@@ -675,7 +678,8 @@ kt_status kt_append_kv_f8(const kt_paged_kv_f8* kv, const kt_sparse_params* p,
  * of sequence b (first NULL: from token 0).  Values are exact in all three types
  * with the scales that kt_append_kv_f8 writes.  A row outside its sequence, or
  * whose page is outside the pool, records KT_ERR_DEVICE_CHECK and is left as it
- * was.  ws as kt_append_kv_f8.
+ * was; one of no sequence (a padded batch) is left as it was.  ws as
+ * kt_append_kv_f8.
  */
 kt_status kt_read_kv_f8(const kt_paged_kv_f8* kv, const int32_t* first, const int32_t* cu_tokens,
                         int32_t tokens, int32_t out_dtype, void* k_out, void* v_out, void* ws,

@@ -344,8 +344,7 @@ def test_append_rotated_equals_rotation_then_append(kt, dtype, layout, rot):
         assert torch.equal(getattr(pg, a), getattr(other, a)), a
     assert torch.equal(torch.nan_to_num(pg.k_scale), torch.nan_to_num(other.k_scale))
     # without a rotation q is only rounded
-    kt.kt_append_kv_f8(pg.kv, p, k, v, ws, q=q, q_out=q2,
-                       cu_tokens=torch.zeros(4, dtype=torch.int32, device="cuda"))
+    kt.kt_append_kv_f8(pg.kv, p, k, v, ws, q=q, q_out=q2, cu_tokens=cu)
     assert torch.equal(q2, q.half())
     assert_status(kt, ws)
 
@@ -427,6 +426,36 @@ def test_long_spans_of_pages_are_checked(kt):
         kt.kt_append_kv_f8(pg.kv, p, x, x, ws, cu_tokens=cu)
         assert pg.lens.tolist() == [0 if bad else n, 3]
         assert_status(kt, ws, kt.KT_ERR_DEVICE_CHECK if bad else kt.KT_OK)
+
+
+@pytest.mark.parametrize("tokens", [40, 4000])  # q beside the tiles, and ahead of them
+@pytest.mark.parametrize("rotated", [False, True])
+def test_append_of_a_padded_batch(kt, tokens, rotated):
+    """Rows in front of the first sequence and behind the last are of no sequence: not appended,
+    and their rows of q_out stay as they were."""
+    H, Hq, lo, hi = 2, 4, 3, tokens - 11
+    rng = torch.Generator().manual_seed(tokens)
+    p = kt.sparse_params(Hq, 1, 1, 2, kt.KT_REP_QUEST, kt.KT_HEAD_SHARED)
+    q, k, v = (rows_of(rng, tokens, h, "f16") for h in (Hq, H, H))
+    rope = kt.rope(64) if rotated else None
+    got = []
+    for a, b in ((0, tokens), (lo, hi)):
+        pg = Paged(kt, [100, 0, 7], H, 34, 17, garbage=False)
+        pg.k_scale.fill_(1.0)
+        pg.v_scale.fill_(1.0)
+        ws = kt.workspace_f8(kt.KT_OP_SPARSE_STEP, pg.kv, p)
+        q_out = torch.full_like(q, 9.0)
+        rows = slice(0, tokens) if a else slice(lo, hi)
+        cu = torch.tensor([0, 1, 1, hi - lo], dtype=torch.int32, device="cuda") + a
+        kt.kt_append_kv_f8(pg.kv, p, k[rows], v[rows], ws, rope=rope, q=q[rows],
+                           q_out=q_out[rows], cu_tokens=cu)
+        assert pg.lens.tolist() == [101, 0, 7 + hi - lo - 1]
+        assert_status(kt, ws)
+        got.append((q_out, pg.k_code, pg.v_code, pg.k_scale, pg.v_scale))
+    for x, y in zip(*got):
+        assert torch.equal(x, y)
+    assert (got[1][0][:lo] == 9.0).all() and (got[1][0][hi:] == 9.0).all()
+    assert (got[1][0][lo:hi] != 9.0).any(-1).all()
 
 
 @pytest.mark.parametrize("B", [33, 257, 1500])
@@ -568,9 +597,10 @@ def test_read_outside_is_left_alone(kt):
     touched = read([-4, (1 << 31) - 5])
     assert touched.tolist() == [False] * 4 + [True] * 6 + [False] * 10
     assert_status(kt, ws, kt.KT_ERR_DEVICE_CHECK)
+    # rows of no sequence are no error
     touched = read([0, 0], torch.tensor([2, 4, 15], dtype=torch.int32, device="cuda"))
     assert touched.tolist() == [False] * 2 + [True] * 13 + [False] * 5
-    assert_status(kt, ws, kt.KT_ERR_DEVICE_CHECK)
+    assert_status(kt, ws)
     pg.table[1, 0] = 77
     touched = read([0, 120])
     assert touched.tolist() == [True] * 10 + [False] * 8 + [True] * 2
