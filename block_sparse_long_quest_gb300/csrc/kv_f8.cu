@@ -17,10 +17,11 @@
 // representatives made from the codes in shared memory.  Few q rows ride in the
 // same launch on CTAs of their own (a warp a token), many go ahead in the rotation
 // kernel; one more CTA writes the lengths (in place: the CTA that finishes last
-// does).  A chunk of 16384 tokens of 32 + 8 heads takes 69.3 us, its bytes at the
+// does).  A chunk of 16384 tokens of 32 + 8 heads takes 68.9 us, its bytes at the
 // measured copy rate 54.6: the q rows run at 6.2 TB/s, and the tiles
-// are bound by their instructions (angles, conversions, representatives).  16
-// decoded tokens take 3.4 us, a chain of dependent loads (length, page, scale).
+// wait: for loads between barriers, and for instructions (half the issue slots at
+// 16 warps an SM: angles, conversions, representatives).  16
+// decoded tokens take 3.3 us, a chain of dependent loads (length, page, scale).
 #include <cstring>
 
 #include "rope.cuh"
@@ -33,8 +34,8 @@ constexpr int WARPS = THREADS / 32;
 constexpr int ROWS_PER = BS / (THREADS / ROPE_UNITS);  // row steps of a lane: 4
 constexpr int RED_BYTES = 2 * WARPS * D * 2;           // representatives: partials per warp
 constexpr int TILE_BYTES = BS * D;
-// K heads of an append CTA at most: a 16K-token chunk of 32 + 8 heads takes 79.6 us
-// with one (the angles are computed for each head), 72.4 with two, 69.3 with four
+// K heads of an append CTA at most: a 16K-token chunk of 32 + 8 heads takes 78.6 us
+// with one (the angles are computed for each head), 72.1 with two, 68.9 with four
 constexpr int APPEND_HEADS = 4;
 
 struct Params {
@@ -93,18 +94,20 @@ __device__ __forceinline__ bool scale_ok(float s) {
 }
 
 // Eight binary16 (four words) / s, as codes.
-__device__ __forceinline__ uint2 code8(const uint32_t (&h)[4], __half2 inv, bool top) {
+__device__ __forceinline__ uint2 code8(const uint32_t (&h)[4], __half2 inv) {
   uint32_t y[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    __half2 v = __hmul2(as_h2(h[i]), inv);  // exact where the code is not zero
-    if (top) {
-      const __half2 m = __float2half2_rn(240.0f);
-      v = __hmax2_nan(__hmin2_nan(v, m), __hneg2(m));
-    }
-    y[i] = as_u32(v);
-  }
+  for (int i = 0; i < 4; ++i) y[i] = as_u32(__hmul2(as_h2(h[i]), inv));  // exact but for codes of 0
   return make_uint2(h4_to_f8(y[0], y[1]), h4_to_f8(y[2], y[3]));
+}
+
+// The values that a scale of 2^8 holds: up to 240 of it.  Ahead of the coding, not
+// inside it: a branch there for every eight values cost 1.1 us of a 16K-token chunk.
+__device__ __forceinline__ void clamp8(uint32_t (&h)[4]) {
+  const __half2 m = __float2half2_rn(61440.0f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    h[i] = as_u32(__hmax2_nan(__hmin2_nan(as_h2(h[i]), m), __hneg2(m)));
 }
 
 // Codes of an old scale under a new one: round(code * ratio), ratio a power of two.
@@ -118,6 +121,13 @@ __device__ __forceinline__ uint32_t recode4(uint32_t c, float ratio) {
     h[i] = as_u32(__floats2half2_rn(f.x * ratio, f.y * ratio));
   }
   return h4_to_f8(h[0], h[1]);
+}
+
+// acc + h in binary32, in one instruction.
+__device__ __forceinline__ float add_f16(float acc, uint16_t h) {
+  float d;
+  asm("add.rn.f32.f16 %0, %1, %2;" : "=f"(d) : "h"(h), "f"(acc));
+  return d;
 }
 
 // A tile of codes in shared memory: word w (four channels) of row r.  Odd rows
@@ -149,12 +159,11 @@ __device__ void tile_reps(const uint8_t* tile, float s, int rep, int R, int fix_
 #pragma unroll 4
     for (int r = r0; r < r0 + BS / WARPS; ++r) {
       const uint32_t c = words[tile_word(r, lane)];
-      const float2 a = __half22float2(as_h2(f8x2_lo(c)));
-      const float2 b = __half22float2(as_h2(f8x2_hi(c)));
-      acc[0] += a.x;
-      acc[1] += a.y;
-      acc[2] += b.x;
-      acc[3] += b.y;
+      const uint32_t a = f8x2_lo(c), b = f8x2_hi(c);
+      acc[0] = add_f16(acc[0], (uint16_t)a);
+      acc[1] = add_f16(acc[1], (uint16_t)(a >> 16));
+      acc[2] = add_f16(acc[2], (uint16_t)b);
+      acc[3] = add_f16(acc[3], (uint16_t)(b >> 16));
     }
     int4* part = reinterpret_cast<int4*>(red);
     part[warp * 32 + lane] = make_int4(
@@ -214,6 +223,27 @@ __device__ bool find_tile(const Params& p, int tile, int* sh, int tid, int* b_ou
     return a_out->blocks > 0;
   }
   const int warp = tid >> 5, lane = tid & 31;
+  if (p.B <= 32) {  // every warp by itself: no barrier (16.3 -> 15.9 us, 21006 rows of 7 sequences)
+    Span a;
+    a.n = a.m = a.c0 = a.blocks = 0;
+    if (lane < p.B) a = seq_span(p, lane, true);
+    int incl = a.blocks;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const unsigned int in = __ballot_sync(0xffffffffu, tile < incl);
+    if (!in) return false;
+    const int s = __ffs(in) - 1;
+    *b_out = s;
+    a_out->n = __shfl_sync(0xffffffffu, a.n, s);
+    a_out->m = __shfl_sync(0xffffffffu, a.m, s);
+    a_out->c0 = __shfl_sync(0xffffffffu, a.c0, s);
+    *j_out = a_out->n / BS + tile - __shfl_sync(0xffffffffu, incl - a.blocks, s);
+    a_out->blocks = 1;
+    return true;
+  }
   int before = 0;
   for (int s0 = 0; s0 < p.B; s0 += THREADS) {
     const int s = s0 + tid;
@@ -410,12 +440,18 @@ __device__ void append_tile(const Params& p, int cta, const unsigned long long* 
       }
     }
     const __half2 inv = __float2half2_rn(1.0f / s);
-    const bool top = s == 256.0f;
+    if (s == 256.0f) {
+#pragma unroll
+      for (int i = 0; i < ROWS_PER; ++i) {
+        clamp8(xa[i]);
+        clamp8(xb[i]);
+      }
+    }
 #pragma unroll
     for (int i = 0; i < ROWS_PER; ++i) {
       const int r = (tid >> 3) + i * (THREADS / ROPE_UNITS);
       if (r >= r0 && r < r1) {
-        const uint2 ca = code8(xa[i], inv, top), cb = code8(xb[i], inv, top);
+        const uint2 ca = code8(xa[i], inv), cb = code8(xb[i], inv);
         *reinterpret_cast<uint2*>(dst + r * D + 8 * va) = ca;
         *reinterpret_cast<uint2*>(dst + r * D + 8 * vb) = cb;
         if (complete) {

@@ -458,7 +458,7 @@ def test_append_of_a_padded_batch(kt, tokens, rotated):
     assert (got[1][0][lo:hi] != 9.0).any(-1).all()
 
 
-@pytest.mark.parametrize("B", [33, 257, 1500])
+@pytest.mark.parametrize("B", [32, 33, 257, 1500])
 def test_many_sequences(kt, B):
     """Ragged rows of many sequences, most of them short or empty: appended, then read back."""
     rng = np.random.default_rng(B)
