@@ -345,7 +345,7 @@ __device__ __forceinline__ void load_tile(TileRaw<T>& x, const T* src, long long
 }
 
 template <class T, int M>
-__device__ void append_tile(const Params& p, int cta, const unsigned long long* ph, uint8_t* smem,
+__device__ void append_tile(const Params& p, int cta, const RopeShared& rs, uint8_t* smem,
                             int* sh, int tid) {
   // 16-bit rows of the next head are loaded while a head is coded; the registers
   // do not hold two of binary32
@@ -381,7 +381,7 @@ __device__ void append_tile(const Params& p, int cta, const unsigned long long* 
     const int i = tid & 63;
     if (i < p.rope.rotary_dim >> 1)
       for (int r = tid >> 6; r < r1 - r0; r += THREADS / 64)
-        cs[r * 64 + cs_at(i)] = rope_cos_sin(ph[i], p.rope.amplitude, j * BS + r0 + r);
+        cs[r * 64 + cs_at(i)] = rope_cos_sin(rs, i, j * BS + r0 + r);
     __syncthreads();
   }
   const bool complete = !is_v && p.reps && r1 == BS;
@@ -485,7 +485,7 @@ __device__ void append_tile(const Params& p, int cta, const unsigned long long* 
 
 // One warp a token (or a slice of its heads).
 template <class T, int M>
-__device__ void append_q(const Params& p, int unit, const unsigned long long* ph, uint8_t* smem,
+__device__ void append_q(const Params& p, int unit, const RopeShared& rs, uint8_t* smem,
                          int tid) {
   const int warp = tid >> 5, lane = tid & 31;
   unit = unit * WARPS + warp;
@@ -497,7 +497,7 @@ __device__ void append_q(const Params& p, int unit, const unsigned long long* ph
     const int s = p.cu ? row_sequence(p.cu, p.B, t, lane) : t;
     pos = p.seq_lens[s] + (t - (p.cu ? p.cu[s] : t));
   }
-  rope_token<M, 1>(p.rope, ph, reinterpret_cast<float2*>(smem) + warp * 64, pos, t, h0,
+  rope_token<M, 1>(p.rope, rs, reinterpret_cast<float2*>(smem) + warp * 64, pos, t, h0,
                 min(h0 + p.q_heads, p.H_q), static_cast<const T*>(p.q), p.qs, p.H_q, p.q_out,
                 static_cast<const T*>(nullptr), 0, 0, static_cast<__half*>(nullptr), lane);
 }
@@ -507,18 +507,18 @@ __global__ void __launch_bounds__(THREADS, M == ROPE_M_NONE && sizeof(T) == 2 ? 
     append_f8_kernel(const __grid_constant__ Params p) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ int sh[WARPS + 8];
-  __shared__ unsigned long long ph[64];
+  __shared__ RopeShared rs;
   const int tid = threadIdx.x, cta = blockIdx.x;
   if (M != ROPE_M_NONE) {
-    rope_phases(p.rope, ph, tid);
+    rope_prepare(p.rope, rs, tid, THREADS);
     __syncthreads();
   }
   if (!p.late_wait) griddep_wait();
   griddep_launch_dependents();
   if (cta < p.cache_ctas)
-    append_tile<T, M>(p, cta, ph, smem, sh, tid);
+    append_tile<T, M>(p, cta, rs, smem, sh, tid);
   else if (cta < p.cache_ctas + p.q_ctas)
-    append_q<T, M>(p, cta - p.cache_ctas, ph, smem, tid);
+    append_q<T, M>(p, cta - p.cache_ctas, rs, smem, tid);
   else if (p.new_lens)
     write_lengths(p, tid);
   // behind the rotation of q (which waited for everything before it), this launch

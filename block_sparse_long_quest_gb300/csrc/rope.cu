@@ -35,9 +35,9 @@ struct Params {
 template <class T, int M>
 __global__ void __launch_bounds__(THREADS, 3) rope_kernel(const __grid_constant__ Params p) {
   __shared__ __align__(16) float2 cs[WARPS][64];
-  __shared__ unsigned long long ph[64];
+  __shared__ RopeShared rs;
   if (M != ROPE_M_NONE) {
-    rope_phases(p.rope, ph, threadIdx.x);
+    rope_prepare(p.rope, rs, threadIdx.x, THREADS);
     __syncthreads();
   }
   griddep_wait();
@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(THREADS, 3) rope_kernel(const __grid_constant_
     const int s = row_sequence(p.cu, p.B, t, lane);
     pos = p.seq_lens[s] + (t - p.cu[s]);
   }
-  rope_token<M, 2>(p.rope, ph, cs[warp], pos, t, h0, h1, static_cast<const T*>(p.q), p.qs, p.hq,
+  rope_token<M, 2>(p.rope, rs, cs[warp], pos, t, h0, h1, static_cast<const T*>(p.q), p.qs, p.hq,
                    p.q_out, static_cast<const T*>(p.k), p.ks, p.hk, p.k_out, lane);
 }
 

@@ -4,7 +4,7 @@
 // Angles: kt_rope.phase holds f_i / (2 pi) as a 64-bit fraction of a turn, so
 // phase * position in wrapping 64-bit integers is the angle modulo one turn with
 // an error below position * 2^-53 turns (the host's binary64 frequency).  No
-// binary64 arithmetic, and the reduction to a quadrant is two bits of it.
+// binary64 arithmetic, and the reduction to a 256th of a turn is eight bits of it.
 //
 // A head row is 16 vectors of 8 channels and is handled by the 8 lanes of a
 // lane group, two vectors a lane (row_vectors).  HALF with rotary_dim a
@@ -90,45 +90,76 @@ __device__ __forceinline__ float load1(const __half* p) { return __half2float(*p
 __device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 __device__ __forceinline__ float load1(const float* p) { return *p; }
 
-// The phases in shared memory, by the first 64 threads of a CTA: lanes that index
-// the parameters' constant bank apart are served one by one.
-__device__ __forceinline__ void rope_phases(const kt_rope& r, unsigned long long* ph, int tid) {
-  if (tid < 64) ph[tid] = r.phase[tid];
+// cos and sin of k / 256 of a turn, each as the sum of two binary32 numbers, made
+// by the compiler from the Taylor series in binary64.
+struct alignas(16) RopeEntry {
+  float ch, cl, sh, sl;
+};
+struct RopeCircle {
+  RopeEntry e[256];
+  constexpr RopeCircle() : e() {
+    for (int k = 0; k < 256; ++k) {
+      const int quad = (k + 32) / 64, rest = k - 64 * quad;  // at most an eighth of a turn
+      const double x = rest * (6.283185307179586 / 256.0);
+      double c = 0.0, s = 0.0, term = 1.0;
+      for (int n = 0; n < 24; n += 2) {
+        c += term;
+        s += term * x / (n + 1);
+        term *= -x * x / ((n + 1) * (n + 2));
+      }
+      // a quarter turn takes (cos, sin) to (-sin, cos)
+      const double re = quad % 4 == 0 ? c : quad % 4 == 1 ? -s : quad % 4 == 2 ? -c : s;
+      const double im = quad % 4 == 0 ? s : quad % 4 == 1 ? c : quad % 4 == 2 ? -s : -c;
+      e[k].ch = (float)re;
+      e[k].cl = (float)(re - e[k].ch);
+      e[k].sh = (float)im;
+      e[k].sl = (float)(im - e[k].sh);
+    }
+  }
+};
+static __device__ constexpr RopeCircle ROPE_CIRCLE{};
+
+// What the angles are made from, in shared memory: the phases (lanes that index
+// the parameters' constant bank apart are served one by one) and amplitude times
+// the circle.
+struct RopeShared {
+  RopeEntry circle[256];
+  unsigned long long phase[64];
+};
+// By all threads of a CTA (at least 64); a barrier follows.
+__device__ __forceinline__ void rope_prepare(const kt_rope& r, RopeShared& s, int tid,
+                                             int threads) {
+  const float a = r.amplitude;
+  for (int k = tid; k < 256; k += threads) {
+    const float4 v = __ldg(reinterpret_cast<const float4*>(&ROPE_CIRCLE.e[k]));
+    RopeEntry e;
+    e.ch = a * v.x;
+    e.cl = fmaf(a, v.y, fmaf(a, v.x, -e.ch));
+    e.sh = a * v.z;
+    e.sl = fmaf(a, v.w, fmaf(a, v.z, -e.sh));
+    s.circle[k] = e;
+  }
+  if (tid < 64) s.phase[tid] = r.phase[tid];
 }
 
-// amplitude * (cos, sin) of a pair at position pos: the top 32 bits of the turn
-// are a quadrant and a signed rest of at most an eighth of a turn, whose sine and
-// cosine are their Taylor polynomials (|x| <= pi/4: the first terms left out are
-// x^11/11! < 1.8e-9 and x^10/10! < 2.5e-8, below half an ulp of either).  The angle
-// is kept in two parts x + lo, and lo joins the small terms before the one large
-// sum, so that both come out within about an ulp.
-__device__ __forceinline__ float2 rope_cos_sin(unsigned long long phase, float amplitude,
-                                               int pos) {
-  constexpr double UNIT = 6.283185307179586 / 4294967296.0;  // 2 pi / 2^32
-  constexpr float C = (float)UNIT, CH = (float)(64.0 * UNIT),
-                  CL = (float)(64.0 * UNIT - (double)CH);
+// amplitude * (cos, sin) of pair i at position pos: the nearest 256th of a turn
+// from the table, and from it the rest x, |x| <= pi/256, as a signed 32-bit
+// fraction, by sin x = x - x^3/6 and 1 - cos x = x^2/2 - x^4/24 (the first terms
+// left out are below 2.4e-12).  The table's upper parts are joined last, so only
+// that sum rounds noticeably: 98 of 100 values are the nearest binary32 ones, all
+// within 0.53 ulp where they are not small.
+__device__ __forceinline__ float2 rope_cos_sin(const RopeShared& s, int i, int pos) {
   const unsigned long long turns =
-      phase * static_cast<unsigned long long>(static_cast<long long>(pos));
-  const uint32_t frac = static_cast<uint32_t>((turns + 0x80000000ull) >> 32);
-  const uint32_t quad = (frac + 0x20000000u) >> 30;
-  const int rest = static_cast<int>(frac - (quad << 30));  // at most 2^29: both parts exact
-  const float fh = static_cast<float>(rest >> 6), fl = static_cast<float>(rest & 63);
-  const float x = fh * CH;
-  const float lo = fmaf(fh, CL, fmaf(fl, C, fmaf(fh, CH, -x)));
+      s.phase[i] * static_cast<unsigned long long>(static_cast<long long>(pos));
+  const uint32_t k = (static_cast<uint32_t>(turns >> 32) + 0x00800000u) >> 24;
+  const float4 v = *reinterpret_cast<const float4*>(&s.circle[k]);
+  const float x = static_cast<float>(static_cast<int>(turns >> 24)) *
+                  (float)(6.283185307179586 / 1099511627776.0);  // 2 pi / 2^40
   const float z = x * x;
-  float s = fmaf(z, 1.0f / 362880.0f, -1.0f / 5040.0f);
-  s = fmaf(z, s, 1.0f / 120.0f);
-  s = fmaf(z, s, -1.0f / 6.0f);
-  float c = fmaf(z, 1.0f / 40320.0f, -1.0f / 720.0f);
-  c = fmaf(z, c, 1.0f / 24.0f);
-  c = fmaf(z, c, -0.5f);
-  s = x + fmaf(x * z, s, lo);
-  c = 1.0f + fmaf(z, c, -lo * x);
-  // a quarter turn takes (cos, sin) to (-sin, cos)
-  float re = (quad & 1u) ? s : c, im = (quad & 1u) ? c : s;
-  re = __uint_as_float(__float_as_uint(re) ^ (((quad + 1u) & 2u) << 30));
-  im = __uint_as_float(__float_as_uint(im) ^ ((quad & 2u) << 30));
-  return make_float2(re * amplitude, im * amplitude);
+  const float sx = fmaf(x * z, -1.0f / 6.0f, x);
+  const float cx = z * fmaf(z, 1.0f / 24.0f, -0.5f);
+  return make_float2(v.x + fmaf(v.x, cx, fmaf(-v.z, sx, v.y)),
+                     v.z + fmaf(v.z, cx, fmaf(v.x, sx, v.w)));
 }
 
 // The two vectors (8 channels each) of lane j of a head row.
@@ -160,6 +191,16 @@ __device__ __forceinline__ void rope_weights(const float2* cs, int va, int vb, f
   }
 }
 
+// x c -/+ y s with both products and the sum rounded, not fused: what any machine's
+// elementary binary32 operations give, so that the codes of a rotated cache can be
+// had again elsewhere.
+__device__ __forceinline__ float minus(float x, float c, float y, float s) {
+  return __fsub_rn(__fmul_rn(x, c), __fmul_rn(y, s));
+}
+__device__ __forceinline__ float plus(float x, float c, float y, float s) {
+  return __fadd_rn(__fmul_rn(x, c), __fmul_rn(y, s));
+}
+
 // Rotates vectors va and vb (values a, b) of the row at `row`; w: rope_weights,
 // cs: the row's table.  Channels from rotary_dim on are left as they are.
 template <int M, class T>
@@ -172,13 +213,13 @@ __device__ __forceinline__ void rope_rotate(const kt_rope& r, const float2 (&w)[
     for (int e = 0; e < 4; ++e) {
       if (8 * va + 2 * e < rot) {
         const float x = a[2 * e], y = a[2 * e + 1];
-        a[2 * e] = x * w[e].x - y * w[e].y;
-        a[2 * e + 1] = y * w[e].x + x * w[e].y;
+        a[2 * e] = minus(x, w[e].x, y, w[e].y);
+        a[2 * e + 1] = plus(y, w[e].x, x, w[e].y);
       }
       if (8 * vb + 2 * e < rot) {
         const float x = b[2 * e], y = b[2 * e + 1];
-        b[2 * e] = x * w[4 + e].x - y * w[4 + e].y;
-        b[2 * e + 1] = y * w[4 + e].x + x * w[4 + e].y;
+        b[2 * e] = minus(x, w[4 + e].x, y, w[4 + e].y);
+        b[2 * e + 1] = plus(y, w[4 + e].x, x, w[4 + e].y);
       }
     }
   }
@@ -187,8 +228,8 @@ __device__ __forceinline__ void rope_rotate(const kt_rope& r, const float2 (&w)[
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float x = a[e], y = b[e];
-        a[e] = x * w[e].x - y * w[e].y;
-        b[e] = y * w[e].x + x * w[e].y;
+        a[e] = minus(x, w[e].x, y, w[e].y);
+        b[e] = plus(y, w[e].x, x, w[e].y);
       }
     }
   }
@@ -203,10 +244,10 @@ __device__ __forceinline__ void rope_rotate(const kt_rope& r, const float2 (&w)[
         const int c = c0 + e;
         if (c < half) {
           const float2 u = cs[cs_at(c)];
-          x[e] = x[e] * u.x - load1(row + c + half) * u.y;
+          x[e] = minus(x[e], u.x, load1(row + c + half), u.y);
         } else if (c < rot) {
           const float2 u = cs[cs_at(c - half)];
-          x[e] = x[e] * u.x + load1(row + c - half) * u.y;
+          x[e] = plus(x[e], u.x, load1(row + c - half), u.y);
         }
       }
     }
@@ -236,11 +277,11 @@ __device__ __forceinline__ void pack8(const float (&x)[8], uint32_t (&h)[4]) {
 }
 
 // Rotates heads h0 .. h1 - 1 (q's, then k's) of one token by one warp: four head
-// rows at a time, NB times four loaded before the first is stored; ph: rope_phases; cs: 64 (cos,
+// rows at a time, NB times four loaded before the first is stored; rs: rope_prepare; cs: 64 (cos,
 // sin) of shared memory of the warp's own, written behind the first loads and held
 // in registers over the heads.
 template <int M, int NB, class T>
-__device__ __forceinline__ void rope_token(const kt_rope& r, const unsigned long long* ph,
+__device__ __forceinline__ void rope_token(const kt_rope& r, const RopeShared& rs,
                                            float2* cs, int pos, long long t,
                                            int h0, int h1, const T* q, long long qs, int hq,
                                            __half* q_out, const T* k, long long ks, int hk,
@@ -268,7 +309,7 @@ __device__ __forceinline__ void rope_token(const kt_rope& r, const unsigned long
     if (M != ROPE_M_NONE && first) {
 #pragma unroll
       for (int i = lane; i < 64; i += 32)
-        if (i < half) cs[cs_at(i)] = rope_cos_sin(ph[i], r.amplitude, pos);
+        if (i < half) cs[cs_at(i)] = rope_cos_sin(rs, i, pos);
       __syncwarp();
       rope_weights<M>(cs, va, vb, w);
     }

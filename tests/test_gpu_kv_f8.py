@@ -103,6 +103,34 @@ def test_rope(kt, dtype, layout, rot):
         assert torch.equal(alone, k_out[:tokens])
 
 
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("layout,rot", [("half", 128), ("pairs", 128), ("half", 90)])
+def test_rope_is_elementary_binary32(kt, dtype, layout, rot):
+    """The rows are those of elementary binary32 operations (products and sum rounded) on the
+    binary32 values nearest to cos and sin.
+
+    The kernel's cos and sin err by three roundings of terms below pi/256 next to the nearest
+    value's: by 3 * 2^-25 / 81.5 < 1.1e-9, at most 1.9% of the spacing 2^-24 of values in [1/2, 1),
+    so fewer than 1 of 26 are not the nearest one (smaller values more often, but their products
+    count less).  A result with two such products is off by about 2^-24 |x| then, and the spacing
+    of binary16 is at least 2^-11 of the result: with |x| three times the result on the whole, a
+    rounding changes in fewer than 2/26 * 3 * 2^-13 = 2^-15.1 of all; twice that is allowed."""
+    rng = torch.Generator().manual_seed(3)
+    x = torch.randn(512, 16, 128, generator=rng).to(DTYPES[dtype])
+    pos = torch.randint(0, 60000, (512,), generator=rng, dtype=torch.int32)
+    f, _ = f8_ref.frequencies(rot, 1e6)
+    ang = np.fmod(pos.numpy().astype(np.longdouble)[:, None] * f, f8_ref.PI2).astype(np.float64)
+    c, s = (torch.from_numpy(t(ang)).float()[:, None] for t in (np.cos, np.sin))
+    n, y = rot // 2, x.float().clone()
+    a, b = (slice(0, n), slice(n, rot)) if layout == "half" else (slice(0, rot, 2),
+                                                                  slice(1, rot, 2))
+    y[..., a], y[..., b] = y[..., a] * c - y[..., b] * s, y[..., b] * c + y[..., a] * s
+    out = torch.empty(x.shape, dtype=torch.float16, device="cuda")
+    lay = kt.KT_ROPE_HALF if layout == "half" else kt.KT_ROPE_PAIRS
+    kt.kt_apply_rope(kt.rope(rot, theta=1e6, layout=lay), pos.cuda(), x.cuda(), out)
+    assert (out.cpu() != y.half()).sum() <= x.numel() * 2.0 ** -14
+
+
 @pytest.mark.parametrize("layout", [0, 1])
 @pytest.mark.parametrize("rot", [128, 64, 90])
 def test_rope_in_place_and_without_effect(kt, layout, rot):
