@@ -17,11 +17,11 @@
 // representatives made from the codes in shared memory.  Few q rows ride in the
 // same launch on CTAs of their own (a warp a token), many go ahead in the rotation
 // kernel; one more CTA writes the lengths (in place: the CTA that finishes last
-// does).  A chunk of 16384 tokens of 32 + 8 heads takes 68.9 us, its bytes at the
+// does).  A chunk of 16384 tokens of 32 + 8 heads takes 68.6 us, its bytes at the
 // measured copy rate 54.6: the q rows run at 6.2 TB/s, and the tiles
 // wait: for loads between barriers, and for instructions (half the issue slots at
 // 16 warps an SM: angles, conversions, representatives).  16
-// decoded tokens take 3.3 us, a chain of dependent loads (length, page, scale).
+// decoded tokens take 3.2 us, a chain of dependent loads (length, page, scale).
 #include <cstring>
 
 #include "rope.cuh"
@@ -34,8 +34,8 @@ constexpr int WARPS = THREADS / 32;
 constexpr int ROWS_PER = BS / (THREADS / ROPE_UNITS);  // row steps of a lane: 4
 constexpr int RED_BYTES = 2 * WARPS * D * 2;           // representatives: partials per warp
 constexpr int TILE_BYTES = BS * D;
-// K heads of an append CTA at most: a 16K-token chunk of 32 + 8 heads takes 78.6 us
-// with one (the angles are computed for each head), 72.1 with two, 68.9 with four
+// K heads of an append CTA at most: a 16K-token chunk of 32 + 8 heads takes 81.2 us
+// with one (the angles are computed for each head), 72.9 with two, 68.6 with four
 constexpr int APPEND_HEADS = 4;
 
 struct Params {

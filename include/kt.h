@@ -589,8 +589,8 @@ typedef struct {
 
 /*
  * Rotates the rows of `tokens` tokens: q into q_out and k into k_out, binary16
- * [tokens][heads][128] contiguous, each value computed in binary32 and rounded
- * once.  positions: int32 [tokens] (device).  Either of q / k may be NULL (with
+ * [tokens][heads][128] contiguous: the two products and their sum in binary32
+ * (cos and sin next to exact there), rounded once more to binary16.  positions: int32 [tokens] (device).  Either of q / k may be NULL (with
  * its output); both have one type.  An output may be its own binary16 input
  * where that is contiguous (stride = heads * 128); any other overlap of an
  * output with an input or with the other output is INVALID_ARG.  tokens = 0 does
