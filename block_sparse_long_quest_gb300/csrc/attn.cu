@@ -1765,9 +1765,11 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kernel(const __grid_constant_
 //   - CTAs of its own for every segment, one for each F8_SPLIT of its blocks where
 //     there are enough (two CTAs of a segment meet through global memory, which
 //     takes as long as about eight blocks);
-//   - one list: CTA c takes the units [c W / n, (c + 1) W / n), whatever segments
-//     they belong to, which costs a CTA a combination of its warps' states wherever
-//     a segment ends in its range (a piece).
+//   - one list of all W units over n = min(CTAs, W) CTAs, so that each has one (a
+//     segment waits for every CTA between the holders of its first and last unit):
+//     CTA c takes the units [c W / n, (c + 1) W / n), whatever segments they belong
+//     to, which costs a CTA a combination of its warps' states wherever a segment
+//     ends in its range (a piece).
 // The list is taken where there are more segments than CTAs, and where the longest
 // share of the first way exceeds the mean by more than a quarter and three blocks.
 // Own CTAs and list, us: 16 x 8 segments of 8..63 blocks 43.0 and 31.4, 7 x 8 of 71
@@ -1806,7 +1808,8 @@ struct F8Piece {  // units 0: none
 struct F8Range {
   const int* cum;
   long long x0, x1, W;
-  int n, own_first, own_n;  // n: CTAs that share the list (0: segments have their own)
+  // n: CTAs that share the list, at most W of them (0: segments have their own)
+  int n, own_first, own_n;
 
   // the CTA that holds unit x: the last c with c W / n <= x
   __device__ __forceinline__ int owner(long long x) const {
@@ -2093,9 +2096,11 @@ __global__ void __launch_bounds__(THREADS, 1) attn_f8_kernel(const __grid_consta
       }
     }
   } else {
-    rg.n = grid;
-    rg.x0 = cta * rg.W / grid;
-    rg.x1 = (cta + 1) * rg.W / grid;
+    rg.n = max(1, min(grid, carry_u));
+    if (cta < rg.n) {
+      rg.x0 = cta * rg.W / rg.n;
+      rg.x1 = (cta + 1) * rg.W / rg.n;
+    }
     int lo = 0, hi = S - 1;  // the last s with cum[s] <= x0
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;

@@ -707,6 +707,108 @@ def test_dense_attention_shares_the_blocks_out(kt, G, H, lens):
     assert_status(kt, ws)
 
 
+def segment_counters(ws, segments):
+    """The counters of the segments' parts: behind the workspace's header, zero between calls."""
+    return ws[256:256 + 4 * segments]
+
+
+# more segments than SMs, most of them empty: (KV heads, lengths of 32 or more sequences)
+PADDED = [
+    (8, [200] + [0] * 31),
+    (8, [0] * 31 + [1000]),
+    (8, [300, 300] + [0] * 30),
+    (8, [0, 200, 0, 0, 641] + [0] * 25 + [200, 1]),
+    (4, [200] + [0] * 39),
+    (8, [0] * 13 + [1000, 0, 1000, 257] + [0] * 14 + [1024]),
+    (1, [0] * 100 + [5] + [0] * 99),
+]
+
+
+@pytest.mark.parametrize("ctas", [0, 40, 7])
+@pytest.mark.parametrize("H,lens", PADDED)
+def test_padded_batches_of_more_segments_than_ctas(kt, H, lens, ctas):
+    """Few live sequences in a batch of many slots: fewer blocks in all than CTAs.  Every segment is
+    written, the workspace's counters are back at zero, and calls of other lengths on the same
+    workspace, and the binary16 dense call, are right too."""
+    G = 4
+    B = len(lens)
+    pg = filled(kt, lens, H, 41)
+    q = torch.randn(B, H * G, 128).half().cuda()
+    p = kt.sparse_params(H * G, 1, 1, 3, kt.KT_REP_QUEST, kt.KT_HEAD_SEPARATE)
+    ws = kt.workspace_f8(kt.KT_OP_SPARSE_STEP, pg.kv, p)
+    every = lambda b, h: range(-(-int(pg.host.lens[b]) // 128))  # noqa: E731
+    out = torch.empty(B, H * G, 128, device="cuda")
+
+    def run(call, blocks_of):
+        out.fill_(float("nan"))
+        kt.kt_set_max_ctas(ctas)
+        call()
+        kt.kt_set_max_ctas(0)
+        check_attention(pg, q, out, blocks_of, G)
+        assert (segment_counters(ws, B * H) == 0).all()
+
+    sel = torch.full((B, H, 3), -1, dtype=torch.int32, device="cuda")
+    cnt = torch.zeros(B, H, dtype=torch.int32, device="cuda")
+    rng = np.random.default_rng(5)
+    for b, n in enumerate(lens):  # any choice of the Context blocks: 1 .. nb - 2
+        nb = -(-n // 128)
+        for h in range(H):
+            ids = np.sort(rng.permutation(max(0, nb - 2))[:rng.integers(0, 4)]) + 1
+            sel[b, h, :len(ids)] = torch.from_numpy(ids.astype(np.int32))
+            cnt[b, h] = len(ids)
+    hs, hc = sel.cpu(), cnt.cpu()
+    picked = lambda b, h: chosen(kt, pg, hs, hc, p, b, h)  # noqa: E731
+    dense = lambda: kt.kt_dense_decode_attn_f8(q, pg.kv, H * G, SCALE, out, ws)  # noqa: E731
+    sparse = lambda: kt.kt_sparse_decode_attn_f8(q, pg.kv, p, sel, cnt, out, ws)  # noqa: E731
+    for _ in range(2):
+        run(dense, every)
+        run(sparse, picked)
+    kv16, _k, _v = paged16(kt, pg)
+    out.fill_(float("nan"))
+    kt.kt_dense_decode_attn(q, kv16, H * G, SCALE, out, ws)
+    check_attention(pg, q, out, every, G)
+    # the lengths one block shorter
+    pg.lens.copy_(torch.clamp(pg.lens - 128, min=0))
+    pg.host.lens = pg.lens.cpu().numpy()
+    run(dense, every)
+    assert_status(kt, ws)
+
+
+@pytest.mark.parametrize("live", [{0: 300}, {7: 1000, 30: 200}, {3: 700, 4: 1024, 17: 1, 31: 257}])
+@pytest.mark.parametrize("mode", [0, 1])
+def test_padded_step_in_two_launches(kt, mode, live):
+    """The step and the layer call over a batch of 32 slots with few live sequences."""
+    H, G, B = 8, 4, 32
+    lens = [live.get(b, 0) for b in range(B)]
+    p = kt.sparse_params(H * G, 1, 1, 3, kt.KT_REP_QUEST, mode)
+    pg = filled(kt, lens, H, 43, params=p)
+    kv16 = kt.PagedKV(pg.k_code.data_ptr(), pg.v_code.data_ptr(), pg.table.data_ptr(),
+                      pg.lens.data_ptr(), B, H, 128, 128, pg.table.shape[1], pg.k_code.shape[0])
+    assert kt.kt_sparse_decode_step_kernels(kv16, p) == 2
+    q = torch.randn(B, H * G, 128).half().cuda()
+    pool = reps_pool(kt, pg, p)
+    kt.kt_build_block_reps_f8(pg.kv, p, 0, 100, pool)
+    ws = kt.workspace_f8(kt.KT_OP_SPARSE_STEP, pg.kv, p)
+    U = 1 if mode == kt.KT_HEAD_SHARED else H
+    hist = torch.zeros(1, B, U, 3, dtype=torch.int32, device="cuda")
+    cnts = torch.full((1, B, U), -1, dtype=torch.int32, device="cuda")
+    out = torch.empty(B, H * G, 128, device="cuda")
+    pol = kt.reuse_policy(1, dense_layer_num=0)
+    assert kt.kt_decode_layer_action(pol, 0, 0) == (kt.KT_LAYER_SELECT, 0)
+    for layer in (False, True, False):
+        out.fill_(float("nan"))
+        if layer:
+            kt.kt_decode_layer_f8(pol, 0, 0, q, pg.kv, pool, p, hist, cnts, out, ws)
+        else:
+            kt.kt_sparse_decode_step_f8(q, pg.kv, pool, p, hist[0], cnts[0], out, ws)
+        hs, hc = hist[0].cpu(), cnts[0].cpu()
+        for b, n in enumerate(lens):
+            assert (hc[b] == min(3, max(0, -(-n // 128) - 2))).all()
+        check_attention(pg, q, out, lambda b, h: chosen(kt, pg, hs, hc, p, b, h), G)
+        assert (segment_counters(ws, B * H) == 0).all()
+    assert_status(kt, ws)
+
+
 def chosen(kt, pg, sel, cnt, p, b, h):
     u = 0 if p.head_mode == kt.KT_HEAD_SHARED else h
     nb = -(-int(pg.host.lens[b]) // 128)
