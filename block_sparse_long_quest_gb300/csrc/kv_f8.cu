@@ -135,19 +135,40 @@ __device__ __forceinline__ float add_f16(float acc, uint16_t h) {
 // rows, half a row each) meet every bank twice and not four times.
 __device__ __forceinline__ int tile_word(int r, int w) { return r * 32 + (w ^ ((r & 1) << 4)); }
 
+// Four codes (as binary16) times the block's scale, as binary16.  OWN: a scale that
+// the append writes, 2^e with e in [-15, 8], which is a binary16 value as every
+// product is.  Any other multiplies in binary32, as the read-back does; what
+// exceeds binary16 becomes its largest value, so that the scores of the block stay
+// numbers.
+template <bool OWN>
+__device__ __forceinline__ uint2 times_scale(__half2 a, __half2 b, float s) {
+  if constexpr (OWN) {
+    const __half2 s2 = __float2half2_rn(s);
+    return make_uint2(as_u32(__hmul2(a, s2)), as_u32(__hmul2(b, s2)));
+  }
+  const __half2 m = __float2half2_rn(65504.0f);
+  uint2 r;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float2 f = __half22float2(i ? b : a);
+    const __half2 v = __floats2half2_rn(f.x * s, f.y * s);
+    (i ? r.y : r.x) = as_u32(__hmax2_nan(__hmin2_nan(v, m), __hneg2(m)));
+  }
+  return r;
+}
+
 // Representatives of a full tile of codes in shared memory, written at rep row
 // `row0` of the pool.  red: RED_BYTES of shared memory.  Every thread calls it.
+template <bool OWN>
 __device__ void tile_reps(const uint8_t* tile, float s, int rep, int R, int fix_stride, void* reps,
                           size_t row0, uint8_t* red, int tid) {
   const int warp = tid >> 5, lane = tid & 31;
   const uint32_t* words = reinterpret_cast<const uint32_t*>(tile);
-  const __half2 s2 = __float2half2_rn(s);  // 2^e is a binary16 value, and so is every product
   if (rep == KT_REP_FIX) {
     uint2* out = reinterpret_cast<uint2*>(static_cast<__half*>(reps) + row0 * D);
     for (int i = tid; i < R * 32; i += THREADS) {
       const uint32_t c = words[tile_word((i >> 5) * fix_stride, i & 31)];
-      out[i] = make_uint2(as_u32(__hmul2(as_h2(f8x2_lo(c)), s2)),
-                          as_u32(__hmul2(as_h2(f8x2_hi(c)), s2)));
+      out[i] = times_scale<OWN>(as_h2(f8x2_lo(c)), as_h2(f8x2_hi(c)), s);
     }
     return;
   }
@@ -174,8 +195,10 @@ __device__ void tile_reps(const uint8_t* tile, float s, int rep, int R, int fix_
       int sum = 0;
 #pragma unroll
       for (int w = 0; w < WARPS; ++w) sum += reinterpret_cast<const int*>(red)[w * D + tid];
-      // one rounding; the factors are powers of two
-      static_cast<float*>(reps)[row0 * D + tid] = __int2float_rn(sum) * 0x1.0p-16f * s;
+      // one rounding: the factors are powers of two, or the product is exact in binary64
+      static_cast<float*>(reps)[row0 * D + tid] =
+          OWN ? __int2float_rn(sum) * 0x1.0p-16f * s
+              : __double2float_rn((double)sum * 0x1.0p-16 * (double)s);
     }
     return;
   }
@@ -207,7 +230,7 @@ __device__ void tile_reps(const uint8_t* tile, float s, int rep, int R, int fix_
     }
     const size_t row = row0 + (rep == KT_REP_QUEST && warp == 0 ? 1 : 0);
     reinterpret_cast<uint2*>(static_cast<__half*>(reps) + row * D)[lane] =
-        make_uint2(as_u32(__hmul2(a, s2)), as_u32(__hmul2(b, s2)));
+        times_scale<OWN>(a, b, s);
   }
 }
 static_assert(RED_BYTES >= WARPS * D * 4, "the sums of the means fit the partials");
@@ -478,7 +501,7 @@ __device__ void append_tile(const Params& p, int cta, const RopeShared& rs, uint
     if (tid == 0) *scale = s;
     if (complete) {
       __syncthreads();
-      tile_reps(codes, s, p.rep, p.R, p.fix_stride, p.reps, slab * p.R, red, tid);
+      tile_reps<true>(codes, s, p.rep, p.R, p.fix_stride, p.reps, slab * p.R, red, tid);
     }
   }
 }
@@ -562,7 +585,7 @@ __global__ void __launch_bounds__(THREADS) reps_f8_kernel(const __grid_constant_
   for (int i = tid; i < TILE_BYTES / 16; i += THREADS)
     *reinterpret_cast<uint4*>(tile + 4 * tile_word(i >> 3, 4 * (i & 7))) = __ldg(src + i);
   __syncthreads();
-  tile_reps(tile, p.k_scale[slab], p.rep, p.R, p.fix_stride, p.reps, slab * p.R, red, tid);
+  tile_reps<false>(tile, p.k_scale[slab], p.rep, p.R, p.fix_stride, p.reps, slab * p.R, red, tid);
 }
 
 struct ReadParams {

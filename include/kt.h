@@ -621,7 +621,10 @@ typedef struct {
 
 /* kt_workspace_bytes, kt_reps_pool_bytes and kt_build_block_reps for this cache.
  * Reps are those of the values read back (Max / Mean / Quest / Fix; no ops or
- * reps of the Dynamic method or the preselection: INVALID_ARG, 0 bytes). */
+ * reps of the Dynamic method or the preselection: INVALID_ARG, 0 bytes).  Scales
+ * may be any value in [2^-30, 2^30], as for the attention below: with one that
+ * kt_append_kv_f8 does not write, Max, Quest and Fix hold code * scale in binary32,
+ * rounded to binary16 and at most 65504 in magnitude. */
 kt_status kt_workspace_bytes_f8(kt_op op, const kt_paged_kv_f8* kv, const kt_sparse_params* p,
                                 size_t* bytes);
 size_t kt_reps_pool_bytes_f8(const kt_paged_kv_f8* kv, const kt_sparse_params* p);

@@ -923,6 +923,65 @@ def test_scales_from_elsewhere(kt):
     check_attention(pg, q, out, lambda b, h: [0, 1, 2, 3, 5, 6], G)
 
 
+@pytest.mark.parametrize("rep,stride", [(0, 1), (1, 1), (2, 1), (3, 1), (3, 16), (3, 128)])
+def test_reps_of_scales_from_elsewhere(kt, rep, stride):
+    """Representatives of blocks whose scales the append does not write, from 2^-30 to 2^30: those
+    of the values read back (code * scale in binary32), bit for bit, saturating in binary16; the
+    Mean rounded once.  The step over such blocks selects as the selection call does."""
+    H, G, blocks = 2, 4, 24
+    p = kt.sparse_params(H * G, 1, 1, 4, rep, kt.KT_HEAD_SEPARATE, fix_stride=stride)
+    pg = filled(kt, [128 * blocks], H, 62, params=p)
+    rng = np.random.default_rng(3)
+    scale = 2.0 ** rng.uniform(-30, 30, pg.k_scale.shape)
+    own = [0.3, 2.0 ** -30, 2.0 ** -26, 2.0 ** -15, 1.0, 256.0, 512.0, 65520.0, 2.0 ** 30, 146.25]
+    scale[[int(x) for x in pg.table[0, :len(own)].cpu()]] = np.array(own)[:, None]
+    scale = scale.astype(np.float32)
+    pg.k_scale.copy_(torch.from_numpy(scale))
+    pg.k_code[int(pg.table[0, 5])] = 0  # zeros under 256, and under 2^30
+    pg.k_code[int(pg.table[0, 8]), 0] = 0
+    pool = reps_pool(kt, pg, p)
+    kt.kt_build_block_reps_f8(pg.kv, p, 0, blocks, pool)
+    rows = {0: 1, 1: 1, 2: 2, 3: 128 // stride}[rep]
+    got = pool.cpu().numpy().view(np.float32 if rep == 1 else np.float16)
+    got = got.reshape(pg.k_code.shape[0], H, rows, 128)
+    code = pg.k_code.cpu().numpy()
+    back = torch.empty(128 * blocks, H, 128, dtype=torch.float32, device="cuda")
+    ws = kt.workspace_f8(kt.KT_OP_SPARSE_STEP, pg.kv, p)
+    kt.kt_read_kv_f8(pg.kv, torch.tensor([0, 128 * blocks], dtype=torch.int32, device="cuda"),
+                     back, None, ws)
+    back = back.cpu().numpy().reshape(blocks, 128, H, 128)
+    for j in range(blocks):
+        page = int(pg.host.table[0, j])
+        for h in range(H):
+            x = f8_ref.decode(code[page, h]).astype(np.float32) * scale[page, h]
+            assert np.array_equal(x, back[j, :, h])
+            if rep == 1:  # the sum is exact in 64 bits, and so is its product with the scale
+                s = f8_ref.decode(code[page, h]).sum(0) / 128.0 * np.float64(scale[page, h])
+                want = s.astype(np.float32)[None]
+            else:
+                x = {0: x.max(0, keepdims=True), 2: np.stack([x.min(0), x.max(0)]),
+                     3: x[::stride]}[rep]
+                want = np.clip(x, -65504.0, 65504.0).astype(np.float16)
+            assert np.array_equal(got[page, h], want), (j, h)
+    assert np.isfinite(got[[int(x) for x in pg.host.table[0]]]).all()
+    # the step, with scales of one order
+    scale = rng.uniform(0.01, 0.011, scale.shape).astype(np.float32)
+    pg.k_scale.copy_(torch.from_numpy(scale))
+    kt.kt_build_block_reps_f8(pg.kv, p, 0, blocks, pool)
+    q = torch.randn(1, H * G, 128).half().cuda()
+    sel = torch.zeros(1, H, 4, dtype=torch.int32, device="cuda")
+    cnt = torch.zeros(1, H, dtype=torch.int32, device="cuda")
+    out = torch.empty(1, H * G, 128, device="cuda")
+    kt.kt_sparse_decode_step_f8(q, pg.kv, pool, p, sel, cnt, out, ws)
+    sel16, cnt16 = torch.zeros_like(sel), torch.zeros_like(cnt)
+    kt.kt_score_select_blocks_f8(q, pg.kv, pool, p, sel16, cnt16, None, ws)
+    assert torch.equal(sel.sort(-1)[0], sel16.sort(-1)[0]) and (cnt == 4).all()
+    pg.host.code["k"], pg.host.scale["k"] = code, scale.astype(np.float64)
+    hs, hc = sel.cpu(), cnt.cpu()
+    check_attention(pg, q, out, lambda b, h: chosen(kt, pg, hs, hc, p, b, h), G)
+    assert_status(kt, ws)
+
+
 def test_offsets_beyond_32_bits(kt):
     """Pools of 5.2 GB, the sequence's pages at their end."""
     H, G, pages = 8, 2, 40000
