@@ -22,6 +22,8 @@
 // wait: for loads between barriers, and for instructions (half the issue slots at
 // 16 warps an SM: angles, conversions, representatives).  16
 // decoded tokens take 3.2 us, a chain of dependent loads (length, page, scale).
+#include <climits>
+#include <cmath>
 #include <cstring>
 
 #include "rope.cuh"
@@ -158,7 +160,8 @@ __device__ __forceinline__ uint2 times_scale(__half2 a, __half2 b, float s) {
 }
 
 // Representatives of a full tile of codes in shared memory, written at rep row
-// `row0` of the pool.  red: RED_BYTES of shared memory.  Every thread calls it.
+// `row0` of the pool.  A channel with a NaN among its 128 values has NaN for its
+// Max, Mean and Quest.  red: RED_BYTES of shared memory.  Every thread calls it.
 template <bool OWN>
 __device__ void tile_reps(const uint8_t* tile, float s, int rep, int R, int fix_stride, void* reps,
                           size_t row0, uint8_t* red, int tid) {
@@ -186,19 +189,24 @@ __device__ void tile_reps(const uint8_t* tile, float s, int rep, int R, int fix_
       acc[2] = add_f16(acc[2], (uint16_t)b);
       acc[3] = add_f16(acc[3], (uint16_t)(b >> 16));
     }
+    // NaN as INT_MIN, far below any sum
+    auto fixed = [](float a) { return a != a ? INT_MIN : __float2int_rn(a * 512.0f); };
     int4* part = reinterpret_cast<int4*>(red);
-    part[warp * 32 + lane] = make_int4(
-        __float2int_rn(acc[0] * 512.0f), __float2int_rn(acc[1] * 512.0f),
-        __float2int_rn(acc[2] * 512.0f), __float2int_rn(acc[3] * 512.0f));
+    part[warp * 32 + lane] = make_int4(fixed(acc[0]), fixed(acc[1]), fixed(acc[2]), fixed(acc[3]));
     __syncthreads();
     if (tid < D) {
       int sum = 0;
+      bool nan = false;
 #pragma unroll
-      for (int w = 0; w < WARPS; ++w) sum += reinterpret_cast<const int*>(red)[w * D + tid];
+      for (int w = 0; w < WARPS; ++w) {
+        const int v = reinterpret_cast<const int*>(red)[w * D + tid];
+        nan = nan || v == INT_MIN;
+        sum += v == INT_MIN ? 0 : v;
+      }
       // one rounding: the factors are powers of two, or the product is exact in binary64
-      static_cast<float*>(reps)[row0 * D + tid] =
-          OWN ? __int2float_rn(sum) * 0x1.0p-16f * s
-              : __double2float_rn((double)sum * 0x1.0p-16 * (double)s);
+      const float mean = OWN ? __int2float_rn(sum) * 0x1.0p-16f * s
+                             : __double2float_rn((double)sum * 0x1.0p-16 * (double)s);
+      static_cast<float*>(reps)[row0 * D + tid] = nan ? NAN : mean;
     }
     return;
   }
@@ -209,10 +217,10 @@ __device__ void tile_reps(const uint8_t* tile, float s, int rep, int R, int fix_
   for (int r = r0; r < r0 + BS / WARPS; ++r) {
     const uint32_t c = words[tile_word(r, lane)];
     const __half2 a = as_h2(f8x2_lo(c)), b = as_h2(f8x2_hi(c));
-    mx[0] = __hmax2(mx[0], a);
-    mx[1] = __hmax2(mx[1], b);
-    mn[0] = __hmin2(mn[0], a);
-    mn[1] = __hmin2(mn[1], b);
+    mx[0] = __hmax2_nan(mx[0], a);
+    mx[1] = __hmax2_nan(mx[1], b);
+    mn[0] = __hmin2_nan(mn[0], a);
+    mn[1] = __hmin2_nan(mn[1], b);
   }
   uint2* part = reinterpret_cast<uint2*>(red);
   part[warp * 32 + lane] = make_uint2(as_u32(mx[0]), as_u32(mx[1]));
@@ -225,8 +233,8 @@ __device__ void tile_reps(const uint8_t* tile, float s, int rep, int R, int fix_
 #pragma unroll
     for (int w = 1; w < WARPS; ++w) {
       v = part[(warp * WARPS + w) * 32 + lane];
-      a = warp ? __hmin2(a, as_h2(v.x)) : __hmax2(a, as_h2(v.x));
-      b = warp ? __hmin2(b, as_h2(v.y)) : __hmax2(b, as_h2(v.y));
+      a = warp ? __hmin2_nan(a, as_h2(v.x)) : __hmax2_nan(a, as_h2(v.x));
+      b = warp ? __hmin2_nan(b, as_h2(v.y)) : __hmax2_nan(b, as_h2(v.y));
     }
     const size_t row = row0 + (rep == KT_REP_QUEST && warp == 0 ? 1 : 0);
     reinterpret_cast<uint2*>(static_cast<__half*>(reps) + row * D)[lane] =

@@ -624,7 +624,8 @@ typedef struct {
  * reps of the Dynamic method or the preselection: INVALID_ARG, 0 bytes).  Scales
  * may be any value in [2^-30, 2^30], as for the attention below: with one that
  * kt_append_kv_f8 does not write, Max, Quest and Fix hold code * scale in binary32,
- * rounded to binary16 and at most 65504 in magnitude. */
+ * rounded to binary16 and at most 65504 in magnitude.  A channel with a NaN among a
+ * block's values has NaN for its Max, Mean and Quest. */
 kt_status kt_workspace_bytes_f8(kt_op op, const kt_paged_kv_f8* kv, const kt_sparse_params* p,
                                 size_t* bytes);
 size_t kt_reps_pool_bytes_f8(const kt_paged_kv_f8* kv, const kt_sparse_params* p);

@@ -982,6 +982,63 @@ def test_reps_of_scales_from_elsewhere(kt, rep, stride):
     assert_status(kt, ws)
 
 
+@pytest.mark.parametrize("rep,stride", [(0, 1), (1, 1), (2, 1), (3, 8), (3, 128)])
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_reps_of_nan_keys(kt, rep, stride, dtype):
+    """A channel with a NaN key has NaN for its representative (Fix: the row's own), whether the
+    append builds it, over one call or two, or kt_build_block_reps_f8; other channels, heads and
+    sequences are as without it, and their attention is."""
+    H, G, lens = 2, 4, [128 * 6 + 5, 128 * 4]
+    p = kt.sparse_params(H * G, 1, 1, 2, rep, kt.KT_HEAD_SEPARATE, fix_stride=stride)
+    rng = torch.Generator().manual_seed(9)
+    m = sum(lens)
+    k, v = rows_of(rng, m, H, dtype, 4.0), rows_of(rng, m, H, dtype, 4.0)
+    k[3, 0, 7] = float("nan")                   # one value, in the block's first warp
+    k[127, 0, 64] = -float("nan")               # and in its last
+    k[128:256, 0, 9] = float("nan")             # a channel through a block
+    k[256 + 40, 0] = float("nan")               # a row
+    k[lens[0] + 200, 0, 1] = float("inf")       # no NaN: the largest code
+    for first in (0, 128 * 2 + 40):             # in one call, and split inside a block
+        pg = Paged(kt, [0, 0], H, 7, 12)
+        ws = kt.workspace_f8(kt.KT_OP_SPARSE_STEP, pg.kv, p)
+        pool, done = reps_pool(kt, pg, p), []
+        parts = [[0, 0], lens] if first == 0 else [[first, 0], [lens[0] - first, lens[1]]]
+        at = [0, lens[0]]
+        for counts in parts:
+            rows = torch.cat([torch.arange(a, a + n) for a, n in zip(at, counts)]).cuda()
+            at = [a + n for a, n in zip(at, counts)]
+            cu = torch.tensor(np.cumsum([0] + counts), dtype=torch.int32, device="cuda")
+            kt.kt_append_kv_f8(pg.kv, p, k[rows], v[rows], ws, cu_tokens=cu, reps_pool=pool)
+            done += pg.host.append(host16(k[rows]), host16(v[rows]), counts)
+        pg.check()
+        again = reps_pool(kt, pg, p)
+        kt.kt_build_block_reps_f8(pg.kv, p, 0, 7, again)
+        rows = {0: 1, 1: 1, 2: 2, 3: 128 // stride}[rep]
+        for t in (pool, again):
+            got = t.cpu().numpy().view(np.float32 if rep == 1 else np.float16)
+            got = got.reshape(-1, H, rows, 128)
+            assert len(done) == 10
+            for b, j in done:
+                page = int(pg.host.table[b, j])
+                for h in range(H):
+                    want = pg.host.reps(page, h, rep, stride).astype(got.dtype)
+                    assert np.array_equal(got[page, h], want, equal_nan=True), (b, j, h)
+        if rep != 3:
+            page = int(pg.host.table[0, 0])
+            assert np.isnan(got[page, 0]).sum() == 2 * rows
+    q = torch.randn(2, H * G, 128).half().cuda()
+    sel = torch.zeros(2, H, 2, dtype=torch.int32, device="cuda")
+    cnt = torch.zeros(2, H, dtype=torch.int32, device="cuda")
+    out = torch.empty(2, H * G, 128, device="cuda")
+    kt.kt_sparse_decode_step_f8(q, pg.kv, pool, p, sel, cnt, out, ws)
+    hs, hc = sel.cpu(), cnt.cpu()
+    assert (hc == 2).all()
+    assert torch.isnan(out[0, :G]).all()        # block 0 is an Initial one
+    out[0, :G] = 0.0
+    check_attention(pg, q, out, lambda b, h: chosen(kt, pg, hs, hc, p, b, h) if b or h else [], G)
+    assert_status(kt, ws)
+
+
 def test_offsets_beyond_32_bits(kt):
     """Pools of 5.2 GB, the sequence's pages at their end."""
     H, G, pages = 8, 2, 40000
