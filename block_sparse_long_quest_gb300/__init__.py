@@ -456,8 +456,9 @@ def _dtype(t):
     return _DTYPES.get(t.dtype)
 
 
-def _check_int32(t, call):
-    if t is not None and _dtype(t) != _INT32:
+def _check_int32(t, n, call):
+    """An index tensor of which the kernels read (or write) the first n entries."""
+    if t is not None and (_dtype(t) != _INT32 or t.numel() < n or not t.is_contiguous()):
         raise KtError(KT_ERR_INVALID_ARG, call)
 
 
@@ -489,8 +490,8 @@ def _check_rows(t, tokens, out, call):
 def kt_apply_rope(rope, positions, q=None, q_out=None, k=None, k_out=None, stream=None):
     """Rotates q into q_out and k into k_out ([tokens][heads][128]; outputs float16); positions:
     int32 [tokens]."""
-    _check_int32(positions, "kt_apply_rope")
     tokens = positions.numel()
+    _check_int32(positions, tokens, "kt_apply_rope")
     qr = kr = None
     if q is not None:
         _check_rows(q, tokens, q_out, "kt_apply_rope")
@@ -539,10 +540,11 @@ def kt_build_block_reps_f8(kv, params, first_block, num_blocks, reps_pool, strea
 def kt_append_kv_f8(kv, params, k, v, ws, *, rope=None, q=None, q_out=None, cu_tokens=None,
                     new_lens=None, reps_pool=None, stream=None):
     """Appends the rows k / v ([tokens][H_kv][128]) to the cache.  cu_tokens None: one row per
-    sequence; new_lens None: kv's lengths advance in place."""
+    sequence, else int32 [batch + 1] or longer; new_lens None: kv's lengths advance in place, else
+    int32 [batch] or longer."""
     tokens = k.shape[0]
-    _check_int32(cu_tokens, "kt_append_kv_f8")
-    _check_int32(new_lens, "kt_append_kv_f8")
+    _check_int32(cu_tokens, kv.batch + 1, "kt_append_kv_f8")
+    _check_int32(new_lens, kv.batch, "kt_append_kv_f8")
     _check_rows(v, tokens, None, "kt_append_kv_f8")
     qr = None
     if q is not None:
@@ -562,15 +564,15 @@ def _check_out(out, shape, call):
 
 def kt_read_kv_f8(kv, cu_tokens, k_out, v_out, ws, *, first=None, stream=None):
     """Tokens first[b] .. of every sequence into the rows of k_out / v_out ([tokens][H_kv][128];
-    either may be None)."""
+    either may be None); cu_tokens: int32 [batch + 1] or longer, first: int32 [batch] or longer."""
     out = k_out if k_out is not None else v_out
     if out is None or (k_out is not None and v_out is not None and k_out.dtype != v_out.dtype):
         raise KtError(KT_ERR_INVALID_ARG, "kt_read_kv_f8")
     dtype = _dtype(out)
     if dtype is None or dtype < 0:
         raise KtError(KT_ERR_UNSUPPORTED, "kt_read_kv_f8")
-    _check_int32(cu_tokens, "kt_read_kv_f8")
-    _check_int32(first, "kt_read_kv_f8")
+    _check_int32(cu_tokens, kv.batch + 1, "kt_read_kv_f8")
+    _check_int32(first, kv.batch, "kt_read_kv_f8")
     shape = (out.shape[0], kv.num_kv_heads, 128)
     _check_out(k_out, shape, "kt_read_kv_f8")
     _check_out(v_out, shape, "kt_read_kv_f8")

@@ -334,3 +334,30 @@ def test_binding_refuses_other_tensors():
         kt.kt_read_kv_f8(cache(), pos, None, None, x, stream=0)
     with pytest.raises(kt.KtError):
         kt.kt_read_kv_f8(cache(), pos, x[:, :4], None, x, stream=0)
+
+
+def test_binding_refuses_short_and_strided_index_tensors():
+    """The kernels read batch + 1 offsets and batch lengths one behind the other: a tensor with
+    fewer, or with gaps, is refused; a longer one (a padded buffer) is not."""
+    torch = pytest.importorskip("torch")
+    x = torch.zeros(4, 8, 128, dtype=torch.float16)
+    c, p, r = cache(batch=2), params(), kt.rope()
+    ints = lambda n: torch.zeros(n, dtype=torch.int32)  # noqa: E731
+
+    def refused(call):
+        with pytest.raises(kt.KtError) as e:
+            call()
+        return e.value.status == kt.KT_ERR_INVALID_ARG
+
+    assert refused(lambda: kt.kt_apply_rope(r, ints(8)[::2], x, x, stream=0))
+    assert refused(lambda: kt.kt_apply_rope(r, ints(1).expand(4), x, x, stream=0))
+    for bad in (ints(2), ints(6)[::2], ints(1).expand(3), ints(0)):
+        assert refused(lambda: kt.kt_append_kv_f8(c, p, x, x, x, cu_tokens=bad, stream=0))
+        assert refused(lambda: kt.kt_read_kv_f8(c, bad, x, None, x, stream=0))
+    assert refused(lambda: kt.kt_read_kv_f8(c, None, x, None, x, stream=0))
+    for bad in (ints(1), ints(4)[::2], ints(1).expand(2), ints(0)):
+        assert refused(lambda: kt.kt_append_kv_f8(c, p, x, x, x, cu_tokens=ints(3), new_lens=bad,
+                                                  stream=0))
+        assert refused(lambda: kt.kt_read_kv_f8(c, ints(3), x, None, x, first=bad, stream=0))
+    kt._check_int32(ints(9), 3, "a call")
+    kt._check_int32(None, 3, "a call")
