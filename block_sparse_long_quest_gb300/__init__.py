@@ -465,8 +465,8 @@ def _check_int32(t, n, call):
 def rows(t) -> Rows:
     """kt_rows of a tensor [tokens][heads][128] (it may be a part of a packed projection); the
     last two dimensions are contiguous."""
-    if type(t) is Rows:
-        return t
+    if type(t) is Rows:  # without the number of its tokens
+        raise KtError(KT_ERR_INVALID_ARG, "rows")
     tokens, heads, d = t.shape
     s0, s1, s2 = t.stride()
     dtype = _dtype(t)
@@ -494,11 +494,11 @@ def kt_apply_rope(rope, positions, q=None, q_out=None, k=None, k_out=None, strea
     _check_int32(positions, tokens, "kt_apply_rope")
     qr = kr = None
     if q is not None:
-        _check_rows(q, tokens, q_out, "kt_apply_rope")
         qr = _byref(rows(q))
+        _check_rows(q, tokens, q_out, "kt_apply_rope")
     if k is not None:
-        _check_rows(k, tokens, k_out, "kt_apply_rope")
         kr = _byref(rows(k))
+        _check_rows(k, tokens, k_out, "kt_apply_rope")
     _check(lib.kt_apply_rope(_byref(rope), _ptr(positions), tokens, qr, _ptr(q_out), kr,
                              _ptr(k_out), _stream(stream)),
            "kt_apply_rope")
@@ -542,16 +542,17 @@ def kt_append_kv_f8(kv, params, k, v, ws, *, rope=None, q=None, q_out=None, cu_t
     """Appends the rows k / v ([tokens][H_kv][128]) to the cache.  cu_tokens None: one row per
     sequence, else int32 [batch + 1] or longer; new_lens None: kv's lengths advance in place, else
     int32 [batch] or longer."""
+    kr, vr = rows(k), rows(v)
     tokens = k.shape[0]
     _check_int32(cu_tokens, kv.batch + 1, "kt_append_kv_f8")
     _check_int32(new_lens, kv.batch, "kt_append_kv_f8")
     _check_rows(v, tokens, None, "kt_append_kv_f8")
     qr = None
     if q is not None:
-        _check_rows(q, tokens, q_out, "kt_append_kv_f8")
         qr = _byref(rows(q))
+        _check_rows(q, tokens, q_out, "kt_append_kv_f8")
     _check(lib.kt_append_kv_f8(_byref(kv), _byref(params), None if rope is None else _byref(rope),
-                               qr, _ptr(q_out), _byref(rows(k)), _byref(rows(v)),
+                               qr, _ptr(q_out), _byref(kr), _byref(vr),
                                _ptr(cu_tokens), tokens, _ptr(new_lens), _ptr(reps_pool), _ptr(ws),
                                ws.numel(), _stream(stream)),
            "kt_append_kv_f8")

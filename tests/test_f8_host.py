@@ -361,3 +361,22 @@ def test_binding_refuses_short_and_strided_index_tensors():
         assert refused(lambda: kt.kt_read_kv_f8(c, ints(3), x, None, x, first=bad, stream=0))
     kt._check_int32(ints(9), 3, "a call")
     kt._check_int32(None, 3, "a call")
+
+
+def test_binding_refuses_prepared_rows():
+    """A kt_rows does not hold its number of tokens, which the calls check: only tensors are taken,
+    and a kt_rows is refused like any other wrong argument."""
+    torch = pytest.importorskip("torch")
+    x = torch.zeros(4, 8, 128, dtype=torch.float16)
+    pos = torch.zeros(4, dtype=torch.int32)
+    r, c, p = kt.rope(), cache(batch=4), params(num_q_heads=8)
+    y = kt.rows(x)
+    assert (y.stride, y.heads, y.dtype) == (8 * 128, 8, kt.KT_F16)
+    for call in (lambda: kt.rows(y), lambda: kt.kt_apply_rope(r, pos, y, x, stream=0),
+                 lambda: kt.kt_apply_rope(r, pos, k=y, k_out=x, stream=0),
+                 lambda: kt.kt_append_kv_f8(c, p, y, x, x, stream=0),
+                 lambda: kt.kt_append_kv_f8(c, p, x, y, x, stream=0),
+                 lambda: kt.kt_append_kv_f8(c, p, x, x, x, q=y, q_out=x, stream=0)):
+        with pytest.raises(kt.KtError) as e:
+            call()
+        assert e.value.status == kt.KT_ERR_INVALID_ARG
