@@ -148,6 +148,32 @@ def test_rope_in_place_and_without_effect(kt, layout, rot):
     assert torch.equal(y, x)
 
 
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("layout,rot", [("half", 128), ("half", 48), ("pairs", 96), ("half", 90)])
+@pytest.mark.parametrize("tokens,hq,hk", [(3000, 32, 8), (2501, 13, 0), (2433, 9, 9)])
+def test_rope_of_many_tokens(kt, dtype, layout, rot, tokens, hq, hk):
+    """Enough tokens for a warp to take all heads of one, eight rows at a time: whole turns and a
+    last one of fewer heads, that ends inside q or inside k."""
+    rng = torch.Generator().manual_seed(tokens + rot)
+    assert tokens >= 16 * torch.cuda.get_device_properties(0).multi_processor_count
+    x = torch.randn(tokens, hq + hk, 128, generator=rng).to(DTYPES[dtype]).cuda()
+    pos = torch.randint(0, 1 << 21, (tokens,), generator=rng, dtype=torch.int32)
+    r = kt.rope(rot, theta=5e5, layout=kt.KT_ROPE_HALF if layout == "half" else kt.KT_ROPE_PAIRS)
+    f, amp = f8_ref.frequencies(rot, 5e5)
+    q, k = x[:, :hq], x[:, hq:] if hk else None
+    q_out = torch.full((tokens + 1, hq, 128), 7.0, dtype=torch.float16, device="cuda")
+    k_out = torch.full((tokens + 1, max(hk, 1), 128), 7.0, dtype=torch.float16, device="cuda")
+    kt.kt_apply_rope(r, pos.cuda(), q, q_out[:tokens], k, k_out[:tokens] if hk else None)
+    check_rope(q_out[:tokens], q, pos.numpy(), f, amp, layout)
+    if hk:
+        check_rope(k_out[:tokens], k, pos.numpy(), f, amp, layout)
+    assert (q_out[tokens:] == 7.0).all() and (k_out[tokens if hk else 0:] == 7.0).all()
+    if dtype == "f16":  # in place
+        y = q.contiguous()
+        kt.kt_apply_rope(r, pos.cuda(), y, y)
+        assert torch.equal(y, q_out[:tokens])
+
+
 def test_rope_turns_back(kt):
     """The rotation by -p undoes the rotation by p: what its transpose, and so its gradient, is."""
     x = torch.randn(50, 4, 128, dtype=torch.float32).cuda()
@@ -375,6 +401,74 @@ def test_append_rotated_equals_rotation_then_append(kt, dtype, layout, rot):
     kt.kt_append_kv_f8(pg.kv, p, k, v, ws, q=q, q_out=q2, cu_tokens=cu)
     assert torch.equal(q2, q.half())
     assert_status(kt, ws)
+
+
+HEADS_A_CTA = [  # KV heads, query heads a KV head, K heads a CTA, cached lengths and new rows
+    (8, 4, 4, [80], [9900]),
+    (8, 8, 4, [(53 * b) % 300 for b in range(30)], [(71 * b) % 150 for b in range(30)]),
+    (5, 1, 3, [(53 * b) % 300 for b in range(40)], [(37 * b) % 130 for b in range(40)]),
+    (3, 2, 2, [(29 * b) % 200 for b in range(50)], [(41 * b) % 140 for b in range(50)]),
+    (8, 1, 2, [(53 * b) % 300 for b in range(20)], [(91 * b) % 170 for b in range(20)]),
+]
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("case", range(len(HEADS_A_CTA)))
+def test_append_with_several_heads_a_cta(kt, dtype, case):
+    """Rotated appends of so many blocks that a CTA takes several K heads of one, the last group
+    fewer: codes, scales, representatives and q, bit for bit, from begun blocks whose scale grows
+    and into blocks that the call completes."""
+    H, G, heads, lens, counts = HEADS_A_CTA[case]
+    n = case + list(DTYPES).index(dtype)
+    layout, rot = [("half", 128), ("pairs", 64), ("half", 90)][n % 3]
+    rep, stride = [(0, 1), (1, 1), (2, 1), (3, 8)][n % 4]
+    B, m = len(lens), sum(counts)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    per = min(4, (m // 128 + 2 * B) * H // sms)
+    groups = -(-H // per)
+    assert -(-H // groups) == heads  # the launch takes as many heads a CTA as meant here
+    rng = torch.Generator().manual_seed(case)
+    blocks = max(-(-(a + c) // 128) for a, c in zip(lens, counts))
+    pg, other = Paged(kt, [0] * B, H, blocks, 15), Paged(kt, [0] * B, H, blocks, 15)
+    p = kt.sparse_params(H * G, 1, 1, 2, rep, kt.KT_HEAD_SHARED, fix_stride=stride)
+    ws = kt.workspace_f8(kt.KT_OP_SPARSE_STEP, pg.kv, p)
+    k, v = rows_of(rng, sum(lens), H, "f16", 6.0), rows_of(rng, sum(lens), H, "f16", 6.0)
+    cu = torch.tensor(np.cumsum([0] + lens), dtype=torch.int32, device="cuda")
+    for x in (pg, other):
+        kt.kt_append_kv_f8(x.kv, p, k, v, ws, cu_tokens=cu)
+    pg.host.append(host16(k), host16(v), lens)
+    qkv = rows_of(rng, m, H * G + 2 * H, dtype, 8.0)
+    q, k, v = qkv[:, :H * G], qkv[:, H * G:H * G + H], qkv[:, H * G + H:]
+    pos = torch.cat([torch.arange(a, a + c) for a, c in zip(lens, counts)]).to(torch.int32)
+    r = kt.rope(rot, theta=1e5, layout=kt.KT_ROPE_HALF if layout == "half" else kt.KT_ROPE_PAIRS)
+    q1, k1 = (torch.empty(m, h, 128, dtype=torch.float16, device="cuda") for h in (H * G, H))
+    kt.kt_apply_rope(r, pos.cuda(), q, q1, k, k1)
+    f, amp = f8_ref.frequencies(rot, 1e5)
+    check_rope(k1, k, pos.numpy(), f, amp, layout)
+    check_rope(q1, q, pos.numpy(), f, amp, layout)
+    cu = torch.tensor(np.cumsum([0] + counts), dtype=torch.int32, device="cuda")
+    pools = [reps_pool(kt, pg, p), reps_pool(kt, pg, p)]
+    q2 = torch.zeros_like(q1)
+    kt.kt_append_kv_f8(pg.kv, p, k, v, ws, rope=r, q=q, q_out=q2, cu_tokens=cu,
+                       reps_pool=pools[0])
+    assert torch.equal(q1, q2)
+    done = pg.host.append(host16(k1), host16(v), counts)
+    pg.check()
+    # representatives: as an unrotated append of the rotated rows builds them, a head a CTA
+    kt.kt_append_kv_f8(other.kv, p, k1, v.half().contiguous(), ws, cu_tokens=cu,
+                       reps_pool=pools[1])
+    assert torch.equal(pools[0], pools[1]) and torch.equal(other.k_code, pg.k_code)
+    rows = {0: 1, 1: 1, 2: 2, 3: 128 // stride}[rep]
+    got = pools[0].cpu().numpy().view(np.float32 if rep == 1 else np.float16)
+    got = got.reshape(-1, H, rows, 128)
+    assert done
+    for b, j in done:
+        page = int(pg.host.table[b, j])
+        for h in range(H):
+            assert np.array_equal(got[page, h],
+                                  pg.host.reps(page, h, rep, stride).astype(got.dtype)), (b, j, h)
+    assert_status(kt, ws)
+    assert (ws[:256] == 0).all()
 
 
 def test_append_refuses_on_the_device(kt):
