@@ -22,8 +22,6 @@
 // wait: for loads between barriers, and for instructions (half the issue slots at
 // 16 warps an SM: angles, conversions, representatives).  16
 // decoded tokens take 3.2 us, a chain of dependent loads (length, page, scale).
-#include <climits>
-#include <cmath>
 #include <cstring>
 
 #include "rope.cuh"
@@ -177,8 +175,9 @@ __device__ void tile_reps(const uint8_t* tile, float s, int rep, int R, int fix_
   }
   const int r0 = warp * (BS / WARPS);
   if (rep == KT_REP_MEAN) {
-    // a code is a whole number of 2^-9, at most 448 * 2^9: the sums of a warp's 16
-    // rows stay below 2^22 of them (exact in binary32), all 128 below 2^25
+    // a code is a whole number of 2^-9, at most 448 * 2^9: sums of up to four warps'
+    // 16 rows stay below 2^24 of them, exact in binary32 in any order, so that of the
+    // two halves of the block is the only one that rounds; NaN stays NaN
     float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 4
     for (int r = r0; r < r0 + BS / WARPS; ++r) {
@@ -189,24 +188,20 @@ __device__ void tile_reps(const uint8_t* tile, float s, int rep, int R, int fix_
       acc[2] = add_f16(acc[2], (uint16_t)b);
       acc[3] = add_f16(acc[3], (uint16_t)(b >> 16));
     }
-    // NaN as INT_MIN, far below any sum
-    auto fixed = [](float a) { return a != a ? INT_MIN : __float2int_rn(a * 512.0f); };
-    int4* part = reinterpret_cast<int4*>(red);
-    part[warp * 32 + lane] = make_int4(fixed(acc[0]), fixed(acc[1]), fixed(acc[2]), fixed(acc[3]));
+    float4* part = reinterpret_cast<float4*>(red);
+    part[warp * 32 + lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
     __syncthreads();
     if (tid < D) {
-      int sum = 0;
-      bool nan = false;
+      const float* sums = reinterpret_cast<const float*>(red) + tid;
+      float half[2];
 #pragma unroll
-      for (int w = 0; w < WARPS; ++w) {
-        const int v = reinterpret_cast<const int*>(red)[w * D + tid];
-        nan = nan || v == INT_MIN;
-        sum += v == INT_MIN ? 0 : v;
-      }
+      for (int i = 0; i < 2; ++i)
+        half[i] = (sums[4 * i * D] + sums[(4 * i + 1) * D]) +
+                  (sums[(4 * i + 2) * D] + sums[(4 * i + 3) * D]);
       // one rounding: the factors are powers of two, or the product is exact in binary64
-      const float mean = OWN ? __int2float_rn(sum) * 0x1.0p-16f * s
-                             : __double2float_rn((double)sum * 0x1.0p-16 * (double)s);
-      static_cast<float*>(reps)[row0 * D + tid] = nan ? NAN : mean;
+      static_cast<float*>(reps)[row0 * D + tid] =
+          OWN ? (half[0] + half[1]) * 0x1.0p-7f * s
+              : __double2float_rn(((double)half[0] + (double)half[1]) * 0x1.0p-7 * (double)s);
     }
     return;
   }
@@ -241,7 +236,7 @@ __device__ void tile_reps(const uint8_t* tile, float s, int rep, int R, int fix_
         times_scale<OWN>(a, b, s);
   }
 }
-static_assert(RED_BYTES >= WARPS * D * 4, "the sums of the means fit the partials");
+static_assert(WARPS == 8 && RED_BYTES >= WARPS * D * 4, "the sums of the means fit the partials");
 
 // The sequence and block of tile `tile` of the call (false: behind the last), by
 // all threads.  sh: WARPS + 8 ints.
