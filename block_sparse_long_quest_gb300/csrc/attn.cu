@@ -181,7 +181,7 @@ __device__ __forceinline__ Part partition(int n, int I, int L) {
 }
 
 __device__ __forceinline__ int seq_len(const Params& p, int b) {
-  int n = __ldg(p.seq_lens + b);
+  int n = p.seq_lens[b];
   if (n < 0 || n > p.max_blocks * BS) {
     set_status(p.status, KT_ERR_DEVICE_CHECK);
     n = n < 0 ? 0 : p.max_blocks * BS;
@@ -264,7 +264,7 @@ __device__ __forceinline__ void fused_weights(const Params& p, float* wts, int b
     uint4 v[MAX_G];
 #pragma unroll
     for (int hh = 0; hh < MAX_G; ++hh)
-      v[hh] = hh < p.G ? __ldg(reinterpret_cast<const uint4*>(qu + (size_t)(gi * p.G + hh) * D) + c8)
+      v[hh] = hh < p.G ? reinterpret_cast<const uint4*>(qu + (size_t)(gi * p.G + hh) * D)[c8]
                        : make_uint4(0u, 0u, 0u, 0u);
     float sum[8], neg[8], pos[8];
 #pragma unroll

@@ -408,6 +408,10 @@ __device__ __forceinline__ int atom_acq_rel_gpu_add(int* p, int v) {
   return old;
 }
 
+// The kernel before on the stream may still run when this one starts, and has ended,
+// its writes visible, behind this wait.  What it may have written (lengths, rotated
+// queries, scales, representatives) is read by plain loads: the non-coherent ones
+// (__ldg) are for what does not change while a kernel runs.
 __device__ __forceinline__ void griddep_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }

@@ -685,7 +685,7 @@ __global__ void __launch_bounds__(THREADS) read_f8_kernel(const __grid_constant_
           if (p.out[side]) {
             c[i][side] = __ldcs(reinterpret_cast<const uint2*>(
                 p.code[side] + slab * TILE_BYTES + sh_row[rr] * D + c8));
-            s[i][side] = __ldg(p.scale[side] + slab);
+            s[i][side] = p.scale[side][slab];
           }
       }
     }

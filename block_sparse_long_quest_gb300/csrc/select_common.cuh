@@ -536,7 +536,7 @@ __device__ __forceinline__ void score_linear(const void* reps, int P, int H_kv, 
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         const int vec = lane + 32 * v;
-        x[bi][v] = (ok && vec < V) ? __ldg(src + vec) : make_uint4(0u, 0u, 0u, 0u);
+        x[bi][v] = (ok && vec < V) ? src[vec] : make_uint4(0u, 0u, 0u, 0u);
       }
     }
   };
@@ -888,8 +888,8 @@ __device__ __forceinline__ void score_multi_mma_smem(uint32_t sbase, int sb, int
         bf[ks][0] = bf[ks][1] = 0u;
         if (g < G) {
           const __half* qr = q_unit + (size_t)(gi * G + g) * D + ks * 16 + 2 * t;
-          bf[ks][0] = __ldg(reinterpret_cast<const unsigned int*>(qr));
-          bf[ks][1] = __ldg(reinterpret_cast<const unsigned int*>(qr + 8));
+          bf[ks][0] = *reinterpret_cast<const unsigned int*>(qr);
+          bf[ks][1] = *reinterpret_cast<const unsigned int*>(qr + 8);
         }
       }
       float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
