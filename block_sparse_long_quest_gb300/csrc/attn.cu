@@ -838,23 +838,31 @@ __device__ __forceinline__ void f8_block(const F8Lane& cx, F8State& z, const uin
         perm[h][i] = f8_permute(cx.w0 + h * 16 + i * 8 + 2 * cx.t, in.ntok);
       }
   }
+  // exponent of a token: (x - mx) sc + (mx sc - m), so that the largest of a block has
+  // its own to the last bit.  x sc - m in one rounding would keep what m lost of the
+  // product, whole powers of two where scores reach 2^24.
   const float sc = q_scale_log2 * in.ks;
-  float mu[2], m_new[2];
+  float mu[2], m_new[2], mxs[2], off[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     float mx = fmaxf(fmaxf(x[0][i], x[0][2 + i]), fmaxf(x[1][i], x[1][2 + i]));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-    m_new[i] = fmaxf(z.m[i], mx * sc);
+    const float top = mx * sc;
+    m_new[i] = fmaxf(z.m[i], top);
     mu[i] = m_new[i] == -INFINITY ? 0.0f : m_new[i];
+    mxs[i] = mx;
+    // what top lost, where that is small: blocks then meet as exactly as before
+    const float rest = fabsf(top) < 0x1.0p20f ? fmaf(mx, sc, -top) : 0.0f;
+    off[i] = F8_P_SHIFT + ((top - mu[i]) + rest);
   }
   float pr[2][4];
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      pr[h][i] = ex2(fmaf(x[h][i], sc, F8_P_SHIFT - mu[i & 1]));
+      pr[h][i] = ex2(fmaf(x[h][i] - mxs[i & 1], sc, off[i & 1]));
   // acc goes over to the new maxima and to this block's V scale
   const float a0 = ex2(z.m[0] - mu[0]), a1 = ex2(z.m[1] - mu[1]);
   const float rv = in.vs == z.vs ? 1.0f : z.vs / in.vs;

@@ -1017,6 +1017,55 @@ def test_scales_from_elsewhere(kt):
     check_attention(pg, q, out, lambda b, h: [0, 1, 2, 3, 5, 6], G)
 
 
+@pytest.mark.parametrize("G", [1, 3, 4, 8])
+@pytest.mark.parametrize("exps", [[17], [20], [23], [24], [26], [30], [30, -30, 8, 22, 0]])
+def test_large_scores(kt, G, exps):
+    """K scales up to 2^30: scores so large that one token takes all of the weight.
+
+    A score errs by 8 * 2^-23 of sum |q k| (eight truncated steps of the tensor core), one of
+    them and the maximum by 2^-24 each where they are rounded; where the best is ahead of the next by
+    64 more than twice that (in base 2), the others' weights are below 2^-64 and the output is the
+    best token's V: a product in units of the block's scale (exact, P in two parts 2^-22), and one
+    division, 2^-20 in all.  Elsewhere it stays among the values of V."""
+    H, lens = 2, [128 * 7 + 9, 300]
+    pg = filled(kt, lens, H, 63)
+    for b in range(2):
+        for j in range(8):
+            pg.k_scale[int(pg.host.table[b, j])] = 2.0 ** exps[j % len(exps)]
+    pg.host.scale["k"] = pg.k_scale.cpu().double().numpy()
+    q = torch.randn(2, H * G, 128).half().cuda()
+    p = kt.sparse_params(H * G, 8, 1, 1, kt.KT_REP_QUEST, kt.KT_HEAD_SEPARATE)
+    ws = kt.workspace_f8(kt.KT_OP_SPARSE_STEP, pg.kv, p)
+    pool = reps_pool(kt, pg, p)
+    kt.kt_build_block_reps_f8(pg.kv, p, 0, 8, pool)
+    sel = torch.zeros(2, H, 1, dtype=torch.int32, device="cuda")
+    cnt = torch.zeros(2, H, dtype=torch.int32, device="cuda")
+    dense, step, given = (torch.empty(2, H * G, 128, device="cuda") for _ in "abc")
+    kt.kt_dense_decode_attn_f8(q, pg.kv, H * G, SCALE, dense, ws)
+    kt.kt_sparse_decode_step_f8(q, pg.kv, pool, p, sel, cnt, step, ws)  # every block is Initial
+    kt.kt_sparse_decode_attn_f8(q, pg.kv, p, sel, cnt, given, ws)
+    assert (cnt == 0).all()
+    assert_status(kt, ws)
+    clear = 0
+    for out in (dense, step, given):
+        got = out.cpu().double().numpy()
+        for b, n in enumerate(lens):
+            for h in range(H):
+                k, v = (np.concatenate([pg.host.values(s, int(pg.host.table[b, j]), h)
+                                        for j in range(-(-n // 128))])[:n] for s in "kv")
+                for i in range(h * G, h * G + G):
+                    x = q[b, i].cpu().double().numpy()
+                    base2 = SCALE * 1.4426950408889634
+                    s, err = k @ x * base2, np.abs(k) @ np.abs(x) * base2 * 10 * 2.0 ** -23
+                    best = s.argmax()
+                    assert (np.abs(got[b, i]) <= np.abs(v).max(0) * (1 + 2.0 ** -20)).all()
+                    if (s[best] - err[best] - np.delete(s + err, best)).min() >= 64:
+                        clear += 1
+                        assert (np.abs(got[b, i] - v[best]) <= np.abs(v[best]) * 2.0 ** -20 +
+                                np.abs(v).max(0) * 2.0 ** -50).all(), (b, i)
+    assert clear >= (3 * 2 * H * G * 3) // 4
+
+
 @pytest.mark.parametrize("rep,stride", [(0, 1), (1, 1), (2, 1), (3, 1), (3, 16), (3, 128)])
 def test_reps_of_scales_from_elsewhere(kt, rep, stride):
     """Representatives of blocks whose scales the append does not write, from 2^-30 to 2^30: those
