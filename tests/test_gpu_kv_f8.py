@@ -903,6 +903,49 @@ def test_padded_step_in_two_launches(kt, mode, live):
     assert_status(kt, ws)
 
 
+def test_captured_batch_that_empties_and_fills(kt):
+    """Sequences of a captured batch of more segments than SMs end and begin between replays: each
+    replay gives what eager calls on a workspace of their own give, to the bit."""
+    H, G, B = 8, 4, 32
+    full = [128 * 9 + 5 * b for b in range(B)]
+    p = kt.sparse_params(H * G, 1, 2, 3, kt.KT_REP_QUEST, kt.KT_HEAD_SEPARATE)
+    pg = filled(kt, full, H, 45, params=p)
+    q = torch.randn(B, H * G, 128).half().cuda()
+    pool = reps_pool(kt, pg, p)
+    kt.kt_build_block_reps_f8(pg.kv, p, 0, 100, pool)
+
+    def buffers():
+        return (kt.workspace_f8(kt.KT_OP_SPARSE_STEP, pg.kv, p),
+                torch.zeros(B, H, 3, dtype=torch.int32, device="cuda"),
+                torch.zeros(B, H, dtype=torch.int32, device="cuda"),
+                torch.empty(B, H * G, 128, device="cuda"), torch.empty(B, H * G, 128, device="cuda"))
+
+    def run(ws, sel, cnt, step, dense):
+        kt.kt_sparse_decode_step_f8(q, pg.kv, pool, p, sel, cnt, step, ws)
+        kt.kt_dense_decode_attn_f8(q, pg.kv, H * G, SCALE, dense, ws)
+
+    a, c = buffers(), buffers()
+    run(*a)
+    side, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side), torch.cuda.graph(g, stream=side):
+        run(*a)
+    torch.cuda.current_stream().wait_stream(side)
+    for live in ({}, {3: 200}, None, {0: 1000, 31: 1}, {b: 5 for b in range(B)}, {17: 1237}, None):
+        lens = full if live is None else [live.get(b, 0) for b in range(B)]
+        pg.lens.copy_(torch.tensor(lens, dtype=torch.int32))
+        for x in (a, c):
+            x[3].fill_(float("nan")), x[4].fill_(float("nan"))
+        g.replay()
+        run(*c)
+        assert torch.equal(a[3], c[3]) and torch.equal(a[4], c[4]) and torch.equal(a[2], c[2])
+        assert torch.isfinite(a[3]).all() and torch.isfinite(a[4]).all()
+        pg.host.lens = np.array(lens)
+        check_attention(pg, q, a[4], lambda b, h: range(-(-lens[b] // 128)), G)
+        assert (segment_counters(a[0], B * H) == 0).all()
+    assert_status(kt, a[0])
+
+
 def chosen(kt, pg, sel, cnt, p, b, h):
     u = 0 if p.head_mode == kt.KT_HEAD_SHARED else h
     nb = -(-int(pg.host.lens[b]) // 128)
