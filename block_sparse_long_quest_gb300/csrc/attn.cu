@@ -874,7 +874,7 @@ __device__ __forceinline__ void f8_block(const F8Lane& cx, F8State& z, const uin
   const float b0 = a0 * rv, b1 = a1 * rv;
   // The block's product is summed apart and added rounded to the nearest: the MMA
   // truncates its sum, and over the blocks of a long sequence that would gather to
-  // one side (2.0e-6 of the output's norm at 128K tokens instead of 5.3e-7).
+  // one side (2.0e-6 of the output's norm at 128K tokens instead of about 5e-7).
   float y[8][4];
 #pragma unroll
   for (int i = 0; i < 8; ++i) y[i][0] = y[i][1] = y[i][2] = y[i][3] = 0.0f;

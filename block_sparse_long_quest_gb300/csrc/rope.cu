@@ -29,9 +29,10 @@ struct Params {
 };
 
 // Two groups of four rows in flight a warp (NB 2, at most 80 registers, 24 warps an
-// SM): 8192 tokens of 32 + 8 bf16 heads take 30.0 us, 82% of the measured copy
-// rate.  When the phases still came from the parameters, NB 2 took 31.1, one group
-// at 64 registers 32.1, two at 128 registers 34.6 and at 64 34.2.
+// SM): 8192 tokens of 32 + 8 bf16 heads take 29.9 us, 83% of the measured copy
+// rate; 5003 of 16 + 4 binary32 heads 15.4 us, 74% (626 CTAs at three an SM: a wave
+// and four tenths).  When the phases still came from the parameters, NB 2 took 31.1,
+// one group at 64 registers 32.1, two at 128 registers 34.6 and at 64 34.2.
 template <class T, int M>
 __global__ void __launch_bounds__(THREADS, 3) rope_kernel(const __grid_constant__ Params p) {
   __shared__ __align__(16) float2 cs[WARPS][64];

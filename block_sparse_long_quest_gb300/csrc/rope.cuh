@@ -277,9 +277,9 @@ __device__ __forceinline__ void pack8(const float (&x)[8], uint32_t (&h)[4]) {
 }
 
 // Rotates heads h0 .. h1 - 1 (q's, then k's) of one token by one warp: four head
-// rows at a time, NB times four loaded before the first is stored; rs: rope_prepare; cs: 64 (cos,
-// sin) of shared memory of the warp's own, written behind the first loads and held
-// in registers over the heads.
+// rows at a time, NB times four loaded before the first is stored; rs: rope_prepare;
+// cs: 64 (cos, sin) of shared memory of the warp's own, written behind the first
+// loads and held in registers over the heads.
 template <int M, int NB, class T>
 __device__ __forceinline__ void rope_token(const kt_rope& r, const RopeShared& rs,
                                            float2* cs, int pos, long long t,

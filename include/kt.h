@@ -590,11 +590,12 @@ typedef struct {
 /*
  * Rotates the rows of `tokens` tokens: q into q_out and k into k_out, binary16
  * [tokens][heads][128] contiguous: the two products and their sum in binary32
- * (cos and sin next to exact there), rounded once more to binary16.  positions: int32 [tokens] (device).  Either of q / k may be NULL (with
- * its output); both have one type.  An output may be its own binary16 input
- * where that is contiguous (stride = heads * 128); any other overlap of an
- * output with an input or with the other output is INVALID_ARG.  tokens = 0 does
- * nothing.
+ * (cos and sin next to exact there), rounded once more to binary16.  positions:
+ * int32 [tokens] (device).  Either of q / k may be NULL (with its output); both
+ * have one type.  An output may be its own binary16 input where that is contiguous
+ * (stride = heads * 128; not a part of a packed projection); any other overlap of
+ * an output with an input or with the other output is INVALID_ARG.  tokens = 0
+ * does nothing.
  */
 kt_status kt_apply_rope(const kt_rope* rope, const int32_t* positions, int32_t tokens,
                         const kt_rows* q, void* q_out, const kt_rows* k, void* k_out,
