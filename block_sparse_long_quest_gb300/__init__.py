@@ -44,7 +44,8 @@ EXPORTS = (
     "kt_rope_init", "kt_apply_rope", "kt_workspace_bytes_f8", "kt_reps_pool_bytes_f8",
     "kt_build_block_reps_f8", "kt_append_kv_f8", "kt_read_kv_f8", "kt_sparse_decode_attn_f8",
     "kt_dense_decode_attn_f8", "kt_score_select_blocks_f8", "kt_sparse_decode_step_f8",
-    "kt_decode_layer_f8",
+    "kt_decode_layer_f8", "kt_page_workspace_bytes", "kt_free_seqs", "kt_fork_seqs",
+    "kt_reserve_pages", "kt_compact_pages", "kt_copy_pages",
 )
 
 
@@ -111,6 +112,19 @@ class Rows(ctypes.Structure):
     """kt_rows: head rows of a projection (pointer, token stride in elements, heads, type)."""
     _fields_ = [("data", ctypes.c_void_p), ("stride", ctypes.c_int64), ("heads", ctypes.c_int32),
                 ("dtype", ctypes.c_int32)]
+
+
+class PageMap(ctypes.Structure):
+    """kt_page_map: block table, lengths, pages held and reference counts."""
+    _fields_ = [("block_table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
+                ("num_blocks", ctypes.c_void_p), ("page_refs", ctypes.c_void_p),
+                ("batch", ctypes.c_int32), ("block_size", ctypes.c_int32),
+                ("max_blocks_per_seq", ctypes.c_int32), ("num_pages", ctypes.c_int32)]
+
+
+class PagePool(ctypes.Structure):
+    """kt_page_pool: a pool's address and the bytes of a page."""
+    _fields_ = [("data", ctypes.c_void_p), ("page_bytes", ctypes.c_int64)]
 
 
 class ReusePolicy(ctypes.Structure):
@@ -196,6 +210,14 @@ def _load():
                                                     vp, vp, vp, sz, vp]),
         "kt_decode_layer_f8": (ctypes.c_int, [P(ReusePolicy), i32, i32, vp, P(PagedKVF8), vp,
                                               P(SparseParams), vp, vp, vp, vp, sz, vp]),
+    })
+    sig.update({
+        "kt_page_workspace_bytes": (ctypes.c_int, [P(PageMap), P(sz)]),
+        "kt_free_seqs": (ctypes.c_int, [P(PageMap), vp, i32, vp, sz, vp]),
+        "kt_fork_seqs": (ctypes.c_int, [P(PageMap), vp, vp, i32, vp, vp, vp, sz, vp]),
+        "kt_reserve_pages": (ctypes.c_int, [P(PageMap), vp, vp, sz, vp]),
+        "kt_compact_pages": (ctypes.c_int, [P(PageMap), vp, vp, vp, vp, vp, sz, vp]),
+        "kt_copy_pages": (ctypes.c_int, [P(PagePool), i32, i32, vp, vp, i32, vp, sz, vp]),
     })
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -618,6 +640,105 @@ def kt_decode_layer_f8(pol, token_idx, layer_idx, q, kv, reps_pool, params, hist
                                   _ptr(hist_sel), _ptr(hist_cnt), _ptr(out), _ptr(ws),
                                   ws.numel(), _stream(stream)),
            "kt_decode_layer_f8")
+
+
+def page_map(block_table, seq_lens, num_blocks, page_refs) -> PageMap:
+    """block_table: int32 [B][MB]; seq_lens, num_blocks: int32 [B]; page_refs: int32 [P]."""
+    batch, width = block_table.shape
+    for t, n in ((block_table, batch * width), (seq_lens, batch), (num_blocks, batch),
+                 (page_refs, 1)):
+        _check_int32(t, n, "page_map")
+    return PageMap(_ptr(block_table), _ptr(seq_lens), _ptr(num_blocks), _ptr(page_refs), batch, 128,
+                   width, page_refs.numel())
+
+
+def kt_page_workspace_bytes(map) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib.kt_page_workspace_bytes(_byref(map), _byref(n)), "kt_page_workspace_bytes")
+    return int(n.value)
+
+
+def page_workspace(map, device="cuda"):
+    """A zero-filled workspace tensor (uint8) for the calls on a page map."""
+    import torch
+    ws = torch.empty(kt_page_workspace_bytes(map), dtype=torch.uint8, device=device)
+    kt_workspace_init(ws)
+    return ws
+
+
+class PagePools:
+    """The kt_page_pool array of contiguous tensors [P][...] (K, V, codes, scales and
+    representatives of every layer)."""
+
+    def __init__(self, tensors):
+        n = tensors[0].shape[0] if tensors else 0
+        if n == 0 or any(t.shape[0] != n or not t.is_contiguous() for t in tensors):
+            raise KtError(KT_ERR_INVALID_ARG, "page_pools")
+        self.num_pages = n
+        self.array = (PagePool * len(tensors))(
+            *[PagePool(t.data_ptr(), t.numel() // n * t.element_size()) for t in tensors])
+
+
+def page_pools(tensors) -> PagePools:
+    return PagePools(tensors)
+
+
+def kt_free_seqs(map, seqs, ws, stream=None):
+    """Frees the sequences seqs (int32 [n])."""
+    n = seqs.numel()
+    _check_int32(seqs, n, "kt_free_seqs")
+    _check(lib.kt_free_seqs(_byref(map), _ptr(seqs), n, _ptr(ws), ws.numel(), _stream(stream)),
+           "kt_free_seqs")
+
+
+def _check_moves(moves, num_moves, n, call):
+    if moves is None or num_moves is None:
+        raise KtError(KT_ERR_INVALID_ARG, call)
+    _check_int32(moves, 2 * n, call)
+    _check_int32(num_moves, 1, call)
+
+
+def kt_fork_seqs(map, src, dst, moves, num_moves, ws, stream=None):
+    """Slots dst become copies of the sequences src (int32 [n] both); moves: int32 [n][2],
+    num_moves: int32 [1]."""
+    n = src.numel()
+    _check_int32(src, n, "kt_fork_seqs")
+    _check_int32(dst, n, "kt_fork_seqs")
+    if dst.numel() != n:
+        raise KtError(KT_ERR_INVALID_ARG, "kt_fork_seqs")
+    _check_moves(moves, num_moves, n, "kt_fork_seqs")
+    _check(lib.kt_fork_seqs(_byref(map), _ptr(src), _ptr(dst), n, _ptr(moves), _ptr(num_moves),
+                            _ptr(ws), ws.numel(), _stream(stream)),
+           "kt_fork_seqs")
+
+
+def kt_reserve_pages(map, ws, new_tokens=None, stream=None):
+    """Pages for new_tokens (int32 [batch]; None: one) more tokens of every sequence."""
+    _check_int32(new_tokens, map.batch, "kt_reserve_pages")
+    _check(lib.kt_reserve_pages(_byref(map), _ptr(new_tokens), _ptr(ws), ws.numel(),
+                                _stream(stream)),
+           "kt_reserve_pages")
+
+
+def kt_compact_pages(map, moves, num_moves, ws, *, new_table=None, new_refs=None, stream=None):
+    """moves: int32 [num_pages // 2][2], num_moves: int32 [1]; new_table / new_refs None: in
+    place."""
+    _check_moves(moves, num_moves, map.num_pages // 2, "kt_compact_pages")
+    _check_int32(new_table, map.batch * map.max_blocks_per_seq, "kt_compact_pages")
+    _check_int32(new_refs, map.num_pages, "kt_compact_pages")
+    _check(lib.kt_compact_pages(_byref(map), _ptr(new_table), _ptr(new_refs), _ptr(moves),
+                                _ptr(num_moves), _ptr(ws), ws.numel(), _stream(stream)),
+           "kt_compact_pages")
+
+
+def kt_copy_pages(pools, moves, num_moves, ws, stream=None):
+    """Copies the pages of moves (as kt_fork_seqs and kt_compact_pages write them) in all pools
+    (a PagePools)."""
+    n = moves.numel() // 2
+    _check_moves(moves, num_moves, n, "kt_copy_pages")
+    _check(lib.kt_copy_pages(pools.array, len(pools.array), pools.num_pages, _ptr(moves),
+                             _ptr(num_moves), n, _ptr(ws), ws.numel(), _stream(stream)),
+           "kt_copy_pages")
 
 
 def kt_set_phase_stamps(stamps, max_ctas: int = 0):

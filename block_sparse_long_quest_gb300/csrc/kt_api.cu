@@ -1490,6 +1490,156 @@ kt_status kt_decode_layer_f8(const kt_reuse_policy* pol, int32_t token_idx, int3
   return kt_sparse_decode_attn_f8(q, kv, p, sel, cnt, out, ws, ws_bytes, stream);
 }
 
+// ---- sequences that share pages ----------------------------------------------
+namespace {
+constexpr int MAX_MAP_BATCH = MAX_SEGS;
+
+kt_status check_map(const kt_page_map* m) {
+  if (!m || !m->block_table || !m->seq_lens || !m->num_blocks || !m->page_refs)
+    return KT_ERR_INVALID_ARG;
+  if (!aligned16(m->block_table) || !aligned16(m->seq_lens) || !aligned16(m->num_blocks) ||
+      !aligned16(m->page_refs))
+    return KT_ERR_INVALID_ARG;
+  if (m->batch < 1 || m->max_blocks_per_seq < 1 || m->num_pages < 1) return KT_ERR_INVALID_ARG;
+  if (m->block_size != BS || m->batch > MAX_MAP_BATCH) return KT_ERR_UNSUPPORTED;
+  if ((long long)m->max_blocks_per_seq * BS > 0x7FFFFFFFLL ||
+      m->num_pages > 0x7FFFFFFF - 4096 * 8)
+    return KT_ERR_UNSUPPORTED;
+  return KT_OK;
+}
+
+size_t page_ws_bytes(const kt_page_map* m) {
+  return 256 + 2 * align256((size_t)m->num_pages * 4);
+}
+
+kt_status pages_launch(const kt_page_map* m, void* ws, size_t ws_bytes, PagesLaunch* a) {
+  if (!ws || !aligned16(ws)) return KT_ERR_INVALID_ARG;
+  if (ws_bytes < page_ws_bytes(m)) return KT_ERR_WORKSPACE_TOO_SMALL;
+  std::memset(a, 0, sizeof(*a));
+  a->table = m->block_table;
+  a->lens = m->seq_lens;
+  a->blocks = m->num_blocks;
+  a->refs = m->page_refs;
+  a->status = at<int>(ws, 0);
+  a->list = at<int32_t>(ws, 256);
+  a->list2 = at<int32_t>(ws, 256 + align256((size_t)m->num_pages * 4));
+  a->batch = m->batch;
+  a->max_blocks = m->max_blocks_per_seq;
+  a->P = m->num_pages;
+  return KT_OK;
+}
+}  // namespace
+
+kt_status kt_page_workspace_bytes(const kt_page_map* map, size_t* bytes) {
+  const kt_status s = check_map(map);
+  if (s != KT_OK) return s;
+  if (!bytes) return KT_ERR_INVALID_ARG;
+  *bytes = page_ws_bytes(map);
+  return KT_OK;
+}
+
+kt_status kt_free_seqs(const kt_page_map* map, const int32_t* seqs, int32_t n, void* ws,
+                       size_t ws_bytes, kt_stream_t stream) {
+  kt_status s = check_map(map);
+  if (s != KT_OK) return s;
+  if (!seqs || !aligned16(seqs) || n < 1) return KT_ERR_INVALID_ARG;
+  PagesLaunch a;
+  s = pages_launch(map, ws, ws_bytes, &a);
+  if (s != KT_OK) return s;
+  a.a = seqs;
+  a.n = n;
+  return cuda_status(launch_free_seqs(a, (cudaStream_t)stream));
+}
+
+kt_status kt_fork_seqs(const kt_page_map* map, const int32_t* src, const int32_t* dst, int32_t n,
+                       int32_t* moves, int32_t* num_moves, void* ws, size_t ws_bytes,
+                       kt_stream_t stream) {
+  kt_status s = check_map(map);
+  if (s != KT_OK) return s;
+  if (!src || !dst || !moves || !num_moves || !aligned16(src) || !aligned16(dst) ||
+      !aligned16(moves) || !aligned16(num_moves) || n < 1 || n > map->batch)
+    return KT_ERR_INVALID_ARG;
+  PagesLaunch a;
+  s = pages_launch(map, ws, ws_bytes, &a);
+  if (s != KT_OK) return s;
+  a.a = src;
+  a.b = dst;
+  a.n = n;
+  a.moves = moves;
+  a.num_moves = num_moves;
+  return cuda_status(launch_fork_seqs(a, (cudaStream_t)stream));
+}
+
+kt_status kt_reserve_pages(const kt_page_map* map, const int32_t* new_tokens, void* ws,
+                           size_t ws_bytes, kt_stream_t stream) {
+  kt_status s = check_map(map);
+  if (s != KT_OK) return s;
+  if (new_tokens && !aligned16(new_tokens)) return KT_ERR_INVALID_ARG;
+  PagesLaunch a;
+  s = pages_launch(map, ws, ws_bytes, &a);
+  if (s != KT_OK) return s;
+  a.a = new_tokens;
+  return cuda_status(launch_reserve_pages(a, (cudaStream_t)stream));
+}
+
+kt_status kt_compact_pages(const kt_page_map* map, int32_t* new_table, int32_t* new_refs,
+                           int32_t* moves, int32_t* num_moves, void* ws, size_t ws_bytes,
+                           kt_stream_t stream) {
+  kt_status s = check_map(map);
+  if (s != KT_OK) return s;
+  if (!moves || !num_moves || !aligned16(moves) || !aligned16(num_moves) ||
+      !new_table != !new_refs || !aligned16(new_table) || !aligned16(new_refs))
+    return KT_ERR_INVALID_ARG;
+  PagesLaunch a;
+  s = pages_launch(map, ws, ws_bytes, &a);
+  if (s != KT_OK) return s;
+  const size_t tb = (size_t)map->batch * map->max_blocks_per_seq * 4;
+  const size_t rb = (size_t)map->num_pages * 4;
+  if (new_table) {
+    // apart from each other and from the map's own, or exactly those
+    const Bytes t = bytes_of(new_table, tb), r = bytes_of(new_refs, rb);
+    const Bytes t0 = bytes_of(map->block_table, tb), r0 = bytes_of(map->page_refs, rb);
+    if (overlap(t, r) || overlap(t, r0) || overlap(r, t0) ||
+        (overlap(t, t0) && new_table != map->block_table) ||
+        (overlap(r, r0) && new_refs != map->page_refs))
+      return KT_ERR_INVALID_ARG;
+  }
+  a.new_table = new_table ? new_table : map->block_table;
+  a.new_refs = new_refs ? new_refs : map->page_refs;
+  a.moves = moves;
+  a.num_moves = num_moves;
+  return cuda_status(launch_compact_pages(a, (cudaStream_t)stream));
+}
+
+kt_status kt_copy_pages(const kt_page_pool* pools, int32_t n_pools, int32_t num_pages,
+                        const int32_t* moves, const int32_t* num_moves, int32_t max_moves,
+                        void* ws, size_t ws_bytes, kt_stream_t stream) {
+  if (!pools || n_pools < 1 || num_pages < 1 || !moves || !num_moves || max_moves < 1 || !ws ||
+      ws_bytes < 256 || !aligned16(moves) || !aligned16(num_moves) || !aligned16(ws))
+    return KT_ERR_INVALID_ARG;
+  if (n_pools > MAX_PAGE_POOLS) return KT_ERR_UNSUPPORTED;
+  long long units = 0;
+  for (int i = 0; i < n_pools; ++i) {
+    if (!pools[i].data || !aligned16(pools[i].data) || pools[i].page_bytes < 4 ||
+        pools[i].page_bytes % 4 != 0)
+      return KT_ERR_INVALID_ARG;
+    if (pools[i].page_bytes > (1ll << 32)) return KT_ERR_UNSUPPORTED;
+    units += pools[i].page_bytes / 1024 + 1;
+  }
+  if (units > 0x7FFFFFFFll) return KT_ERR_UNSUPPORTED;
+  CopyLaunch a;
+  a.pools = pools;
+  a.n_pools = n_pools;
+  a.moves = moves;
+  a.num_moves = num_moves;
+  a.status = at<int>(ws, 0);
+  a.max_moves = max_moves;
+  a.P = num_pages;
+  a.num_sms = num_sms();
+  if (a.num_sms <= 0) return KT_ERR_CUDA;
+  return cuda_status(launch_copy_pages(a, (cudaStream_t)stream));
+}
+
 kt_status kt_read_device_status(void* ws, size_t ws_bytes, kt_stream_t stream,
                                 int32_t* device_status) {
   if (!ws || ws_bytes < 256 || !device_status) return KT_ERR_INVALID_ARG;

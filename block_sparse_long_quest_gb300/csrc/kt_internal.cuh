@@ -688,6 +688,39 @@ struct ReadF8Launch {
 };
 cudaError_t launch_read_f8(const ReadF8Launch& a, cudaStream_t stream);
 
+// Pages shared by sequences (kt_page_map).
+constexpr int MAX_PAGE_POOLS = 256;
+struct PagesLaunch {
+  int32_t* table;
+  int32_t* lens;
+  int32_t* blocks;
+  int32_t* refs;
+  int* status;
+  int32_t* list;   // workspace [P]
+  int32_t* list2;  // workspace [P]
+  const int32_t* a;  // fork: sources; free: sequences; reserve: new tokens (nullable)
+  const int32_t* b;  // fork: destinations
+  int32_t* moves;
+  int32_t* num_moves;
+  int32_t* new_table;  // compact (may be table)
+  int32_t* new_refs;   // compact (may be refs)
+  int n, batch, max_blocks, P;
+};
+cudaError_t launch_free_seqs(const PagesLaunch& a, cudaStream_t stream);
+cudaError_t launch_fork_seqs(const PagesLaunch& a, cudaStream_t stream);
+cudaError_t launch_reserve_pages(const PagesLaunch& a, cudaStream_t stream);
+cudaError_t launch_compact_pages(const PagesLaunch& a, cudaStream_t stream);
+
+struct CopyLaunch {
+  const kt_page_pool* pools;  // host
+  int n_pools;
+  const int32_t* moves;
+  const int32_t* num_moves;
+  int* status;
+  int max_moves, P, num_sms;
+};
+cudaError_t launch_copy_pages(const CopyLaunch& a, cudaStream_t stream);
+
 struct RepsLaunch {
   const __half* k_pool;
   const int32_t* table;

@@ -722,6 +722,114 @@ kt_status kt_decode_layer_f8(const kt_reuse_policy* pol, int32_t token_idx, int3
                              float* out, void* ws, size_t ws_bytes, kt_stream_t stream);
 
 /*
+ * ---- sequences that share pages ------------------------------------------------
+ * Several sequences of a batch may hold the same page of a paged cache: the samples
+ * of one prompt, the chats behind one system prompt.  A kt_page_map is the block
+ * table and the lengths that the caches of all layers are used with, and beside them
+ * how many pages each sequence holds and how many sequences hold each page:
+ *   block_table : as in kt_paged_kv; sequence b holds the pages
+ *                 block_table[b][0 .. num_blocks[b] - 1].
+ *   seq_lens    : tokens of each sequence, at most 128 * num_blocks[b].
+ *   num_blocks  : int32 [batch].
+ *   page_refs   : int32 [num_pages], the table entries that hold each page; a page
+ *                 is free where that is 0 (or less).
+ * All four are written by the calls below.  A slot of the batch that holds no
+ * sequence has length 0 and num_blocks 0.  Free pages are always taken lowest first,
+ * requests in the order of the call, so the outcome is the same every time.  Only
+ * whole blocks are ever shared, so appending (kt_append_kv, kt_append_kv_f8) writes
+ * into pages of one sequence.  batch is at most 2048 (UNSUPPORTED beyond).  Pointers
+ * are 16-byte aligned device pointers; calls that share a map, a pool or a workspace
+ * must not overlap on the GPU.
+ */
+typedef struct {
+  int32_t* block_table;
+  int32_t* seq_lens;
+  int32_t* num_blocks;
+  int32_t* page_refs;
+  int32_t batch;
+  int32_t block_size;          /* 128 */
+  int32_t max_blocks_per_seq;
+  int32_t num_pages;
+} kt_page_map;
+
+/* Workspace of the calls below (zero-filled before its first use): a status header of
+ * 256 bytes and two int32 per page. */
+kt_status kt_page_workspace_bytes(const kt_page_map* map, size_t* bytes);
+
+/*
+ * Frees n sequences (n >= 1): seqs int32 [n].  Their pages lose a holder each,
+ * their lengths and num_blocks become 0; table entries stay as they were.  A sequence
+ * listed twice is freed once.  An index or table entry out of range, and a page that
+ * nobody held, record KT_ERR_DEVICE_CHECK and are skipped.
+ */
+kt_status kt_free_seqs(const kt_page_map* map, const int32_t* seqs, int32_t n, void* ws,
+                       size_t ws_bytes, kt_stream_t stream);
+
+/*
+ * Forks n sequences (1 <= n <= batch): slot dst[i], which holds none, becomes a copy of
+ * sequence src[i] as it was before the call.  The whole blocks' pages are shared; a
+ * partial last block gets a page of its own, and moves[r] = (from, to) says which page
+ * kt_copy_pages has to copy for the r-th fork that has one.  Entries behind the last
+ * block (pages reserved ahead) are not taken over.
+ *   src, dst  : int32 [n]; a source may be listed many times.
+ *   moves     : int32 [n][2]; num_moves: int32 [1].  Entries of moves from num_moves on
+ *               stay as they were.
+ * Refused, recording KT_ERR_DEVICE_CHECK and leaving the slot empty: indices out of
+ * range, a slot that holds a sequence, a slot listed before, a source whose length and
+ * num_blocks do not agree, and the forks from the first one on (of those with a partial
+ * block) for which no page is free.  A table entry out of range records it too and is
+ * taken over as it is.
+ */
+kt_status kt_fork_seqs(const kt_page_map* map, const int32_t* src, const int32_t* dst, int32_t n,
+                       int32_t* moves, int32_t* num_moves, void* ws, size_t ws_bytes,
+                       kt_stream_t stream);
+
+/*
+ * Gives every sequence b the pages that new_tokens[b] more tokens need (int32 [batch],
+ * NULL: one token each, empty slots included), as kt_append_kv and kt_append_kv_f8 expect
+ * them.  Pages reserved before are counted, so a call repeated without an append changes
+ * nothing.  A sequence whose table has no room, or whose length, num_blocks or count make
+ * no sense, records KT_ERR_DEVICE_CHECK and gets none; where the pages run out, that is
+ * recorded too and the sequence at which they do and all later ones that need any get none.
+ */
+kt_status kt_reserve_pages(const kt_page_map* map, const int32_t* new_tokens, void* ws,
+                           size_t ws_bytes, kt_stream_t stream);
+
+/*
+ * Moves the pages in use to the front: with n pages in use, those from page n on move,
+ * lowest first, to the free pages below n, lowest first.  moves (int32 [num_pages / 2][2])
+ * and num_moves as in kt_fork_seqs; kt_copy_pages then copies the pages (of every pool
+ * that goes with the map), before anything else reads or writes them.
+ *   new_table, new_refs : int32, as block_table and page_refs, receive the new table (entries
+ *                 of held pages; others stay as they were) and counts; both NULL: the map's
+ *                 own are changed.  A table entry that is out of range or counted as free
+ *                 records KT_ERR_DEVICE_CHECK and is taken over as it is.
+ */
+kt_status kt_compact_pages(const kt_page_map* map, int32_t* new_table, int32_t* new_refs,
+                           int32_t* moves, int32_t* num_moves, void* ws, size_t ws_bytes,
+                           kt_stream_t stream);
+
+/* One pool of a cache: page p is the page_bytes bytes at data + p * page_bytes.  K, V, codes,
+ * scales and representatives of every layer are pools. */
+typedef struct {
+  void* data;          /* 16-byte aligned */
+  int64_t page_bytes;  /* a multiple of 4 */
+} kt_page_pool;
+
+/*
+ * Copies page moves[r][0] onto page moves[r][1] in each of n_pools pools (host array, read
+ * before the call returns; at most 256, UNSUPPORTED beyond) for r < *num_moves, in one launch.
+ *   moves, num_moves : device, as kt_fork_seqs and kt_compact_pages write them: no page is
+ *                      copied onto twice, nor both copied and copied onto.
+ *   max_moves        : entries that moves has room for.
+ * A page out of range, or more moves than max_moves, record KT_ERR_DEVICE_CHECK and are
+ * skipped.  ws: any zero-initialised workspace of at least 256 bytes (its header is used).
+ */
+kt_status kt_copy_pages(const kt_page_pool* pools, int32_t n_pools, int32_t num_pages,
+                        const int32_t* moves, const int32_t* num_moves, int32_t max_moves,
+                        void* ws, size_t ws_bytes, kt_stream_t stream);
+
+/*
  * kt_sparse_decode_attn without a workspace, for callers that cannot allocate
  * device memory: for example a kernel plugged into an engine or framework
  * that hands it only its input and output buffers and owns every other byte
