@@ -23,7 +23,7 @@ KT_ERR_TIMEOUT = 6
 KT_REP_MAX, KT_REP_MEAN, KT_REP_QUEST, KT_REP_FIX, KT_REP_DYNAMIC = 0, 1, 2, 3, 4
 KT_HEAD_SHARED, KT_HEAD_SEPARATE = 0, 1
 (KT_OP_SCORE_SELECT, KT_OP_SPARSE_ATTN, KT_OP_DENSE_ATTN, KT_OP_SPARSE_STEP,
- KT_OP_DYNAMIC_REPS, KT_OP_PRESELECT) = 0, 1, 2, 3, 4, 5
+ KT_OP_DYNAMIC_REPS, KT_OP_PRESELECT, KT_OP_PREFIX_ATTN) = 0, 1, 2, 3, 4, 5, 6
 KT_LAYER_DENSE, KT_LAYER_SELECT, KT_LAYER_REUSE = 0, 1, 2
 KT_F16, KT_BF16, KT_F32 = 0, 1, 2
 KT_ROPE_HALF, KT_ROPE_PAIRS = 0, 1
@@ -45,7 +45,7 @@ EXPORTS = (
     "kt_build_block_reps_f8", "kt_append_kv_f8", "kt_read_kv_f8", "kt_sparse_decode_attn_f8",
     "kt_dense_decode_attn_f8", "kt_score_select_blocks_f8", "kt_sparse_decode_step_f8",
     "kt_decode_layer_f8", "kt_page_workspace_bytes", "kt_free_seqs", "kt_fork_seqs",
-    "kt_reserve_pages", "kt_compact_pages", "kt_copy_pages",
+    "kt_reserve_pages", "kt_compact_pages", "kt_copy_pages", "kt_prefix_decode_attn",
 )
 
 
@@ -112,6 +112,12 @@ class Rows(ctypes.Structure):
     """kt_rows: head rows of a projection (pointer, token stride in elements, heads, type)."""
     _fields_ = [("data", ctypes.c_void_p), ("stride", ctypes.c_int64), ("heads", ctypes.c_int32),
                 ("dtype", ctypes.c_int32)]
+
+
+class PrefixGroups(ctypes.Structure):
+    """kt_prefix_groups: consecutive sequences of each group and their shared blocks."""
+    _fields_ = [("cu_groups", ctypes.c_void_p), ("prefix_blocks", ctypes.c_void_p),
+                ("groups", ctypes.c_int32)]
 
 
 class PageMap(ctypes.Structure):
@@ -217,6 +223,8 @@ def _load():
         "kt_fork_seqs": (ctypes.c_int, [P(PageMap), vp, vp, i32, vp, vp, vp, sz, vp]),
         "kt_reserve_pages": (ctypes.c_int, [P(PageMap), vp, vp, sz, vp]),
         "kt_compact_pages": (ctypes.c_int, [P(PageMap), vp, vp, vp, vp, vp, sz, vp]),
+        "kt_prefix_decode_attn": (ctypes.c_int, [vp, P(PagedKV), P(PrefixGroups), i32,
+                                                 ctypes.c_float, vp, vp, sz, vp]),
         "kt_copy_pages": (ctypes.c_int, [P(PagePool), i32, i32, vp, vp, i32, vp, sz, vp]),
     })
     for name, (res, args) in sig.items():
@@ -640,6 +648,21 @@ def kt_decode_layer_f8(pol, token_idx, layer_idx, q, kv, reps_pool, params, hist
                                   _ptr(hist_sel), _ptr(hist_cnt), _ptr(out), _ptr(ws),
                                   ws.numel(), _stream(stream)),
            "kt_decode_layer_f8")
+
+
+def prefix_groups(cu_groups, prefix_blocks) -> PrefixGroups:
+    """cu_groups: int32 [groups + 1], prefix_blocks: int32 [groups]."""
+    n = prefix_blocks.numel()
+    _check_int32(prefix_blocks, n, "prefix_groups")
+    _check_int32(cu_groups, n + 1, "prefix_groups")
+    return PrefixGroups(_ptr(cu_groups), _ptr(prefix_blocks), n)
+
+
+def kt_prefix_decode_attn(q, kv, groups, num_q_heads, softmax_scale, out, ws, stream=None):
+    _check(lib.kt_prefix_decode_attn(_ptr(q), _byref(kv), _byref(groups), num_q_heads,
+                                     softmax_scale, _ptr(out), _ptr(ws), ws.numel(),
+                                     _stream(stream)),
+           "kt_prefix_decode_attn")
 
 
 def page_map(block_table, seq_lens, num_blocks, page_refs) -> PageMap:

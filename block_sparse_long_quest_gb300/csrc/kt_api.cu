@@ -388,7 +388,7 @@ size_t kt_reps_pool_bytes(const kt_paged_kv* kv, const kt_sparse_params* p) {
 kt_status kt_workspace_bytes(kt_op op, const kt_paged_kv* kv, const kt_sparse_params* p,
                              int32_t T, size_t* bytes) {
   if (!bytes) return KT_ERR_INVALID_ARG;
-  if (op < KT_OP_SCORE_SELECT || op > KT_OP_PRESELECT) return KT_ERR_INVALID_ARG;
+  if (op < KT_OP_SCORE_SELECT || op > KT_OP_PREFIX_ATTN) return KT_ERR_INVALID_ARG;
   kt_status s = check_kv(kv);
   if (s != KT_OK) return s;
   if (op == KT_OP_DENSE_ATTN) {
@@ -400,6 +400,9 @@ kt_status kt_workspace_bytes(kt_op op, const kt_paged_kv* kv, const kt_sparse_pa
   if (s != KT_OK) return s;
   if (op == KT_OP_DYNAMIC_REPS && T < 1) return KT_ERR_INVALID_ARG;
   *bytes = layout(op, kv, p, T).total;
+  // behind the other calls' regions
+  if (op == KT_OP_PREFIX_ATTN)
+    *bytes += prefix_ws_bytes(kv->batch, kv->num_kv_heads, p->num_q_heads / kv->num_kv_heads);
   return KT_OK;
 }
 
@@ -962,6 +965,66 @@ kt_status kt_dense_decode_attn(const void* q, const kt_paged_kv* kv, int32_t num
   if (ws_bytes < L.total) return KT_ERR_WORKSPACE_TOO_SMALL;
   return attn_impl(q, kv, num_q_heads, softmax_scale, &p, nullptr, nullptr, out, ws, L, true,
                    false, (cudaStream_t)stream);
+}
+
+// ---- attention behind shared prefixes ------------------------------------------
+namespace {
+// The kernel counts the blocks of all (sequence, KV head) together in 32 bits.
+bool prefix_units_ok(const kt_paged_kv& kv) {
+  return (long long)kv.batch * kv.num_kv_heads * (kv.max_blocks_per_seq + 2ll) <= 0x3FFFFFFFll;
+}
+
+kt_status prefix_impl(const void* q, const kt_paged_kv* kv, const kt_prefix_groups* groups,
+                      int32_t num_q_heads, float softmax_scale, float* out, void* ws,
+                      size_t ws_bytes, cudaStream_t stream) {
+  const kt_status s = check_heads(kv, num_q_heads, softmax_scale);
+  if (s != KT_OK) return s;
+  if (!q || !out || !ws || !aligned16(q) || !aligned16(out) || !aligned16(ws))
+    return KT_ERR_INVALID_ARG;
+  if (!groups || !groups->cu_groups || !groups->prefix_blocks || !aligned16(groups->cu_groups) ||
+      !aligned16(groups->prefix_blocks) || groups->groups < 1)
+    return KT_ERR_INVALID_ARG;
+  if (!prefix_units_ok(*kv) || groups->groups > MAX_SEGS) return KT_ERR_UNSUPPORTED;
+  const int G = num_q_heads / kv->num_kv_heads;
+  // the last bytes of the workspace: what lies before them keeps the other calls' state
+  const size_t need = prefix_ws_bytes(kv->batch, kv->num_kv_heads, G);
+  if (ws_bytes < 256 + need) return KT_ERR_WORKSPACE_TOO_SMALL;
+  CUtensorMap kmap, vmap;
+  if (!make_pool_map(&kmap, kv->k_pool, kv) || !make_pool_map(&vmap, kv->v_pool, kv))
+    return KT_ERR_CUDA;
+  PrefixLaunch a;
+  std::memset(&a, 0, sizeof(a));
+  a.kmap = &kmap;
+  a.vmap = &vmap;
+  a.q = static_cast<const __half*>(q);
+  a.table = kv->block_table;
+  a.seq_lens = kv->seq_lens;
+  a.cu = groups->cu_groups;
+  a.prefix = groups->prefix_blocks;
+  a.out = out;
+  a.status = at<int>(ws, 0);
+  a.ws = at<uint8_t>(ws, (ws_bytes - need) & ~(size_t)255);
+  a.B = kv->batch;
+  a.H_kv = kv->num_kv_heads;
+  a.G = G;
+  a.groups = groups->groups;
+  a.max_blocks = kv->max_blocks_per_seq;
+  a.P = kv->num_pages;
+  a.ctas = cta_budget();
+  if (a.ctas <= 0) return KT_ERR_CUDA;
+  a.scale_log2 = softmax_scale * 1.4426950408889634f;
+  return cuda_status(launch_prefix(a, stream));
+}
+}  // namespace
+
+kt_status kt_prefix_decode_attn(const void* q, const kt_paged_kv* kv,
+                                const kt_prefix_groups* groups, int32_t num_q_heads,
+                                float softmax_scale, float* out, void* ws, size_t ws_bytes,
+                                kt_stream_t stream) {
+  const kt_status s = check_kv(kv);
+  if (s != KT_OK) return s;
+  return prefix_impl(q, kv, groups, num_q_heads, softmax_scale, out, ws, ws_bytes,
+                     (cudaStream_t)stream);
 }
 
 // ---- decoding with selection reuse [LC §4.5, §4.6 decode loop] --------------

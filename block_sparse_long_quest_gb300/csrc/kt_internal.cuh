@@ -688,6 +688,25 @@ struct ReadF8Launch {
 };
 cudaError_t launch_read_f8(const ReadF8Launch& a, cudaStream_t stream);
 
+// Decode attention behind shared prefixes.
+constexpr int PREFIX_MAX_CTAS = 192;  // the workspace is sized for this many CTAs
+struct PrefixLaunch {
+  const CUtensorMap* kmap;
+  const CUtensorMap* vmap;
+  const __half* q;
+  const int32_t* table;
+  const int32_t* seq_lens;
+  const int32_t* cu;      // [groups + 1]
+  const int32_t* prefix;  // [groups]
+  float* out;
+  int* status;
+  void* ws;  // prefix_ws_bytes(B, H_kv, G) bytes
+  int B, H_kv, G, groups, max_blocks, P, ctas;
+  float scale_log2;
+};
+cudaError_t launch_prefix(const PrefixLaunch& a, cudaStream_t stream);
+size_t prefix_ws_bytes(int B, int H_kv, int G);
+
 // Pages shared by sequences (kt_page_map).
 constexpr int MAX_PAGE_POOLS = 256;
 struct PagesLaunch {

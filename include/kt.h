@@ -79,7 +79,8 @@ typedef enum {
   KT_OP_DENSE_ATTN = 2,
   KT_OP_SPARSE_STEP = 3,   /* score/select + sparse attention in one call */
   KT_OP_DYNAMIC_REPS = 4,
-  KT_OP_PRESELECT = 5      /* kt_preselect_blocks (needs T like KT_OP_DYNAMIC_REPS) */
+  KT_OP_PRESELECT = 5,     /* kt_preselect_blocks (needs T like KT_OP_DYNAMIC_REPS) */
+  KT_OP_PREFIX_ATTN = 6    /* kt_prefix_decode_attn */
 } kt_op;
 
 /*
@@ -437,6 +438,45 @@ kt_status kt_sparse_decode_step_host(const void* q_host, void* q_dev, const kt_p
 kt_status kt_dense_decode_attn(const void* q, const kt_paged_kv* kv, int32_t num_q_heads,
                                float softmax_scale, float* out, void* ws, size_t ws_bytes,
                                kt_stream_t stream);
+
+/*
+ * ---- attention behind shared prefixes ----------------------------------------
+ * kt_dense_decode_attn for a batch whose sequences share prefixes (kt_fork_seqs, a common
+ * system prompt, several questions to one document): each shared prefix is read once for
+ * all its sequences, whose queries meet it as the rows of one matrix on the tensor cores.
+ *   cu_groups     : int32 [groups + 1] (device), not decreasing, within [0, batch]: group g
+ *                   is the sequences cu_groups[g] .. cu_groups[g + 1] - 1.  Sequences of no
+ *                   group are attended by themselves.
+ *   prefix_blocks : int32 [groups] (device): the first prefix_blocks[g] entries of the block
+ *                   table are the same pages for all sequences of group g that hold that many
+ *                   whole blocks; the others (shorter ones, empty slots) are attended by
+ *                   themselves.  The call reads these pages in the table of the group's first
+ *                   such sequence only.
+ *   groups        : 1 .. 2048; a group may be empty.
+ */
+typedef struct {
+  const int32_t* cu_groups;
+  const int32_t* prefix_blocks;
+  int32_t groups;
+} kt_prefix_groups;
+
+/*
+ * Arguments, results and errors as kt_dense_decode_attn (fp32 out; rows of an empty sequence
+ * are zeros).  Groups out of order or out of range record KT_ERR_DEVICE_CHECK and every
+ * sequence is attended by itself; a prefix_blocks entry outside [0, max_blocks_per_seq] records
+ * it and counts as 0; a page outside the pool records it and its block is skipped.  Pool rows
+ * behind seq_lens[b] in the last page may be anything.  The probabilities are two binary16
+ * parts of either sign, so an infinite V value makes its channel of the rows that attend it
+ * infinite or NaN.  Three launches.  The groups, lengths and
+ * tables are read on the device, so a captured call follows their changes.
+ * Workspace: KT_OP_PREFIX_ATTN of the same shapes; the call uses its header and its last bytes,
+ * so ws_bytes is the size kt_workspace_bytes reported (a workspace of that size also serves the
+ * other calls with the parameters it was sized for).  At most 192 CTAs are used.
+ */
+kt_status kt_prefix_decode_attn(const void* q, const kt_paged_kv* kv,
+                                const kt_prefix_groups* groups, int32_t num_q_heads,
+                                float softmax_scale, float* out, void* ws, size_t ws_bytes,
+                                kt_stream_t stream);
 
 /*
  * Decoding over many layers and tokens with selection reuse [LC §4.5
