@@ -21,7 +21,7 @@ namespace {
 
 constexpr int ROWS = 128;                // rows of a tile: the M of the tensor-core steps
 constexpr int SLOTS = 2;                 // tiles (each with its own scores and output) a CTA
-constexpr int SOFT_WARPS = 16;           // two threads a row
+constexpr int SOFT_WARPS = 8;            // a thread a row
 constexpr int THREADS = (SOFT_WARPS + 4) * 32;
 constexpr int BOX = BS * 64 * 2;         // 128 tokens (or rows) x 64 channels, binary16
 constexpr int TILE = 2 * BOX;            // 128 x 128
@@ -54,7 +54,7 @@ struct Head {
 
 // Offsets in the workspace's part.
 struct PrefixWs {
-  size_t head, items_a, items_b, start_a, start_b, members, rows, suffix, parts, stats, total;
+  size_t head, items_a, items_b, start_a, start_b, q_rows, rows, suffix, parts, stats, total;
   long long rows_a;  // parts of A items come first
 };
 
@@ -72,11 +72,11 @@ struct Params {
   Item* items_b;
   Start* start_a;
   Start* start_b;
-  int* members;
+  int* q_rows;     // of members' rows: row of q (head 0)
   RowPlan* rows;   // [B][G]
   int* suffix;     // [B]: the B item of a sequence's own blocks
-  float* parts;    // [rows][128]
-  float* stats;    // [rows][4]: m, l of the first and second 64 tokens of each block
+  float* parts;    // of n rows: [32][n][4], the groups of four channels of all rows
+  float2* stats;   // [rows]: m, l
   long long rows_a;
   int B, H_kv, G, groups, max_blocks, P, ctas, row_max;
   float scale_log2;
@@ -92,33 +92,53 @@ __device__ __forceinline__ float ex2_fast(float x) {
 struct PlanShared {
   int cu[MAX_SEGS + 1];
   int member[MAX_SEGS + 1];     // members before sequence b (each in its group)
-  int start[MAX_SEGS];          // first block of its own, -1: no member
+  int start[MAX_SEGS];          // prefix blocks that b holds, -1: no member
+  int group[MAX_SEGS];          // of sequence b
+  int pairs[MAX_SEGS];          // of group g: first A item (-1: nothing shared) ...
+  int single[MAX_SEGS];         // ... and its B item
   int cum_b[2 * MAX_SEGS + 1];
   int cum_a[MAX_SEGS + 1];
-  int warp_sum[PLAN_THREADS / 32];
+  int4 warp_sum[PLAN_THREADS / 32];
   int bad;
 };
 
-__device__ __forceinline__ int plan_scan(int x, int* total, PlanShared& sh) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int incl = x;
+__device__ __forceinline__ int4 add4(int4 a, int4 b) {
+  return make_int4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+}
+__device__ __forceinline__ int4 up4(int4 v, int o) {
+  return make_int4(__shfl_up_sync(0xffffffffu, v.x, o), __shfl_up_sync(0xffffffffu, v.y, o),
+                   __shfl_up_sync(0xffffffffu, v.z, o), __shfl_up_sync(0xffffffffu, v.w, o));
+}
+__device__ __forceinline__ int4 at4(int4 v, int i) {
+  return make_int4(__shfl_sync(0xffffffffu, v.x, i), __shfl_sync(0xffffffffu, v.y, i),
+                   __shfl_sync(0xffffffffu, v.z, i), __shfl_sync(0xffffffffu, v.w, i));
+}
+// Exclusive prefixes of four numbers over the CTA's threads, from `base`, to which the totals
+// are added.
+__device__ __forceinline__ int4 plan_scan(int4 x, int4& base, PlanShared& sh) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  int4 incl = x;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
+    const int4 v = up4(incl, o);
+    if (lane >= o) incl = add4(incl, v);
   }
   __syncthreads();
   if (lane == 31) sh.warp_sum[warp] = incl;
   __syncthreads();
-  int s = sh.warp_sum[lane];
+  int4 s = lane < warps ? sh.warp_sum[lane] : make_int4(0, 0, 0, 0);
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, s, o);
-    if (lane >= o) s += v;
+    const int4 v = up4(s, o);
+    if (lane >= o) s = add4(s, v);
   }
-  *total = __shfl_sync(0xffffffffu, s, 31);
-  const int before = __shfl_sync(0xffffffffu, s, warp > 0 ? warp - 1 : 0);
-  return (warp > 0 ? before : 0) + incl - x;
+  int4 before = at4(s, warp > 0 ? warp - 1 : 0);
+  if (warp == 0) before = make_int4(0, 0, 0, 0);
+  const int4 excl =
+      make_int4(base.x + before.x + incl.x - x.x, base.y + before.y + incl.y - x.y,
+                base.z + before.z + incl.z - x.z, base.w + before.w + incl.w - x.w);
+  base = add4(base, at4(s, 31));
+  return excl;
 }
 
 // The last index i of [0, n) with cum[i] <= x.
@@ -132,9 +152,22 @@ __device__ __forceinline__ int last_at(const int* cum, int n, int x) {
   return lo;
 }
 
-// Workers among whom `all` steps are shared out: each gets at least one.
-__device__ __forceinline__ int workers(int n, int all) { return min(n, all); }
+// Shares of `all` steps among up to n workers: each has at least one step, the first ones one
+// more than the others.
+struct Shares {
+  int n, each, more;  // the first `more` workers have each + 1
+  __device__ __forceinline__ Shares(int workers, int all) : n(min(workers, all)) {
+    each = n > 0 ? all / n : 1;
+    more = all - n * each;
+  }
+  __device__ __forceinline__ int first(int w) const { return w * each + min(w, more); }
+  __device__ __forceinline__ int worker_of(int x) const {
+    const int cut = more * (each + 1);
+    return x < cut ? x / (each + 1) : more + (x - cut) / each;
+  }
+};
 
+// The length of sequence b, within what its table can hold.
 __device__ __forceinline__ int seq_len(const Params& p, int b) {
   int n = p.seq_lens[b];
   if (n < 0 || n > p.max_blocks * BS) {
@@ -144,15 +177,16 @@ __device__ __forceinline__ int seq_len(const Params& p, int b) {
   return n;
 }
 
+// Launched with as many threads as there are sequences, groups or slots, at most PLAN_THREADS.
 __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constant__ Params p) {
-  extern __shared__ uint8_t plan_smem[];
+  extern __shared__ __align__(16) uint8_t plan_smem[];
   PlanShared& sh = *reinterpret_cast<PlanShared*>(plan_smem);
+  const int tid = threadIdx.x, threads = blockDim.x;
+  if (tid == 0) sh.bad = 0;
   griddep_wait();
   griddep_launch_dependents();
-  const int tid = threadIdx.x;
-  if (tid == 0) sh.bad = 0;
   __syncthreads();
-  for (int g = tid; g <= p.groups; g += PLAN_THREADS) {
+  for (int g = tid; g <= p.groups; g += threads) {
     const int c = p.cu[g];
     sh.cu[g] = c;
     if (c < 0 || c > p.B || (g > 0 && c < p.cu[g - 1])) sh.bad = 1;
@@ -162,111 +196,83 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constan
   if (!grouped && tid == 0) set_status(p.status, KT_ERR_DEVICE_CHECK);
 
   // members: sequences that hold all blocks of their group's prefix
-  int members = 0;
-  for (int b0 = 0; b0 < p.B; b0 += PLAN_THREADS) {
+  int4 members = make_int4(0, 0, 0, 0);
+  for (int b0 = 0; b0 < p.B; b0 += threads) {
     const int b = b0 + tid;
-    int start = -1;
+    int start = -1, g = p.groups;
     if (b < p.B && grouped) {
-      const int g = last_at(sh.cu, p.groups + 1, b);
+      g = last_at(sh.cu, p.groups + 1, b);
       if (g < p.groups && sh.cu[g] <= b) {
         const int blocks = p.prefix[g];
         if (blocks < 0 || blocks > p.max_blocks) set_status(p.status, KT_ERR_DEVICE_CHECK);
         else if (blocks > 0 && seq_len(p, b) >= blocks * BS) start = blocks;
       }
     }
-    int total;
-    const int r = members + plan_scan(start >= 0, &total, sh);
+    const int r = plan_scan(make_int4(start >= 0, 0, 0, 0), members, sh).x;
     if (b < p.B) {
       sh.start[b] = start;
+      sh.group[b] = g;
       sh.member[b] = r;
-      if (start >= 0) p.members[r] = b;
+      if (start >= 0)
+        for (int i = 0; i < p.G; ++i) p.q_rows[r * p.G + i] = b * p.H_kv * p.G + i;
     }
-    members += total;
   }
-  if (tid == 0) sh.member[p.B] = members;
+  if (tid == 0) sh.member[p.B] = members.x;
   __syncthreads();
 
   // groups: rows in tiles of 128, two at a time (A items), a last single one a B item
-  int pairs = 0, singles = 0, steps_a = 0, steps_b = 0, rows_b = 0;
-  for (int g0 = 0; g0 < (grouped ? p.groups : 0); g0 += PLAN_THREADS) {
+  int4 sums = make_int4(0, 0, 0, 0);  // A and B items (16 bits each), steps of both, rows of B
+  for (int g0 = 0; g0 < (grouped ? p.groups : 0); g0 += threads) {
     const int g = g0 + tid;
-    int rows = 0, first = 0, blocks = 0;
+    int rows = 0, first = 0, blocks = 0, seq = 0;
     if (g < p.groups) {
-      first = sh.member[sh.cu[g]];
-      const int n = sh.member[sh.cu[g + 1]] - first;
+      const int c0 = sh.cu[g], c1 = sh.cu[g + 1];
+      first = sh.member[c0];
+      const int n = sh.member[c1] - first;
       if (n >= 2) {
         rows = n * p.G;
-        blocks = p.prefix[g];
+        for (seq = c0; sh.start[seq] < 0;) ++seq;  // its first member
+        blocks = sh.start[seq];
       }
     }
     const int tiles = (rows + ROWS - 1) / ROWS, np = tiles / 2, ns = tiles & 1;
     const int left = ns ? rows - np * 2 * ROWS : 0;
-    int tp, ts, ta, tb, tr;
-    const int ip = pairs + plan_scan(np, &tp, sh);
-    const int is = singles + plan_scan(ns, &ts, sh);
-    const int sa = steps_a + plan_scan(np * blocks, &ta, sh);
-    const int sb = steps_b + plan_scan(ns * blocks, &tb, sh);
-    const int rb = rows_b + plan_scan(left, &tr, sh);
-    for (int i = 0; i < np; ++i) {
+    const int4 at = plan_scan(make_int4(np << 16 | ns, np * blocks, ns * blocks, left), sums, sh);
+    const int ip = at.x >> 16, is = at.x & 0xffff;
+    if (g < p.groups) {
+      sh.pairs[g] = rows > 0 ? ip : -1;
+      sh.single[g] = is;
+    }
+    for (int i = 0; i < np + ns; ++i) {
+      const bool a = i < np;
       Item it;
-      it.seq = p.members[first];
+      it.seq = seq;
       it.start = 0;
       it.blocks = blocks;
-      it.rows = min(2 * ROWS, rows - i * 2 * ROWS);
+      it.rows = a ? min(2 * ROWS, rows - i * 2 * ROWS) : left;
       it.member = first * p.G + i * 2 * ROWS;
       it.tokens = blocks * BS;
-      it.row_base = 0;
-      it.cum = (sa + i * blocks) * p.H_kv;
-      p.items_a[ip + i] = it;
-      sh.cum_a[ip + i] = it.cum;
+      it.row_base = a ? 0 : at.w * p.H_kv;
+      it.cum = (a ? at.y + i * blocks : at.z) * p.H_kv;
+      (a ? p.items_a[ip + i] : p.items_b[is]) = it;
+      (a ? sh.cum_a[ip + i] : sh.cum_b[is]) = it.cum;
     }
-    if (ns) {
-      Item it;
-      it.seq = p.members[first];
-      it.start = 0;
-      it.blocks = blocks;
-      it.rows = left;
-      it.member = first * p.G + np * 2 * ROWS;
-      it.tokens = blocks * BS;
-      it.row_base = rb * p.H_kv;
-      it.cum = sb * p.H_kv;
-      p.items_b[is] = it;
-      sh.cum_b[is] = it.cum;
-    }
-    // where the rows of the group's members find their parts
-    for (int r = 0; r < rows; ++r) {
-      RowPlan rp;
-      const int t = r / ROWS;
-      rp.kind = t < 2 * np ? 1 : 2;
-      rp.item = t < 2 * np ? ip + t / 2 : is;
-      rp.row = t < 2 * np ? r % (2 * ROWS) : r - np * 2 * ROWS;
-      rp.pad = 0;
-      p.rows[(size_t)p.members[first + r / p.G] * p.G + r % p.G] = rp;
-    }
-    pairs += tp;
-    singles += ts;
-    steps_a += ta;
-    steps_b += tb;
-    rows_b += tr;
   }
   __syncthreads();
+  const int pairs = sums.x >> 16, singles = sums.x & 0xffff;
 
-  // what each sequence has of its own
-  for (int b0 = 0; b0 < p.B; b0 += PLAN_THREADS) {
+  // what each sequence has of its own, and where the parts of its rows' prefix are
+  int4 own = make_int4(sums.z, 0, 0, 0);
+  for (int b0 = 0; b0 < p.B; b0 += threads) {
     const int b = b0 + tid;
-    int start = 0, n = 0, nb = 0;
+    int start = 0, n = 0, nb = 0, first_a = -1;
     if (b < p.B) {
       n = seq_len(p, b);
       nb = (n + BS - 1) / BS;
-      if (sh.start[b] >= 0) {
-        const int g = last_at(sh.cu, p.groups + 1, b);
-        if (sh.member[sh.cu[g + 1]] - sh.member[sh.cu[g]] >= 2) start = sh.start[b];
-      }
-      if (start == 0)
-        for (int r = 0; r < p.G; ++r) p.rows[(size_t)b * p.G + r] = RowPlan{0, 0, 0, 0};
+      if (sh.start[b] >= 0) first_a = sh.pairs[sh.group[b]];
+      if (first_a >= 0) start = sh.start[b];
     }
-    int total;
-    const int sb = steps_b + plan_scan(nb - start, &total, sh);
+    const int sb = plan_scan(make_int4(nb - start, 0, 0, 0), own, sh).x;
     if (b < p.B) {
       Item it;
       it.seq = b;
@@ -275,32 +281,49 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constan
       it.rows = p.G;
       it.member = -1;
       it.tokens = n - start * BS;
-      it.row_base = (rows_b + b * p.G) * p.H_kv;
+      it.row_base = (sums.w + b * p.G) * p.H_kv;
       it.cum = sb * p.H_kv;
       p.items_b[singles + b] = it;
       sh.cum_b[singles + b] = it.cum;
       p.suffix[b] = singles + b;
+      const int g = sh.group[b];
+      int r0 = 0, np = 0;
+      if (first_a >= 0) {
+        const int c0 = sh.member[sh.cu[g]];
+        const int rows = (sh.member[sh.cu[g + 1]] - c0) * p.G;
+        r0 = (sh.member[b] - c0) * p.G;
+        np = (rows + ROWS - 1) / ROWS / 2;
+      }
+      for (int i = 0; i < p.G; ++i) {
+        RowPlan rp = {0, 0, 0, 0};
+        if (first_a >= 0) {
+          const int pair = (r0 + i) / (2 * ROWS);
+          rp.kind = pair < np ? 1 : 2;
+          rp.item = pair < np ? first_a + pair : sh.single[g];
+          rp.row = r0 + i - pair * 2 * ROWS;
+        }
+        p.rows[(size_t)b * p.G + i] = rp;
+      }
     }
-    steps_b += total;
   }
   __syncthreads();
-  steps_a *= p.H_kv;
-  steps_b *= p.H_kv;
+  const int steps_a = sums.y * p.H_kv, steps_b = own.x * p.H_kv;
   const int items_b = singles + p.B;
   if (tid == 0) *p.head = Head{steps_a, steps_b, items_b, 0};
   // equal shares: A steps over the CTAs, B steps over their slots
-  for (int c = tid; c < p.ctas * (1 + SLOTS); c += PLAN_THREADS) {
+  for (int c = tid; c < p.ctas * (1 + SLOTS); c += threads) {
     const bool a = c < p.ctas;
     const int w = a ? c : c - p.ctas;
-    const long long all = a ? steps_a : steps_b;
-    const int n = workers(a ? p.ctas : p.ctas * SLOTS, (int)all);
+    const int all = a ? steps_a : steps_b;
+    const Shares shares(a ? p.ctas : p.ctas * SLOTS, all);
     Start st = {0, 0, 0, 0};
-    if (w < n) {
-      const int lo = (int)(all * w / n);
-      st.steps = (int)(all * (w + 1) / n) - lo;
+    if (w < shares.n) {
+      const int lo = shares.first(w);
+      st.steps = shares.first(w + 1) - lo;
       const int* cum = a ? sh.cum_a : sh.cum_b;
-      st.item = last_at(cum, a ? pairs : items_b, lo);  // never one without blocks
-      const int next = st.item + 1 < (a ? pairs : items_b) ? cum[st.item + 1] : (int)all;
+      const int items = a ? pairs : items_b;
+      st.item = last_at(cum, items, lo);  // never one without blocks
+      const int next = st.item + 1 < items ? cum[st.item + 1] : all;
       const int blocks = (next - cum[st.item]) / p.H_kv;
       st.head = (lo - cum[st.item]) / blocks;
       st.block = (lo - cum[st.item]) % blocks;
@@ -310,47 +333,70 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constan
 }
 
 // ---- attend ------------------------------------------------------------------------------
-// Warps 0-15 hold the rows: warp w has slot w / 8, the 32 TMEM lanes of quarter w % 4 and
-// half (w / 4) % 2 of the columns, so a row's 128 scores and 128 output channels are two
-// threads'.  Warps 16 and 17 issue the tensor-core steps of a slot each, so that one slot's
-// fill the pauses of the other's; warp 18 loads K and V tiles into a ring of 32 KB entries.
+// Warps 0-7 hold the rows, a thread a row: warp w has slot w / 4 and the 32 TMEM lanes of
+// quarter w % 4.  Warps 8 and 9 issue the tensor-core steps of a slot each, so that one slot's
+// fill the pauses of the other's; warp 10 loads K and V tiles into a ring of 32 KB entries;
+// warp 11 fetches the queries of the next run of blocks.  A run of up to 64 rows takes one
+// half of the slot's 128 in turn with the next one, so that its queries come while the other
+// half's are in use.  (Two threads a row have 104 registers each for half an output row and a
+// chunk of scores, and spill: 4400 cycles a softmax instead of TBD.)
 //
-// A slot's block: S (TMEM, 128 columns) = Q K^T; the row threads turn it into P, which takes
-// the place of S; O (128 columns) = P V; the row threads add it to their running output in
-// registers: out = out * 2^(m_old - m_new) + O.  So a block's P V is summed apart from the
-// running output, and no output is rescaled in TMEM.
+// A slot's block: S (TMEM, 128 columns) = Q K^T; the row threads turn it into P, which goes
+// where the last block's output was; O = P V takes the place of S; the row threads add it to
+// their running output in registers: out = out * alpha + O, and the next S takes the place of
+// P.  So a block's P V is summed apart from the running output, no output is rescaled in
+// TMEM, and the scores stay until P is whole: the exponentials use the running maximum of the
+// blocks before and are made again, after a search for the block's own, where their sum shows
+// that one may not fit binary16 (alpha then scales what was summed before).  A run's first
+// block takes its maximum first.
 //
-// P is held as two binary16, 2^15 p = hi + lo (22 bits, exact to 2^-24 of the largest), and
-// P V as two products: with one alone the output would be good to 11 bits only, and it is
+// P is held as two binary16, 2^8 p = hi - lo (22 bits; at least 2^-25), and
+// P V as two products (the tensor cores negate lo): with one alone the output would be good to 11 bits only, and it is
 // binary32.  For 16 tokens, the K of a tensor-core step, columns 0-7 are hi, 8-15 lo.
 //
 // A items (two tiles of rows over the same blocks) go through both slots at once, each K/V
 // tile read once; with B items the slots are on their own, each with its own share.
+struct Unit {      // a run of blocks of one (item, head) in a slot
+  int rows, row0;  // the slot's rows row0 .. row0 + rows - 1
+  int run;         // blocks
+  int tokens;      // tokens from its first block on
+  long long part;  // its part's first row in the workspace
+};
+// A run's queries are fetched once the tensor cores are done with those of the run before
+// last (their half) and the row threads have begun the run before that: four descriptions.
+constexpr int UNITS = 4;
+constexpr int STEPS_AHEAD = 8;  // flags of the ring's steps: more than it holds
 struct Misc {
   uint64_t full[ENTRIES], empty[ENTRIES];
-  uint64_t s_full[SLOTS], p_full[SLOTS], o_full[SLOTS], q_full[SLOTS];
+  uint64_t s_full[SLOTS], p_full[SLOTS], o_full[SLOTS];
+  uint64_t q_full[SLOTS][UNITS], q_done[SLOTS][2];
+  Unit unit[SLOTS][UNITS];
   uint32_t tmem;
-  int bad[ENTRIES];              // the entry's page is outside the pool
-  float most[SLOTS][2][ROWS];    // a row's two halves' maxima
+  int bad[STEPS_AHEAD];          // the step's page is outside the pool
 };
 constexpr int SMEM = SLOTS * TILE + ENTRIES * TILE + sizeof(Misc);
 static_assert(SMEM <= 232448, "shared memory of a CTA");
 static_assert(SMEM > 233472 / 2, "one CTA an SM: it holds all of TMEM");
 constexpr uint32_t TMEM_COLS = 512;
 
-// 16 columns of this thread's TMEM lane to and from registers.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
-  uint32_t r[16];
+// Columns of this thread's TMEM lane: loads without their wait (a register of an earlier load
+// may be used behind tmem_wait_ld, which names it), and stores.
+__device__ __forceinline__ void tmem_ld16_async(uint32_t taddr, float (&v)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
       "%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+        "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]),
+        "=f"(v[14]), "=f"(v[15])
       : "r"(taddr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_wait_ld(float (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]),
+                 "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]),
+                 "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
+               :
+               : "memory");
 }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -362,6 +408,45 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 }
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// Two binary32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mov.b64 z, {%6, %7};\n\tfma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// 2^8 p of 16 tokens as two binary16 each: rounded, and the rounding (hi - x, in one mixed-
+// precision instruction on the FMA pipe; unpacking hi, or cutting x off, would go through the
+// pipe that the conversions keep busy: 1880 cycles a block of two rows a lane instead of 1624).
+__device__ __forceinline__ void split16(const float* x, uint32_t (&w)[16]) {
+#pragma unroll
+  for (int j = 0; j < 16; j += 2) {
+    float a, b;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[j / 2]) : "f"(x[j + 1]), "f"(x[j]));
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "sub.f32.f16 %0, l, %3;\n\tsub.f32.f16 %1, h, %4;\n\t}"
+        : "=f"(a), "=f"(b)
+        : "r"(w[j / 2]), "f"(x[j]), "f"(x[j + 1]));
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[8 + j / 2]) : "f"(b), "f"(a));
+  }
 }
 
 // D[tmem] (+)= A[tmem] . B[sdesc]^T
@@ -386,6 +471,7 @@ __device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr) {
 }
 constexpr uint32_t IDESC_S = umma_idesc_f16_f32(ROWS, BS);
 constexpr uint32_t IDESC_O = umma_idesc_f16_f32(ROWS, D) | (1u << 16);  // B transposed
+constexpr uint32_t NEGATE_A = 1u << 13;
 
 // Scores of tokens from `valid` on leave the softmax; v holds those of tokens first ...
 __device__ __forceinline__ void mask16(float (&v)[16], int first, int valid) {
@@ -394,10 +480,14 @@ __device__ __forceinline__ void mask16(float (&v)[16], int first, int valid) {
     if (first + j >= valid) v[j] = -INFINITY;
 }
 
-// Registers pass from the control warps to the row threads: five warpgroups are launched with
+// log2 of the factor of P, and the largest sum of a block's 2^8 p whose terms surely are
+// binary16 (65504 at most).
+constexpr float P_SHIFT = 8.0f, SUM_MAX = 65000.0f;
+
+// Registers pass from the control warps to the row threads: three warpgroups are launched with
 // LAUNCH_REGS a thread (the host checks that), and the shares must not add up to more.
-constexpr int LAUNCH_REGS = 96, ROW_REGS = 104, CONTROL_REGS = 64;
-static_assert(4 * ROW_REGS + CONTROL_REGS <= 5 * LAUNCH_REGS, "registers of a CTA");
+constexpr int LAUNCH_REGS = 168, ROW_REGS = 224, CONTROL_REGS = 56;
+static_assert(2 * ROW_REGS + CONTROL_REGS <= 3 * LAUNCH_REGS, "registers of a CTA");
 template <int N>
 __device__ __forceinline__ void regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -405,6 +495,83 @@ __device__ __forceinline__ void regs_inc() {
 template <int N>
 __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// A row's largest score (columns from taddr on).
+template <bool MASK>
+__device__ __forceinline__ float row_max(uint32_t taddr, int valid) {
+  float v[2][16];
+  float top = -INFINITY, top2 = -INFINITY;
+  tmem_ld16_async(taddr, v[0]);
+  tmem_wait_ld(v[0]);
+#pragma unroll
+  for (int c = 0; c < BS; c += 16) {
+    float(&x)[16] = v[(c / 16) & 1];
+    float(&next)[16] = v[(c / 16 + 1) & 1];
+    if (c + 16 < BS) tmem_ld16_async(taddr + c + 16, next);
+    if (MASK) mask16(x, c, valid);
+#pragma unroll
+    for (int j = 0; j < 16; j += 4) {
+      top = max3(top, x[j], x[j + 1]);
+      top2 = max3(top2, x[j + 2], x[j + 3]);
+    }
+    if (c + 16 < BS) tmem_wait_ld(next);
+  }
+  return fmaxf(top, top2);
+}
+
+// 2^(s scale + shift) of a row's scores at `from`, in two parts to `to`; returns their sum.
+// No branch between the chunks, so that their instructions interleave.  An element costs four
+// issue slots (half an FMA and an addition of two, the exponential, two halves of conversions, a
+// mixed-precision FMA); the exponentials bound it, 4 cycles a warp's: 512 a block.
+template <bool MASK>
+__device__ __forceinline__ float row_exp(uint32_t from, uint32_t to, int valid, float2 scale2,
+                                         float shift) {
+  const float2 shift2 = make_float2(shift, shift);
+  float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+  float v[2][16];
+  tmem_ld16_async(from, v[0]);
+  tmem_wait_ld(v[0]);
+#pragma unroll
+  for (int c = 0; c < BS; c += 16) {
+    float(&x)[16] = v[(c / 16) & 1];
+    float(&next)[16] = v[(c / 16 + 1) & 1];
+    if (c + 16 < BS) tmem_ld16_async(from + c + 16, next);
+    if (MASK) mask16(x, c, valid);
+#pragma unroll
+    for (int j = 0; j < 16; j += 2) {
+      const float2 y = fma2(make_float2(x[j], x[j + 1]), scale2, shift2);
+      x[j] = ex2_fast(y.x);
+      x[j + 1] = ex2_fast(y.y);
+      sum[j / 2 & 1] = add2(sum[j / 2 & 1], make_float2(x[j], x[j + 1]));
+    }
+    uint32_t w16[16];
+    split16(x, w16);
+    if (c + 16 < BS) tmem_wait_ld(next);
+    tmem_st16(to + c, w16);
+  }
+  return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+}
+
+// The same number in every lane, and known as such to the compiler.
+__device__ __forceinline__ int uniform(int x) { return __reduce_max_sync(0xffffffffu, x); }
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(r));
+  return r != 0;
+}
+// mbar_wait by a whole warp, with the same answer in every lane.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, int* status) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  const uint64_t t0 = globaltimer();
+  for (uint32_t i = 1;; ++i) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if ((i & 255u) == 0 && __any_sync(0xffffffffu, globaltimer() - t0 > WAIT_LIMIT_NS)) {
+      set_status(status, KT_ERR_TIMEOUT);
+      return false;
+    }
+  }
 }
 
 // A walk over the steps of a share: runs of blocks of one (item, head).
@@ -437,6 +604,36 @@ __device__ __forceinline__ int entry_b(int s, int k, int a, int other) {
 
 __device__ __forceinline__ uint32_t entry_parity(int e) { return (uint32_t)(e / ENTRIES) & 1u; }
 
+// Queries of a run into two swizzled boxes (chunk c of row i: box c / 8, slot (c % 8) ^ (i % 8)).
+// A lane finds where four of the rows are; then 16 lanes copy a row.
+__device__ __forceinline__ void load_queries(const Params& p, const Item& it, int head, int off,
+                                             int rows, uint32_t q, int row0, int lane) {
+  int at[ROWS / 32];  // row of q, without the K/V head's offset
+#pragma unroll
+  for (int j = 0; j < ROWS / 32; ++j) {
+    const int i = j * 32 + lane;
+    at[j] = 0;
+    if (i < rows) at[j] = it.member >= 0 ? p.q_rows[it.member + off + i] : it.seq * p.H_kv * p.G + i;
+  }
+  const int c = lane & 15;
+#pragma unroll
+  for (int j = 0; j < ROWS / 32; ++j) {
+    if (j * 32 >= rows) break;
+#pragma unroll 4
+    for (int i0 = 0; i0 < 32; i0 += 2) {
+      if (j * 32 + i0 >= rows) break;
+      const int i = j * 32 + i0 + (lane >> 4), r = row0 + i;
+      const int row = __shfl_sync(0xffffffffu, at[j], i0 + (lane >> 4)) + head * p.G;
+      if (i < rows)
+        cp_async_16(q + (c >> 3) * BOX + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+                    p.q + (size_t)row * D + c * 8);
+    }
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
 __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constant__ Params p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   Misc& ms = *reinterpret_cast<Misc*>(smem + (SLOTS + ENTRIES) * TILE);
@@ -445,7 +642,8 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
   const uint32_t sQ = smem_u32(smem), ring = sQ + SLOTS * TILE;
   const uint32_t full = smem_u32(ms.full), empty = smem_u32(ms.empty);
   const uint32_t s_full = smem_u32(ms.s_full), p_full = smem_u32(ms.p_full);
-  const uint32_t o_full = smem_u32(ms.o_full), q_full = smem_u32(ms.q_full);
+  const uint32_t o_full = smem_u32(ms.o_full);
+  const uint32_t q_full = smem_u32(ms.q_full), q_done = smem_u32(ms.q_done);
   if (tid == 0) {
     for (int i = 0; i < ENTRIES; ++i) {
       mbar_init(full + 8 * i, 1);
@@ -455,8 +653,9 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
       mbar_init(s_full + 8 * i, 1);
       mbar_init(p_full + 8 * i, SOFT_WARPS / SLOTS);
       mbar_init(o_full + 8 * i, 1);
-      mbar_init(q_full + 8 * i, SOFT_WARPS / SLOTS);
     }
+    for (int i = 0; i < UNITS * SLOTS; ++i) mbar_init(q_full + 8 * i, 1);
+    for (int i = 0; i < 2 * SLOTS; ++i) mbar_init(q_done + 8 * i, 1);
     fence_mbar_init();
     prefetch_tensormap(&p.kmap);
     prefetch_tensormap(&p.vmap);
@@ -473,251 +672,321 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
   const uint32_t tmem = ms.tmem;
   griddep_wait();
   griddep_launch_dependents();
-  const Start sa = p.start_a[cta];
-  const Start sb0 = p.start_b[cta], sb1 = p.start_b[p.ctas + cta];
 
-  if (warp < SOFT_WARPS) regs_inc<ROW_REGS>();
-  else regs_dec<CONTROL_REGS>();
+  if (warp >= SOFT_WARPS) {
+  regs_dec<CONTROL_REGS>();
   if (warp == SOFT_WARPS + 2) {
     // ============================ K and V tiles ============================
-    if (lane == 0) {
-      const uint64_t pol = l2_evict_first_policy();
-      const int row_end = p.P * p.H_kv * BS;  // reads zeros
-      int e = 0;
-      bool ok = true;
-      auto load = [&](const Item& it, int head, int block) {
-        const int page = p.table[(size_t)it.seq * p.max_blocks + it.start + block];
-        const bool bad = page < 0 || page >= p.P;
+    const Start sa = p.start_a[cta];
+    const Start sb0 = p.start_b[cta], sb1 = p.start_b[p.ctas + cta];
+    const uint64_t pol = l2_evict_first_policy();
+    const int row_end = p.P * p.H_kv * BS;  // reads zeros
+    int e = 0;
+    bool ok = true;
+    auto load = [&](int page, int head) {
+      const bool bad = page < 0 || page >= p.P;
+      const int row = bad ? row_end : (page * p.H_kv + head) * BS;
+      if (lane == 0) {
         if (bad) set_status(p.status, KT_ERR_DEVICE_CHECK);
-        const int row = bad ? row_end : (page * p.H_kv + head) * BS;
-        for (int side = 0; side < 2; ++side, ++e) {
-          const int st = e % ENTRIES;
-          if (e >= ENTRIES && !mbar_wait(empty + 8 * st, entry_parity(e) ^ 1, p.status)) return false;
+        ms.bad[(e >> 1) % STEPS_AHEAD] = bad;
+      }
+      for (int side = 0; side < 2 && ok; ++side, ++e) {
+        const int st = e % ENTRIES;
+        if (e >= ENTRIES) ok = mbar_wait(empty + 8 * st, entry_parity(e) ^ 1, p.status);
+        if (!ok) break;
+        if (lane == 0) {
           const CUtensorMap* map = side == 0 ? &p.kmap : &p.vmap;
           const uint32_t dst = ring + st * TILE;
-          ms.bad[st] = bad;
           mbar_arrive_expect_tx(full + 8 * st, TILE);
           tma_load_2d(dst, map, 0, row, full + 8 * st, pol);
           tma_load_2d(dst + BOX, map, 64, row, full + 8 * st, pol);
         }
-        return true;
-      };
-      Walk w = walk_of(p.items_a, sa);
-      while (ok && w.left > 0) {
-        const Item it = w.items[w.item];
-        const int run = run_of(w, it);
-        for (int i = 0; i < run && ok; ++i) ok = load(it, w.head, w.block + i);
-        advance(w, run, p.H_kv);
+        __syncwarp();
       }
-      Walk ws[SLOTS] = {walk_of(p.items_b, sb0), walk_of(p.items_b, sb1)};
-      while (ok && (ws[0].left > 0 || ws[1].left > 0)) {
-#pragma unroll
-        for (int s = 0; s < SLOTS; ++s) {
-          Walk& x = ws[s];
-          if (x.left > 0 && ok) {
-            const Item it = x.items[x.item];
-            ok = load(it, x.head, x.block);
-            if (x.block + 1 < it.blocks) {
-              --x.left;
-              ++x.block;
-            } else {
-              advance(x, 1, p.H_kv);
-            }
-          }
-        }
+    };
+    // the pages of a run's next 32 blocks, one a lane
+    auto fetch = [&](const Item& it, int block) {
+      const int j = block + lane;
+      return j < it.blocks ? p.table[(size_t)it.seq * p.max_blocks + it.start + j] : -1;
+    };
+    Walk w = walk_of(p.items_a, sa);
+    while (ok && w.left > 0) {
+      const Item it = w.items[w.item];
+      const int run = run_of(w, it);
+      int pages = 0;
+      for (int i = 0; i < run && ok; ++i) {
+        if ((i & 31) == 0) pages = fetch(it, w.block + i);
+        load(__shfl_sync(0xffffffffu, pages, i & 31), w.head);
       }
-      // nothing of this CTA's is in flight when it ends
-      for (int i = max(0, e - ENTRIES); i < e; ++i)
-        mbar_wait(full + 8 * (i % ENTRIES), entry_parity(i), p.status);
+      advance(w, run, p.H_kv);
     }
-    __syncwarp();
-  } else if (warp == SOFT_WARPS || warp == SOFT_WARPS + 1) {
-    // ============================ tensor-core steps ============================
-    if (lane == 0) {
-      const int s = warp - SOFT_WARPS;
-      const uint32_t q = sQ + s * TILE, st = tmem + s * 256, ot = st + 128;
-      const int other = s == 0 ? sb1.steps : sb0.steps;
-      int k = 0, units = 0;
-      bool ok = true;
-      for (int part = 0; part < 2 && ok; ++part) {
-        const bool a = part == 0;
-        Walk w = a ? walk_of(p.items_a, sa) : walk_of(p.items_b, s == 0 ? sb0 : sb1);
-        while (ok && w.left > 0) {
-          const int run = min(w.left, w.items[w.item].blocks - w.block);
-          for (int i = 0; i < run && ok; ++i, ++k) {
-            const int e = a ? 2 * k : entry_b(s, k - sa.steps, sa.steps, other);
-            const int ek = e % ENTRIES, ev = (e + 1) % ENTRIES;
-            // S = Q K^T once K, the run's Q and the end of the last P V are there
-            ok = mbar_wait(full + 8 * ek, entry_parity(e), p.status) &&
-                 (i > 0 || mbar_wait(q_full + 8 * s, units & 1, p.status)) &&
-                 (k == 0 || mbar_wait(o_full + 8 * s, (k - 1) & 1, p.status));
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t kb = ring + ek * TILE;
-#pragma unroll
-            for (int ks = 0; ks < 8; ++ks)
-              umma_f16(st, umma_sdesc_sw128(q + (ks >> 2) * BOX + (ks & 3) * 32),
-                       umma_sdesc_sw128(kb + (ks >> 2) * BOX + (ks & 3) * 32), IDESC_S, ks > 0);
-            umma_commit(s_full + 8 * s);
-            umma_commit(empty + 8 * ek);
-            if (!a) umma_commit(empty + 8 * ek);  // the other slot has no part in this one
-            // O = P V, the high and the low parts of P
-            ok = mbar_wait(full + 8 * ev, entry_parity(e + 1), p.status) &&
-                 mbar_wait(p_full + 8 * s, k & 1, p.status);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t vb = ring + ev * TILE;
-#pragma unroll
-            for (int ks = 0; ks < 16; ++ks)
-              umma_f16_ta(ot, st + (ks & 7) * 16 + (ks >> 3) * 8,
-                          sdesc_mn_sw128(vb + (ks & 7) * 2048), IDESC_O, ks > 0);
-            umma_commit(o_full + 8 * s);
-            umma_commit(empty + 8 * ev);
-            if (!a) umma_commit(empty + 8 * ev);
-          }
-          ++units;
-          advance(w, run, p.H_kv);
-        }
+    Walk x0 = walk_of(p.items_b, sb0), x1 = walk_of(p.items_b, sb1);
+    int at0 = 0, at1 = 0, run0 = 0, run1 = 0, pages0 = 0, pages1 = 0;
+    auto turn = [&](Walk& x, int& at, int& run, int& pages) {
+      if (x.left == 0) return;
+      if (at == 0 || (at & 31) == 0) {
+        const Item it = x.items[x.item];
+        run = run_of(x, it);
+        pages = fetch(it, x.block + at);
       }
+      load(__shfl_sync(0xffffffffu, pages, at & 31), x.head);
+      if (++at == run) {
+        advance(x, run, p.H_kv);
+        at = 0;
+      }
+    };
+    while (ok && (x0.left > 0 || x1.left > 0)) {
+      turn(x0, at0, run0, pages0);
+      if (ok) turn(x1, at1, run1, pages1);
     }
-    __syncwarp();
-  } else if (warp < SOFT_WARPS) {
-    // ============================ rows ============================
-    const int s = warp >> 3, quarter = warp & 3, half = (warp >> 2) & 1;
-    const int r = quarter * 32 + lane;       // this thread's row
-    const int st_tid = tid & 255;
-    const uint32_t tb = tmem + s * 256 + ((uint32_t)(quarter * 32) << 16) + half * 64;
-    const int H_q = p.H_kv * p.G;
-    const Start sb = s == 0 ? sb0 : sb1;
-    const int other = s == 0 ? sb1.steps : sb0.steps;
-    int k = 0;
+    // nothing of this CTA's is in flight when it ends
+    for (int i = max(0, e - ENTRIES); i < e; ++i)
+      mbar_wait(full + 8 * (i % ENTRIES), entry_parity(i), p.status);
+  } else if (warp == SOFT_WARPS + 3) {
+    // ============================ runs and their queries ============================
+    Walk w[SLOTS];
+    int units[SLOTS] = {0, 0}, rows_before[SLOTS] = {0, 0};
     bool ok = true;
     for (int part = 0; part < 2 && ok; ++part) {
       const bool a = part == 0;
-      Walk w = a ? walk_of(p.items_a, sa) : walk_of(p.items_b, sb);
-      while (w.left > 0 && ok) {
-        const Item it = w.items[w.item];
-        const int run = run_of(w, it);
-        const int off = a ? s * ROWS : 0;    // the slot's tile of an A item
-        const int rows = min(ROWS, it.rows - off);
-        // queries into two swizzled boxes (chunk c of row i: box c / 8, slot (c % 8) ^ (i % 8))
-        uint8_t* q = smem + s * TILE;
-        for (int idx = st_tid; idx < rows * 16; idx += 256) {
-          const int i = idx >> 4, c = idx & 15;
-          int b = it.seq, g = i;
-          if (it.member >= 0) {
-            const int m = it.member + off + i;
-            b = p.members[m / p.G];
-            g = m % p.G;
+      w[0] = a ? walk_of(p.items_a, p.start_a[cta]) : walk_of(p.items_b, p.start_b[cta]);
+      w[1] = a ? w[0] : walk_of(p.items_b, p.start_b[p.ctas + cta]);
+      // a slot whose next run has no room yet does not hold up the other's: in the ring their
+      // steps wait for one another
+      uint64_t t0 = globaltimer();
+      while (ok && (w[0].left > 0 || w[1].left > 0)) {
+        bool moved = false;
+#pragma unroll
+        for (int s = 0; s < SLOTS; ++s) {
+          if (w[s].left == 0) continue;
+          const Item it = w[s].items[w[s].item];
+          const int off = a ? s * ROWS : 0, n = units[s], buf = n & 1;
+          const int rows = min(ROWS, it.rows - off);
+          // the run before last is done with this half; a run of both halves waits for, and is
+          // waited for by, its neighbours
+          bool room = n < 2 || mbar_try_wait(q_done + 8 * (2 * s + buf), ((n >> 1) - 1) & 1);
+          if (n >= 1 && (rows > ROWS / 2 || rows_before[s] > ROWS / 2))
+            room = room && mbar_try_wait(q_done + 8 * (2 * s + (buf ^ 1)), ((n - 1) >> 1) & 1);
+          if (!__all_sync(0xffffffffu, room)) continue;
+          moved = true;
+          Unit u;
+          u.rows = rows;
+          u.row0 = u.rows <= ROWS / 2 ? buf * (ROWS / 2) : 0;
+          u.run = run_of(w[s], it);
+          u.tokens = it.tokens - w[s].block * BS;
+          u.part = a ? ((long long)cta + (long long)w[s].item * p.H_kv + w[s].head) * (2 * ROWS) + off
+                     : p.rows_a + (long long)(s * p.ctas + cta) * p.row_max + it.row_base +
+                           (long long)w[s].head * it.rows;
+          load_queries(p, it, w[s].head, off, u.rows, sQ + s * TILE, u.row0, lane);
+          if (lane == 0) {
+            ms.unit[s][n % UNITS] = u;
+            mbar_arrive(q_full + 8 * (UNITS * s + n % UNITS));
           }
-          const uint4 v = *(reinterpret_cast<const uint4*>(
-                                p.q + ((size_t)b * H_q + w.head * p.G + g) * D) + c);
-          *reinterpret_cast<uint4*>(q + (c >> 3) * BOX + i * 128 + (((c & 7) ^ (i & 7)) << 4)) = v;
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(q_full + 8 * s);
-
-        const bool active = quarter * 32 < rows;
-        float acc[64], m = -INFINITY, l = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 64; ++i) acc[i] = 0.0f;
-        for (int i = 0; i < run && ok; ++i, ++k) {
-          const int e = (a ? 2 * k : entry_b(s, k - sa.steps, sa.steps, other)) + 1;  // V's entry
-          const int ev = e % ENTRIES;
-          ok = mbar_wait(s_full + 8 * s, k & 1, p.status);
-          if (!ok) break;
-          tc_fence_after();
-          int valid = min(BS, it.tokens - (w.block + i) * BS);
-          if (valid < BS) {
-            // V behind the last token may be anything, and 0 * NaN is NaN: zeros there
-            ok = mbar_wait(full + 8 * ev, entry_parity(e), p.status);
-            if (!ok) break;
-            uint8_t* v = smem + SLOTS * TILE + ev * TILE;
-            for (int idx = valid * 8 + st_tid; idx < BS * 8; idx += 256) {
-              *reinterpret_cast<uint4*>(v + idx * 16) = make_uint4(0, 0, 0, 0);
-              *reinterpret_cast<uint4*>(v + BOX + idx * 16) = make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async_smem();
-          }
-          float alpha = 1.0f;
-          if (active) {
-            if (!mbar_try_wait(full + 8 * ev, entry_parity(e)))
-              ok = mbar_wait(full + 8 * ev, entry_parity(e), p.status);
-            if (ms.bad[ev]) valid = 0;
-            float mx = -INFINITY;
-#pragma unroll
-            for (int c = 0; c < 64; c += 16) {
-              float v[16];
-              tmem_ld16(tb + c, v);
-              if (valid < BS) mask16(v, half * 64 + c, valid);
-              float m4[4] = {v[0], v[1], v[2], v[3]};
-#pragma unroll
-              for (int j = 4; j < 16; ++j) m4[j & 3] = fmaxf(m4[j & 3], v[j]);
-              mx = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
-            }
-            ms.most[s][half][r] = mx;
-            named_bar_sync(1 + s * 4 + quarter, 64);
-            mx = fmaxf(mx, ms.most[s][half ^ 1][r]);
-            const float m_new = fmaxf(m, mx * p.scale_log2);
-            const float base = m_new == -INFINITY ? 0.0f : m_new;
-            alpha = ex2_fast(m - base);
-            m = m_new;
-            const float shift = 15.0f - base;
-            float sum4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int c = 0; c < 64; c += 16) {
-              float v[16];
-              uint32_t w16[16];
-              tmem_ld16(tb + c, v);
-              if (valid < BS) mask16(v, half * 64 + c, valid);
-#pragma unroll
-              for (int j = 0; j < 16; j += 2) {
-                const float x = ex2_fast(fmaf(v[j], p.scale_log2, shift));
-                const float y = ex2_fast(fmaf(v[j + 1], p.scale_log2, shift));
-                sum4[j & 3] += x;
-                sum4[(j & 3) + 1] += y;
-                const __half2 hi = __floats2half2_rn(x, y);
-                const float2 back = __half22float2(hi);
-                const __half2 lo = __floats2half2_rn(x - back.x, y - back.y);
-                w16[j / 2] = *reinterpret_cast<const uint32_t*>(&hi);
-                w16[8 + j / 2] = *reinterpret_cast<const uint32_t*>(&lo);
-              }
-              tmem_st16(tb + c, w16);
-            }
-            l = fmaf(l, alpha, (sum4[0] + sum4[1]) + (sum4[2] + sum4[3]));
-            tmem_wait_st();
-          }
-          tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(p_full + 8 * s);
-          ok = mbar_wait(o_full + 8 * s, k & 1, p.status) && ok;
+          ++units[s];
+          rows_before[s] = u.rows;
+          advance(w[s], u.run, p.H_kv);
+        }
+        const uint64_t t = globaltimer();
+        if (moved) t0 = t;
+        else if (__any_sync(0xffffffffu, t - t0 > WAIT_LIMIT_NS)) {
+          if (lane == 0) set_status(p.status, KT_ERR_TIMEOUT);
+          ok = false;
+        }
+      }
+    }
+  } else {
+    // ============================ tensor-core steps ============================
+    // The whole warp runs this, and what it loads goes through a warp reduction: the compiler
+    // then keeps it in uniform registers, where the tensor-core instructions want their operands
+    // (moving them there one by one took longer than the steps themselves).
+    const bool leader = elect_one();
+    const int na = uniform(p.start_a[cta].steps);
+    const int nb0 = uniform(p.start_b[cta].steps), nb1 = uniform(p.start_b[p.ctas + cta].steps);
+    bool ok = true;
+    // S = Q K^T of slot s's step k, once K, the run's Q and the end of the last P V are there;
+    // n counts the runs begun, left the steps of the one at hand
+    auto scores = [&](int s, int k, int e, bool both, int& n, int& left) {
+      const int ek = e % ENTRIES;
+      if (left == 0) {
+        ok = ok && mbar_wait_warp(q_full + 8 * (UNITS * s + n % UNITS), (n / UNITS) & 1, p.status);
+        left = uniform(ms.unit[s][n % UNITS].run);
+        ++n;
+      }
+      ok = ok && mbar_wait_warp(full + 8 * ek, entry_parity(e), p.status) &&
+           (k == 0 || mbar_wait_warp(o_full + 8 * s, (k - 1) & 1, p.status));
+      if (!ok) return;
+      tc_fence_after();
+      const uint64_t q = umma_sdesc_sw128(sQ + s * TILE), kb = umma_sdesc_sw128(ring + ek * TILE);
+      const uint32_t st = tmem + s * 256 + (k & 1) * 128;
+      --left;
+      if (leader) {
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) {
+          const int at = ((ks >> 2) * BOX + (ks & 3) * 32) >> 4;
+          umma_f16(st, q + at, kb + at, IDESC_S, ks > 0);
+        }
+        umma_commit(s_full + 8 * s);
+        if (left == 0) umma_commit(q_done + 8 * (2 * s + (~n & 1)));  // the run's last use of Q
+        umma_commit(empty + 8 * ek);
+        if (!both) umma_commit(empty + 8 * ek);  // the other slot has no part in this one
+      }
+      __syncwarp();
+    };
+    // O = P V, the high and the low parts of P
+    auto values = [&](int s, int k, int e, bool both) {
+      const int ev = e % ENTRIES;
+      ok = ok && mbar_wait_warp(full + 8 * ev, entry_parity(e), p.status) &&
+           mbar_wait_warp(p_full + 8 * s, k & 1, p.status);
+      if (!ok) return;
+      tc_fence_after();
+      const uint64_t vb = sdesc_mn_sw128(ring + ev * TILE);
+      const uint32_t st = tmem + s * 256 + (k & 1) * 128, pt = tmem + s * 256 + (~k & 1) * 128;
+      if (leader) {
+#pragma unroll
+        for (int ks = 0; ks < 16; ++ks)
+          umma_f16_ta(st, pt + (ks & 7) * 16 + (ks >> 3) * 8, vb + (ks & 7) * (2048 >> 4),
+                      IDESC_O | (ks >= 8 ? NEGATE_A : 0u), ks > 0);
+        umma_commit(o_full + 8 * s);
+        umma_commit(empty + 8 * ev);
+        if (!both) umma_commit(empty + 8 * ev);
+      }
+      __syncwarp();
+    };
+    if (warp == SOFT_WARPS) {
+      // A steps: both slots from one warp, P V and the next scores of one in a row, so that
+      // the softmax of each falls into the tensor-core time of the other.  (Two warps that
+      // issue as operands come keep the slots in step, and the tensor cores idle meanwhile.)
+      int n0 = 0, n1 = 0, left0 = 0, left1 = 0;
+      for (int k = 0; k <= na && ok; ++k) {
+        if (k > 0) values(0, k - 1, 2 * k - 1, true);
+        if (k < na) scores(0, k, 2 * k, true, n0, left0);
+        if (k > 0) values(1, k - 1, 2 * k - 1, true);
+        if (k < na) scores(1, k, 2 * k, true, n1, left1);
+      }
+      // B steps: each slot at its own pace
+      for (int k = 0; k < nb0 && ok; ++k) {
+        const int e = entry_b(0, k, na, nb1);
+        scores(0, na + k, e, false, n0, left0);
+        values(0, na + k, e + 1, false);
+      }
+    } else {
+      // the runs that the other warp issues
+      int n = 0, left = 0;
+      Walk w = walk_of(p.items_a, p.start_a[cta]);
+      for (; w.left > 0; ++n) advance(w, run_of(w, w.items[w.item]), p.H_kv);
+      n = uniform(n);
+      for (int k = 0; k < nb1 && ok; ++k) {
+        const int e = entry_b(1, k, na, nb0);
+        scores(1, na + k, e, false, n, left);
+        values(1, na + k, e + 1, false);
+      }
+    }
+    __syncwarp();
+  }
+  } else {
+    // ============================ rows ============================
+    regs_inc<ROW_REGS>();
+    const int s = warp >> 2, quarter = warp & 3;
+    const int r = quarter * 32 + lane;       // this thread's row of the slot
+    const uint32_t tb = tmem + s * 256 + ((uint32_t)(quarter * 32) << 16);
+    const int na = p.start_a[cta].steps;
+    const int steps = na + p.start_b[s * p.ctas + cta].steps;
+    const int other = p.start_b[(1 - s) * p.ctas + cta].steps;
+    const float2 scale2 = make_float2(p.scale_log2, p.scale_log2);
+    bool ok = true;
+    for (int k = 0, n = 0; k < steps && ok; ++n) {
+      ok = mbar_wait(q_full + 8 * (UNITS * s + n % UNITS), (n / UNITS) & 1, p.status);
+      if (!ok) break;
+      const Unit unit = ms.unit[s][n % UNITS];
+      const bool active = quarter * 32 < unit.row0 + unit.rows && quarter * 32 + 32 > unit.row0;
+      bool fresh = true;
+      int tokens = unit.tokens;
+      const int end = k + unit.run;
+      float acc[D], m = -INFINITY, l = 0.0f;
+#pragma unroll
+      for (int i = 0; i < D; ++i) acc[i] = 0.0f;
+      for (; k < end; ++k, tokens -= BS) {
+        int valid = min(BS, tokens);
+        const int e = k < na ? 2 * k : entry_b(s, k - na, na, other);
+        const volatile int* bad = &ms.bad[(e >> 1) % STEPS_AHEAD];
+        ok = mbar_wait(s_full + 8 * s, k & 1, p.status);
+        if (!ok) break;
+        tc_fence_after();
+        if (valid < BS) {
+          // V behind the last token may be anything, and 0 * NaN is NaN: zeros there
+          const int ev = (e + 1) % ENTRIES;
+          ok = mbar_wait(full + 8 * ev, entry_parity(e + 1), p.status);
           if (!ok) break;
-          tc_fence_after();
-          if (active) {
-#pragma unroll
-            for (int c = 0; c < 64; c += 16) {
-              float v[16];
-              tmem_ld16(tb + 128 + c, v);
-#pragma unroll
-              for (int j = 0; j < 16; ++j) acc[c + j] = fmaf(acc[c + j], alpha, v[j]);
+          uint8_t* v = smem + SLOTS * TILE + ev * TILE;
+          for (int idx = valid * 8 + r; idx < BS * 8; idx += ROWS) {
+            *reinterpret_cast<uint4*>(v + idx * 16) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(v + BOX + idx * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
+        float alpha = 1.0f;
+        const uint32_t ts = tb + (k & 1) * 128, tp = tb + (~k & 1) * 128;
+        if (active) {
+          if (*bad) valid = 0;
+          float sum = 0.0f;
+          bool search = fresh;
+          fresh = false;
+          while (true) {
+            if (search) {
+              const float top =
+                  (valid < BS ? row_max<true>(ts, valid) : row_max<false>(ts, valid)) * p.scale_log2;
+              if (top > m) {
+                alpha = ex2_fast(m - top);  // 0 where there was nothing yet
+                m = top;
+              }
             }
+            const float shift = P_SHIFT - (m == -INFINITY ? 0.0f : m);
+            sum = valid < BS ? row_exp<true>(ts, tp, valid, scale2, shift)
+                             : row_exp<false>(ts, tp, valid, scale2, shift);
+            // with its own maximum a block's sum is at most 128 * 2^8 = 2^15
+            if (search || !__any_sync(0xffffffffu, sum > SUM_MAX)) break;
+            search = true;
+          }
+          l = fmaf(l, alpha, sum);
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full + 8 * s);
+        ok = mbar_wait(o_full + 8 * s, k & 1, p.status) && ok;
+        if (!ok) break;
+        tc_fence_after();
+        if (active) {
+          const float2 alpha2 = make_float2(alpha, alpha);
+          float v[2][16];
+          tmem_ld16_async(ts, v[0]);
+          tmem_wait_ld(v[0]);
+#pragma unroll
+          for (int c = 0; c < D; c += 16) {
+            float(&x)[16] = v[(c / 16) & 1];
+            float(&next)[16] = v[(c / 16 + 1) & 1];
+            if (c + 16 < D) tmem_ld16_async(ts + c + 16, next);
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+              const float2 y = fma2(make_float2(acc[c + j], acc[c + j + 1]), alpha2,
+                                    make_float2(x[j], x[j + 1]));
+              acc[c + j] = y.x;
+              acc[c + j + 1] = y.y;
+            }
+            if (c + 16 < D) tmem_wait_ld(next);
           }
         }
-        // this run's part of the rows
-        if (r < rows && ok) {
-          const size_t row =
-              a ? ((size_t)cta + (size_t)w.item * p.H_kv + w.head) * (2 * ROWS) + off + r
-                : (size_t)p.rows_a + (size_t)(s * p.ctas + cta) * p.row_max + it.row_base +
-                      (size_t)w.head * it.rows + r;
-          float4* o = reinterpret_cast<float4*>(p.parts + row * D + half * 64);
+      }
+      // this run's part of the rows: [32 groups of 4 channels][rows][4]
+      const int rows = unit.rows, i = r - unit.row0;
+      if (i >= 0 && i < rows && ok) {
+        const long long part = unit.part;
+        float4* o = reinterpret_cast<float4*>(p.parts + part * D) + i;
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            o[i] = make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
-          if (half == 0) p.stats[row * 4] = m;
-          p.stats[row * 4 + 1 + half] = l;
-        }
-        advance(w, run, p.H_kv);
+        for (int c = 0; c < D / 4; ++c)
+          o[(size_t)c * rows] = make_float4(acc[4 * c], acc[4 * c + 1], acc[4 * c + 2], acc[4 * c + 3]);
+        p.stats[part + i] = make_float2(m, l);
       }
     }
   }
@@ -730,78 +999,84 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
 }
 
 // ---- combine -----------------------------------------------------------------------------
+// A warp takes 8 rows (consecutive ones of the batch, which mostly are of a tile too) and 16
+// channels: its 8 x 16 bytes of a part's channel group are contiguous.
 constexpr int COMBINE_WARPS = 8;
-
-// The worker of `n` with equal shares of `all` steps that takes step x.
-__device__ __forceinline__ int worker_of(int x, int all, int n) {
-  int w = (int)((long long)x * n / all);
-  while (w + 1 < n && (long long)all * (w + 1) / n <= x) ++w;
-  while (w > 0 && (long long)all * w / n > x) --w;
-  return w;
-}
+constexpr int COMBINE_ROWS = 8;
 
 __global__ void __launch_bounds__(COMBINE_WARPS * 32) combine_kernel(const __grid_constant__ Params p) {
   griddep_wait();
   griddep_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const int H_q = p.H_kv * p.G;
-  const int row = blockIdx.x * COMBINE_WARPS + (threadIdx.x >> 5);
-  if (row >= p.B * H_q) return;
-  const int b = row / H_q, hq = row % H_q, h = hq / p.G, g = hq % p.G;
+  const int lane = threadIdx.x & 31, all_rows = p.B * p.G;
+  const int chunks = (all_rows + COMBINE_ROWS - 1) / COMBINE_ROWS;
+  const int job = blockIdx.x * COMBINE_WARPS + (threadIdx.x >> 5);
+  const int h = job / (chunks * 8), col = job % 8 * 4 + (lane >> 3);  // channels 4 col .. + 3
+  const int row = job / 8 % chunks * COMBINE_ROWS + (lane & 7);
+  if (h >= p.H_kv || row >= all_rows) return;
+  const int b = row / p.G, g = row % p.G;
   const Head head = *p.head;
-  const RowPlan rp = p.rows[(size_t)b * p.G + g];
+  const RowPlan rp = p.rows[row];
   const Item own = p.items_b[p.suffix[b]];
-  // parts: of the prefix, then of the sequence's own blocks; place i is a + i * stride
-  size_t at[2] = {0, 0};
-  size_t stride[2] = {0, 0};
-  int n[2] = {0, 0};
-  const int workers_a = workers(p.ctas, head.steps_a);
-  const int workers_b = workers(p.ctas * SLOTS, head.steps_b);
+  // parts: of the prefix, then of the sequence's own blocks; the i-th one's rows start at
+  // at + i * stride, it has `rows` of them and this row is number r
+  long long at[2] = {0, 0};
+  int stride[2] = {0, 0}, rows[2] = {0, 0}, r[2] = {0, 0}, n[2] = {0, 0};
+  const Shares shares_b(p.ctas * SLOTS, head.steps_b);
   if (rp.kind == 1) {
     const Item it = p.items_a[rp.item];
     const int x = it.cum + h * it.blocks;
-    const int c0 = worker_of(x, head.steps_a, workers_a);
-    n[0] = worker_of(x + it.blocks - 1, head.steps_a, workers_a) - c0 + 1;
-    at[0] = ((size_t)c0 + (size_t)rp.item * p.H_kv + h) * (2 * ROWS) + rp.row;
+    const Shares shares_a(p.ctas, head.steps_a);
+    const int c0 = shares_a.worker_of(x);
+    const int off = rp.row / ROWS * ROWS;
+    n[0] = shares_a.worker_of(x + it.blocks - 1) - c0 + 1;
+    at[0] = ((long long)c0 + (long long)rp.item * p.H_kv + h) * (2 * ROWS) + off;
     stride[0] = 2 * ROWS;
+    rows[0] = min(ROWS, it.rows - off);
+    r[0] = rp.row - off;
   } else if (rp.kind == 2) {
     const Item it = p.items_b[rp.item];
     const int x = it.cum + h * it.blocks;
-    const int c0 = worker_of(x, head.steps_b, workers_b);
-    n[0] = worker_of(x + it.blocks - 1, head.steps_b, workers_b) - c0 + 1;
-    at[0] = (size_t)p.rows_a + (size_t)c0 * p.row_max + it.row_base + (size_t)h * it.rows + rp.row;
+    const int c0 = shares_b.worker_of(x);
+    n[0] = shares_b.worker_of(x + it.blocks - 1) - c0 + 1;
+    at[0] = p.rows_a + (long long)c0 * p.row_max + it.row_base + (long long)h * it.rows;
     stride[0] = p.row_max;
+    rows[0] = it.rows;
+    r[0] = rp.row;
   }
   if (own.blocks > 0) {
     const int x = own.cum + h * own.blocks;
-    const int c0 = worker_of(x, head.steps_b, workers_b);
-    n[1] = worker_of(x + own.blocks - 1, head.steps_b, workers_b) - c0 + 1;
-    at[1] = (size_t)p.rows_a + (size_t)c0 * p.row_max + own.row_base + (size_t)h * own.rows + g;
+    const int c0 = shares_b.worker_of(x);
+    n[1] = shares_b.worker_of(x + own.blocks - 1) - c0 + 1;
+    at[1] = p.rows_a + (long long)c0 * p.row_max + own.row_base + (long long)h * own.rows;
     stride[1] = p.row_max;
+    rows[1] = own.rows;
+    r[1] = g;
   }
   float M = -INFINITY;
-  for (int k = 0; k < 2; ++k)
-    for (int i = lane; i < n[k]; i += 32) M = fmaxf(M, p.stats[(at[k] + i * stride[k]) * 4]);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  for (int k = 0; k < 2; ++k)
+    for (int i = 0; i < n[k]; ++i)
+      M = fmaxf(M, p.stats[at[k] + (long long)i * stride[k] + r[k]].x);
   const float base = M == -INFINITY ? 0.0f : M;
   float L = 0.0f;
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
   for (int k = 0; k < 2; ++k)
 #pragma unroll 4
     for (int i = 0; i < n[k]; ++i) {
-      const size_t r = at[k] + i * stride[k];
-      const float4 st = *reinterpret_cast<const float4*>(p.stats + r * 4);
-      const float4 o = *reinterpret_cast<const float4*>(p.parts + r * D + lane * 4);
+      const long long first = at[k] + (long long)i * stride[k];
+      const float2 st = p.stats[first + r[k]];
+      const float4 o = reinterpret_cast<const float4*>(p.parts + first * D)[(size_t)col * rows[k] + r[k]];
       const float w = ex2_fast(st.x - base);
-      L = fmaf(st.y + st.z, w, L);
+      L = fmaf(st.y, w, L);
       acc.x = fmaf(o.x, w, acc.x);
       acc.y = fmaf(o.y, w, acc.y);
       acc.z = fmaf(o.z, w, acc.z);
       acc.w = fmaf(o.w, w, acc.w);
     }
   const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-  reinterpret_cast<float4*>(p.out + (size_t)row * D)[lane] =
+  float* out = p.out + ((size_t)b * p.H_kv * p.G + h * p.G + g) * D;
+  reinterpret_cast<float4*>(out)[col] =
       make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
 }
 
@@ -821,8 +1096,8 @@ PrefixWs prefix_layout(int B, int H_kv, int G) {
   off = align256(off + PREFIX_MAX_CTAS * sizeof(Start));
   L.start_b = off;
   off = align256(off + PREFIX_MAX_CTAS * SLOTS * sizeof(Start));
-  L.members = off;
-  off = align256(off + (size_t)B * 4);
+  L.q_rows = off;
+  off = align256(off + (size_t)B * G * 4);
   L.rows = off;
   off = align256(off + (size_t)B * G * sizeof(RowPlan));
   L.suffix = off;
@@ -834,7 +1109,7 @@ PrefixWs prefix_layout(int B, int H_kv, int G) {
   L.parts = off;
   off = align256(off + total_rows * D * 4);
   L.stats = off;
-  off = align256(off + total_rows * 16);
+  off = align256(off + total_rows * 8);
   L.total = off + 256;  // (its start is aligned down)
   return L;
 }
@@ -879,11 +1154,11 @@ cudaError_t launch_prefix(const PrefixLaunch& a, cudaStream_t stream) {
   p.items_b = reinterpret_cast<Item*>(ws + L.items_b);
   p.start_a = reinterpret_cast<Start*>(ws + L.start_a);
   p.start_b = reinterpret_cast<Start*>(ws + L.start_b);
-  p.members = reinterpret_cast<int*>(ws + L.members);
+  p.q_rows = reinterpret_cast<int*>(ws + L.q_rows);
   p.rows = reinterpret_cast<RowPlan*>(ws + L.rows);
   p.suffix = reinterpret_cast<int*>(ws + L.suffix);
   p.parts = reinterpret_cast<float*>(ws + L.parts);
-  p.stats = reinterpret_cast<float*>(ws + L.stats);
+  p.stats = reinterpret_cast<float2*>(ws + L.stats);
   p.rows_a = L.rows_a;
   p.B = a.B;
   p.H_kv = a.H_kv;
@@ -906,12 +1181,15 @@ cudaError_t launch_prefix(const PrefixLaunch& a, cudaStream_t stream) {
                                      (int)sizeof(PlanShared));
   });
   if (e != cudaSuccess) return e;
-  e = launch(plan_kernel, p, 1, PLAN_THREADS, sizeof(PlanShared), stream);
+  int threads = a.B > a.groups ? a.B : a.groups;
+  threads = threads < 3 * p.ctas ? 3 * p.ctas : threads;
+  threads = threads < PLAN_THREADS ? (threads + 31) & ~31 : PLAN_THREADS;
+  e = launch(plan_kernel, p, 1, threads, sizeof(PlanShared), stream);
   if (e != cudaSuccess) return e;
   e = launch(attend_kernel, p, p.ctas, THREADS, SMEM, stream);
   if (e != cudaSuccess) return e;
-  const int rows = a.B * a.H_kv * a.G;
-  return launch(combine_kernel, p, (rows + COMBINE_WARPS - 1) / COMBINE_WARPS, COMBINE_WARPS * 32, 0,
+  const int jobs = a.H_kv * ((a.B * a.G + COMBINE_ROWS - 1) / COMBINE_ROWS) * (D / 16);
+  return launch(combine_kernel, p, (jobs + COMBINE_WARPS - 1) / COMBINE_WARPS, COMBINE_WARPS * 32, 0,
                 stream);
 }
 

@@ -28,13 +28,13 @@ def tolerance(mag, want, score, all_v, steps):
     each of `steps` additions, rescaling by an exponential (2^-22 and the rounded difference of two
     maxima, 2^-23 of at most 32 or 2.9 score) at most as often as the maximum grows, which a
     bound of 16 covers together with the joins.  Numerator and denominator both carry these.
-    2^15 P / max P in binary16 parts ends at 2^-24, half a step of which is 2^-40 of the largest P
-    for every token."""
+    P in binary16 parts ends at 2^-24, half a step of which is 2^-33 of 2^8 for every token, where 2^8
+    stands for a P no greater than the largest."""
     score = max(score, 11.0)
     arg = max(32.0, 2.9 * score)
     p = 8 * 2.0 ** -23 * score + 2.0 ** -23 * arg + 2 * 2.0 ** -22
     p += 16 * 2.0 ** -23 + steps * 2.0 ** -24 + 16 * (2.0 ** -22 + 2.0 ** -23 * arg)
-    return 2 * p * mag + 2.0 ** -22 * np.abs(want) + 2.0 ** -40 * all_v
+    return 2 * p * mag + 2.0 ** -22 * np.abs(want) + 2.0 ** -33 * all_v
 
 
 class Batch:
