@@ -36,25 +36,33 @@ struct Item {      // blocks of one K/V head that a set of rows attends, for eve
   int member;      // first row's place in the list of members times G, -1: seq's own rows
   int tokens;      // tokens of seq from block `start` on
   int row_base;    // B items: first row of the item's parts (head 0)
-  int cum;         // steps of all items before (all heads)
+  int pad;
 };
 
 struct Start {     // where a CTA (A) or a slot (B; slot s of CTA c is worker s * CTAs + c) begins
   int item, head, block, steps;
+  Item first;      // that item
 };
 
-struct RowPlan {   // where the parts of a row's prefix are
+struct Place {     // where the blocks of an item are among all steps (head 0), and its parts
+  int cum, cost, blocks, base;
+};
+
+struct RowPlan {   // the prefix of a row
+  Place at;        // base: A items: item * heads, B items: row_base
   int kind;        // 0 none, 1 A item, 2 B item
-  int item, row, pad;
+  int rows;        // of its tile
+  int row, off;    // its place in the tile, and the tile's in the item
 };
 
 struct Head {
-  int steps_a, steps_b, items_b, pad;
+  int steps_a, cost_a, steps_b, cost_b;
 };
 
 // Offsets in the workspace's part.
 struct PrefixWs {
-  size_t head, items_a, items_b, start_a, start_b, q_rows, rows, suffix, parts, stats, total;
+  size_t head, items_a, items_b, start_a, start_b, first_a, first_b, q_rows, rows, own, parts,
+      stats, total;
   long long rows_a;  // parts of A items come first
 };
 
@@ -74,7 +82,9 @@ struct Params {
   Start* start_b;
   int* q_rows;     // of members' rows: row of q (head 0)
   RowPlan* rows;   // [B][G]
-  int* suffix;     // [B]: the B item of a sequence's own blocks
+  Place* own;      // [B]: a sequence's own blocks
+  int* first_a;    // [CTAs + 1] first step of each CTA ...
+  int* first_b;    // ... and of each slot
   float* parts;    // of n rows: [32][n][4], the groups of four channels of all rows
   float2* stats;   // [rows]: m, l
   long long rows_a;
@@ -89,15 +99,19 @@ __device__ __forceinline__ float ex2_fast(float x) {
 }
 
 // ---- plan --------------------------------------------------------------------------------
+// Equal shares of the cost of all steps, one a block and one a run (its queries, its part):
+// a run of one block takes about twice the time of a block in the middle of a long one.
 struct PlanShared {
   int cu[MAX_SEGS + 1];
+  int prefix[MAX_SEGS];
+  int len[MAX_SEGS];
   int member[MAX_SEGS + 1];     // members before sequence b (each in its group)
   int start[MAX_SEGS];          // prefix blocks that b holds, -1: no member
   int group[MAX_SEGS];          // of sequence b
   int pairs[MAX_SEGS];          // of group g: first A item (-1: nothing shared) ...
   int single[MAX_SEGS];         // ... and its B item
-  int cum_b[2 * MAX_SEGS + 1];
-  int cum_a[MAX_SEGS + 1];
+  int2 items_a[MAX_SEGS + 1];   // steps and cost of the items before
+  int2 items_b[2 * MAX_SEGS + 1];
   int4 warp_sum[PLAN_THREADS / 32];
   int bad;
 };
@@ -105,60 +119,55 @@ struct PlanShared {
 __device__ __forceinline__ int4 add4(int4 a, int4 b) {
   return make_int4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
 }
-__device__ __forceinline__ int4 up4(int4 v, int o) {
-  return make_int4(__shfl_up_sync(0xffffffffu, v.x, o), __shfl_up_sync(0xffffffffu, v.y, o),
-                   __shfl_up_sync(0xffffffffu, v.z, o), __shfl_up_sync(0xffffffffu, v.w, o));
-}
-__device__ __forceinline__ int4 at4(int4 v, int i) {
-  return make_int4(__shfl_sync(0xffffffffu, v.x, i), __shfl_sync(0xffffffffu, v.y, i),
-                   __shfl_sync(0xffffffffu, v.z, i), __shfl_sync(0xffffffffu, v.w, i));
+// Inclusive prefixes of four numbers over a warp.
+__device__ __noinline__ int4 warp_scan4(int4 v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int o = 1; o < 32; o <<= 1) {
+    const int4 u = make_int4(__shfl_up_sync(0xffffffffu, v.x, o), __shfl_up_sync(0xffffffffu, v.y, o),
+                             __shfl_up_sync(0xffffffffu, v.z, o), __shfl_up_sync(0xffffffffu, v.w, o));
+    if (lane >= o) v = add4(v, u);
+  }
+  return v;
 }
 // Exclusive prefixes of four numbers over the CTA's threads, from `base`, to which the totals
-// are added.
-__device__ __forceinline__ int4 plan_scan(int4 x, int4& base, PlanShared& sh) {
+// are added.  (Out of line like everything here that is used more than once: the kernel runs its
+// code once, and fetching it is what takes the time.)
+__device__ __noinline__ int4 plan_scan(int4 x, int4& base, PlanShared& sh) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  int4 incl = x;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int4 v = up4(incl, o);
-    if (lane >= o) incl = add4(incl, v);
-  }
+  const int4 incl = warp_scan4(x);
   __syncthreads();
   if (lane == 31) sh.warp_sum[warp] = incl;
   __syncthreads();
-  int4 s = lane < warps ? sh.warp_sum[lane] : make_int4(0, 0, 0, 0);
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int4 v = up4(s, o);
-    if (lane >= o) s = add4(s, v);
+  if (warp == 0) {
+    const int4 s = warp_scan4(lane < warps ? sh.warp_sum[lane] : make_int4(0, 0, 0, 0));
+    sh.warp_sum[lane] = s;
   }
-  int4 before = at4(s, warp > 0 ? warp - 1 : 0);
-  if (warp == 0) before = make_int4(0, 0, 0, 0);
-  const int4 excl =
-      make_int4(base.x + before.x + incl.x - x.x, base.y + before.y + incl.y - x.y,
-                base.z + before.z + incl.z - x.z, base.w + before.w + incl.w - x.w);
-  base = add4(base, at4(s, 31));
-  return excl;
+  __syncthreads();
+  int4 excl = add4(base, incl);
+  if (warp > 0) excl = add4(excl, sh.warp_sum[warp - 1]);
+  base = add4(base, sh.warp_sum[warps - 1]);
+  return make_int4(excl.x - x.x, excl.y - x.y, excl.z - x.z, excl.w - x.w);
 }
 
-// The last index i of [0, n) with cum[i] <= x.
-__device__ __forceinline__ int last_at(const int* cum, int n, int x) {
+// The last index i of [0, n) with cum[i * stride] <= x.
+__device__ __noinline__ int last_at(const int* cum, int stride, int n, int x) {
   int lo = 0, hi = n;
   while (lo + 1 < hi) {
     const int mid = (lo + hi) / 2;
-    if (cum[mid] <= x) lo = mid;
+    if (cum[mid * stride] <= x) lo = mid;
     else hi = mid;
   }
   return lo;
 }
 
-// Shares of `all` steps among up to n workers: each has at least one step, the first ones one
-// more than the others.
+// Shares of a cost among up to n workers, but no more than there are steps: the first ones have
+// one more than the others.
 struct Shares {
-  int n, each, more;  // the first `more` workers have each + 1
-  __device__ __forceinline__ Shares(int workers, int all) : n(min(workers, all)) {
-    each = n > 0 ? all / n : 1;
-    more = all - n * each;
+  int n, each, more;
+  __device__ __forceinline__ Shares(int workers, int steps, int cost) : n(min(workers, steps)) {
+    each = n > 0 ? cost / n : 1;
+    more = cost - n * each;
   }
   __device__ __forceinline__ int first(int w) const { return w * each + min(w, more); }
   __device__ __forceinline__ int worker_of(int x) const {
@@ -166,16 +175,6 @@ struct Shares {
     return x < cut ? x / (each + 1) : more + (x - cut) / each;
   }
 };
-
-// The length of sequence b, within what its table can hold.
-__device__ __forceinline__ int seq_len(const Params& p, int b) {
-  int n = p.seq_lens[b];
-  if (n < 0 || n > p.max_blocks * BS) {
-    set_status(p.status, KT_ERR_DEVICE_CHECK);
-    n = n < 0 ? 0 : p.max_blocks * BS;
-  }
-  return n;
-}
 
 // Launched with as many threads as there are sequences, groups or slots, at most PLAN_THREADS.
 __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constant__ Params p) {
@@ -185,11 +184,22 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constan
   if (tid == 0) sh.bad = 0;
   griddep_wait();
   griddep_launch_dependents();
+  for (int g = tid; g <= p.groups; g += threads) {
+    sh.cu[g] = p.cu[g];
+    if (g < p.groups) sh.prefix[g] = p.prefix[g];
+  }
+  for (int b = tid; b < p.B; b += threads) {
+    int n = p.seq_lens[b];
+    if (n < 0 || n > p.max_blocks * BS) {
+      set_status(p.status, KT_ERR_DEVICE_CHECK);
+      n = n < 0 ? 0 : p.max_blocks * BS;
+    }
+    sh.len[b] = n;
+  }
   __syncthreads();
   for (int g = tid; g <= p.groups; g += threads) {
-    const int c = p.cu[g];
-    sh.cu[g] = c;
-    if (c < 0 || c > p.B || (g > 0 && c < p.cu[g - 1])) sh.bad = 1;
+    const int c = sh.cu[g];
+    if (c < 0 || c > p.B || (g > 0 && c < sh.cu[g - 1])) sh.bad = 1;
   }
   __syncthreads();
   const bool grouped = !sh.bad;  // else every sequence is attended by itself
@@ -201,11 +211,11 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constan
     const int b = b0 + tid;
     int start = -1, g = p.groups;
     if (b < p.B && grouped) {
-      g = last_at(sh.cu, p.groups + 1, b);
+      g = last_at(sh.cu, 1, p.groups + 1, b);
       if (g < p.groups && sh.cu[g] <= b) {
-        const int blocks = p.prefix[g];
+        const int blocks = sh.prefix[g];
         if (blocks < 0 || blocks > p.max_blocks) set_status(p.status, KT_ERR_DEVICE_CHECK);
-        else if (blocks > 0 && seq_len(p, b) >= blocks * BS) start = blocks;
+        else if (blocks > 0 && sh.len[b] >= blocks * BS) start = blocks;
       }
     }
     const int r = plan_scan(make_int4(start >= 0, 0, 0, 0), members, sh).x;
@@ -253,26 +263,27 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constan
       it.member = first * p.G + i * 2 * ROWS;
       it.tokens = blocks * BS;
       it.row_base = a ? 0 : at.w * p.H_kv;
-      it.cum = (a ? at.y + i * blocks : at.z) * p.H_kv;
-      (a ? p.items_a[ip + i] : p.items_b[is]) = it;
-      (a ? sh.cum_a[ip + i] : sh.cum_b[is]) = it.cum;
+      it.pad = 0;
+      const int cum = a ? at.y + i * blocks : at.z, n = a ? ip + i : is;
+      (a ? p.items_a : p.items_b)[n] = it;
+      (a ? sh.items_a : sh.items_b)[n] = make_int2(cum * p.H_kv, (cum + n) * p.H_kv);
     }
   }
   __syncthreads();
   const int pairs = sums.x >> 16, singles = sums.x & 0xffff;
 
   // what each sequence has of its own, and where the parts of its rows' prefix are
-  int4 own = make_int4(sums.z, 0, 0, 0);
+  int4 own = make_int4(sums.z, singles, 0, 0);
   for (int b0 = 0; b0 < p.B; b0 += threads) {
     const int b = b0 + tid;
     int start = 0, n = 0, nb = 0, first_a = -1;
     if (b < p.B) {
-      n = seq_len(p, b);
+      n = sh.len[b];
       nb = (n + BS - 1) / BS;
       if (sh.start[b] >= 0) first_a = sh.pairs[sh.group[b]];
       if (first_a >= 0) start = sh.start[b];
     }
-    const int sb = plan_scan(make_int4(nb - start, 0, 0, 0), own, sh).x;
+    const int4 at = plan_scan(make_int4(nb - start, nb > start, 0, 0), own, sh);
     if (b < p.B) {
       Item it;
       it.seq = b;
@@ -282,51 +293,72 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constan
       it.member = -1;
       it.tokens = n - start * BS;
       it.row_base = (sums.w + b * p.G) * p.H_kv;
-      it.cum = sb * p.H_kv;
+      it.pad = 0;
       p.items_b[singles + b] = it;
-      sh.cum_b[singles + b] = it.cum;
-      p.suffix[b] = singles + b;
-      const int g = sh.group[b];
-      int r0 = 0, np = 0;
+      sh.items_b[singles + b] = make_int2(at.x * p.H_kv, (at.x + at.y) * p.H_kv);
+      p.own[b] = Place{at.x * p.H_kv, (at.x + at.y) * p.H_kv, it.blocks, it.row_base};
+      int r0 = 0, np = 0, rows = 0, single = 0;
       if (first_a >= 0) {
-        const int c0 = sh.member[sh.cu[g]];
-        const int rows = (sh.member[sh.cu[g + 1]] - c0) * p.G;
+        const int g = sh.group[b], c0 = sh.member[sh.cu[g]];
+        rows = (sh.member[sh.cu[g + 1]] - c0) * p.G;
         r0 = (sh.member[b] - c0) * p.G;
         np = (rows + ROWS - 1) / ROWS / 2;
+        single = sh.single[g];
       }
       for (int i = 0; i < p.G; ++i) {
-        RowPlan rp = {0, 0, 0, 0};
+        RowPlan rp;
+        rp.kind = 0;
         if (first_a >= 0) {
-          const int pair = (r0 + i) / (2 * ROWS);
-          rp.kind = pair < np ? 1 : 2;
-          rp.item = pair < np ? first_a + pair : sh.single[g];
-          rp.row = r0 + i - pair * 2 * ROWS;
+          const int r = r0 + i, pair = r / (2 * ROWS), tile = r / ROWS * ROWS;
+          const bool a = pair < np;
+          const int2 c = a ? sh.items_a[first_a + pair] : sh.items_b[single];
+          rp.kind = a ? 1 : 2;
+          rp.at.cum = c.x;
+          rp.at.cost = c.y;
+          rp.at.blocks = start;
+          rp.at.base = a ? (first_a + pair) * p.H_kv : p.items_b[single].row_base;
+          rp.rows = min(ROWS, rows - tile);
+          rp.row = r - tile;
+          rp.off = tile - pair * 2 * ROWS;
         }
         p.rows[(size_t)b * p.G + i] = rp;
       }
     }
   }
   __syncthreads();
-  const int steps_a = sums.y * p.H_kv, steps_b = own.x * p.H_kv;
+  const int steps_a = sums.y * p.H_kv, cost_a = (sums.y + pairs) * p.H_kv;
+  const int steps_b = own.x * p.H_kv, cost_b = (own.x + own.y) * p.H_kv;
   const int items_b = singles + p.B;
-  if (tid == 0) *p.head = Head{steps_a, steps_b, items_b, 0};
-  // equal shares: A steps over the CTAs, B steps over their slots
+  if (tid == 0) *p.head = Head{steps_a, cost_a, steps_b, cost_b};
   for (int c = tid; c < p.ctas * (1 + SLOTS); c += threads) {
     const bool a = c < p.ctas;
     const int w = a ? c : c - p.ctas;
-    const int all = a ? steps_a : steps_b;
-    const Shares shares(a ? p.ctas : p.ctas * SLOTS, all);
-    Start st = {0, 0, 0, 0};
+    const int steps = a ? steps_a : steps_b;
+    const Shares shares(a ? p.ctas : p.ctas * SLOTS, steps, a ? cost_a : cost_b);
+    int* firsts = a ? p.first_a : p.first_b;
+    Start st;
+    st.item = st.head = st.block = st.steps = 0;
     if (w < shares.n) {
-      const int lo = shares.first(w);
-      st.steps = shares.first(w + 1) - lo;
-      const int* cum = a ? sh.cum_a : sh.cum_b;
-      const int items = a ? pairs : items_b;
-      st.item = last_at(cum, items, lo);  // never one without blocks
-      const int next = st.item + 1 < items ? cum[st.item + 1] : all;
-      const int blocks = (next - cum[st.item]) / p.H_kv;
-      st.head = (lo - cum[st.item]) / blocks;
-      st.block = (lo - cum[st.item]) % blocks;
+      const int2* at = a ? sh.items_a : sh.items_b;
+      const int n = a ? pairs : items_b;
+      // the places where this share and the next one begin: the first unit of a run's cost is
+      // its own, then its blocks
+      int end = steps;
+#pragma unroll 1
+      for (int next = w + 1 < shares.n; next >= 0; --next) {
+        const int x = shares.first(w + next);
+        const int i = last_at(&at[0].y, 2, n, x);  // never one without blocks
+        const int blocks = ((i + 1 < n ? at[i + 1].x : steps) - at[i].x) / p.H_kv;
+        st.item = i;
+        st.head = (x - at[i].y) / (blocks + 1);
+        st.block = max(0, x - at[i].y - st.head * (blocks + 1) - 1);
+        const int step = at[i].x + st.head * blocks + st.block;
+        if (next) end = step;
+        else firsts[w] = step;
+      }
+      st.steps = end - firsts[w];
+      if (w + 1 == shares.n) firsts[w + 1] = steps;
+      st.first = (a ? p.items_a : p.items_b)[st.item];
     }
     (a ? p.start_a : p.start_b)[w] = st;
   }
@@ -343,14 +375,14 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constan
 //
 // A slot's block: S (TMEM, 128 columns) = Q K^T; the row threads turn it into P, which goes
 // where the last block's output was; O = P V takes the place of S; the row threads add it to
-// their running output in registers: out = out * alpha + O, and the next S takes the place of
+// their running output in registers, out = out * alpha + O, and the next S takes the place of
 // P.  So a block's P V is summed apart from the running output, no output is rescaled in
 // TMEM, and the scores stay until P is whole: the exponentials use the running maximum of the
 // blocks before and are made again, after a search for the block's own, where their sum shows
-// that one may not fit binary16 (alpha then scales what was summed before).  A run's first
-// block takes its maximum first.
+// that one may not fit binary16 (alpha then scales what was summed before).  Where there is no
+// maximum yet it is taken first.
 //
-// P is held as two binary16, 2^8 p = hi - lo (22 bits; at least 2^-25), and
+// P is held as two binary16, 2^8 p = hi - lo (22 bits; steps of at least 2^-24), and
 // P V as two products (the tensor cores negate lo): with one alone the output would be good to 11 bits only, and it is
 // binary32.  For 16 tokens, the K of a tensor-core step, columns 0-7 are hi, 8-15 lo.
 //
@@ -363,7 +395,8 @@ struct Unit {      // a run of blocks of one (item, head) in a slot
   long long part;  // its part's first row in the workspace
 };
 // A run's queries are fetched once the tensor cores are done with those of the run before
-// last (their half) and the row threads have begun the run before that: four descriptions.
+// last (their half): all row warps have then arrived for a block of the run before that, so
+// they have read the description before, whose place in four the new one takes.
 constexpr int UNITS = 4;
 constexpr int STEPS_AHEAD = 8;  // flags of the ring's steps: more than it holds
 struct Misc {
@@ -486,7 +519,7 @@ constexpr float P_SHIFT = 8.0f, SUM_MAX = 65000.0f;
 
 // Registers pass from the control warps to the row threads: three warpgroups are launched with
 // LAUNCH_REGS a thread (the host checks that), and the shares must not add up to more.
-constexpr int LAUNCH_REGS = 168, ROW_REGS = 224, CONTROL_REGS = 56;
+constexpr int LAUNCH_REGS = 168, ROW_REGS = 216, CONTROL_REGS = 72;
 static_assert(2 * ROW_REGS + CONTROL_REGS <= 3 * LAUNCH_REGS, "registers of a CTA");
 template <int N>
 __device__ __forceinline__ void regs_inc() {
@@ -497,6 +530,10 @@ __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// The softmax runs over chunks of 16 columns, the next one's load in flight, two a turn of the
+// loop: eight in a row are ten kilobytes of code, which every launch fetches anew (3300 cycles
+// for its first block instead of TBD).
+//
 // A row's largest score (columns from taddr on).
 template <bool MASK>
 __device__ __forceinline__ float row_max(uint32_t taddr, int valid) {
@@ -504,26 +541,29 @@ __device__ __forceinline__ float row_max(uint32_t taddr, int valid) {
   float top = -INFINITY, top2 = -INFINITY;
   tmem_ld16_async(taddr, v[0]);
   tmem_wait_ld(v[0]);
+#pragma unroll 1
+  for (int c0 = 0; c0 < BS; c0 += 32) {
 #pragma unroll
-  for (int c = 0; c < BS; c += 16) {
-    float(&x)[16] = v[(c / 16) & 1];
-    float(&next)[16] = v[(c / 16 + 1) & 1];
-    if (c + 16 < BS) tmem_ld16_async(taddr + c + 16, next);
-    if (MASK) mask16(x, c, valid);
+    for (int i = 0; i < 2; ++i) {
+      const int c = c0 + 16 * i;
+      float(&x)[16] = v[i];
+      tmem_ld16_async(taddr + min(c + 16, BS - 16), v[i ^ 1]);
+      if (MASK) mask16(x, c, valid);
 #pragma unroll
-    for (int j = 0; j < 16; j += 4) {
-      top = max3(top, x[j], x[j + 1]);
-      top2 = max3(top2, x[j + 2], x[j + 3]);
+      for (int j = 0; j < 16; j += 4) {
+        top = max3(top, x[j], x[j + 1]);
+        top2 = max3(top2, x[j + 2], x[j + 3]);
+      }
+      tmem_wait_ld(v[i ^ 1]);
     }
-    if (c + 16 < BS) tmem_wait_ld(next);
   }
   return fmaxf(top, top2);
 }
 
 // 2^(s scale + shift) of a row's scores at `from`, in two parts to `to`; returns their sum.
-// No branch between the chunks, so that their instructions interleave.  An element costs four
-// issue slots (half an FMA and an addition of two, the exponential, two halves of conversions, a
-// mixed-precision FMA); the exponentials bound it, 4 cycles a warp's: 512 a block.
+// An element costs four issue slots (half an FMA and an addition of two, the exponential, two
+// halves of conversions, a mixed-precision subtraction); the exponentials bound it, 4 cycles a
+// warp's: 512 a block.
 template <bool MASK>
 __device__ __forceinline__ float row_exp(uint32_t from, uint32_t to, int valid, float2 scale2,
                                          float shift) {
@@ -532,23 +572,26 @@ __device__ __forceinline__ float row_exp(uint32_t from, uint32_t to, int valid, 
   float v[2][16];
   tmem_ld16_async(from, v[0]);
   tmem_wait_ld(v[0]);
+#pragma unroll 1
+  for (int c0 = 0; c0 < BS; c0 += 32) {
 #pragma unroll
-  for (int c = 0; c < BS; c += 16) {
-    float(&x)[16] = v[(c / 16) & 1];
-    float(&next)[16] = v[(c / 16 + 1) & 1];
-    if (c + 16 < BS) tmem_ld16_async(from + c + 16, next);
-    if (MASK) mask16(x, c, valid);
+    for (int i = 0; i < 2; ++i) {
+      const int c = c0 + 16 * i;
+      float(&x)[16] = v[i];
+      tmem_ld16_async(from + min(c + 16, BS - 16), v[i ^ 1]);
+      if (MASK) mask16(x, c, valid);
 #pragma unroll
-    for (int j = 0; j < 16; j += 2) {
-      const float2 y = fma2(make_float2(x[j], x[j + 1]), scale2, shift2);
-      x[j] = ex2_fast(y.x);
-      x[j + 1] = ex2_fast(y.y);
-      sum[j / 2 & 1] = add2(sum[j / 2 & 1], make_float2(x[j], x[j + 1]));
+      for (int j = 0; j < 16; j += 2) {
+        const float2 y = fma2(make_float2(x[j], x[j + 1]), scale2, shift2);
+        x[j] = ex2_fast(y.x);
+        x[j + 1] = ex2_fast(y.y);
+        sum[j / 2 & 1] = add2(sum[j / 2 & 1], make_float2(x[j], x[j + 1]));
+      }
+      uint32_t w16[16];
+      split16(x, w16);
+      tmem_wait_ld(v[i ^ 1]);
+      tmem_st16(to + c, w16);
     }
-    uint32_t w16[16];
-    split16(x, w16);
-    if (c + 16 < BS) tmem_wait_ld(next);
-    tmem_st16(to + c, w16);
   }
   return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
 }
@@ -577,23 +620,22 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, in
 // A walk over the steps of a share: runs of blocks of one (item, head).
 struct Walk {
   const Item* items;
+  Item it;                      // the item at hand
   int item, head, block, left;  // `left` steps of the share
 };
 __device__ __forceinline__ Walk walk_of(const Item* items, const Start& s) {
-  return Walk{items, s.item, s.head, s.block, s.steps};
+  return Walk{items, s.first, s.item, s.head, s.block, s.steps};
 }
-// The run at the walk's place; call advance(run) afterwards.
-__device__ __forceinline__ int run_of(const Walk& w, const Item& it) {
-  return min(w.left, it.blocks - w.block);
-}
+__device__ __forceinline__ int run_of(const Walk& w) { return min(w.left, w.it.blocks - w.block); }
+// To the next run, behind one of `run` blocks.
 __device__ __forceinline__ void advance(Walk& w, int run, int heads) {
   w.left -= run;
   w.block = 0;
-  if (++w.head == heads) {
-    w.head = 0;
-    ++w.item;
-    while (w.left > 0 && w.items[w.item].blocks == 0) ++w.item;
-  }
+  if (++w.head < heads || w.left == 0) return;
+  w.head = 0;
+  do {
+    w.it = w.items[++w.item];
+  } while (w.it.blocks == 0);
 }
 
 // First ring entry of slot s's B step k (K; V is the next one), behind `a` A steps: the
@@ -677,8 +719,6 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
   regs_dec<CONTROL_REGS>();
   if (warp == SOFT_WARPS + 2) {
     // ============================ K and V tiles ============================
-    const Start sa = p.start_a[cta];
-    const Start sb0 = p.start_b[cta], sb1 = p.start_b[p.ctas + cta];
     const uint64_t pol = l2_evict_first_policy();
     const int row_end = p.P * p.H_kv * BS;  // reads zeros
     int e = 0;
@@ -692,7 +732,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
       }
       for (int side = 0; side < 2 && ok; ++side, ++e) {
         const int st = e % ENTRIES;
-        if (e >= ENTRIES) ok = mbar_wait(empty + 8 * st, entry_parity(e) ^ 1, p.status);
+        if (e >= ENTRIES) ok = mbar_wait_warp(empty + 8 * st, entry_parity(e) ^ 1, p.status);
         if (!ok) break;
         if (lane == 0) {
           const CUtensorMap* map = side == 0 ? &p.kmap : &p.vmap;
@@ -709,39 +749,35 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
       const int j = block + lane;
       return j < it.blocks ? p.table[(size_t)it.seq * p.max_blocks + it.start + j] : -1;
     };
-    Walk w = walk_of(p.items_a, sa);
-    while (ok && w.left > 0) {
-      const Item it = w.items[w.item];
-      const int run = run_of(w, it);
-      int pages = 0;
-      for (int i = 0; i < run && ok; ++i) {
-        if ((i & 31) == 0) pages = fetch(it, w.block + i);
-        load(__shfl_sync(0xffffffffu, pages, i & 31), w.head);
+    struct Turn {
+      Walk w;
+      int at, run, pages;
+    };
+    auto turn = [&](Turn& t) {
+      if (t.w.left == 0) return;
+      if ((t.at & 31) == 0) {
+        t.run = run_of(t.w);
+        t.pages = fetch(t.w.it, t.w.block + t.at);
       }
-      advance(w, run, p.H_kv);
-    }
-    Walk x0 = walk_of(p.items_b, sb0), x1 = walk_of(p.items_b, sb1);
-    int at0 = 0, at1 = 0, run0 = 0, run1 = 0, pages0 = 0, pages1 = 0;
-    auto turn = [&](Walk& x, int& at, int& run, int& pages) {
-      if (x.left == 0) return;
-      if (at == 0 || (at & 31) == 0) {
-        const Item it = x.items[x.item];
-        run = run_of(x, it);
-        pages = fetch(it, x.block + at);
-      }
-      load(__shfl_sync(0xffffffffu, pages, at & 31), x.head);
-      if (++at == run) {
-        advance(x, run, p.H_kv);
-        at = 0;
+      load(__shfl_sync(0xffffffffu, t.pages, t.at & 31), t.w.head);
+      if (++t.at == t.run) {
+        advance(t.w, t.run, p.H_kv);
+        t.at = 0;
       }
     };
-    while (ok && (x0.left > 0 || x1.left > 0)) {
-      turn(x0, at0, run0, pages0);
-      if (ok) turn(x1, at1, run1, pages1);
+    {
+      Turn t = {walk_of(p.items_a, p.start_a[cta]), 0, 0, 0};
+      while (ok && t.w.left > 0) turn(t);
+    }
+    Turn t0 = {walk_of(p.items_b, p.start_b[cta]), 0, 0, 0};
+    Turn t1 = {walk_of(p.items_b, p.start_b[p.ctas + cta]), 0, 0, 0};
+    while (ok && (t0.w.left > 0 || t1.w.left > 0)) {
+      turn(t0);
+      if (ok) turn(t1);
     }
     // nothing of this CTA's is in flight when it ends
     for (int i = max(0, e - ENTRIES); i < e; ++i)
-      mbar_wait(full + 8 * (i % ENTRIES), entry_parity(i), p.status);
+      mbar_wait_warp(full + 8 * (i % ENTRIES), entry_parity(i), p.status);
   } else if (warp == SOFT_WARPS + 3) {
     // ============================ runs and their queries ============================
     Walk w[SLOTS];
@@ -759,8 +795,8 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
 #pragma unroll
         for (int s = 0; s < SLOTS; ++s) {
           if (w[s].left == 0) continue;
-          const Item it = w[s].items[w[s].item];
-          const int off = a ? s * ROWS : 0, n = units[s], buf = n & 1;
+          const Item& it = w[s].it;
+          const int off = a ? s * ROWS : 0, n = units[s], u = n % UNITS, buf = n & 1;
           const int rows = min(ROWS, it.rows - off);
           // the run before last is done with this half; a run of both halves waits for, and is
           // waited for by, its neighbours
@@ -769,23 +805,25 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
             room = room && mbar_try_wait(q_done + 8 * (2 * s + (buf ^ 1)), ((n - 1) >> 1) & 1);
           if (!__all_sync(0xffffffffu, room)) continue;
           moved = true;
-          Unit u;
-          u.rows = rows;
-          u.row0 = u.rows <= ROWS / 2 ? buf * (ROWS / 2) : 0;
-          u.run = run_of(w[s], it);
-          u.tokens = it.tokens - w[s].block * BS;
-          u.part = a ? ((long long)cta + (long long)w[s].item * p.H_kv + w[s].head) * (2 * ROWS) + off
-                     : p.rows_a + (long long)(s * p.ctas + cta) * p.row_max + it.row_base +
-                           (long long)w[s].head * it.rows;
-          load_queries(p, it, w[s].head, off, u.rows, sQ + s * TILE, u.row0, lane);
+          const int run = run_of(w[s]);
+          // the slots' halves differ, so that both keep other schedulers busy
+          const int row0 = rows <= ROWS / 2 ? ((n + s) & 1) * (ROWS / 2) : 0;
+          load_queries(p, it, w[s].head, off, rows, sQ + s * TILE, row0, lane);
           if (lane == 0) {
-            ms.unit[s][n % UNITS] = u;
-            mbar_arrive(q_full + 8 * (UNITS * s + n % UNITS));
+            Unit& unit = ms.unit[s][u];
+            unit.rows = rows;
+            unit.row0 = row0;
+            unit.run = run;
+            unit.tokens = it.tokens - w[s].block * BS;
+            unit.part = a ? ((long long)cta + (long long)w[s].item * p.H_kv + w[s].head) * (2 * ROWS) + off
+                          : p.rows_a + (long long)(s * p.ctas + cta) * p.row_max + it.row_base +
+                                (long long)w[s].head * it.rows;
+            mbar_arrive(q_full + 8 * (UNITS * s + u));
           }
           __syncwarp();
           ++units[s];
-          rows_before[s] = u.rows;
-          advance(w[s], u.run, p.H_kv);
+          rows_before[s] = rows;
+          advance(w[s], run, p.H_kv);
         }
         const uint64_t t = globaltimer();
         if (moved) t0 = t;
@@ -874,7 +912,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
       // the runs that the other warp issues
       int n = 0, left = 0;
       Walk w = walk_of(p.items_a, p.start_a[cta]);
-      for (; w.left > 0; ++n) advance(w, run_of(w, w.items[w.item]), p.H_kv);
+      for (; w.left > 0; ++n) advance(w, run_of(w), p.H_kv);
       n = uniform(n);
       for (int k = 0; k < nb1 && ok; ++k) {
         const int e = entry_b(1, k, na, nb0);
@@ -896,13 +934,21 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
     const float2 scale2 = make_float2(p.scale_log2, p.scale_log2);
     bool ok = true;
     for (int k = 0, n = 0; k < steps && ok; ++n) {
-      ok = mbar_wait(q_full + 8 * (UNITS * s + n % UNITS), (n / UNITS) & 1, p.status);
+      ok = mbar_wait_warp(q_full + 8 * (UNITS * s + n % UNITS), (n / UNITS) & 1, p.status);
       if (!ok) break;
       const Unit unit = ms.unit[s][n % UNITS];
-      const bool active = quarter * 32 < unit.row0 + unit.rows && quarter * 32 + 32 > unit.row0;
-      bool fresh = true;
-      int tokens = unit.tokens;
+      const int q0 = unit.row0 / 32, warps = (unit.row0 + unit.rows + 31) / 32 - q0;
       const int end = k + unit.run;
+      if (quarter < q0 || quarter >= q0 + warps) {
+        // no rows here; the warp keeps in step by arriving for each block
+        for (; k < end && ok; ++k) {
+          ok = mbar_wait_warp(s_full + 8 * s, k & 1, p.status);
+          if (ok && lane == 0) mbar_arrive(p_full + 8 * s);
+        }
+        continue;
+      }
+      const bool mine = r >= unit.row0 && r < unit.row0 + unit.rows;
+      int tokens = unit.tokens;
       float acc[D], m = -INFINITY, l = 0.0f;
 #pragma unroll
       for (int i = 0; i < D; ++i) acc[i] = 0.0f;
@@ -910,54 +956,52 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
         int valid = min(BS, tokens);
         const int e = k < na ? 2 * k : entry_b(s, k - na, na, other);
         const volatile int* bad = &ms.bad[(e >> 1) % STEPS_AHEAD];
-        ok = mbar_wait(s_full + 8 * s, k & 1, p.status);
+        const uint32_t ts = tb + (k & 1) * 128, tp = tb + (~k & 1) * 128;
+        ok = mbar_wait_warp(s_full + 8 * s, k & 1, p.status);
         if (!ok) break;
         tc_fence_after();
         if (valid < BS) {
           // V behind the last token may be anything, and 0 * NaN is NaN: zeros there
           const int ev = (e + 1) % ENTRIES;
-          ok = mbar_wait(full + 8 * ev, entry_parity(e + 1), p.status);
+          ok = mbar_wait_warp(full + 8 * ev, entry_parity(e + 1), p.status);
           if (!ok) break;
           uint8_t* v = smem + SLOTS * TILE + ev * TILE;
-          for (int idx = valid * 8 + r; idx < BS * 8; idx += ROWS) {
+          for (int idx = valid * 8 + (quarter - q0) * 32 + lane; idx < BS * 8; idx += warps * 32) {
             *reinterpret_cast<uint4*>(v + idx * 16) = make_uint4(0, 0, 0, 0);
             *reinterpret_cast<uint4*>(v + BOX + idx * 16) = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
         }
-        float alpha = 1.0f;
-        const uint32_t ts = tb + (k & 1) * 128, tp = tb + (~k & 1) * 128;
-        if (active) {
-          if (*bad) valid = 0;
-          float sum = 0.0f;
-          bool search = fresh;
-          fresh = false;
-          while (true) {
-            if (search) {
-              const float top =
-                  (valid < BS ? row_max<true>(ts, valid) : row_max<false>(ts, valid)) * p.scale_log2;
-              if (top > m) {
-                alpha = ex2_fast(m - top);  // 0 where there was nothing yet
-                m = top;
-              }
+        if (*bad) valid = 0;
+        float sum = 0.0f, alpha = 1.0f;
+        // (a row takes a new maximum for its own need only: its numbers do not depend on others')
+        bool need = m == -INFINITY && mine;
+        for (int round = 0;; ++round) {
+          if (__any_sync(0xffffffffu, need)) {
+            const float top =
+                (valid < BS ? row_max<true>(ts, valid) : row_max<false>(ts, valid)) * p.scale_log2;
+            if (need && top > m) {
+              alpha = ex2_fast(m - top);  // 0 where there was nothing yet
+              m = top;
             }
-            const float shift = P_SHIFT - (m == -INFINITY ? 0.0f : m);
-            sum = valid < BS ? row_exp<true>(ts, tp, valid, scale2, shift)
-                             : row_exp<false>(ts, tp, valid, scale2, shift);
-            // with its own maximum a block's sum is at most 128 * 2^8 = 2^15
-            if (search || !__any_sync(0xffffffffu, sum > SUM_MAX)) break;
-            search = true;
+          } else if (round > 0) {
+            break;
           }
-          l = fmaf(l, alpha, sum);
-          tmem_wait_st();
+          const float shift = P_SHIFT - (m == -INFINITY ? 0.0f : m);
+          sum = valid < BS ? row_exp<true>(ts, tp, valid, scale2, shift)
+                           : row_exp<false>(ts, tp, valid, scale2, shift);
+          if (round > 0) break;
+          need = !need && sum > SUM_MAX;  // with its own maximum at most 128 * 2^8 = 2^15
         }
+        l = fmaf(l, alpha, sum);
+        tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full + 8 * s);
-        ok = mbar_wait(o_full + 8 * s, k & 1, p.status) && ok;
+        ok = mbar_wait_warp(o_full + 8 * s, k & 1, p.status);
         if (!ok) break;
         tc_fence_after();
-        if (active) {
+        {
           const float2 alpha2 = make_float2(alpha, alpha);
           float v[2][16];
           tmem_ld16_async(ts, v[0]);
@@ -980,7 +1024,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
       }
       // this run's part of the rows: [32 groups of 4 channels][rows][4]
       const int rows = unit.rows, i = r - unit.row0;
-      if (i >= 0 && i < rows && ok) {
+      if (mine && ok) {
         const long long part = unit.part;
         float4* o = reinterpret_cast<float4*>(p.parts + part * D) + i;
 #pragma unroll
@@ -1016,64 +1060,44 @@ __global__ void __launch_bounds__(COMBINE_WARPS * 32) combine_kernel(const __gri
   const int b = row / p.G, g = row % p.G;
   const Head head = *p.head;
   const RowPlan rp = p.rows[row];
-  const Item own = p.items_b[p.suffix[b]];
-  // parts: of the prefix, then of the sequence's own blocks; the i-th one's rows start at
-  // at + i * stride, it has `rows` of them and this row is number r
-  long long at[2] = {0, 0};
-  int stride[2] = {0, 0}, rows[2] = {0, 0}, r[2] = {0, 0}, n[2] = {0, 0};
-  const Shares shares_b(p.ctas * SLOTS, head.steps_b);
-  if (rp.kind == 1) {
-    const Item it = p.items_a[rp.item];
-    const int x = it.cum + h * it.blocks;
-    const Shares shares_a(p.ctas, head.steps_a);
-    const int c0 = shares_a.worker_of(x);
-    const int off = rp.row / ROWS * ROWS;
-    n[0] = shares_a.worker_of(x + it.blocks - 1) - c0 + 1;
-    at[0] = ((long long)c0 + (long long)rp.item * p.H_kv + h) * (2 * ROWS) + off;
-    stride[0] = 2 * ROWS;
-    rows[0] = min(ROWS, it.rows - off);
-    r[0] = rp.row - off;
-  } else if (rp.kind == 2) {
-    const Item it = p.items_b[rp.item];
-    const int x = it.cum + h * it.blocks;
-    const int c0 = shares_b.worker_of(x);
-    n[0] = shares_b.worker_of(x + it.blocks - 1) - c0 + 1;
-    at[0] = p.rows_a + (long long)c0 * p.row_max + it.row_base + (long long)h * it.rows;
-    stride[0] = p.row_max;
-    rows[0] = it.rows;
-    r[0] = rp.row;
-  }
-  if (own.blocks > 0) {
-    const int x = own.cum + h * own.blocks;
-    const int c0 = shares_b.worker_of(x);
-    n[1] = shares_b.worker_of(x + own.blocks - 1) - c0 + 1;
-    at[1] = p.rows_a + (long long)c0 * p.row_max + own.row_base + (long long)h * own.rows;
-    stride[1] = p.row_max;
-    rows[1] = own.rows;
-    r[1] = g;
-  }
-  float M = -INFINITY;
-#pragma unroll
-  for (int k = 0; k < 2; ++k)
-    for (int i = 0; i < n[k]; ++i)
-      M = fmaxf(M, p.stats[at[k] + (long long)i * stride[k] + r[k]].x);
-  const float base = M == -INFINITY ? 0.0f : M;
-  float L = 0.0f;
+  const Place own = p.own[b];
+  float M = -INFINITY, L = 0.0f;
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-  for (int k = 0; k < 2; ++k)
+  // the prefix, then the sequence's own blocks: the parts of each worker that has steps of it
+#pragma unroll 1
+  for (int turn = rp.kind > 0 ? 0 : 1; turn < 2; ++turn) {
+    const bool a = turn == 0 && rp.kind == 1;
+    const Place at = turn == 0 ? rp.at : own;
+    if (at.blocks == 0) continue;
+    const int rows = turn == 0 ? rp.rows : p.G, r = turn == 0 ? rp.row : g;
+    const int stride = a ? 2 * ROWS : p.row_max;
+    const long long base = a ? (long long)(at.base + h) * (2 * ROWS) + rp.off
+                             : p.rows_a + at.base + (long long)h * rows;
+    const int* firsts = a ? p.first_a : p.first_b;
+    const Shares shares(a ? p.ctas : p.ctas * SLOTS, a ? head.steps_a : head.steps_b,
+                        a ? head.cost_a : head.cost_b);
+    const int begin = at.cum + h * at.blocks, x = at.cost + h * (at.blocks + 1);
+    const int w0 = shares.worker_of(x), w1 = shares.worker_of(x + at.blocks);
 #pragma unroll 4
-    for (int i = 0; i < n[k]; ++i) {
-      const long long first = at[k] + (long long)i * stride[k];
-      const float2 st = p.stats[first + r[k]];
-      const float4 o = reinterpret_cast<const float4*>(p.parts + first * D)[(size_t)col * rows[k] + r[k]];
-      const float w = ex2_fast(st.x - base);
-      L = fmaf(st.y, w, L);
-      acc.x = fmaf(o.x, w, acc.x);
-      acc.y = fmaf(o.y, w, acc.y);
-      acc.z = fmaf(o.z, w, acc.z);
-      acc.w = fmaf(o.w, w, acc.w);
+    for (int w = w0; w <= w1; ++w) {
+      const bool has = max(firsts[w], begin) < min(firsts[w + 1], begin + at.blocks);
+      const long long first = base + (long long)w * stride;
+      float2 st = p.stats[first + r];
+      float4 o = reinterpret_cast<const float4*>(p.parts + first * D)[(size_t)col * rows + r];
+      if (!has) {
+        st = make_float2(-INFINITY, 0.0f);
+        o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      }
+      const float m = fmaxf(M, st.x), ref = m == -INFINITY ? 0.0f : m;
+      const float a0 = ex2_fast(M - ref), c = ex2_fast(st.x - ref);
+      M = m;
+      L = fmaf(L, a0, st.y * c);
+      acc.x = fmaf(acc.x, a0, o.x * c);
+      acc.y = fmaf(acc.y, a0, o.y * c);
+      acc.z = fmaf(acc.z, a0, o.z * c);
+      acc.w = fmaf(acc.w, a0, o.w * c);
     }
+  }
   const float inv = L == 0.0f ? 0.0f : 1.0f / L;
   float* out = p.out + ((size_t)b * p.H_kv * p.G + h * p.G + g) * D;
   reinterpret_cast<float4*>(out)[col] =
@@ -1096,12 +1120,16 @@ PrefixWs prefix_layout(int B, int H_kv, int G) {
   off = align256(off + PREFIX_MAX_CTAS * sizeof(Start));
   L.start_b = off;
   off = align256(off + PREFIX_MAX_CTAS * SLOTS * sizeof(Start));
+  L.first_a = off;
+  off = align256(off + (PREFIX_MAX_CTAS + 1) * 4);
+  L.first_b = off;
+  off = align256(off + (PREFIX_MAX_CTAS * SLOTS + 1) * 4);
   L.q_rows = off;
   off = align256(off + (size_t)B * G * 4);
   L.rows = off;
   off = align256(off + (size_t)B * G * sizeof(RowPlan));
-  L.suffix = off;
-  off = align256(off + (size_t)B * 4);
+  L.own = off;
+  off = align256(off + (size_t)B * sizeof(Place));
   // A items: 256 rows for each (CTA, item and head) that meet; there are fewer than CTAs +
   // items of those.  B items: row_max rows a slot and the rows of all items.
   L.rows_a = B * G > ROWS ? (long long)(PREFIX_MAX_CTAS + max_pairs * H_kv) * 2 * ROWS : 0;
@@ -1156,7 +1184,9 @@ cudaError_t launch_prefix(const PrefixLaunch& a, cudaStream_t stream) {
   p.start_b = reinterpret_cast<Start*>(ws + L.start_b);
   p.q_rows = reinterpret_cast<int*>(ws + L.q_rows);
   p.rows = reinterpret_cast<RowPlan*>(ws + L.rows);
-  p.suffix = reinterpret_cast<int*>(ws + L.suffix);
+  p.own = reinterpret_cast<Place*>(ws + L.own);
+  p.first_a = reinterpret_cast<int*>(ws + L.first_a);
+  p.first_b = reinterpret_cast<int*>(ws + L.first_b);
   p.parts = reinterpret_cast<float*>(ws + L.parts);
   p.stats = reinterpret_cast<float2*>(ws + L.stats);
   p.rows_a = L.rows_a;
