@@ -36,33 +36,23 @@ struct Item {      // blocks of one K/V head that a set of rows attends, for eve
   int member;      // first row's place in the list of members times G, -1: seq's own rows
   int tokens;      // tokens of seq from block `start` on
   int row_base;    // B items: first row of the item's parts (head 0)
-  int pad;
+  int cum;         // steps of the items before
 };
 
-struct Start {     // where a CTA (A) or a slot (B; slot s of CTA c is worker s * CTAs + c) begins
-  int item, head, block, steps;
-  Item first;      // that item
+struct SeqPlan {   // where the parts of a sequence's rows are
+  int item, r0, rows, pairs;  // B item of its own blocks; its first row among its group's rows
+                              // (-1: nothing shared), those, and the group's first A item
+  int single, pad[3];         // the group's B item
 };
 
-struct Place {     // where the blocks of an item are among all steps (head 0), and its parts
-  int cum, cost, blocks, base;
-};
-
-struct RowPlan {   // the prefix of a row
-  Place at;        // base: A items: item * heads, B items: row_base
-  int kind;        // 0 none, 1 A item, 2 B item
-  int rows;        // of its tile
-  int row, off;    // its place in the tile, and the tile's in the item
-};
-
-struct Head {
-  int steps_a, cost_a, steps_b, cost_b;
+struct Head {      // A and B items: their steps, and the cost that is shared out
+  int items_a, steps_a, cost_a;
+  int items_b, steps_b, cost_b;
 };
 
 // Offsets in the workspace's part.
 struct PrefixWs {
-  size_t head, items_a, items_b, start_a, start_b, first_a, first_b, q_rows, rows, own, parts,
-      stats, total;
+  size_t head, items_a, items_b, cost_a, cost_b, first_a, first_b, q_rows, seqs, parts, stats, total;
   long long rows_a;  // parts of A items come first
 };
 
@@ -78,13 +68,12 @@ struct Params {
   Head* head;
   Item* items_a;
   Item* items_b;
-  Start* start_a;
-  Start* start_b;
-  int* q_rows;     // of members' rows: row of q (head 0)
-  RowPlan* rows;   // [B][G]
-  Place* own;      // [B]: a sequence's own blocks
+  int* cost_a;     // cost of the items before
+  int* cost_b;
   int* first_a;    // [CTAs + 1] first step of each CTA ...
   int* first_b;    // ... and of each slot
+  int* q_rows;     // of members' rows: row of q (head 0)
+  SeqPlan* seqs;   // [B]
   float* parts;    // of n rows: [32][n][4], the groups of four channels of all rows
   float2* stats;   // [rows]: m, l
   long long rows_a;
@@ -99,27 +88,25 @@ __device__ __forceinline__ float ex2_fast(float x) {
 }
 
 // ---- plan --------------------------------------------------------------------------------
-// Equal shares of the cost of all steps, one a block and one a run (its queries, its part):
-// a run of one block takes about twice the time of a block in the middle of a long one.
+// The kernel runs its code once, and fetching it is what takes the time: few instructions, loops
+// that are not unrolled.
 struct PlanShared {
   int cu[MAX_SEGS + 1];
   int prefix[MAX_SEGS];
+  int count[MAX_SEGS];          // members of group g
   int len[MAX_SEGS];
-  int member[MAX_SEGS + 1];     // members before sequence b (each in its group)
-  int start[MAX_SEGS];          // prefix blocks that b holds, -1: no member
-  int group[MAX_SEGS];          // of sequence b
-  int pairs[MAX_SEGS];          // of group g: first A item (-1: nothing shared) ...
-  int single[MAX_SEGS];         // ... and its B item
-  int2 items_a[MAX_SEGS + 1];   // steps and cost of the items before
-  int2 items_b[2 * MAX_SEGS + 1];
-  int4 warp_sum[PLAN_THREADS / 32];
+  int start[MAX_SEGS];          // prefix blocks that sequence b holds (0: no member)
+  int group[MAX_SEGS];
+  int4 seq_at[MAX_SEGS];        // exclusive sums over sequences: members, blocks, runs of their own
+  int4 group_at[MAX_SEGS];      // over groups: A and B items (16 bits each), steps of both, rows of B
+  int4 warp_sum[2][PLAN_THREADS / 32];
   int bad;
 };
 
 __device__ __forceinline__ int4 add4(int4 a, int4 b) {
   return make_int4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
 }
-// Inclusive prefixes of four numbers over a warp.
+// Inclusive sums over a warp.
 __device__ __noinline__ int4 warp_scan4(int4 v) {
   const int lane = threadIdx.x & 31;
 #pragma unroll 1
@@ -130,39 +117,178 @@ __device__ __noinline__ int4 warp_scan4(int4 v) {
   }
   return v;
 }
-// Exclusive prefixes of four numbers over the CTA's threads, from `base`, to which the totals
-// are added.  (Out of line like everything here that is used more than once: the kernel runs its
-// code once, and fetching it is what takes the time.)
-__device__ __noinline__ int4 plan_scan(int4 x, int4& base, PlanShared& sh) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  const int4 incl = warp_scan4(x);
-  __syncthreads();
-  if (lane == 31) sh.warp_sum[warp] = incl;
-  __syncthreads();
-  if (warp == 0) {
-    const int4 s = warp_scan4(lane < warps ? sh.warp_sum[lane] : make_int4(0, 0, 0, 0));
-    sh.warp_sum[lane] = s;
+
+// A group's rows in tiles of 128, two at a time (A items), a last single one a B item.
+struct Tiles {
+  int rows, pairs, single;
+  __device__ __forceinline__ Tiles(int members, int G)
+      : rows(members >= 2 ? members * G : 0),
+        pairs((rows + ROWS - 1) / ROWS / 2),
+        single((rows + ROWS - 1) / ROWS & 1) {}
+};
+
+// Launched with as many threads as there are sequences or groups, at most PLAN_THREADS.
+__global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constant__ Params p) {
+  extern __shared__ __align__(16) uint8_t plan_smem[];
+  PlanShared& sh = *reinterpret_cast<PlanShared*>(plan_smem);
+  const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) sh.bad = 0;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int most = max(p.B, p.groups + 1);
+#pragma unroll 1
+  for (int i = tid; i < most; i += threads) {
+    if (i <= p.groups) sh.cu[i] = p.cu[i];
+    if (i < p.groups) {
+      sh.prefix[i] = p.prefix[i];
+      sh.count[i] = 0;
+    }
+    if (i < p.B) sh.len[i] = p.seq_lens[i];
   }
   __syncthreads();
-  int4 excl = add4(base, incl);
-  if (warp > 0) excl = add4(excl, sh.warp_sum[warp - 1]);
-  base = add4(base, sh.warp_sum[warps - 1]);
-  return make_int4(excl.x - x.x, excl.y - x.y, excl.z - x.z, excl.w - x.w);
-}
-
-// The last index i of [0, n) with cum[i * stride] <= x.
-__device__ __noinline__ int last_at(const int* cum, int stride, int n, int x) {
-  int lo = 0, hi = n;
-  while (lo + 1 < hi) {
-    const int mid = (lo + hi) / 2;
-    if (cum[mid * stride] <= x) lo = mid;
-    else hi = mid;
+  const int limit = p.max_blocks * BS;
+#pragma unroll 1
+  for (int i = tid; i < most; i += threads) {
+    if (i <= p.groups) {
+      const int c = sh.cu[i];
+      if (c < 0 || c > p.B || (i > 0 && c < sh.cu[i - 1])) sh.bad = 1;  // nothing is shared then
+    }
+    if (i < p.groups && (sh.prefix[i] < 0 || sh.prefix[i] > p.max_blocks)) {
+      set_status(p.status, KT_ERR_DEVICE_CHECK);
+      sh.prefix[i] = 0;
+    }
+    if (i < p.B && (sh.len[i] < 0 || sh.len[i] > limit)) {
+      set_status(p.status, KT_ERR_DEVICE_CHECK);
+      sh.len[i] = sh.len[i] < 0 ? 0 : limit;
+    }
   }
-  return lo;
+  __syncthreads();
+  if (sh.bad && tid == 0) set_status(p.status, KT_ERR_DEVICE_CHECK);
+  // members: sequences that hold all blocks of their group's prefix
+#pragma unroll 1
+  for (int b = tid; b < p.B; b += threads) {
+    int lo = 0, hi = p.groups + 1;  // the last group that begins at or before b
+    while (lo + 1 < hi) {
+      const int mid = (lo + hi) / 2;
+      if (sh.cu[mid] <= b) lo = mid;
+      else hi = mid;
+    }
+    int start = 0;
+    if (!sh.bad && lo < p.groups && sh.cu[lo] <= b) start = sh.prefix[lo];
+    if (sh.len[b] < start * BS) start = 0;
+    if (start > 0) atomicAdd(&sh.count[lo], 1);
+    sh.start[b] = start;
+    sh.group[b] = lo;
+  }
+  __syncthreads();
+  // sums over sequences and over groups
+  int4 seqs = make_int4(0, 0, 0, 0), groups = seqs;
+#pragma unroll 1
+  for (int i0 = 0; i0 < most; i0 += threads) {
+    const int i = i0 + tid;
+    int4 x[2] = {make_int4(0, 0, 0, 0), make_int4(0, 0, 0, 0)};
+    if (i < p.B) {
+      int start = sh.start[i];
+      if (start > 0 && sh.count[sh.group[i]] < 2) sh.start[i] = start = 0;
+      const int own = (sh.len[i] + BS - 1) / BS - start;
+      x[0] = make_int4(start > 0, own, own > 0, 0);
+    }
+    if (i < p.groups) {
+      const Tiles t(sh.count[i], p.G);
+      const int blocks = sh.prefix[i];
+      x[1] = make_int4(t.pairs << 16 | t.single, t.pairs * blocks, t.single * blocks,
+                       t.single ? t.rows - t.pairs * 2 * ROWS : 0);
+    }
+    int4 incl[2];
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k) {
+      incl[k] = warp_scan4(x[k]);
+      if (lane == 31) sh.warp_sum[k][warp] = incl[k];
+    }
+    __syncthreads();
+    if (warp < 2) {
+      const int4 v = lane < threads / 32 ? sh.warp_sum[warp][lane] : make_int4(0, 0, 0, 0);
+      sh.warp_sum[warp][lane] = warp_scan4(v);
+    }
+    __syncthreads();
+    if (warp > 0) {
+      incl[0] = add4(incl[0], sh.warp_sum[0][warp - 1]);
+      incl[1] = add4(incl[1], sh.warp_sum[1][warp - 1]);
+    }
+    const int4 s = add4(seqs, incl[0]), g = add4(groups, incl[1]);
+    if (i < p.B) sh.seq_at[i] = make_int4(s.x - x[0].x, s.y - x[0].y, s.z - x[0].z, 0);
+    if (i < p.groups)
+      sh.group_at[i] = make_int4(g.x - x[1].x, g.y - x[1].y, g.z - x[1].z, g.w - x[1].w);
+    seqs = add4(seqs, sh.warp_sum[0][threads / 32 - 1]);
+    groups = add4(groups, sh.warp_sum[1][threads / 32 - 1]);
+    __syncthreads();
+  }
+  const int pairs = groups.x >> 16, singles = groups.x & 0xffff;
+  if (tid == 0)
+    *p.head = Head{pairs,         groups.y * p.H_kv,           (groups.y + pairs) * p.H_kv,
+                   singles + p.B, (groups.z + seqs.y) * p.H_kv, (groups.z + singles + seqs.y + seqs.z) * p.H_kv};
+  // items and rows; an item's cost is its blocks and one for its run
+#pragma unroll 1
+  for (int i = tid; i < most; i += threads) {
+    Item it;
+    if (i < p.B) {
+      const int4 at = sh.seq_at[i];
+      const int start = sh.start[i], n = sh.len[i], g = sh.group[i];
+      const int cum = groups.z + at.y;
+      it.seq = i;
+      it.start = start;
+      it.blocks = (n + BS - 1) / BS - start;
+      it.rows = p.G;
+      it.member = -1;
+      it.tokens = n - start * BS;
+      it.row_base = (groups.w + i * p.G) * p.H_kv;
+      it.cum = cum * p.H_kv;
+      p.items_b[singles + i] = it;
+      p.cost_b[singles + i] = (cum + singles + at.z) * p.H_kv;
+      SeqPlan sp;
+      sp.item = singles + i;
+      sp.r0 = -1;
+      sp.rows = sp.pairs = sp.single = 0;
+      if (start > 0) {
+        const int c0 = sh.seq_at[sh.cu[g]].x;  // members before the group
+        sp.r0 = (at.x - c0) * p.G;
+        sp.rows = sh.count[g] * p.G;
+        sp.pairs = sh.group_at[g].x >> 16;
+        sp.single = sh.group_at[g].x & 0xffff;
+#pragma unroll 1
+        for (int j = 0; j < p.G; ++j) p.q_rows[at.x * p.G + j] = i * p.H_kv * p.G + j;
+        if (sp.r0 == 0) sh.group[sh.cu[g]] = i;  // its first member, for its items
+      }
+      p.seqs[i] = sp;
+    }
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int i = tid; i < p.groups; i += threads) {
+    const Tiles t(sh.count[i], p.G);
+    const int4 at = sh.group_at[i];
+    Item it;
+    if (t.rows > 0) it.seq = sh.group[sh.cu[i]];
+    it.start = 0;
+    it.blocks = sh.prefix[i];
+    it.tokens = it.blocks * BS;
+    it.row_base = at.w * p.H_kv;
+#pragma unroll 1
+    for (int j = 0; j < t.pairs + t.single; ++j) {
+      const bool a = j < t.pairs;
+      const int n = a ? (at.x >> 16) + j : at.x & 0xffff, cum = a ? at.y + j * it.blocks : at.z;
+      it.rows = min(a ? 2 * ROWS : ROWS, t.rows - j * 2 * ROWS);
+      it.member = sh.seq_at[sh.cu[i]].x * p.G + j * 2 * ROWS;
+      it.cum = cum * p.H_kv;
+      (a ? p.items_a : p.items_b)[n] = it;
+      (a ? p.cost_a : p.cost_b)[n] = (cum + n) * p.H_kv;
+    }
+  }
 }
 
-// Shares of a cost among up to n workers, but no more than there are steps: the first ones have
-// one more than the others.
+// Equal shares of the cost of all steps, one a block and one a run (its queries, its part: a run
+// of one block takes about twice the time of a block in the middle of a long one), among up to n
+// workers, but no more than there are steps: the first ones have one more than the others.
 struct Shares {
   int n, each, more;
   __device__ __forceinline__ Shares(int workers, int steps, int cost) : n(min(workers, steps)) {
@@ -176,192 +302,38 @@ struct Shares {
   }
 };
 
-// Launched with as many threads as there are sequences, groups or slots, at most PLAN_THREADS.
-__global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constant__ Params p) {
-  extern __shared__ __align__(16) uint8_t plan_smem[];
-  PlanShared& sh = *reinterpret_cast<PlanShared*>(plan_smem);
-  const int tid = threadIdx.x, threads = blockDim.x;
-  if (tid == 0) sh.bad = 0;
-  griddep_wait();
-  griddep_launch_dependents();
-  for (int g = tid; g <= p.groups; g += threads) {
-    sh.cu[g] = p.cu[g];
-    if (g < p.groups) sh.prefix[g] = p.prefix[g];
-  }
-  for (int b = tid; b < p.B; b += threads) {
-    int n = p.seq_lens[b];
-    if (n < 0 || n > p.max_blocks * BS) {
-      set_status(p.status, KT_ERR_DEVICE_CHECK);
-      n = n < 0 ? 0 : p.max_blocks * BS;
-    }
-    sh.len[b] = n;
-  }
-  __syncthreads();
-  for (int g = tid; g <= p.groups; g += threads) {
-    const int c = sh.cu[g];
-    if (c < 0 || c > p.B || (g > 0 && c < sh.cu[g - 1])) sh.bad = 1;
-  }
-  __syncthreads();
-  const bool grouped = !sh.bad;  // else every sequence is attended by itself
-  if (!grouped && tid == 0) set_status(p.status, KT_ERR_DEVICE_CHECK);
+struct Start {     // where a CTA (A) or a slot (B; slot s of CTA c is worker s * CTAs + c) begins
+  Item first;      // its first item, that one's number, a head and a block of it
+  int item, head, block;
+  int step;        // its number among all steps
+};
 
-  // members: sequences that hold all blocks of their group's prefix
-  int4 members = make_int4(0, 0, 0, 0);
-  for (int b0 = 0; b0 < p.B; b0 += threads) {
-    const int b = b0 + tid;
-    int start = -1, g = p.groups;
-    if (b < p.B && grouped) {
-      g = last_at(sh.cu, 1, p.groups + 1, b);
-      if (g < p.groups && sh.cu[g] <= b) {
-        const int blocks = sh.prefix[g];
-        if (blocks < 0 || blocks > p.max_blocks) set_status(p.status, KT_ERR_DEVICE_CHECK);
-        else if (blocks > 0 && sh.len[b] >= blocks * BS) start = blocks;
-      }
-    }
-    const int r = plan_scan(make_int4(start >= 0, 0, 0, 0), members, sh).x;
-    if (b < p.B) {
-      sh.start[b] = start;
-      sh.group[b] = g;
-      sh.member[b] = r;
-      if (start >= 0)
-        for (int i = 0; i < p.G; ++i) p.q_rows[r * p.G + i] = b * p.H_kv * p.G + i;
-    }
-  }
-  if (tid == 0) sh.member[p.B] = members.x;
-  __syncthreads();
-
-  // groups: rows in tiles of 128, two at a time (A items), a last single one a B item
-  int4 sums = make_int4(0, 0, 0, 0);  // A and B items (16 bits each), steps of both, rows of B
-  for (int g0 = 0; g0 < (grouped ? p.groups : 0); g0 += threads) {
-    const int g = g0 + tid;
-    int rows = 0, first = 0, blocks = 0, seq = 0;
-    if (g < p.groups) {
-      const int c0 = sh.cu[g], c1 = sh.cu[g + 1];
-      first = sh.member[c0];
-      const int n = sh.member[c1] - first;
-      if (n >= 2) {
-        rows = n * p.G;
-        for (seq = c0; sh.start[seq] < 0;) ++seq;  // its first member
-        blocks = sh.start[seq];
-      }
-    }
-    const int tiles = (rows + ROWS - 1) / ROWS, np = tiles / 2, ns = tiles & 1;
-    const int left = ns ? rows - np * 2 * ROWS : 0;
-    const int4 at = plan_scan(make_int4(np << 16 | ns, np * blocks, ns * blocks, left), sums, sh);
-    const int ip = at.x >> 16, is = at.x & 0xffff;
-    if (g < p.groups) {
-      sh.pairs[g] = rows > 0 ? ip : -1;
-      sh.single[g] = is;
-    }
-    for (int i = 0; i < np + ns; ++i) {
-      const bool a = i < np;
-      Item it;
-      it.seq = seq;
-      it.start = 0;
-      it.blocks = blocks;
-      it.rows = a ? min(2 * ROWS, rows - i * 2 * ROWS) : left;
-      it.member = first * p.G + i * 2 * ROWS;
-      it.tokens = blocks * BS;
-      it.row_base = a ? 0 : at.w * p.H_kv;
-      it.pad = 0;
-      const int cum = a ? at.y + i * blocks : at.z, n = a ? ip + i : is;
-      (a ? p.items_a : p.items_b)[n] = it;
-      (a ? sh.items_a : sh.items_b)[n] = make_int2(cum * p.H_kv, (cum + n) * p.H_kv);
-    }
-  }
-  __syncthreads();
-  const int pairs = sums.x >> 16, singles = sums.x & 0xffff;
-
-  // what each sequence has of its own, and where the parts of its rows' prefix are
-  int4 own = make_int4(sums.z, singles, 0, 0);
-  for (int b0 = 0; b0 < p.B; b0 += threads) {
-    const int b = b0 + tid;
-    int start = 0, n = 0, nb = 0, first_a = -1;
-    if (b < p.B) {
-      n = sh.len[b];
-      nb = (n + BS - 1) / BS;
-      if (sh.start[b] >= 0) first_a = sh.pairs[sh.group[b]];
-      if (first_a >= 0) start = sh.start[b];
-    }
-    const int4 at = plan_scan(make_int4(nb - start, nb > start, 0, 0), own, sh);
-    if (b < p.B) {
-      Item it;
-      it.seq = b;
-      it.start = start;
-      it.blocks = nb - start;
-      it.rows = p.G;
-      it.member = -1;
-      it.tokens = n - start * BS;
-      it.row_base = (sums.w + b * p.G) * p.H_kv;
-      it.pad = 0;
-      p.items_b[singles + b] = it;
-      sh.items_b[singles + b] = make_int2(at.x * p.H_kv, (at.x + at.y) * p.H_kv);
-      p.own[b] = Place{at.x * p.H_kv, (at.x + at.y) * p.H_kv, it.blocks, it.row_base};
-      int r0 = 0, np = 0, rows = 0, single = 0;
-      if (first_a >= 0) {
-        const int g = sh.group[b], c0 = sh.member[sh.cu[g]];
-        rows = (sh.member[sh.cu[g + 1]] - c0) * p.G;
-        r0 = (sh.member[b] - c0) * p.G;
-        np = (rows + ROWS - 1) / ROWS / 2;
-        single = sh.single[g];
-      }
-      for (int i = 0; i < p.G; ++i) {
-        RowPlan rp;
-        rp.kind = 0;
-        if (first_a >= 0) {
-          const int r = r0 + i, pair = r / (2 * ROWS), tile = r / ROWS * ROWS;
-          const bool a = pair < np;
-          const int2 c = a ? sh.items_a[first_a + pair] : sh.items_b[single];
-          rp.kind = a ? 1 : 2;
-          rp.at.cum = c.x;
-          rp.at.cost = c.y;
-          rp.at.blocks = start;
-          rp.at.base = a ? (first_a + pair) * p.H_kv : p.items_b[single].row_base;
-          rp.rows = min(ROWS, rows - tile);
-          rp.row = r - tile;
-          rp.off = tile - pair * 2 * ROWS;
-        }
-        p.rows[(size_t)b * p.G + i] = rp;
-      }
-    }
-  }
-  __syncthreads();
-  const int steps_a = sums.y * p.H_kv, cost_a = (sums.y + pairs) * p.H_kv;
-  const int steps_b = own.x * p.H_kv, cost_b = (own.x + own.y) * p.H_kv;
-  const int items_b = singles + p.B;
-  if (tid == 0) *p.head = Head{steps_a, cost_a, steps_b, cost_b};
-  for (int c = tid; c < p.ctas * (1 + SLOTS); c += threads) {
-    const bool a = c < p.ctas;
-    const int w = a ? c : c - p.ctas;
-    const int steps = a ? steps_a : steps_b;
-    const Shares shares(a ? p.ctas : p.ctas * SLOTS, steps, a ? cost_a : cost_b);
-    int* firsts = a ? p.first_a : p.first_b;
-    Start st;
-    st.item = st.head = st.block = st.steps = 0;
-    if (w < shares.n) {
-      const int2* at = a ? sh.items_a : sh.items_b;
-      const int n = a ? pairs : items_b;
-      // the places where this share and the next one begin: the first unit of a run's cost is
-      // its own, then its blocks
-      int end = steps;
+// The place of worker w's first step, found by a warp; its share is what lies before w + 1's.
+__device__ __noinline__ Start find_start(const Item* items, const int* cost, int n_items,
+                                         const Shares shares, int steps, int w) {
+  const int lane = threadIdx.x & 31;
+  Start s;
+  s.item = s.head = s.block = 0;
+  s.step = steps;
+  if (w >= shares.n) return s;
+  const int x = shares.first(w);
+  int lo = 0, n = n_items, at = 0;  // the last item with cost <= x: never one without blocks
 #pragma unroll 1
-      for (int next = w + 1 < shares.n; next >= 0; --next) {
-        const int x = shares.first(w + next);
-        const int i = last_at(&at[0].y, 2, n, x);  // never one without blocks
-        const int blocks = ((i + 1 < n ? at[i + 1].x : steps) - at[i].x) / p.H_kv;
-        st.item = i;
-        st.head = (x - at[i].y) / (blocks + 1);
-        st.block = max(0, x - at[i].y - st.head * (blocks + 1) - 1);
-        const int step = at[i].x + st.head * blocks + st.block;
-        if (next) end = step;
-        else firsts[w] = step;
-      }
-      st.steps = end - firsts[w];
-      if (w + 1 == shares.n) firsts[w + 1] = steps;
-      st.first = (a ? p.items_a : p.items_b)[st.item];
-    }
-    (a ? p.start_a : p.start_b)[w] = st;
+  while (n > 1) {
+    const int stride = (n + 31) / 32, i = lane * stride;
+    const int c = i < n ? cost[lo + i] : 0x7fffffff;
+    const int k = __popc(__ballot_sync(0xffffffffu, c <= x)) - 1;
+    lo += k * stride;
+    n = min(stride, n - k * stride);
   }
+  at = cost[lo];
+  s.first = items[lo];
+  s.item = lo;
+  s.head = (x - at) / (s.first.blocks + 1);
+  // the first unit of a run's cost is its own, then its blocks
+  s.block = max(0, x - at - s.head * (s.first.blocks + 1) - 1);
+  s.step = s.first.cum + s.head * s.first.blocks + s.block;
+  return s;
 }
 
 // ---- attend ------------------------------------------------------------------------------
@@ -406,6 +378,7 @@ struct Misc {
   Unit unit[SLOTS][UNITS];
   uint32_t tmem;
   int bad[STEPS_AHEAD];          // the step's page is outside the pool
+  Start start[1 + SLOTS][2];     // of the A share and the slots' B shares, and of the next worker
 };
 constexpr int SMEM = SLOTS * TILE + ENTRIES * TILE + sizeof(Misc);
 static_assert(SMEM <= 232448, "shared memory of a CTA");
@@ -623,8 +596,8 @@ struct Walk {
   Item it;                      // the item at hand
   int item, head, block, left;  // `left` steps of the share
 };
-__device__ __forceinline__ Walk walk_of(const Item* items, const Start& s) {
-  return Walk{items, s.first, s.item, s.head, s.block, s.steps};
+__device__ __forceinline__ Walk walk_of(const Item* items, const Start* s) {
+  return Walk{items, s[0].first, s[0].item, s[0].head, s[0].block, s[1].step - s[0].step};
 }
 __device__ __forceinline__ int run_of(const Walk& w) { return min(w.left, w.it.blocks - w.block); }
 // To the next run, behind one of `run` blocks.
@@ -714,6 +687,22 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
   const uint32_t tmem = ms.tmem;
   griddep_wait();
   griddep_launch_dependents();
+  if (warp < 2 * (1 + SLOTS)) {
+    // this CTA's shares: their beginnings and their ends
+    const Head h = *p.head;
+    const bool a = warp < 2;
+    const int n = a ? p.ctas : p.ctas * SLOTS, steps = a ? h.steps_a : h.steps_b;
+    const int w = (warp < 4 ? cta : p.ctas + cta) + (warp & 1);
+    const Shares shares(n, steps, a ? h.cost_a : h.cost_b);
+    const Start st = find_start(a ? p.items_a : p.items_b, a ? p.cost_a : p.cost_b,
+                                a ? h.items_a : h.items_b, shares, steps, w);
+    if (lane == 0) {
+      ms.start[warp >> 1][warp & 1] = st;
+      (a ? p.first_a : p.first_b)[w] = st.step;  // (two write the same)
+    }
+  }
+  __syncthreads();
+  const int na = ms.start[0][1].step - ms.start[0][0].step;
 
   if (warp >= SOFT_WARPS) {
   regs_dec<CONTROL_REGS>();
@@ -766,11 +755,11 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
       }
     };
     {
-      Turn t = {walk_of(p.items_a, p.start_a[cta]), 0, 0, 0};
+      Turn t = {walk_of(p.items_a, ms.start[0]), 0, 0, 0};
       while (ok && t.w.left > 0) turn(t);
     }
-    Turn t0 = {walk_of(p.items_b, p.start_b[cta]), 0, 0, 0};
-    Turn t1 = {walk_of(p.items_b, p.start_b[p.ctas + cta]), 0, 0, 0};
+    Turn t0 = {walk_of(p.items_b, ms.start[1]), 0, 0, 0};
+    Turn t1 = {walk_of(p.items_b, ms.start[2]), 0, 0, 0};
     while (ok && (t0.w.left > 0 || t1.w.left > 0)) {
       turn(t0);
       if (ok) turn(t1);
@@ -785,8 +774,8 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
     bool ok = true;
     for (int part = 0; part < 2 && ok; ++part) {
       const bool a = part == 0;
-      w[0] = a ? walk_of(p.items_a, p.start_a[cta]) : walk_of(p.items_b, p.start_b[cta]);
-      w[1] = a ? w[0] : walk_of(p.items_b, p.start_b[p.ctas + cta]);
+      w[0] = a ? walk_of(p.items_a, ms.start[0]) : walk_of(p.items_b, ms.start[1]);
+      w[1] = a ? w[0] : walk_of(p.items_b, ms.start[2]);
       // a slot whose next run has no room yet does not hold up the other's: in the ring their
       // steps wait for one another
       uint64_t t0 = globaltimer();
@@ -839,8 +828,9 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
     // then keeps it in uniform registers, where the tensor-core instructions want their operands
     // (moving them there one by one took longer than the steps themselves).
     const bool leader = elect_one();
-    const int na = uniform(p.start_a[cta].steps);
-    const int nb0 = uniform(p.start_b[cta].steps), nb1 = uniform(p.start_b[p.ctas + cta].steps);
+    const int na_u = uniform(na);
+    const int nb0 = uniform(ms.start[1][1].step - ms.start[1][0].step);
+    const int nb1 = uniform(ms.start[2][1].step - ms.start[2][0].step);
     bool ok = true;
     // S = Q K^T of slot s's step k, once K, the run's Q and the end of the last P V are there;
     // n counts the runs begun, left the steps of the one at hand
@@ -891,33 +881,41 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
       }
       __syncwarp();
     };
-    if (warp == SOFT_WARPS) {
-      // A steps: both slots from one warp, P V and the next scores of one in a row, so that
-      // the softmax of each falls into the tensor-core time of the other.  (Two warps that
-      // issue as operands come keep the slots in step, and the tensor cores idle meanwhile.)
-      int n0 = 0, n1 = 0, left0 = 0, left1 = 0;
-      for (int k = 0; k <= na && ok; ++k) {
-        if (k > 0) values(0, k - 1, 2 * k - 1, true);
-        if (k < na) scores(0, k, 2 * k, true, n0, left0);
-        if (k > 0) values(1, k - 1, 2 * k - 1, true);
-        if (k < na) scores(1, k, 2 * k, true, n1, left1);
-      }
-      // B steps: each slot at its own pace
-      for (int k = 0; k < nb0 && ok; ++k) {
-        const int e = entry_b(0, k, na, nb1);
-        scores(0, na + k, e, false, n0, left0);
-        values(0, na + k, e + 1, false);
-      }
-    } else {
-      // the runs that the other warp issues
-      int n = 0, left = 0;
-      Walk w = walk_of(p.items_a, p.start_a[cta]);
+    // A steps: both slots from one warp, P V and the next scores of one in a row, so that the
+    // softmax of each falls into the tensor-core time of the other.  (Two warps that issue as
+    // operands come keep the slots in step, and the tensor cores idle meanwhile.)  Then B steps:
+    // each slot from a warp of its own, at its own pace.
+    int s = warp - SOFT_WARPS, n = 0, left = 0, n_other = 0, left_other = 0;
+    if (s == 1) {  // the runs that the other warp issues
+      Walk w = walk_of(p.items_a, ms.start[0]);
       for (; w.left > 0; ++n) advance(w, run_of(w), p.H_kv);
       n = uniform(n);
-      for (int k = 0; k < nb1 && ok; ++k) {
-        const int e = entry_b(1, k, na, nb0);
-        scores(1, na + k, e, false, n, left);
-        values(1, na + k, e + 1, false);
+    }
+    const int nb = s == 0 ? nb0 : nb1, other = s == 0 ? nb1 : nb0;
+    int k = s == 0 ? 0 : na_u;
+    if (k < na_u) {  // the first scores of both slots
+#pragma unroll 1
+      for (int x = 0; x < 2; ++x) {
+        scores(x, 0, 0, true, n, left);
+        const int t = n, u = left;
+        n = n_other, left = left_other, n_other = t, left_other = u;
+      }
+    }
+#pragma unroll 1
+    while (ok && k < na_u + nb) {
+      const bool a = k < na_u;
+      // an A step: P V of step k and the scores of k + 1, slot by slot; a B step: its scores, P V
+      const int e = a ? 2 * k : entry_b(s, k - na_u, na_u, other);
+      if (!a) scores(s, k, e, false, n, left);
+      values(s, k, e + 1, a);
+      if (a && k + 1 < na_u) scores(s, k + 1, e + 2, true, n, left);
+      if (a) {
+        const int t = n, u = left;
+        n = n_other, left = left_other, n_other = t, left_other = u;
+        s ^= 1;
+        if (s == 0) ++k;
+      } else {
+        ++k;
       }
     }
     __syncwarp();
@@ -928,9 +926,8 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
     const int s = warp >> 2, quarter = warp & 3;
     const int r = quarter * 32 + lane;       // this thread's row of the slot
     const uint32_t tb = tmem + s * 256 + ((uint32_t)(quarter * 32) << 16);
-    const int na = p.start_a[cta].steps;
-    const int steps = na + p.start_b[s * p.ctas + cta].steps;
-    const int other = p.start_b[(1 - s) * p.ctas + cta].steps;
+    const int steps = na + ms.start[1 + s][1].step - ms.start[1 + s][0].step;
+    const int other = ms.start[2 - s][1].step - ms.start[2 - s][0].step;
     const float2 scale2 = make_float2(p.scale_log2, p.scale_log2);
     bool ok = true;
     for (int k = 0, n = 0; k < steps && ok; ++n) {
@@ -1059,28 +1056,38 @@ __global__ void __launch_bounds__(COMBINE_WARPS * 32) combine_kernel(const __gri
   if (h >= p.H_kv || row >= all_rows) return;
   const int b = row / p.G, g = row % p.G;
   const Head head = *p.head;
-  const RowPlan rp = p.rows[row];
-  const Place own = p.own[b];
+  const SeqPlan sp = p.seqs[b];
   float M = -INFINITY, L = 0.0f;
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   // the prefix, then the sequence's own blocks: the parts of each worker that has steps of it
 #pragma unroll 1
-  for (int turn = rp.kind > 0 ? 0 : 1; turn < 2; ++turn) {
-    const bool a = turn == 0 && rp.kind == 1;
-    const Place at = turn == 0 ? rp.at : own;
-    if (at.blocks == 0) continue;
-    const int rows = turn == 0 ? rp.rows : p.G, r = turn == 0 ? rp.row : g;
+  for (int turn = sp.r0 >= 0 ? 0 : 1; turn < 2; ++turn) {
+    int item = sp.item, r = g, off = 0;
+    bool a = false;
+    if (turn == 0) {
+      r = sp.r0 + g;
+      const int pair = r / (2 * ROWS);
+      a = pair < (sp.rows + ROWS - 1) / ROWS / 2;
+      item = a ? sp.pairs + pair : sp.single;
+      r -= pair * 2 * ROWS;
+      off = r / ROWS * ROWS;
+      r -= off;
+    }
+    const Item it = (a ? p.items_a : p.items_b)[item];
+    const int cost = (a ? p.cost_a : p.cost_b)[item];
+    if (it.blocks == 0) continue;
+    const int rows = min(ROWS, it.rows - off);
     const int stride = a ? 2 * ROWS : p.row_max;
-    const long long base = a ? (long long)(at.base + h) * (2 * ROWS) + rp.off
-                             : p.rows_a + at.base + (long long)h * rows;
+    const long long base = a ? (long long)(item * p.H_kv + h) * (2 * ROWS) + off
+                             : p.rows_a + it.row_base + (long long)h * rows;
     const int* firsts = a ? p.first_a : p.first_b;
     const Shares shares(a ? p.ctas : p.ctas * SLOTS, a ? head.steps_a : head.steps_b,
                         a ? head.cost_a : head.cost_b);
-    const int begin = at.cum + h * at.blocks, x = at.cost + h * (at.blocks + 1);
-    const int w0 = shares.worker_of(x), w1 = shares.worker_of(x + at.blocks);
+    const int begin = it.cum + h * it.blocks, x = cost + h * (it.blocks + 1);
+    const int w0 = shares.worker_of(x), w1 = shares.worker_of(x + it.blocks);
 #pragma unroll 4
     for (int w = w0; w <= w1; ++w) {
-      const bool has = max(firsts[w], begin) < min(firsts[w + 1], begin + at.blocks);
+      const bool has = max(firsts[w], begin) < min(firsts[w + 1], begin + it.blocks);
       const long long first = base + (long long)w * stride;
       float2 st = p.stats[first + r];
       float4 o = reinterpret_cast<const float4*>(p.parts + first * D)[(size_t)col * rows + r];
@@ -1116,20 +1123,18 @@ PrefixWs prefix_layout(int B, int H_kv, int G) {
   off = align256(off + max_pairs * sizeof(Item));
   L.items_b = off;
   off = align256(off + 2 * (size_t)B * sizeof(Item));
-  L.start_a = off;
-  off = align256(off + PREFIX_MAX_CTAS * sizeof(Start));
-  L.start_b = off;
-  off = align256(off + PREFIX_MAX_CTAS * SLOTS * sizeof(Start));
+  L.cost_a = off;
+  off = align256(off + max_pairs * 4);
+  L.cost_b = off;
+  off = align256(off + 2 * (size_t)B * 4);
   L.first_a = off;
   off = align256(off + (PREFIX_MAX_CTAS + 1) * 4);
   L.first_b = off;
   off = align256(off + (PREFIX_MAX_CTAS * SLOTS + 1) * 4);
   L.q_rows = off;
   off = align256(off + (size_t)B * G * 4);
-  L.rows = off;
-  off = align256(off + (size_t)B * G * sizeof(RowPlan));
-  L.own = off;
-  off = align256(off + (size_t)B * sizeof(Place));
+  L.seqs = off;
+  off = align256(off + (size_t)B * sizeof(SeqPlan));
   // A items: 256 rows for each (CTA, item and head) that meet; there are fewer than CTAs +
   // items of those.  B items: row_max rows a slot and the rows of all items.
   L.rows_a = B * G > ROWS ? (long long)(PREFIX_MAX_CTAS + max_pairs * H_kv) * 2 * ROWS : 0;
@@ -1180,13 +1185,12 @@ cudaError_t launch_prefix(const PrefixLaunch& a, cudaStream_t stream) {
   p.head = reinterpret_cast<Head*>(ws + L.head);
   p.items_a = reinterpret_cast<Item*>(ws + L.items_a);
   p.items_b = reinterpret_cast<Item*>(ws + L.items_b);
-  p.start_a = reinterpret_cast<Start*>(ws + L.start_a);
-  p.start_b = reinterpret_cast<Start*>(ws + L.start_b);
-  p.q_rows = reinterpret_cast<int*>(ws + L.q_rows);
-  p.rows = reinterpret_cast<RowPlan*>(ws + L.rows);
-  p.own = reinterpret_cast<Place*>(ws + L.own);
+  p.cost_a = reinterpret_cast<int*>(ws + L.cost_a);
+  p.cost_b = reinterpret_cast<int*>(ws + L.cost_b);
   p.first_a = reinterpret_cast<int*>(ws + L.first_a);
   p.first_b = reinterpret_cast<int*>(ws + L.first_b);
+  p.q_rows = reinterpret_cast<int*>(ws + L.q_rows);
+  p.seqs = reinterpret_cast<SeqPlan*>(ws + L.seqs);
   p.parts = reinterpret_cast<float*>(ws + L.parts);
   p.stats = reinterpret_cast<float2*>(ws + L.stats);
   p.rows_a = L.rows_a;
@@ -1211,9 +1215,8 @@ cudaError_t launch_prefix(const PrefixLaunch& a, cudaStream_t stream) {
                                      (int)sizeof(PlanShared));
   });
   if (e != cudaSuccess) return e;
-  int threads = a.B > a.groups ? a.B : a.groups;
-  threads = threads < 3 * p.ctas ? 3 * p.ctas : threads;
-  threads = threads < PLAN_THREADS ? (threads + 31) & ~31 : PLAN_THREADS;
+  int threads = a.B > a.groups + 1 ? a.B : a.groups + 1;
+  threads = threads < 64 ? 64 : threads < PLAN_THREADS ? (threads + 31) & ~31 : PLAN_THREADS;
   e = launch(plan_kernel, p, 1, threads, sizeof(PlanShared), stream);
   if (e != cudaSuccess) return e;
   e = launch(attend_kernel, p, p.ctas, THREADS, SMEM, stream);
