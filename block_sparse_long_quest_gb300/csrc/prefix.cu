@@ -620,28 +620,28 @@ __device__ __forceinline__ int entry_b(int s, int k, int a, int other) {
 __device__ __forceinline__ uint32_t entry_parity(int e) { return (uint32_t)(e / ENTRIES) & 1u; }
 
 // Queries of a run into two swizzled boxes (chunk c of row i: box c / 8, slot (c % 8) ^ (i % 8)).
-// A lane finds where four of the rows are; then 16 lanes copy a row.
+// A lane finds where four of the rows are; then 16 lanes copy a row, two rows at a time.
 __device__ __forceinline__ void load_queries(const Params& p, const Item& it, int head, int off,
                                              int rows, uint32_t q, int row0, int lane) {
-  int at[ROWS / 32];  // row of q, without the K/V head's offset
+  int at[ROWS / 32];  // rows of q
 #pragma unroll
   for (int j = 0; j < ROWS / 32; ++j) {
-    const int i = j * 32 + lane;
-    at[j] = 0;
-    if (i < rows) at[j] = it.member >= 0 ? p.q_rows[it.member + off + i] : it.seq * p.H_kv * p.G + i;
+    const int i = min(j * 32 + lane, rows - 1);
+    at[j] = (it.member >= 0 ? p.q_rows[it.member + off + i] : it.seq * p.H_kv * p.G + i) + head * p.G;
   }
-  const int c = lane & 15;
+  const int c = lane & 15, odd = lane >> 4;
+  const char* src = reinterpret_cast<const char*>(p.q) + c * 16;
+  const uint32_t dst = q + (c >> 3) * BOX + (row0 + odd) * 128;  // row0 is a multiple of 8
 #pragma unroll
   for (int j = 0; j < ROWS / 32; ++j) {
-    if (j * 32 >= rows) break;
-#pragma unroll 4
-    for (int i0 = 0; i0 < 32; i0 += 2) {
-      if (j * 32 + i0 >= rows) break;
-      const int i = j * 32 + i0 + (lane >> 4), r = row0 + i;
-      const int row = __shfl_sync(0xffffffffu, at[j], i0 + (lane >> 4)) + head * p.G;
-      if (i < rows)
-        cp_async_16(q + (c >> 3) * BOX + r * 128 + (((c & 7) ^ (r & 7)) << 4),
-                    p.q + (size_t)row * D + c * 8);
+#pragma unroll 1
+    for (int i0 = 0; i0 < 32 && j * 32 + i0 < rows; i0 += 8) {
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {  // behind the last row that one again
+        const int row = __shfl_sync(0xffffffffu, at[j], i0 + i + odd);
+        cp_async_16(dst + (j * 32 + i0 + i) * 128 + (((c & 7) ^ (i + odd)) << 4),
+                    src + (size_t)row * (D * 2));
+      }
     }
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
@@ -797,7 +797,6 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
           const int run = run_of(w[s]);
           // the slots' halves differ, so that both keep other schedulers busy
           const int row0 = rows <= ROWS / 2 ? ((n + s) & 1) * (ROWS / 2) : 0;
-          load_queries(p, it, w[s].head, off, rows, sQ + s * TILE, row0, lane);
           if (lane == 0) {
             Unit& unit = ms.unit[s][u];
             unit.rows = rows;
@@ -807,8 +806,9 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
             unit.part = a ? ((long long)cta + (long long)w[s].item * p.H_kv + w[s].head) * (2 * ROWS) + off
                           : p.rows_a + (long long)(s * p.ctas + cta) * p.row_max + it.row_base +
                                 (long long)w[s].head * it.rows;
-            mbar_arrive(q_full + 8 * (UNITS * s + u));
           }
+          load_queries(p, it, w[s].head, off, rows, sQ + s * TILE, row0, lane);
+          if (lane == 0) mbar_arrive(q_full + 8 * (UNITS * s + u));
           __syncwarp();
           ++units[s];
           rows_before[s] = rows;
@@ -1060,21 +1060,29 @@ __global__ void __launch_bounds__(COMBINE_WARPS * 32) combine_kernel(const __gri
   float M = -INFINITY, L = 0.0f;
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   // the prefix, then the sequence's own blocks: the parts of each worker that has steps of it
+  int r = sp.r0 + g, off = 0, item = sp.item;
+  bool a = false;
+  if (sp.r0 >= 0) {
+    const int pair = r / (2 * ROWS);
+    a = pair < (sp.rows + ROWS - 1) / ROWS / 2;
+    item = a ? sp.pairs + pair : sp.single;
+    r -= pair * 2 * ROWS;
+    off = r / ROWS * ROWS;
+    r -= off;
+  }
+  Item it = (a ? p.items_a : p.items_b)[item], own = p.items_b[sp.item];
+  int cost = (a ? p.cost_a : p.cost_b)[item];
+  const int own_cost = p.cost_b[sp.item];
 #pragma unroll 1
   for (int turn = sp.r0 >= 0 ? 0 : 1; turn < 2; ++turn) {
-    int item = sp.item, r = g, off = 0;
-    bool a = false;
-    if (turn == 0) {
-      r = sp.r0 + g;
-      const int pair = r / (2 * ROWS);
-      a = pair < (sp.rows + ROWS - 1) / ROWS / 2;
-      item = a ? sp.pairs + pair : sp.single;
-      r -= pair * 2 * ROWS;
-      off = r / ROWS * ROWS;
-      r -= off;
+    if (turn == 1) {
+      it = own;
+      cost = own_cost;
+      item = sp.item;
+      r = g;
+      off = 0;
+      a = false;
     }
-    const Item it = (a ? p.items_a : p.items_b)[item];
-    const int cost = (a ? p.cost_a : p.cost_b)[item];
     if (it.blocks == 0) continue;
     const int rows = min(ROWS, it.rows - off);
     const int stride = a ? 2 * ROWS : p.row_max;
@@ -1085,7 +1093,7 @@ __global__ void __launch_bounds__(COMBINE_WARPS * 32) combine_kernel(const __gri
                         a ? head.cost_a : head.cost_b);
     const int begin = it.cum + h * it.blocks, x = cost + h * (it.blocks + 1);
     const int w0 = shares.worker_of(x), w1 = shares.worker_of(x + it.blocks);
-#pragma unroll 4
+#pragma unroll 8
     for (int w = w0; w <= w1; ++w) {
       const bool has = max(firsts[w], begin) < min(firsts[w + 1], begin + it.blocks);
       const long long first = base + (long long)w * stride;
@@ -1173,9 +1181,9 @@ cudaError_t launch_prefix(const PrefixLaunch& a, cudaStream_t stream) {
   std::memset(&p, 0, sizeof(p));
   const PrefixWs L = prefix_layout(a.B, a.H_kv, a.G);
   uint8_t* ws = static_cast<uint8_t*>(a.ws);
+  p.q = a.q;
   p.kmap = *a.kmap;
   p.vmap = *a.vmap;
-  p.q = a.q;
   p.table = a.table;
   p.seq_lens = a.seq_lens;
   p.cu = a.cu;
