@@ -46,6 +46,7 @@ EXPORTS = (
     "kt_dense_decode_attn_f8", "kt_score_select_blocks_f8", "kt_sparse_decode_step_f8",
     "kt_decode_layer_f8", "kt_page_workspace_bytes", "kt_free_seqs", "kt_fork_seqs",
     "kt_reserve_pages", "kt_compact_pages", "kt_copy_pages", "kt_prefix_decode_attn",
+    "kt_prefix_decode_attn_f8",
 )
 
 
@@ -225,6 +226,8 @@ def _load():
         "kt_compact_pages": (ctypes.c_int, [P(PageMap), vp, vp, vp, vp, vp, sz, vp]),
         "kt_prefix_decode_attn": (ctypes.c_int, [vp, P(PagedKV), P(PrefixGroups), i32,
                                                  ctypes.c_float, vp, vp, sz, vp]),
+        "kt_prefix_decode_attn_f8": (ctypes.c_int, [vp, P(PagedKVF8), P(PrefixGroups), i32,
+                                                    ctypes.c_float, vp, vp, sz, vp]),
         "kt_copy_pages": (ctypes.c_int, [P(PagePool), i32, i32, vp, vp, i32, vp, sz, vp]),
     })
     for name, (res, args) in sig.items():
@@ -663,6 +666,13 @@ def kt_prefix_decode_attn(q, kv, groups, num_q_heads, softmax_scale, out, ws, st
                                      softmax_scale, _ptr(out), _ptr(ws), ws.numel(),
                                      _stream(stream)),
            "kt_prefix_decode_attn")
+
+
+def kt_prefix_decode_attn_f8(q, kv, groups, num_q_heads, softmax_scale, out, ws, stream=None):
+    _check(lib.kt_prefix_decode_attn_f8(_ptr(q), _byref(kv), _byref(groups), num_q_heads,
+                                        softmax_scale, _ptr(out), _ptr(ws), ws.numel(),
+                                        _stream(stream)),
+           "kt_prefix_decode_attn_f8")
 
 
 def page_map(block_table, seq_lens, num_blocks, page_refs) -> PageMap:

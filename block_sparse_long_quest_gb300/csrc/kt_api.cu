@@ -976,7 +976,8 @@ bool prefix_units_ok(const kt_paged_kv& kv) {
 
 kt_status prefix_impl(const void* q, const kt_paged_kv* kv, const kt_prefix_groups* groups,
                       int32_t num_q_heads, float softmax_scale, float* out, void* ws,
-                      size_t ws_bytes, cudaStream_t stream) {
+                      size_t ws_bytes, cudaStream_t stream, const float* k_scale = nullptr,
+                      const float* v_scale = nullptr) {
   const kt_status s = check_heads(kv, num_q_heads, softmax_scale);
   if (s != KT_OK) return s;
   if (!q || !out || !ws || !aligned16(q) || !aligned16(out) || !aligned16(ws))
@@ -990,13 +991,16 @@ kt_status prefix_impl(const void* q, const kt_paged_kv* kv, const kt_prefix_grou
   const size_t need = prefix_ws_bytes(kv->batch, kv->num_kv_heads, G);
   if (ws_bytes < 256 + need) return KT_ERR_WORKSPACE_TOO_SMALL;
   CUtensorMap kmap, vmap;
-  if (!make_pool_map(&kmap, kv->k_pool, kv) || !make_pool_map(&vmap, kv->v_pool, kv))
+  const bool codes = k_scale != nullptr;  // the 8-bit cache, whose code pools kv holds
+  if (!make_pool_map(&kmap, kv->k_pool, kv, codes) || !make_pool_map(&vmap, kv->v_pool, kv, codes))
     return KT_ERR_CUDA;
   PrefixLaunch a;
   std::memset(&a, 0, sizeof(a));
   a.kmap = &kmap;
   a.vmap = &vmap;
   a.q = static_cast<const __half*>(q);
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
   a.table = kv->block_table;
   a.seq_lens = kv->seq_lens;
   a.cu = groups->cu_groups;
@@ -1506,6 +1510,17 @@ kt_status kt_dense_decode_attn_f8(const void* q, const kt_paged_kv_f8* kvf, int3
   if (ws_bytes < L.total) return KT_ERR_WORKSPACE_TOO_SMALL;
   return attn_impl(q, &kv, num_q_heads, softmax_scale, &p, nullptr, nullptr, out, ws, L, true,
                    false, (cudaStream_t)stream, false, false, source_f8(kvf));
+}
+
+kt_status kt_prefix_decode_attn_f8(const void* q, const kt_paged_kv_f8* kvf,
+                                   const kt_prefix_groups* groups, int32_t num_q_heads,
+                                   float softmax_scale, float* out, void* ws, size_t ws_bytes,
+                                   kt_stream_t stream) {
+  kt_paged_kv kv;
+  const kt_status s = check_kv_f8(kvf, &kv);
+  if (s != KT_OK) return s;
+  return prefix_impl(q, &kv, groups, num_q_heads, softmax_scale, out, ws, ws_bytes,
+                     (cudaStream_t)stream, kvf->k_scale, kvf->v_scale);
 }
 
 kt_status kt_score_select_blocks_f8(const void* q, const kt_paged_kv_f8* kvf,

@@ -694,6 +694,8 @@ struct PrefixLaunch {
   const CUtensorMap* kmap;
   const CUtensorMap* vmap;
   const __half* q;
+  const float* k_scale;   // 8-bit cache: binary32 [pages][H_kv]; else NULL
+  const float* v_scale;
   const int32_t* table;
   const int32_t* seq_lens;
   const int32_t* cu;      // [groups + 1]

@@ -22,10 +22,8 @@ namespace {
 constexpr int ROWS = 128;                // rows of a tile: the M of the tensor-core steps
 constexpr int SLOTS = 2;                 // tiles (each with its own scores and output) a CTA
 constexpr int SOFT_WARPS = 8;            // a thread a row
-constexpr int THREADS = (SOFT_WARPS + 4) * 32;
 constexpr int BOX = BS * 64 * 2;         // 128 tokens (or rows) x 64 channels, binary16
 constexpr int TILE = 2 * BOX;            // 128 x 128
-constexpr int ENTRIES = 5;               // K or V tiles in the ring
 constexpr int PLAN_THREADS = 1024;
 
 struct Item {      // blocks of one K/V head that a set of rows attends, for every K/V head
@@ -59,6 +57,8 @@ struct PrefixWs {
 struct Params {
   CUtensorMap kmap, vmap;
   const __half* q;
+  const float* k_scale;  // 8-bit cache
+  const float* v_scale;
   const int32_t* table;
   const int32_t* seq_lens;
   const int32_t* cu;
@@ -75,11 +75,22 @@ struct Params {
   int* q_rows;     // of members' rows: row of q (head 0)
   SeqPlan* seqs;   // [B]
   float* parts;    // of n rows: [32][n][4], the groups of four channels of all rows
-  float2* stats;   // [rows]: m, l
+  float2* stats;   // [rows]: m (up to a constant), l
   long long rows_a;
   int B, H_kv, G, groups, max_blocks, P, ctas, row_max;
   float scale_log2;
 };
+
+// What the kernel ahead has written is read past L1.
+__device__ __forceinline__ Item load_item(const Item* p) {
+  const int4 a = __ldcg(reinterpret_cast<const int4*>(p));
+  const int4 b = __ldcg(reinterpret_cast<const int4*>(p) + 1);
+  return Item{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+}
+__device__ __forceinline__ Head load_head(const Head* p) {
+  const int* v = reinterpret_cast<const int*>(p);
+  return Head{__ldcg(v), __ldcg(v + 1), __ldcg(v + 2), __ldcg(v + 3), __ldcg(v + 4), __ldcg(v + 5)};
+}
 
 __device__ __forceinline__ float ex2_fast(float x) {
   float y;
@@ -321,13 +332,13 @@ __device__ __noinline__ Start find_start(const Item* items, const int* cost, int
 #pragma unroll 1
   while (n > 1) {
     const int stride = (n + 31) / 32, i = lane * stride;
-    const int c = i < n ? cost[lo + i] : 0x7fffffff;
+    const int c = i < n ? __ldcg(cost + lo + i) : 0x7fffffff;
     const int k = __popc(__ballot_sync(0xffffffffu, c <= x)) - 1;
     lo += k * stride;
     n = min(stride, n - k * stride);
   }
-  at = cost[lo];
-  s.first = items[lo];
+  at = __ldcg(cost + lo);
+  s.first = load_item(items + lo);
   s.item = lo;
   s.head = (x - at) / (s.first.blocks + 1);
   // the first unit of a run's cost is its own, then its blocks
@@ -350,9 +361,9 @@ __device__ __noinline__ Start find_start(const Item* items, const int* cost, int
 // their running output in registers, out = out * alpha + O, and the next S takes the place of
 // P.  So a block's P V is summed apart from the running output, no output is rescaled in
 // TMEM, and the scores stay until P is whole: the exponentials use the running maximum of the
-// blocks before and are made again, after a search for the block's own, where their sum shows
-// that one may not fit binary16 (alpha then scales what was summed before).  Where there is no
-// maximum yet it is taken first.
+// blocks before (as h = 8 - maximum, one rounded number that all blocks' p share) and are made
+// again, after a search for the block's own, where their sum shows that one may not fit binary16
+// (alpha then scales what was summed before).  Where there is no maximum yet it is taken first.
 //
 // P is held as two binary16, 2^8 p = hi - lo (22 bits; steps of at least 2^-24), and
 // P V as two products (the tensor cores negate lo): with one alone the output would be good to 11 bits only, and it is
@@ -370,19 +381,55 @@ struct Unit {      // a run of blocks of one (item, head) in a slot
 // last (their half): all row warps have then arrived for a block of the run before that, so
 // they have read the description before, whose place in four the new one takes.
 constexpr int UNITS = 4;
-constexpr int STEPS_AHEAD = 8;  // flags of the ring's steps: more than it holds
+constexpr int STEPS_AHEAD = 8;  // steps described: more than the rings hold
+
+// The 8-bit cache: its codes arrive in a ring of their own, and four more warps (12-15) turn each
+// tile into a binary16 one in the ring that the tensor cores read.  Two tiles of codes are all
+// that the shared memory has room for beside four of binary16 (with three, a slot's next K waits
+// for its V), so the tiles after them are fetched into L2 ahead of their loads.
+template <bool F8>
+struct Config {
+  static constexpr int entries = F8 ? 4 : 5;  // K or V tiles that the tensor cores read
+  static constexpr int codes = F8 ? 2 : 0;    // tiles of codes
+  static constexpr int threads = (SOFT_WARPS + (F8 ? 8 : 4)) * 32;
+  // Registers pass from the other warps to the row threads: three (four) warpgroups are launched
+  // with launch_regs a thread (the host checks that), and the shares must not add up to more.
+  static constexpr int launch_regs = F8 ? 128 : 168, row_regs = F8 ? 192 : 216,
+                       control_regs = F8 ? 64 : 72;
+  static_assert(2 * row_regs + (F8 ? 2 : 1) * control_regs <= (F8 ? 4 : 3) * launch_regs,
+                "registers of a CTA");
+};
+constexpr int CODE_TILE = BS * D;
+constexpr int FETCH_AHEAD = 4;  // steps of a slot fetched into L2 ahead of their loads
+
+struct Step {
+  int bad;                // the page is outside the pool (or a scale is out of range)
+  int valid;              // tokens
+  float k_scale, v_scale;
+  int slot;               // whose `full` barriers say that its tiles are there (A steps: 0) ...
+  uint32_t v_parity;      // ... and the parity of V's
+};
+template <bool F8>
 struct Misc {
-  uint64_t full[ENTRIES], empty[ENTRIES];
+  // An entry has a barrier `full` for each slot: a slot does not wait for the tiles of the other
+  // one, and on a barrier that both share it would take the phase before the last for its own
+  // when a tile of the other's is late (tiles do not arrive in order).
+  uint64_t full[SLOTS][Config<F8>::entries], empty[Config<F8>::entries];
+  uint64_t code_full[F8 ? 2 : 1], code_empty[F8 ? 2 : 1];
   uint64_t s_full[SLOTS], p_full[SLOTS], o_full[SLOTS];
   uint64_t q_full[SLOTS][UNITS], q_done[SLOTS][2];
+  uint64_t a_done;               // the A steps have been issued
   Unit unit[SLOTS][UNITS];
   uint32_t tmem;
-  int bad[STEPS_AHEAD];          // the step's page is outside the pool
+  Step step[STEPS_AHEAD];
   Start start[1 + SLOTS][2];     // of the A share and the slots' B shares, and of the next worker
 };
-constexpr int SMEM = SLOTS * TILE + ENTRIES * TILE + sizeof(Misc);
-static_assert(SMEM <= 232448, "shared memory of a CTA");
-static_assert(SMEM > 233472 / 2, "one CTA an SM: it holds all of TMEM");
+template <bool F8>
+constexpr int smem_bytes() {
+  return SLOTS * TILE + Config<F8>::entries * TILE + Config<F8>::codes * CODE_TILE + sizeof(Misc<F8>);
+}
+static_assert(smem_bytes<false>() <= 232448 && smem_bytes<true>() <= 232448, "shared memory of a CTA");
+static_assert(smem_bytes<false>() > 233472 / 2, "one CTA an SM: it holds all of TMEM");
 constexpr uint32_t TMEM_COLS = 512;
 
 // Columns of this thread's TMEM lane: loads without their wait (a register of an earlier load
@@ -429,6 +476,14 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   float2 d;
   asm("{\n\t.reg .b64 x, y, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
       "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
       : "=f"(d.x), "=f"(d.y)
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
@@ -486,14 +541,16 @@ __device__ __forceinline__ void mask16(float (&v)[16], int first, int valid) {
     if (first + j >= valid) v[j] = -INFINITY;
 }
 
+constexpr float SCALE_MIN = 0x1p-30f, SCALE_MAX = 0x1p30f;  // of the 8-bit cache
+
 // log2 of the factor of P, and the largest sum of a block's 2^8 p whose terms surely are
 // binary16 (65504 at most).
 constexpr float P_SHIFT = 8.0f, SUM_MAX = 65000.0f;
+// From here on (and where there is none yet) a row takes every block's own maximum, and the
+// differences to it before they are scaled: next to 2^20 a binary32 shift is off by up to 2^-4,
+// further up by so much that 2^8 p would leave binary16.
+constexpr float BIG_SHIFT = 0x1p20f;
 
-// Registers pass from the control warps to the row threads: three warpgroups are launched with
-// LAUNCH_REGS a thread (the host checks that), and the shares must not add up to more.
-constexpr int LAUNCH_REGS = 168, ROW_REGS = 216, CONTROL_REGS = 72;
-static_assert(2 * ROW_REGS + CONTROL_REGS <= 3 * LAUNCH_REGS, "registers of a CTA");
 template <int N>
 __device__ __forceinline__ void regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -533,13 +590,14 @@ __device__ __forceinline__ float row_max(uint32_t taddr, int valid) {
   return fmaxf(top, top2);
 }
 
-// 2^(s scale + shift) of a row's scores at `from`, in two parts to `to`; returns their sum.
+// 2^(s scale + shift) of a row's scores at `from`, in two parts to `to`; returns their sum.  BIG:
+// 2^((s - s0) scale + shift).
 // An element costs four issue slots (half an FMA and an addition of two, the exponential, two
 // halves of conversions, a mixed-precision subtraction); the exponentials bound it, 4 cycles a
 // warp's: 512 a block.
-template <bool MASK>
+template <bool MASK, bool BIG>
 __device__ __forceinline__ float row_exp(uint32_t from, uint32_t to, int valid, float2 scale2,
-                                         float shift) {
+                                         float shift, float s0) {
   const float2 shift2 = make_float2(shift, shift);
   float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
   float v[2][16];
@@ -555,7 +613,9 @@ __device__ __forceinline__ float row_exp(uint32_t from, uint32_t to, int valid, 
       if (MASK) mask16(x, c, valid);
 #pragma unroll
       for (int j = 0; j < 16; j += 2) {
-        const float2 y = fma2(make_float2(x[j], x[j + 1]), scale2, shift2);
+        float2 y = make_float2(x[j], x[j + 1]);
+        if (BIG) y = add2(y, make_float2(-s0, -s0));
+        y = fma2(y, scale2, shift2);
         x[j] = ex2_fast(y.x);
         x[j + 1] = ex2_fast(y.y);
         sum[j / 2 & 1] = add2(sum[j / 2 & 1], make_float2(x[j], x[j + 1]));
@@ -578,12 +638,13 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 // mbar_wait by a whole warp, with the same answer in every lane.
-__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, int* status) {
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, int* status,
+                                               uint64_t limit = WAIT_LIMIT_NS) {
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   const uint64_t t0 = globaltimer();
   for (uint32_t i = 1;; ++i) {
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-    if ((i & 255u) == 0 && __any_sync(0xffffffffu, globaltimer() - t0 > WAIT_LIMIT_NS)) {
+    if ((i & 255u) == 0 && __any_sync(0xffffffffu, globaltimer() - t0 > limit)) {
       set_status(status, KT_ERR_TIMEOUT);
       return false;
     }
@@ -607,7 +668,7 @@ __device__ __forceinline__ void advance(Walk& w, int run, int heads) {
   if (++w.head < heads || w.left == 0) return;
   w.head = 0;
   do {
-    w.it = w.items[++w.item];
+    w.it = load_item(w.items + ++w.item);
   } while (w.it.blocks == 0);
 }
 
@@ -617,7 +678,39 @@ __device__ __forceinline__ int entry_b(int s, int k, int a, int other) {
   return 2 * (a + k + min(s == 0 ? k : k + 1, other));
 }
 
-__device__ __forceinline__ uint32_t entry_parity(int e) { return (uint32_t)(e / ENTRIES) & 1u; }
+// Parity of the n-th use of an entry of a ring of N.
+template <int N>
+__device__ __forceinline__ uint32_t ring_parity(int n) {
+  return (uint32_t)(n / N) & 1u;
+}
+
+// L2 prefetch of a tile.
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int x, int y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y)
+               : "memory");
+}
+
+// A tile of codes (128-byte swizzled rows of 128 codes) into a tile of binary16 (two boxes of 64
+// channels), rows from `valid` on as zeros, by 128 threads: 8 lanes a row, 16 codes each.  The
+// upper four lanes of a row write their second half first, so that the eight are in different
+// banks (the boxes lie a multiple of 128 bytes apart).
+__device__ __forceinline__ void convert_tile(const uint8_t* code, uint8_t* tile, int valid, int t) {
+  const int c = t & 7;
+#pragma unroll 2
+  for (int r = t >> 3; r < BS; r += 16) {
+    uint4 v = *reinterpret_cast<const uint4*>(code + r * 128 + ((c ^ (r & 7)) << 4));
+    if (r >= valid) v = make_uint4(0, 0, 0, 0);
+    const uint4 lo = make_uint4(f8x2_lo(v.x), f8x2_hi(v.x), f8x2_lo(v.y), f8x2_hi(v.y));
+    const uint4 hi = make_uint4(f8x2_lo(v.z), f8x2_hi(v.z), f8x2_lo(v.w), f8x2_hi(v.w));
+    uint8_t* to = tile + (c >> 2) * BOX + r * 128;
+    const int first = c >> 2;  // which half goes first
+    const int a = ((c & 3) * 2 + first) ^ (r & 7), b = ((c & 3) * 2 + (first ^ 1)) ^ (r & 7);
+    *reinterpret_cast<uint4*>(to + (a << 4)) = first ? hi : lo;
+    *reinterpret_cast<uint4*>(to + (b << 4)) = first ? lo : hi;
+  }
+}
 
 // Queries of a run into two swizzled boxes (chunk c of row i: box c / 8, slot (c % 8) ^ (i % 8)).
 // A lane finds where four of the rows are; then 16 lanes copy a row, two rows at a time.
@@ -627,7 +720,7 @@ __device__ __forceinline__ void load_queries(const Params& p, const Item& it, in
 #pragma unroll
   for (int j = 0; j < ROWS / 32; ++j) {
     const int i = min(j * 32 + lane, rows - 1);
-    at[j] = (it.member >= 0 ? p.q_rows[it.member + off + i] : it.seq * p.H_kv * p.G + i) + head * p.G;
+    at[j] = (it.member >= 0 ? __ldcg(p.q_rows + it.member + off + i) : it.seq * p.H_kv * p.G + i) + head * p.G;
   }
   const int c = lane & 15, odd = lane >> 4;
   const char* src = reinterpret_cast<const char*>(p.q) + c * 16;
@@ -649,9 +742,13 @@ __device__ __forceinline__ void load_queries(const Params& p, const Item& it, in
   __syncwarp();
 }
 
-__global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constant__ Params p) {
+template <bool F8>
+__global__ void __launch_bounds__(Config<F8>::threads, 1)
+    attend_kernel(const __grid_constant__ Params p) {
+  constexpr int ENTRIES = Config<F8>::entries, CODES = F8 ? 2 : 1;
   extern __shared__ __align__(1024) uint8_t smem[];
-  Misc& ms = *reinterpret_cast<Misc*>(smem + (SLOTS + ENTRIES) * TILE);
+  uint8_t* codes = smem + (SLOTS + ENTRIES) * TILE;
+  Misc<F8>& ms = *reinterpret_cast<Misc<F8>*>(codes + Config<F8>::codes * CODE_TILE);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = blockIdx.x;
   const uint32_t sQ = smem_u32(smem), ring = sQ + SLOTS * TILE;
@@ -659,10 +756,16 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
   const uint32_t s_full = smem_u32(ms.s_full), p_full = smem_u32(ms.p_full);
   const uint32_t o_full = smem_u32(ms.o_full);
   const uint32_t q_full = smem_u32(ms.q_full), q_done = smem_u32(ms.q_done);
+  const uint32_t code_full = smem_u32(ms.code_full), code_empty = smem_u32(ms.code_empty);
   if (tid == 0) {
     for (int i = 0; i < ENTRIES; ++i) {
-      mbar_init(full + 8 * i, 1);
       mbar_init(empty + 8 * i, 2);
+    }
+    // (arrivals of four converting warps, or of the load)
+    for (int i = 0; i < SLOTS * ENTRIES; ++i) mbar_init(full + 8 * i, F8 ? 4 : 1);
+    for (int i = 0; i < CODES; ++i) {
+      mbar_init(code_full + 8 * i, 1);
+      mbar_init(code_empty + 8 * i, 4);
     }
     for (int i = 0; i < SLOTS; ++i) {
       mbar_init(s_full + 8 * i, 1);
@@ -671,6 +774,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
     }
     for (int i = 0; i < UNITS * SLOTS; ++i) mbar_init(q_full + 8 * i, 1);
     for (int i = 0; i < 2 * SLOTS; ++i) mbar_init(q_done + 8 * i, 1);
+    mbar_init(smem_u32(&ms.a_done), 1);
     fence_mbar_init();
     prefetch_tensormap(&p.kmap);
     prefetch_tensormap(&p.vmap);
@@ -689,7 +793,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
   griddep_launch_dependents();
   if (warp < 2 * (1 + SLOTS)) {
     // this CTA's shares: their beginnings and their ends
-    const Head h = *p.head;
+    const Head h = load_head(p.head);
     const bool a = warp < 2;
     const int n = a ? p.ctas : p.ctas * SLOTS, steps = a ? h.steps_a : h.steps_b;
     const int w = (warp < 4 ? cta : p.ctas + cta) + (warp & 1);
@@ -703,70 +807,159 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
   }
   __syncthreads();
   const int na = ms.start[0][1].step - ms.start[0][0].step;
+  const int all_steps = na + ms.start[1][1].step - ms.start[1][0].step + ms.start[2][1].step -
+                        ms.start[2][0].step;
+
+  // the bound of a wait for the end of a whole run: a step takes a few microseconds
+  const uint64_t run_limit = WAIT_LIMIT_NS + (uint64_t)all_steps * 20000;
 
   if (warp >= SOFT_WARPS) {
-  regs_dec<CONTROL_REGS>();
+  regs_dec<Config<F8>::control_regs>();
   if (warp == SOFT_WARPS + 2) {
     // ============================ K and V tiles ============================
     const uint64_t pol = l2_evict_first_policy();
     const int row_end = p.P * p.H_kv * BS;  // reads zeros
+    constexpr int RING = F8 ? CODES : ENTRIES;
     int e = 0;
+    uint32_t used[SLOTS] = {0, 0}, last = 0;  // parities of the entries' uses; the last one's slot
     bool ok = true;
-    auto load = [&](int page, int head) {
-      const bool bad = page < 0 || page >= p.P;
+    // (the scales of the 8-bit cache come with the pages: any value of [2^-30, 2^30])
+    auto load = [&](int slot, int page, int head, int valid, float ks, float vs) {
+      bool bad = page < 0 || page >= p.P;
+      if (F8) bad = bad || !(ks >= SCALE_MIN && ks <= SCALE_MAX && vs >= SCALE_MIN && vs <= SCALE_MAX);
       const int row = bad ? row_end : (page * p.H_kv + head) * BS;
       if (lane == 0) {
         if (bad) set_status(p.status, KT_ERR_DEVICE_CHECK);
-        ms.bad[(e >> 1) % STEPS_AHEAD] = bad;
+        ms.step[(e >> 1) % STEPS_AHEAD] =
+            Step{bad, bad ? 0 : min(BS, valid), bad ? 1.0f : ks, bad ? 0.0f : vs, slot,
+                 (slot ? used[1] : used[0]) >> ((e + 1) % ENTRIES) & 1u};
       }
+#pragma unroll 1
       for (int side = 0; side < 2 && ok; ++side, ++e) {
-        const int st = e % ENTRIES;
-        if (e >= ENTRIES) ok = mbar_wait_warp(empty + 8 * st, entry_parity(e) ^ 1, p.status);
+        const CUtensorMap* map = side == 0 ? &p.kmap : &p.vmap;
+        const int st = e % RING;
+        const uint32_t landed = (F8 ? code_full : full + 8 * ENTRIES * slot) + 8 * st;
+        if (e >= RING)
+          ok = mbar_wait_warp((F8 ? code_empty : empty) + 8 * st, ring_parity<RING>(e) ^ 1, p.status);
         if (!ok) break;
+        const uint32_t bit = 1u << (e % ENTRIES);
+        if (slot) used[1] ^= bit, last |= bit;
+        else used[0] ^= bit, last &= ~bit;
         if (lane == 0) {
-          const CUtensorMap* map = side == 0 ? &p.kmap : &p.vmap;
-          const uint32_t dst = ring + st * TILE;
-          mbar_arrive_expect_tx(full + 8 * st, TILE);
-          tma_load_2d(dst, map, 0, row, full + 8 * st, pol);
-          tma_load_2d(dst + BOX, map, 64, row, full + 8 * st, pol);
+          if (F8) {
+            mbar_arrive_expect_tx(landed, CODE_TILE);
+            tma_load_2d(smem_u32(codes) + st * CODE_TILE, map, 0, row, landed, pol);
+          } else {
+            const uint32_t dst = ring + st * TILE;
+            mbar_arrive_expect_tx(landed, TILE);
+            tma_load_2d(dst, map, 0, row, landed, pol);
+            tma_load_2d(dst + BOX, map, 64, row, landed, pol);
+          }
         }
         __syncwarp();
       }
     };
-    // the pages of a run's next 32 blocks, one a lane
-    auto fetch = [&](const Item& it, int block) {
-      const int j = block + lane;
-      return j < it.blocks ? p.table[(size_t)it.seq * p.max_blocks + it.start + j] : -1;
-    };
     struct Turn {
       Walk w;
-      int at, run, pages;
+      int slot, at, run, page;     // the pages of the run's next 32 blocks, one a lane
+      float ks, vs;
     };
     auto turn = [&](Turn& t) {
       if (t.w.left == 0) return;
       if ((t.at & 31) == 0) {
         t.run = run_of(t.w);
-        t.pages = fetch(t.w.it, t.w.block + t.at);
+        const int j = t.w.block + t.at + lane;
+        t.page = -1;
+        t.ks = t.vs = 0.0f;
+        if (j < t.w.it.blocks)
+          t.page = p.table[(size_t)t.w.it.seq * p.max_blocks + t.w.it.start + j];
+        if (F8 && t.page >= 0 && t.page < p.P) {
+          t.ks = p.k_scale[(size_t)t.page * p.H_kv + t.w.head];
+          t.vs = p.v_scale[(size_t)t.page * p.H_kv + t.w.head];
+        }
+        if (F8 && lane < FETCH_AHEAD && t.at + lane < t.run && t.page >= 0 && t.page < p.P) {
+          tma_prefetch_2d(&p.kmap, 0, (t.page * p.H_kv + t.w.head) * BS);
+          tma_prefetch_2d(&p.vmap, 0, (t.page * p.H_kv + t.w.head) * BS);
+        }
+        __syncwarp();
       }
-      load(__shfl_sync(0xffffffffu, t.pages, t.at & 31), t.w.head);
+      const int i = t.at & 31;
+      if (F8 && i + FETCH_AHEAD < 32 && t.at + FETCH_AHEAD < t.run && lane == i + FETCH_AHEAD &&
+          t.page >= 0 && t.page < p.P) {
+        tma_prefetch_2d(&p.kmap, 0, (t.page * p.H_kv + t.w.head) * BS);
+        tma_prefetch_2d(&p.vmap, 0, (t.page * p.H_kv + t.w.head) * BS);
+      }
+      __syncwarp();
+      load(t.slot, __shfl_sync(0xffffffffu, t.page, i), t.w.head,
+           t.w.it.tokens - (t.w.block + t.at) * BS, F8 ? __shfl_sync(0xffffffffu, t.ks, i) : 1.0f,
+           F8 ? __shfl_sync(0xffffffffu, t.vs, i) : 1.0f);
       if (++t.at == t.run) {
         advance(t.w, t.run, p.H_kv);
         t.at = 0;
       }
     };
-    {
-      Turn t = {walk_of(p.items_a, ms.start[0]), 0, 0, 0};
-      while (ok && t.w.left > 0) turn(t);
+    // A steps, then the slots' B steps in turn
+    Turn t0 = {walk_of(p.items_a, ms.start[0]), 0, 0, 0, 0, 0.0f, 0.0f}, t1 = t0;
+    t1.w.left = 0;
+#pragma unroll 1
+    for (int part = 0; part < 2; ++part) {
+#pragma unroll 1
+      while (ok && (t0.w.left > 0 || t1.w.left > 0)) {
+        turn(t0);
+        const Turn t = t0;
+        t0 = t1;
+        t1 = t;
+        if (part == 0 || t0.w.left == 0) {  // (one walk only)
+          t1 = t0;
+          t0 = t;
+        }
+      }
+      if (part == 0) {
+        t0 = Turn{walk_of(p.items_b, ms.start[1]), 0, 0, 0, 0, 0.0f, 0.0f};
+        t1 = Turn{walk_of(p.items_b, ms.start[2]), 1, 0, 0, 0, 0.0f, 0.0f};
+        if (t0.w.left == 0) {
+          const Turn t = t0;
+          t0 = t1;
+          t1 = t;
+        }
+      }
     }
-    Turn t0 = {walk_of(p.items_b, ms.start[1]), 0, 0, 0};
-    Turn t1 = {walk_of(p.items_b, ms.start[2]), 0, 0, 0};
-    while (ok && (t0.w.left > 0 || t1.w.left > 0)) {
-      turn(t0);
-      if (ok) turn(t1);
+    // nothing that arrives in this CTA's shared memory is in flight when it ends: loads, and the
+    // tensor cores' arrivals when they are done with a tile (or queries), which come behind those
+    // that let the rows finish
+#pragma unroll 1
+    for (int i = max(0, e - RING); i < e; ++i) {
+      const int st = i % RING, slot = last >> st & 1;
+      if (F8) {
+        mbar_wait_warp(code_full + 8 * st, ring_parity<RING>(i), p.status);
+      } else {
+        mbar_wait_warp(full + 8 * (ENTRIES * slot + st), ((slot ? used[1] : used[0]) >> st & 1u) ^ 1u, p.status);
+        mbar_wait_warp(empty + 8 * st, ring_parity<RING>(i), p.status);
+      }
     }
-    // nothing of this CTA's is in flight when it ends
-    for (int i = max(0, e - ENTRIES); i < e; ++i)
-      mbar_wait_warp(full + 8 * (i % ENTRIES), entry_parity(i), p.status);
+  } else if (F8 && warp >= SOFT_WARPS + 4) {
+    // ============================ codes to binary16 ============================
+    bool ok = true;
+#pragma unroll 1
+    for (int e = 0; e < 2 * all_steps && ok; ++e) {
+      const int c = e % CODES, st = e % ENTRIES;
+      ok = mbar_wait_warp(code_full + 8 * c, ring_parity<CODES>(e), p.status) &&
+           (e < ENTRIES || mbar_wait_warp(empty + 8 * st, ring_parity<ENTRIES>(e) ^ 1, p.status));
+      if (!ok) break;
+      const Step& step = ms.step[(e >> 1) % STEPS_AHEAD];
+      const int slot = step.slot;
+      convert_tile(codes + c * CODE_TILE, smem + (SLOTS + st) * TILE, step.valid,
+                   tid - (SOFT_WARPS + 4) * 32);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(full + 8 * (ENTRIES * slot + st));
+        mbar_arrive(code_empty + 8 * c);
+      }
+    }
+#pragma unroll 1
+    for (int e = max(0, 2 * all_steps - ENTRIES); e < 2 * all_steps; ++e)
+      mbar_wait_warp(empty + 8 * (e % ENTRIES), ring_parity<ENTRIES>(e), p.status);
   } else if (warp == SOFT_WARPS + 3) {
     // ============================ runs and their queries ============================
     Walk w[SLOTS];
@@ -816,12 +1009,17 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
         }
         const uint64_t t = globaltimer();
         if (moved) t0 = t;
-        else if (__any_sync(0xffffffffu, t - t0 > WAIT_LIMIT_NS)) {
+        else if (__any_sync(0xffffffffu, t - t0 > run_limit)) {
           if (lane == 0) set_status(p.status, KT_ERR_TIMEOUT);
           ok = false;
         }
       }
     }
+#pragma unroll
+    for (int s = 0; s < SLOTS; ++s)
+#pragma unroll 1
+      for (int n = max(0, units[s] - 2); n < units[s]; ++n)
+        mbar_wait_warp(q_done + 8 * (2 * s + (n & 1)), (n >> 1) & 1, p.status);
   } else {
     // ============================ tensor-core steps ============================
     // The whole warp runs this, and what it loads goes through a warp reduction: the compiler
@@ -832,6 +1030,9 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
     const int nb0 = uniform(ms.start[1][1].step - ms.start[1][0].step);
     const int nb1 = uniform(ms.start[2][1].step - ms.start[2][0].step);
     bool ok = true;
+    // K and V of A steps are waited for on slot 0's barriers, by both slots' steps
+    const uint32_t tiles = full + 8 * ENTRIES * (warp - SOFT_WARPS);
+    uint32_t used = 0;  // parities of the entries' uses
     // S = Q K^T of slot s's step k, once K, the run's Q and the end of the last P V are there;
     // n counts the runs begun, left the steps of the one at hand
     auto scores = [&](int s, int k, int e, bool both, int& n, int& left) {
@@ -841,9 +1042,10 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
         left = uniform(ms.unit[s][n % UNITS].run);
         ++n;
       }
-      ok = ok && mbar_wait_warp(full + 8 * ek, entry_parity(e), p.status) &&
+      ok = ok && mbar_wait_warp(tiles + 8 * ek, used >> ek & 1u, p.status) &&
            (k == 0 || mbar_wait_warp(o_full + 8 * s, (k - 1) & 1, p.status));
       if (!ok) return;
+      if (!both || s == 1) used ^= 1u << ek;
       tc_fence_after();
       const uint64_t q = umma_sdesc_sw128(sQ + s * TILE), kb = umma_sdesc_sw128(ring + ek * TILE);
       const uint32_t st = tmem + s * 256 + (k & 1) * 128;
@@ -864,9 +1066,10 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
     // O = P V, the high and the low parts of P
     auto values = [&](int s, int k, int e, bool both) {
       const int ev = e % ENTRIES;
-      ok = ok && mbar_wait_warp(full + 8 * ev, entry_parity(e), p.status) &&
+      ok = ok && mbar_wait_warp(tiles + 8 * ev, used >> ev & 1u, p.status) &&
            mbar_wait_warp(p_full + 8 * s, k & 1, p.status);
       if (!ok) return;
+      if (!both || s == 1) used ^= 1u << ev;
       tc_fence_after();
       const uint64_t vb = sdesc_mn_sw128(ring + ev * TILE);
       const uint32_t st = tmem + s * 256 + (k & 1) * 128, pt = tmem + s * 256 + (~k & 1) * 128;
@@ -890,6 +1093,8 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
       Walk w = walk_of(p.items_a, ms.start[0]);
       for (; w.left > 0; ++n) advance(w, run_of(w), p.H_kv);
       n = uniform(n);
+      // the barriers of those runs are past the phases before the first one waited for here
+      if (na_u > 0) ok = mbar_wait_warp(smem_u32(&ms.a_done), 0, p.status, run_limit);
     }
     const int nb = s == 0 ? nb0 : nb1, other = s == 0 ? nb1 : nb0;
     int k = s == 0 ? 0 : na_u;
@@ -913,7 +1118,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
         const int t = n, u = left;
         n = n_other, left = left_other, n_other = t, left_other = u;
         s ^= 1;
-        if (s == 0) ++k;
+        if (s == 0 && ++k == na_u && lane == 0) mbar_arrive(smem_u32(&ms.a_done));
       } else {
         ++k;
       }
@@ -922,13 +1127,12 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
   }
   } else {
     // ============================ rows ============================
-    regs_inc<ROW_REGS>();
+    regs_inc<Config<F8>::row_regs>();
     const int s = warp >> 2, quarter = warp & 3;
     const int r = quarter * 32 + lane;       // this thread's row of the slot
     const uint32_t tb = tmem + s * 256 + ((uint32_t)(quarter * 32) << 16);
     const int steps = na + ms.start[1 + s][1].step - ms.start[1 + s][0].step;
     const int other = ms.start[2 - s][1].step - ms.start[2 - s][0].step;
-    const float2 scale2 = make_float2(p.scale_log2, p.scale_log2);
     bool ok = true;
     for (int k = 0, n = 0; k < steps && ok; ++n) {
       ok = mbar_wait_warp(q_full + 8 * (UNITS * s + n % UNITS), (n / UNITS) & 1, p.status);
@@ -946,21 +1150,21 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
       }
       const bool mine = r >= unit.row0 && r < unit.row0 + unit.rows;
       int tokens = unit.tokens;
-      float acc[D], m = -INFINITY, l = 0.0f;
+      float acc[D], h = INFINITY, l = 0.0f;  // p = 2^(score + h - P_SHIFT)
 #pragma unroll
       for (int i = 0; i < D; ++i) acc[i] = 0.0f;
       for (; k < end; ++k, tokens -= BS) {
         int valid = min(BS, tokens);
         const int e = k < na ? 2 * k : entry_b(s, k - na, na, other);
-        const volatile int* bad = &ms.bad[(e >> 1) % STEPS_AHEAD];
+        const volatile Step* step = &ms.step[(e >> 1) % STEPS_AHEAD];
         const uint32_t ts = tb + (k & 1) * 128, tp = tb + (~k & 1) * 128;
         ok = mbar_wait_warp(s_full + 8 * s, k & 1, p.status);
         if (!ok) break;
         tc_fence_after();
-        if (valid < BS) {
+        if (!F8 && valid < BS) {
           // V behind the last token may be anything, and 0 * NaN is NaN: zeros there
           const int ev = (e + 1) % ENTRIES;
-          ok = mbar_wait_warp(full + 8 * ev, entry_parity(e + 1), p.status);
+          ok = mbar_wait_warp(full + 8 * ((k < na ? 0 : ENTRIES * s) + ev), step->v_parity, p.status);
           if (!ok) break;
           uint8_t* v = smem + SLOTS * TILE + ev * TILE;
           for (int idx = valid * 8 + (quarter - q0) * 32 + lane; idx < BS * 8; idx += warps * 32) {
@@ -969,26 +1173,46 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
           }
           fence_proxy_async_smem();
         }
-        if (*bad) valid = 0;
-        float sum = 0.0f, alpha = 1.0f;
+        if (step->bad) valid = 0;
+        float scale = p.scale_log2, v_scale = 1.0f;
+        if (F8) {
+          scale *= step->k_scale;
+          v_scale = step->v_scale;
+        }
+        const float2 scale2 = make_float2(scale, scale);
+        float sum = 0.0f, alpha = 1.0f, s0 = 0.0f, shift = h;
         // (a row takes a new maximum for its own need only: its numbers do not depend on others')
-        bool need = m == -INFINITY && mine;
+        bool need = mine && fabsf(h) >= BIG_SHIFT;
         for (int round = 0;; ++round) {
+          bool big = false;
           if (__any_sync(0xffffffffu, need)) {
-            const float top =
-                (valid < BS ? row_max<true>(ts, valid) : row_max<false>(ts, valid)) * p.scale_log2;
-            if (need && top > m) {
-              alpha = ex2_fast(m - top);  // 0 where there was nothing yet
-              m = top;
+            const float top = valid < BS ? row_max<true>(ts, valid) : row_max<false>(ts, valid);
+            if (need) {
+              const float u = P_SHIFT - top * scale;
+              if (u < h) {
+                alpha = ex2_fast(u - h);  // 0 where there was nothing yet
+                h = u;
+              }
+              shift = h;
+              if (fabsf(u) >= BIG_SHIFT && fabsf(u) < INFINITY) {
+                s0 = top;
+                shift = P_SHIFT + (h - u);
+              }
             }
+            big = __any_sync(0xffffffffu, s0 != 0.0f);
           } else if (round > 0) {
             break;
           }
-          const float shift = P_SHIFT - (m == -INFINITY ? 0.0f : m);
-          sum = valid < BS ? row_exp<true>(ts, tp, valid, scale2, shift)
-                           : row_exp<false>(ts, tp, valid, scale2, shift);
+          if (h == INFINITY) shift = 0.0f;  // no token yet: all are masked
+          if (big) {
+            sum = valid < BS ? row_exp<true, true>(ts, tp, valid, scale2, shift, s0)
+                             : row_exp<false, true>(ts, tp, valid, scale2, shift, s0);
+          } else {
+            sum = valid < BS ? row_exp<true, false>(ts, tp, valid, scale2, shift, s0)
+                             : row_exp<false, false>(ts, tp, valid, scale2, shift, s0);
+          }
           if (round > 0) break;
-          need = !need && sum > SUM_MAX;  // with its own maximum at most 128 * 2^8 = 2^15
+          need = mine && !need && sum > SUM_MAX;  // with its own maximum at most 128 * 2^8 = 2^15
         }
         l = fmaf(l, alpha, sum);
         tmem_wait_st();
@@ -1010,8 +1234,10 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
             if (c + 16 < D) tmem_ld16_async(ts + c + 16, next);
 #pragma unroll
             for (int j = 0; j < 16; j += 2) {
-              const float2 y = fma2(make_float2(acc[c + j], acc[c + j + 1]), alpha2,
-                                    make_float2(x[j], x[j + 1]));
+              // (the V scale of the block is the O tile's)
+              const float2 o = F8 ? mul2(make_float2(x[j], x[j + 1]), make_float2(v_scale, v_scale))
+                                  : make_float2(x[j], x[j + 1]);
+              const float2 y = fma2(make_float2(acc[c + j], acc[c + j + 1]), alpha2, o);
               acc[c + j] = y.x;
               acc[c + j + 1] = y.y;
             }
@@ -1027,7 +1253,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
 #pragma unroll
         for (int c = 0; c < D / 4; ++c)
           o[(size_t)c * rows] = make_float4(acc[4 * c], acc[4 * c + 1], acc[4 * c + 2], acc[4 * c + 3]);
-        p.stats[part + i] = make_float2(m, l);
+        p.stats[part + i] = make_float2(-h, l);
       }
     }
   }
@@ -1055,8 +1281,9 @@ __global__ void __launch_bounds__(COMBINE_WARPS * 32) combine_kernel(const __gri
   const int row = job / 8 % chunks * COMBINE_ROWS + (lane & 7);
   if (h >= p.H_kv || row >= all_rows) return;
   const int b = row / p.G, g = row % p.G;
-  const Head head = *p.head;
-  const SeqPlan sp = p.seqs[b];
+  const Head head = load_head(p.head);
+  const int4 sp4 = __ldcg(reinterpret_cast<const int4*>(p.seqs + b));
+  const SeqPlan sp = {sp4.x, sp4.y, sp4.z, sp4.w, __ldcg(&p.seqs[b].single), {0, 0, 0}};
   float M = -INFINITY, L = 0.0f;
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   // the prefix, then the sequence's own blocks: the parts of each worker that has steps of it
@@ -1070,9 +1297,9 @@ __global__ void __launch_bounds__(COMBINE_WARPS * 32) combine_kernel(const __gri
     off = r / ROWS * ROWS;
     r -= off;
   }
-  Item it = (a ? p.items_a : p.items_b)[item], own = p.items_b[sp.item];
-  int cost = (a ? p.cost_a : p.cost_b)[item];
-  const int own_cost = p.cost_b[sp.item];
+  Item it = load_item((a ? p.items_a : p.items_b) + item), own = load_item(p.items_b + sp.item);
+  int cost = __ldcg((a ? p.cost_a : p.cost_b) + item);
+  const int own_cost = __ldcg(p.cost_b + sp.item);
 #pragma unroll 1
   for (int turn = sp.r0 >= 0 ? 0 : 1; turn < 2; ++turn) {
     if (turn == 1) {
@@ -1095,10 +1322,10 @@ __global__ void __launch_bounds__(COMBINE_WARPS * 32) combine_kernel(const __gri
     const int w0 = shares.worker_of(x), w1 = shares.worker_of(x + it.blocks);
 #pragma unroll 8
     for (int w = w0; w <= w1; ++w) {
-      const bool has = max(firsts[w], begin) < min(firsts[w + 1], begin + it.blocks);
+      const bool has = max(__ldcg(firsts + w), begin) < min(__ldcg(firsts + w + 1), begin + it.blocks);
       const long long first = base + (long long)w * stride;
-      float2 st = p.stats[first + r];
-      float4 o = reinterpret_cast<const float4*>(p.parts + first * D)[(size_t)col * rows + r];
+      float2 st = __ldcg(p.stats + first + r);
+      float4 o = __ldcg(reinterpret_cast<const float4*>(p.parts + first * D) + (size_t)col * rows + r);
       if (!has) {
         st = make_float2(-INFINITY, 0.0f);
         o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -1172,6 +1399,16 @@ cudaError_t launch(void (*kernel)(P), const P& p, int grid, int threads, size_t 
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
+template <bool F8>
+cudaError_t prepare_attend() {
+  cudaFuncAttributes attr;
+  const cudaError_t r = cudaFuncGetAttributes(&attr, attend_kernel<F8>);
+  if (r != cudaSuccess) return r;
+  if (attr.numRegs != Config<F8>::launch_regs) return cudaErrorLaunchOutOfResources;
+  return cudaFuncSetAttribute(attend_kernel<F8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              smem_bytes<F8>());
+}
+
 }  // namespace
 
 size_t prefix_ws_bytes(int B, int H_kv, int G) { return prefix_layout(B, H_kv, G).total; }
@@ -1211,13 +1448,12 @@ cudaError_t launch_prefix(const PrefixLaunch& a, cudaStream_t stream) {
   p.ctas = a.ctas < PREFIX_MAX_CTAS ? a.ctas : PREFIX_MAX_CTAS;
   p.row_max = a.B * a.G < ROWS ? a.B * a.G : ROWS;
   p.scale_log2 = a.scale_log2;
+  p.k_scale = a.k_scale;
+  p.v_scale = a.v_scale;
   static std::atomic<int> optin[KT_MAX_DEVICES];
   cudaError_t e = (cudaError_t)per_device_cached(optin, [] {
-    cudaFuncAttributes attr;
-    cudaError_t r = cudaFuncGetAttributes(&attr, attend_kernel);
-    if (r != cudaSuccess) return (int)r;
-    if (attr.numRegs != LAUNCH_REGS) return (int)cudaErrorLaunchOutOfResources;
-    r = cudaFuncSetAttribute(attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    cudaError_t r = prepare_attend<false>();
+    if (r == cudaSuccess) r = prepare_attend<true>();
     if (r != cudaSuccess) return (int)r;
     return (int)cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      (int)sizeof(PlanShared));
@@ -1227,7 +1463,9 @@ cudaError_t launch_prefix(const PrefixLaunch& a, cudaStream_t stream) {
   threads = threads < 64 ? 64 : threads < PLAN_THREADS ? (threads + 31) & ~31 : PLAN_THREADS;
   e = launch(plan_kernel, p, 1, threads, sizeof(PlanShared), stream);
   if (e != cudaSuccess) return e;
-  e = launch(attend_kernel, p, p.ctas, THREADS, SMEM, stream);
+  e = a.k_scale ? launch(attend_kernel<true>, p, p.ctas, Config<true>::threads, smem_bytes<true>(), stream)
+                : launch(attend_kernel<false>, p, p.ctas, Config<false>::threads, smem_bytes<false>(),
+                         stream);
   if (e != cudaSuccess) return e;
   const int jobs = a.H_kv * ((a.B * a.G + COMBINE_ROWS - 1) / COMBINE_ROWS) * (D / 16);
   return launch(combine_kernel, p, (jobs + COMBINE_WARPS - 1) / COMBINE_WARPS, COMBINE_WARPS * 32, 0,

@@ -731,8 +731,8 @@ kt_status kt_read_kv_f8(const kt_paged_kv_f8* kv, const int32_t* first, const in
                         size_t ws_bytes, kt_stream_t stream);
 
 /*
- * kt_sparse_decode_attn, kt_dense_decode_attn, kt_score_select_blocks,
- * kt_sparse_decode_step and kt_decode_layer over this cache: the codes become
+ * kt_sparse_decode_attn, kt_dense_decode_attn, kt_prefix_decode_attn,
+ * kt_score_select_blocks, kt_sparse_decode_step and kt_decode_layer over this cache: the codes become
  * binary16 in registers (exactly), the K scale of a block multiplies its scores
  * and the V scale its share of the output, both in binary32, so the attention is
  * that over the values read back.  Scales may be any value in [2^-30, 2^30];
@@ -748,6 +748,10 @@ kt_status kt_sparse_decode_attn_f8(const void* q, const kt_paged_kv_f8* kv,
 kt_status kt_dense_decode_attn_f8(const void* q, const kt_paged_kv_f8* kv, int32_t num_q_heads,
                                   float softmax_scale, float* out, void* ws, size_t ws_bytes,
                                   kt_stream_t stream);
+kt_status kt_prefix_decode_attn_f8(const void* q, const kt_paged_kv_f8* kv,
+                                   const kt_prefix_groups* groups, int32_t num_q_heads,
+                                   float softmax_scale, float* out, void* ws, size_t ws_bytes,
+                                   kt_stream_t stream);
 kt_status kt_score_select_blocks_f8(const void* q, const kt_paged_kv_f8* kv,
                                     const void* reps_pool, const kt_sparse_params* p,
                                     int32_t* sel, int32_t* cnt, float* sel_scores, void* ws,

@@ -3,6 +3,8 @@ sequence's own table."""
 import numpy as np
 import pytest
 
+import f8_ref
+
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 
@@ -41,7 +43,7 @@ class Batch:
     """Groups of (members, prefix blocks, tails); pages shuffled, tails behind the prefix."""
 
     def __init__(self, groups, heads, group, seed=0, spare=3, sharp=1.0, before=0, after=0,
-                 alone=(70,)):
+                 alone=(70,), cache="f16"):
         rng = np.random.default_rng(seed)
         lens, rows = [], []
         blocks = []
@@ -69,28 +71,50 @@ class Batch:
         self.lens, self.table = np.array(lens, dtype=np.int32), table
         self.cu = np.array(cu, dtype=np.int32)
         self.prefix = np.array([p for p, _ in groups], dtype=np.int32)
-        self.k = (rng.normal(size=(pages, heads, 128, 128)) * sharp).astype(np.float16)
-        self.v = rng.normal(size=(pages, heads, 128, 128)).astype(np.float16)
+        self.cache = cache
+        shape = (pages, heads, 128, 128)
+        if cache == "f16":
+            self.k = (rng.normal(size=shape) * sharp).astype(np.float16)
+            self.v = rng.normal(size=shape).astype(np.float16)
+        else:
+            # codes around 48, one scale a page and head so that values are of unit size times sharp
+            self.kc = f8_ref.encode(rng.normal(size=shape) * 48)
+            self.vc = f8_ref.encode(rng.normal(size=shape) * 48)
+            exp = rng.integers(-2, 2, size=(2, pages, heads))
+            self.ks = (max(sharp, 2.0 ** -20) * 2.0 ** exp[0] / 64).astype(np.float32)
+            self.vs = (2.0 ** exp[1] / 64).astype(np.float32)
+            self.decode()
         self.q = rng.normal(size=(len(rows), heads * group, 128)).astype(np.float16)
         self.skip = set()  # (sequence, block) whose page is no page
+
+    def decode(self):
+        self.k = f8_ref.decode(self.kc) * self.ks.astype(np.float64)[:, :, None, None]
+        self.v = f8_ref.decode(self.vc) * self.vs.astype(np.float64)[:, :, None, None]
 
     def dev(self, x):
         return torch.from_numpy(np.ascontiguousarray(x)).cuda()
 
     def upload(self, kt):
-        self.dk, self.dv, self.dq = self.dev(self.k), self.dev(self.v), self.dev(self.q)
-        self.dt, self.dl = self.dev(self.table), self.dev(self.lens)
+        self.dq, self.dt, self.dl = self.dev(self.q), self.dev(self.table), self.dev(self.lens)
         self.dcu, self.dp = self.dev(self.cu), self.dev(self.prefix)
-        self.kv = kt.paged_kv(self.dk, self.dv, self.dt, self.dl)
+        if self.cache == "f16":
+            self.dk, self.dv = self.dev(self.k), self.dev(self.v)
+            self.kv = kt.paged_kv(self.dk, self.dv, self.dt, self.dl)
+        else:
+            self.dk, self.dv = self.dev(self.kc), self.dev(self.vc)
+            self.dks, self.dvs = self.dev(self.ks), self.dev(self.vs)
+            self.kv = kt.paged_kv_f8(self.dk, self.dks, self.dv, self.dvs, self.dt, self.dl)
         self.groups = kt.prefix_groups(self.dcu, self.dp)
         self.params = kt.sparse_params(self.heads * self.group, 0, 1, 1, kt.KT_REP_QUEST,
                                        kt.KT_HEAD_SHARED)
-        self.ws = kt.workspace(kt.KT_OP_PREFIX_ATTN, self.kv, self.params)
+        make = kt.workspace if self.cache == "f16" else kt.workspace_f8
+        self.ws = make(kt.KT_OP_PREFIX_ATTN, self.kv, self.params)
         self.out = torch.full(self.dq.shape, 7.0, dtype=torch.float32, device="cuda")
 
     def call(self, kt, scale=SCALE, stream=None):
-        kt.kt_prefix_decode_attn(self.dq, self.kv, self.groups, self.heads * self.group, scale,
-                                 self.out, self.ws, stream=stream)
+        f = kt.kt_prefix_decode_attn if self.cache == "f16" else kt.kt_prefix_decode_attn_f8
+        f(self.dq, self.kv, self.groups, self.heads * self.group, scale, self.out, self.ws,
+          stream=stream)
 
     def check(self, scale=SCALE):
         got = self.out.cpu().numpy().astype(np.float64)
@@ -145,33 +169,81 @@ SHAPES = {
 }
 
 
+CACHES = pytest.mark.parametrize("cache", ["f16", "f8"])
+
+
+@CACHES
 @pytest.mark.parametrize("name", list(SHAPES))
-def test_attention(kt, name):
-    run(kt, Batch(**SHAPES[name], seed=len(name)))
+def test_attention(kt, name, cache):
+    run(kt, Batch(**SHAPES[name], seed=len(name), cache=cache))
 
 
+@CACHES
 @pytest.mark.parametrize("ctas", [1, 2, 7])
 @pytest.mark.parametrize("name", ["two-groups", "300-rows", "many-groups", "outside"])
-def test_few_ctas(kt, name, ctas):
+def test_few_ctas(kt, name, ctas, cache):
     kt.kt_set_max_ctas(ctas)
     try:
-        run(kt, Batch(**SHAPES[name], seed=ctas))
+        run(kt, Batch(**SHAPES[name], seed=ctas, cache=cache))
     finally:
         kt.kt_set_max_ctas(0)
 
 
+@CACHES
 @pytest.mark.parametrize("sharp", [0.0, 8.0, 60.0])
-def test_flat_and_sharp_scores(kt, sharp):
-    run(kt, Batch(groups=[(12, [300, 1, 128, 64]), (3, [9, 9])], heads=2, group=4, sharp=sharp))
+def test_flat_and_sharp_scores(kt, sharp, cache):
+    run(kt, Batch(groups=[(12, [300, 1, 128, 64]), (3, [9, 9])], heads=2, group=4, sharp=sharp,
+                  cache=cache))
 
 
-def test_scale(kt):
-    run(kt, Batch(groups=[(5, [30, 150, 260])], heads=2, group=5), scale=0.5)
+@CACHES
+@pytest.mark.parametrize("power", [18, 22, 24, 27, 33])
+def test_scores_beyond_the_steps_of_binary32(kt, power, cache):
+    """One channel counts; its products are whole multiples of 2^power (exact in binary32), so each
+    row's output is the mean of V over the tokens with its largest score: the largest and the next
+    score are 2^power apart.  (Scores near 2^power times 200.)"""
+    b = Batch(groups=[(4, [300, 20, 128]), (0, [200])], heads=2, group=4, cache=cache)
+    rng = np.random.default_rng(power)
+    whole = rng.integers(-8, 9, size=(b.pages, 2, 128))
+    b.q[:] = 0
+    b.q[..., 5] = rng.integers(1, 16, size=b.q.shape[:2]) * 2.0 ** (power // 2 - 8)
+    if cache == "f16":
+        b.k[:] = 0
+        b.k[..., 5] = whole * 2.0 ** ((power + 1) // 2 - 8)
+        scale = 2.0 ** 16
+    else:
+        codes = np.zeros(b.kc.shape)
+        codes[..., 5] = whole
+        b.kc = f8_ref.encode(codes)
+        b.ks[:] = 2.0 ** ((power + 1) // 2)
+        b.decode()
+        scale = 2.0 ** 8
+    b.upload(kt)
+    b.call(kt, scale=scale)
+    assert kt.kt_read_device_status(b.ws) == kt.KT_OK
+    got = b.out.cpu().numpy().astype(np.float64)
+    for i, n in enumerate(b.lens):
+        pg = b.table[i, : -(-int(n) // 128)]
+        for h in range(2):
+            k = b.k[pg, h].reshape(-1, 128)[:n, 5].astype(np.float64)
+            v = b.v[pg, h].reshape(-1, 128)[:n].astype(np.float64)
+            for g in range(4):
+                # the mean of up to n equal weights: each is a power of two, exact in one part;
+                # 16 tensor-core steps a block (2^-23 each), sums of blocks and parts, a division
+                top = v[k == k.max()]
+                tol = (16 * 2.0 ** -23 + 2.0 ** -20) * np.abs(top).mean(0)
+                assert (np.abs(got[i, h * 4 + g] - top.mean(0)) <= tol).all(), (i, h, g)
 
 
-def test_short_members_are_attended_alone(kt):
+@CACHES
+def test_scale(kt, cache):
+    run(kt, Batch(groups=[(5, [30, 150, 260])], heads=2, group=5, cache=cache), scale=0.5)
+
+
+@CACHES
+def test_short_members_are_attended_alone(kt, cache):
     """Of a group with a prefix of 6 blocks: one shorter, one ending inside it, one empty."""
-    b = Batch(groups=[(6, [20, 300, 0, 1, 90])], heads=2, group=4)
+    b = Batch(groups=[(6, [20, 300, 0, 1, 90])], heads=2, group=4, cache=cache)
     b.lens[1], b.lens[3], b.lens[4] = 5 * 128 + 3, 0, 6 * 128 - 1
     run(kt, b)
     b.lens[:] = [100, 0, 90, 0, 6 * 128 + 1]
@@ -199,17 +271,37 @@ def test_groups_that_make_no_sense(kt):
     b.check()
 
 
-def test_bad_pages_are_skipped(kt):
-    b = Batch(groups=[(4, [20, 300, 129])], heads=2, group=4)
+@CACHES
+def test_bad_pages_are_skipped(kt, cache):
+    b = Batch(groups=[(4, [20, 300, 129])], heads=2, group=4, cache=cache)
     b.table[:, 2] = 1 << 30
     b.table[1, 5] = -3
     b.table[2, 4] = b.pages
     b.skip = {(0, 2), (1, 2), (2, 2), (1, 5), (2, 4)}
     run(kt, b, want=kt.KT_ERR_DEVICE_CHECK)
-    b = Batch(groups=[(1, [0, 0])], heads=1, group=2)
+    b = Batch(groups=[(1, [0, 0])], heads=1, group=2, cache=cache)
     b.table[:, 0] = -1
     b.skip = {(0, 0), (1, 0)}
     run(kt, b, want=kt.KT_ERR_DEVICE_CHECK)
+
+
+@pytest.mark.parametrize("value", [0.0, -1.0, float("nan"), float("inf"), 2.0 ** 31, 2.0 ** -31])
+@pytest.mark.parametrize("side", ["ks", "vs"])
+def test_blocks_of_bad_scales_are_skipped(kt, side, value):
+    b = Batch(groups=[(4, [20, 300, 129])], heads=1, group=4, cache="f8")
+    getattr(b, side)[b.table[0, 1]] = value
+    getattr(b, side)[b.table[1, 5]] = value
+    b.skip = {(0, 1), (1, 1), (2, 1), (1, 5)}
+    run(kt, b, want=kt.KT_ERR_DEVICE_CHECK)
+
+
+@pytest.mark.parametrize("k,v", [(2.0 ** -30, 2.0 ** 30), (2.0 ** 3, 2.0 ** -30)])
+def test_scales_at_their_ends(kt, k, v):
+    b = Batch(groups=[(4, [20, 300, 129])], heads=1, group=4, cache="f8")
+    b.ks[b.table[0, 1]] = k
+    b.vs[b.table[1, 5]] = v
+    b.decode()
+    run(kt, b)
 
 
 @pytest.mark.parametrize("value", [float("nan"), float("inf"), -65504.0])
@@ -223,6 +315,20 @@ def test_rows_behind_the_end_may_be_anything(kt, value):
     for page in set(range(b.pages)) - set(b.table.ravel().tolist()):
         b.k[page] = value
         b.v[page] = value
+    run(kt, b)
+
+
+@pytest.mark.parametrize("code", [0x7F, 0xFF, 0x7E])
+def test_codes_behind_the_end_may_be_anything(kt, code):
+    b = Batch(groups=[(3, [1, 64, 127, 130]), (0, [100])], heads=2, group=4, cache="f8")
+    for i, n in enumerate(b.lens):
+        if n % 128:
+            page = b.table[i, n // 128]
+            b.kc[page, :, n % 128:] = code
+            b.vc[page, :, n % 128:] = code
+    for page in set(range(b.pages)) - set(b.table.ravel().tolist()):
+        b.kc[page] = code
+        b.vc[page] = code
     run(kt, b)
 
 
@@ -250,8 +356,9 @@ def test_values_that_are_not_finite(kt):
     assert np.array_equal(ok[keep], clean[keep])
 
 
-def test_the_same_every_time_and_on_other_streams(kt):
-    b = Batch(groups=[(30, [20, 300, 129] * 10), (7, [5] * 20)], heads=4, group=3)
+@CACHES
+def test_the_same_every_time_and_on_other_streams(kt, cache):
+    b = Batch(groups=[(30, [20, 300, 129] * 10), (7, [5] * 20)], heads=4, group=3, cache=cache)
     run(kt, b)
     first = b.out.clone()
     stream = torch.cuda.Stream()
@@ -264,9 +371,11 @@ def test_the_same_every_time_and_on_other_streams(kt):
         assert torch.equal(b.out, first)
 
 
-def test_captured_call_follows_its_inputs(kt):
+@CACHES
+def test_captured_call_follows_its_inputs(kt, cache):
     """Lengths, groups and queries change between replays; a second graph shares the workspace."""
-    b = Batch(groups=[(6, [20, 300, 10, 1, 90]), (2, [400, 500, 600])], heads=2, group=4)
+    b = Batch(groups=[(6, [20, 300, 10, 1, 90]), (2, [400, 500, 600])], heads=2, group=4,
+              cache=cache)
     b.upload(kt)
     graphs = []
     stream = torch.cuda.Stream()
