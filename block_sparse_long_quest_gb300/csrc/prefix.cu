@@ -50,7 +50,7 @@ struct Head {      // A and B items: their steps, and the cost that is shared ou
 
 // Offsets in the workspace's part.
 struct PrefixWs {
-  size_t head, items_a, items_b, cost_a, cost_b, first_a, first_b, q_rows, seqs, parts, stats, total;
+  size_t head, items_a, items_b, cost_a, cost_b, q_rows, seqs, parts, stats, total;
   long long rows_a;  // parts of A items come first
 };
 
@@ -70,8 +70,6 @@ struct Params {
   Item* items_b;
   int* cost_a;     // cost of the items before
   int* cost_b;
-  int* first_a;    // [CTAs + 1] first step of each CTA ...
-  int* first_b;    // ... and of each slot
   int* q_rows;     // of members' rows: row of q (head 0)
   SeqPlan* seqs;   // [B]
   float* parts;    // of n rows: [32][n][4], the groups of four channels of all rows
@@ -313,7 +311,13 @@ struct Shares {
   }
 };
 
-struct Start {     // where a CTA (A) or a slot (B; slot s of CTA c is worker s * CTAs + c) begins
+// The number of slot s among the workers of B steps: backwards, as the first CTAs may have one more
+// A step than the others, and the first workers one more B step.
+__device__ __forceinline__ int b_worker(const Params& p, int s) {
+  return s * p.ctas + p.ctas - 1 - (int)blockIdx.x;
+}
+
+struct Start {     // where a CTA (A) or a slot (B; slot s: worker b_worker) begins
   Item first;      // its first item, that one's number, a head and a block of it
   int item, head, block;
   int step;        // its number among all steps
@@ -389,8 +393,8 @@ constexpr int STEPS_AHEAD = 8;  // steps described: more than the rings hold
 // for its V), so the tiles after them are fetched into L2 ahead of their loads.
 template <bool F8>
 struct Config {
-  static constexpr int entries = F8 ? 4 : 5;  // K or V tiles that the tensor cores read
-  static constexpr int codes = F8 ? 2 : 0;    // tiles of codes
+  static constexpr int entries = F8 ? 3 : 5;  // K or V tiles that the tensor cores read
+  static constexpr int codes = F8 ? 4 : 0;    // tiles of codes
   static constexpr int threads = (SOFT_WARPS + (F8 ? 8 : 4)) * 32;
   // Registers pass from the other warps to the row threads: three (four) warpgroups are launched
   // with launch_regs a thread (the host checks that), and the shares must not add up to more.
@@ -415,7 +419,7 @@ struct Misc {
   // one, and on a barrier that both share it would take the phase before the last for its own
   // when a tile of the other's is late (tiles do not arrive in order).
   uint64_t full[SLOTS][Config<F8>::entries], empty[Config<F8>::entries];
-  uint64_t code_full[F8 ? 2 : 1], code_empty[F8 ? 2 : 1];
+  uint64_t code_full[F8 ? Config<F8>::codes : 1], code_empty[F8 ? Config<F8>::codes : 1];
   uint64_t s_full[SLOTS], p_full[SLOTS], o_full[SLOTS];
   uint64_t q_full[SLOTS][UNITS], q_done[SLOTS][2];
   uint64_t a_done;               // the A steps have been issued
@@ -672,6 +676,17 @@ __device__ __forceinline__ void advance(Walk& w, int run, int heads) {
   } while (w.it.blocks == 0);
 }
 
+// Where the n-th tile goes, and how many tiles have gone there before.  (8-bit: one entry for K,
+// two for V, so that no K waits for the end of a P V.)
+template <bool F8>
+__device__ __forceinline__ int place(int n) {
+  return F8 ? (n & 1) + (n & n >> 1 & 1) : n % Config<F8>::entries;
+}
+template <bool F8>
+__device__ __forceinline__ int use(int n) {
+  return F8 ? n >> 1 >> (n & 1) : n / Config<F8>::entries;
+}
+
 // First ring entry of slot s's B step k (K; V is the next one), behind `a` A steps: the
 // slots' steps take turns as long as both have some.
 __device__ __forceinline__ int entry_b(int s, int k, int a, int other) {
@@ -693,22 +708,31 @@ __device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int x, i
 }
 
 // A tile of codes (128-byte swizzled rows of 128 codes) into a tile of binary16 (two boxes of 64
-// channels), rows from `valid` on as zeros, by 128 threads: 8 lanes a row, 16 codes each.  The
-// upper four lanes of a row write their second half first, so that the eight are in different
-// banks (the boxes lie a multiple of 128 bytes apart).
-__device__ __forceinline__ void convert_tile(const uint8_t* code, uint8_t* tile, int valid, int t) {
-  const int c = t & 7;
-#pragma unroll 2
-  for (int r = t >> 3; r < BS; r += 16) {
-    uint4 v = *reinterpret_cast<const uint4*>(code + r * 128 + ((c ^ (r & 7)) << 4));
-    if (r >= valid) v = make_uint4(0, 0, 0, 0);
-    const uint4 lo = make_uint4(f8x2_lo(v.x), f8x2_hi(v.x), f8x2_lo(v.y), f8x2_hi(v.y));
-    const uint4 hi = make_uint4(f8x2_lo(v.z), f8x2_hi(v.z), f8x2_lo(v.w), f8x2_hi(v.w));
-    uint8_t* to = tile + (c >> 2) * BOX + r * 128;
-    const int first = c >> 2;  // which half goes first
-    const int a = ((c & 3) * 2 + first) ^ (r & 7), b = ((c & 3) * 2 + (first ^ 1)) ^ (r & 7);
-    *reinterpret_cast<uint4*>(to + (a << 4)) = first ? hi : lo;
-    *reinterpret_cast<uint4*>(to + (b << 4)) = first ? lo : hi;
+// channels) by 128 threads: 8 lanes a row, 16 codes each, rows t / 8 + 16 i.
+constexpr int CODE_ROWS = BS / 16;
+__device__ __forceinline__ void load_codes(const uint8_t* code, int t, uint4 (&v)[CODE_ROWS]) {
+  const int r = t >> 3, c = t & 7;
+#pragma unroll
+  for (int i = 0; i < CODE_ROWS; ++i)
+    v[i] = *reinterpret_cast<const uint4*>(code + (r + 16 * i) * 128 + ((c ^ (r & 7)) << 4));
+}
+// Rows from `valid` on become zeros.  The upper four lanes of a row write their second half first,
+// so that the eight are in different banks (the boxes lie a multiple of 128 bytes apart).
+__device__ __forceinline__ void store_codes(uint8_t* tile, int valid, int t, const uint4 (&v)[CODE_ROWS]) {
+  const int r = t >> 3, c = t & 7;
+  const bool up = c >> 2;
+  uint8_t* to = tile + (c >> 2) * BOX + r * 128;
+  const int a = (((c & 3) * 2 + up) ^ (r & 7)) << 4, b = a ^ 16;
+#pragma unroll
+  for (int i = 0; i < CODE_ROWS; ++i) {
+    uint4 w = v[i];
+    if (r + 16 * i >= valid) w = make_uint4(0, 0, 0, 0);
+    const uint2 first = up ? make_uint2(w.z, w.w) : make_uint2(w.x, w.y);
+    const uint2 last = up ? make_uint2(w.x, w.y) : make_uint2(w.z, w.w);
+    *reinterpret_cast<uint4*>(to + i * (16 * 128) + a) =
+        make_uint4(f8x2_lo(first.x), f8x2_hi(first.x), f8x2_lo(first.y), f8x2_hi(first.y));
+    *reinterpret_cast<uint4*>(to + i * (16 * 128) + b) =
+        make_uint4(f8x2_lo(last.x), f8x2_hi(last.x), f8x2_lo(last.y), f8x2_hi(last.y));
   }
 }
 
@@ -745,7 +769,7 @@ __device__ __forceinline__ void load_queries(const Params& p, const Item& it, in
 template <bool F8>
 __global__ void __launch_bounds__(Config<F8>::threads, 1)
     attend_kernel(const __grid_constant__ Params p) {
-  constexpr int ENTRIES = Config<F8>::entries, CODES = F8 ? 2 : 1;
+  constexpr int ENTRIES = Config<F8>::entries, CODES = F8 ? Config<F8>::codes : 1;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* codes = smem + (SLOTS + ENTRIES) * TILE;
   Misc<F8>& ms = *reinterpret_cast<Misc<F8>*>(codes + Config<F8>::codes * CODE_TILE);
@@ -796,14 +820,11 @@ __global__ void __launch_bounds__(Config<F8>::threads, 1)
     const Head h = load_head(p.head);
     const bool a = warp < 2;
     const int n = a ? p.ctas : p.ctas * SLOTS, steps = a ? h.steps_a : h.steps_b;
-    const int w = (warp < 4 ? cta : p.ctas + cta) + (warp & 1);
+    const int w = (a ? cta : b_worker(p, (warp >> 1) - 1)) + (warp & 1);
     const Shares shares(n, steps, a ? h.cost_a : h.cost_b);
     const Start st = find_start(a ? p.items_a : p.items_b, a ? p.cost_a : p.cost_b,
                                 a ? h.items_a : h.items_b, shares, steps, w);
-    if (lane == 0) {
-      ms.start[warp >> 1][warp & 1] = st;
-      (a ? p.first_a : p.first_b)[w] = st.step;  // (two write the same)
-    }
+    if (lane == 0) ms.start[warp >> 1][warp & 1] = st;
   }
   __syncthreads();
   const int na = ms.start[0][1].step - ms.start[0][0].step;
@@ -832,7 +853,7 @@ __global__ void __launch_bounds__(Config<F8>::threads, 1)
         if (bad) set_status(p.status, KT_ERR_DEVICE_CHECK);
         ms.step[(e >> 1) % STEPS_AHEAD] =
             Step{bad, bad ? 0 : min(BS, valid), bad ? 1.0f : ks, bad ? 0.0f : vs, slot,
-                 (slot ? used[1] : used[0]) >> ((e + 1) % ENTRIES) & 1u};
+                 (slot ? used[1] : used[0]) >> place<F8>(e + 1) & 1u};
       }
 #pragma unroll 1
       for (int side = 0; side < 2 && ok; ++side, ++e) {
@@ -842,7 +863,7 @@ __global__ void __launch_bounds__(Config<F8>::threads, 1)
         if (e >= RING)
           ok = mbar_wait_warp((F8 ? code_empty : empty) + 8 * st, ring_parity<RING>(e) ^ 1, p.status);
         if (!ok) break;
-        const uint32_t bit = 1u << (e % ENTRIES);
+        const uint32_t bit = 1u << place<F8>(e);
         if (slot) used[1] ^= bit, last |= bit;
         else used[0] ^= bit, last &= ~bit;
         if (lane == 0) {
@@ -939,27 +960,29 @@ __global__ void __launch_bounds__(Config<F8>::threads, 1)
     }
   } else if (F8 && warp >= SOFT_WARPS + 4) {
     // ============================ codes to binary16 ============================
+    const int t = tid - (SOFT_WARPS + 4) * 32;
     bool ok = true;
 #pragma unroll 1
     for (int e = 0; e < 2 * all_steps && ok; ++e) {
-      const int c = e % CODES, st = e % ENTRIES;
-      ok = mbar_wait_warp(code_full + 8 * c, ring_parity<CODES>(e), p.status) &&
-           (e < ENTRIES || mbar_wait_warp(empty + 8 * st, ring_parity<ENTRIES>(e) ^ 1, p.status));
+      const int c = e % CODES, st = place<F8>(e);
+      ok = mbar_wait_warp(code_full + 8 * c, ring_parity<CODES>(e), p.status);
       if (!ok) break;
-      const Step& step = ms.step[(e >> 1) % STEPS_AHEAD];
-      const int slot = step.slot;
-      convert_tile(codes + c * CODE_TILE, smem + (SLOTS + st) * TILE, step.valid,
-                   tid - (SOFT_WARPS + 4) * 32);
+      const int valid = ms.step[(e >> 1) % STEPS_AHEAD].valid, slot = ms.step[(e >> 1) % STEPS_AHEAD].slot;
+      uint4 v[CODE_ROWS];  // (the next load need not wait for the entry's last use)
+      load_codes(codes + c * CODE_TILE, t, v);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(code_empty + 8 * c);
+      if (use<F8>(e) > 0) ok = mbar_wait_warp(empty + 8 * st, ~use<F8>(e) & 1, p.status);
+      if (!ok) break;
+      store_codes(smem + (SLOTS + st) * TILE, valid, t, v);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(full + 8 * (ENTRIES * slot + st));
-        mbar_arrive(code_empty + 8 * c);
-      }
+      if (lane == 0) mbar_arrive(full + 8 * (ENTRIES * slot + st));
     }
 #pragma unroll 1
-    for (int e = max(0, 2 * all_steps - ENTRIES); e < 2 * all_steps; ++e)
-      mbar_wait_warp(empty + 8 * (e % ENTRIES), ring_parity<ENTRIES>(e), p.status);
+    for (int e = max(0, 2 * all_steps - 4); e < 2 * all_steps; ++e)
+      if (e >= 2 * all_steps - 2 || (e & 1)) // the last K, the last two V
+        mbar_wait_warp(empty + 8 * place<F8>(e), use<F8>(e) & 1, p.status);
   } else if (warp == SOFT_WARPS + 3) {
     // ============================ runs and their queries ============================
     Walk w[SLOTS];
@@ -997,7 +1020,7 @@ __global__ void __launch_bounds__(Config<F8>::threads, 1)
             unit.run = run;
             unit.tokens = it.tokens - w[s].block * BS;
             unit.part = a ? ((long long)cta + (long long)w[s].item * p.H_kv + w[s].head) * (2 * ROWS) + off
-                          : p.rows_a + (long long)(s * p.ctas + cta) * p.row_max + it.row_base +
+                          : p.rows_a + (long long)b_worker(p, s) * p.row_max + it.row_base +
                                 (long long)w[s].head * it.rows;
           }
           load_queries(p, it, w[s].head, off, rows, sQ + s * TILE, row0, lane);
@@ -1036,7 +1059,7 @@ __global__ void __launch_bounds__(Config<F8>::threads, 1)
     // S = Q K^T of slot s's step k, once K, the run's Q and the end of the last P V are there;
     // n counts the runs begun, left the steps of the one at hand
     auto scores = [&](int s, int k, int e, bool both, int& n, int& left) {
-      const int ek = e % ENTRIES;
+      const int ek = place<F8>(e);
       if (left == 0) {
         ok = ok && mbar_wait_warp(q_full + 8 * (UNITS * s + n % UNITS), (n / UNITS) & 1, p.status);
         left = uniform(ms.unit[s][n % UNITS].run);
@@ -1065,7 +1088,7 @@ __global__ void __launch_bounds__(Config<F8>::threads, 1)
     };
     // O = P V, the high and the low parts of P
     auto values = [&](int s, int k, int e, bool both) {
-      const int ev = e % ENTRIES;
+      const int ev = place<F8>(e);
       ok = ok && mbar_wait_warp(tiles + 8 * ev, used >> ev & 1u, p.status) &&
            mbar_wait_warp(p_full + 8 * s, k & 1, p.status);
       if (!ok) return;
@@ -1163,7 +1186,7 @@ __global__ void __launch_bounds__(Config<F8>::threads, 1)
         tc_fence_after();
         if (!F8 && valid < BS) {
           // V behind the last token may be anything, and 0 * NaN is NaN: zeros there
-          const int ev = (e + 1) % ENTRIES;
+          const int ev = place<F8>(e + 1);
           ok = mbar_wait_warp(full + 8 * ((k < na ? 0 : ENTRIES * s) + ev), step->v_parity, p.status);
           if (!ok) break;
           uint8_t* v = smem + SLOTS * TILE + ev * TILE;
@@ -1223,7 +1246,16 @@ __global__ void __launch_bounds__(Config<F8>::threads, 1)
         if (!ok) break;
         tc_fence_after();
         {
-          const float2 alpha2 = make_float2(alpha, alpha);
+          if (__any_sync(0xffffffffu, alpha != 1.0f)) {  // (few blocks have a new maximum)
+            const float2 alpha2 = make_float2(alpha, alpha);
+#pragma unroll
+            for (int i = 0; i < D; i += 2) {
+              const float2 y = mul2(make_float2(acc[i], acc[i + 1]), alpha2);
+              acc[i] = y.x;
+              acc[i + 1] = y.y;
+            }
+          }
+          const float2 v_scale2 = make_float2(v_scale, v_scale);
           float v[2][16];
           tmem_ld16_async(ts, v[0]);
           tmem_wait_ld(v[0]);
@@ -1234,10 +1266,10 @@ __global__ void __launch_bounds__(Config<F8>::threads, 1)
             if (c + 16 < D) tmem_ld16_async(ts + c + 16, next);
 #pragma unroll
             for (int j = 0; j < 16; j += 2) {
+              const float2 o = make_float2(x[j], x[j + 1]);
+              const float2 y0 = make_float2(acc[c + j], acc[c + j + 1]);
               // (the V scale of the block is the O tile's)
-              const float2 o = F8 ? mul2(make_float2(x[j], x[j + 1]), make_float2(v_scale, v_scale))
-                                  : make_float2(x[j], x[j + 1]);
-              const float2 y = fma2(make_float2(acc[c + j], acc[c + j + 1]), alpha2, o);
+              const float2 y = F8 ? fma2(o, v_scale2, y0) : add2(o, y0);
               acc[c + j] = y.x;
               acc[c + j + 1] = y.y;
             }
@@ -1270,16 +1302,16 @@ __global__ void __launch_bounds__(Config<F8>::threads, 1)
 // channels: its 8 x 16 bytes of a part's channel group are contiguous.
 constexpr int COMBINE_WARPS = 8;
 constexpr int COMBINE_ROWS = 8;
+constexpr int COMBINE_BATCH = 16;  // parts in flight
 
-__global__ void __launch_bounds__(COMBINE_WARPS * 32) combine_kernel(const __grid_constant__ Params p) {
-  griddep_wait();
-  griddep_launch_dependents();
+__global__ void __launch_bounds__(COMBINE_WARPS * 32, 2) combine_kernel(const __grid_constant__ Params p) {
+  // What the plan says was there before the kernel ahead let this one start.
   const int lane = threadIdx.x & 31, all_rows = p.B * p.G;
   const int chunks = (all_rows + COMBINE_ROWS - 1) / COMBINE_ROWS;
   const int job = blockIdx.x * COMBINE_WARPS + (threadIdx.x >> 5);
   const int h = job / (chunks * 8), col = job % 8 * 4 + (lane >> 3);  // channels 4 col .. + 3
   const int row = job / 8 % chunks * COMBINE_ROWS + (lane & 7);
-  if (h >= p.H_kv || row >= all_rows) return;
+  if (h >= p.H_kv || row >= all_rows) return;  // (its share of the grid's dependence ends with it)
   const int b = row / p.G, g = row % p.G;
   const Head head = load_head(p.head);
   const int4 sp4 = __ldcg(reinterpret_cast<const int4*>(p.seqs + b));
@@ -1300,6 +1332,9 @@ __global__ void __launch_bounds__(COMBINE_WARPS * 32) combine_kernel(const __gri
   Item it = load_item((a ? p.items_a : p.items_b) + item), own = load_item(p.items_b + sp.item);
   int cost = __ldcg((a ? p.cost_a : p.cost_b) + item);
   const int own_cost = __ldcg(p.cost_b + sp.item);
+  const Shares shares_a(p.ctas, head.steps_a, head.cost_a), shares_b(p.ctas * SLOTS, head.steps_b, head.cost_b);
+  griddep_wait();
+  griddep_launch_dependents();
 #pragma unroll 1
   for (int turn = sp.r0 >= 0 ? 0 : 1; turn < 2; ++turn) {
     if (turn == 1) {
@@ -1315,35 +1350,54 @@ __global__ void __launch_bounds__(COMBINE_WARPS * 32) combine_kernel(const __gri
     const int stride = a ? 2 * ROWS : p.row_max;
     const long long base = a ? (long long)(item * p.H_kv + h) * (2 * ROWS) + off
                              : p.rows_a + it.row_base + (long long)h * rows;
-    const int* firsts = a ? p.first_a : p.first_b;
-    const Shares shares(a ? p.ctas : p.ctas * SLOTS, a ? head.steps_a : head.steps_b,
-                        a ? head.cost_a : head.cost_b);
-    const int begin = it.cum + h * it.blocks, x = cost + h * (it.blocks + 1);
-    const int w0 = shares.worker_of(x), w1 = shares.worker_of(x + it.blocks);
-#pragma unroll 8
-    for (int w = w0; w <= w1; ++w) {
-      const bool has = max(__ldcg(firsts + w), begin) < min(__ldcg(firsts + w + 1), begin + it.blocks);
-      const long long first = base + (long long)w * stride;
-      float2 st = __ldcg(p.stats + first + r);
-      float4 o = __ldcg(reinterpret_cast<const float4*>(p.parts + first * D) + (size_t)col * rows + r);
-      if (!has) {
-        st = make_float2(-INFINITY, 0.0f);
-        o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const Shares& shares = a ? shares_a : shares_b;
+    // the run's first unit of cost is its own, then its blocks
+    const int x = cost + h * (it.blocks + 1) + 1;
+    const int w0 = shares.worker_of(x), w1 = shares.worker_of(x + it.blocks - 1);
+    for (int w = w0; w <= w1; w += COMBINE_BATCH) {
+      float2 st[COMBINE_BATCH];
+      float4 o[COMBINE_BATCH];
+      float m = M;
+#pragma unroll
+      for (int i = 0; i < COMBINE_BATCH; ++i) {
+        st[i] = make_float2(-INFINITY, 0.0f);
+        o[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (w + i <= w1) {
+          const long long first = base + (long long)(w + i) * stride;
+          st[i] = __ldcg(p.stats + first + r);
+          o[i] = __ldcg(reinterpret_cast<const float4*>(p.parts + first * D) + (size_t)col * rows + r);
+        }
       }
-      const float m = fmaxf(M, st.x), ref = m == -INFINITY ? 0.0f : m;
-      const float a0 = ex2_fast(M - ref), c = ex2_fast(st.x - ref);
+#pragma unroll
+      for (int i = 0; i < COMBINE_BATCH; ++i) m = fmaxf(m, st[i].x);
+      const float ref = m == -INFINITY ? 0.0f : m, a0 = ex2_fast(M - ref);
       M = m;
-      L = fmaf(L, a0, st.y * c);
-      acc.x = fmaf(acc.x, a0, o.x * c);
-      acc.y = fmaf(acc.y, a0, o.y * c);
-      acc.z = fmaf(acc.z, a0, o.z * c);
-      acc.w = fmaf(acc.w, a0, o.w * c);
+      L *= a0;
+      acc = make_float4(acc.x * a0, acc.y * a0, acc.z * a0, acc.w * a0);
+#pragma unroll
+      for (int i = 0; i < COMBINE_BATCH; ++i) {
+        const float c = ex2_fast(st[i].x - ref);
+        L = fmaf(st[i].y, c, L);
+        acc.x = fmaf(o[i].x, c, acc.x);
+        acc.y = fmaf(o[i].y, c, acc.y);
+        acc.z = fmaf(o[i].z, c, acc.z);
+        acc.w = fmaf(o[i].w, c, acc.w);
+      }
     }
   }
   const float inv = L == 0.0f ? 0.0f : 1.0f / L;
   float* out = p.out + ((size_t)b * p.H_kv * p.G + h * p.G + g) * D;
   reinterpret_cast<float4*>(out)[col] =
       make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+}
+
+// Its CTAs start as those of attend end; without a limit the first SMs that are free take them
+// all, eight each.  The shared memory that they ask for (and do not use) leaves room for an even
+// share an SM.
+size_t combine_smem(int grid, int sms) {
+  constexpr int SM_BYTES = 233472, CTA_BYTES = 1024;  // of an SM; what a CTA takes beside its own
+  const int share = (grid + sms - 1) / sms;
+  return share >= 8 ? 0 : (size_t)(SM_BYTES / share / 1024 * 1024 - CTA_BYTES);
 }
 
 PrefixWs prefix_layout(int B, int H_kv, int G) {
@@ -1362,10 +1416,6 @@ PrefixWs prefix_layout(int B, int H_kv, int G) {
   off = align256(off + max_pairs * 4);
   L.cost_b = off;
   off = align256(off + 2 * (size_t)B * 4);
-  L.first_a = off;
-  off = align256(off + (PREFIX_MAX_CTAS + 1) * 4);
-  L.first_b = off;
-  off = align256(off + (PREFIX_MAX_CTAS * SLOTS + 1) * 4);
   L.q_rows = off;
   off = align256(off + (size_t)B * G * 4);
   L.seqs = off;
@@ -1432,8 +1482,6 @@ cudaError_t launch_prefix(const PrefixLaunch& a, cudaStream_t stream) {
   p.items_b = reinterpret_cast<Item*>(ws + L.items_b);
   p.cost_a = reinterpret_cast<int*>(ws + L.cost_a);
   p.cost_b = reinterpret_cast<int*>(ws + L.cost_b);
-  p.first_a = reinterpret_cast<int*>(ws + L.first_a);
-  p.first_b = reinterpret_cast<int*>(ws + L.first_b);
   p.q_rows = reinterpret_cast<int*>(ws + L.q_rows);
   p.seqs = reinterpret_cast<SeqPlan*>(ws + L.seqs);
   p.parts = reinterpret_cast<float*>(ws + L.parts);
@@ -1454,6 +1502,9 @@ cudaError_t launch_prefix(const PrefixLaunch& a, cudaStream_t stream) {
   cudaError_t e = (cudaError_t)per_device_cached(optin, [] {
     cudaError_t r = prepare_attend<false>();
     if (r == cudaSuccess) r = prepare_attend<true>();
+    if (r == cudaSuccess)
+      r = cudaFuncSetAttribute(combine_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)combine_smem(1, 1));
     if (r != cudaSuccess) return (int)r;
     return (int)cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      (int)sizeof(PlanShared));
@@ -1468,8 +1519,8 @@ cudaError_t launch_prefix(const PrefixLaunch& a, cudaStream_t stream) {
                          stream);
   if (e != cudaSuccess) return e;
   const int jobs = a.H_kv * ((a.B * a.G + COMBINE_ROWS - 1) / COMBINE_ROWS) * (D / 16);
-  return launch(combine_kernel, p, (jobs + COMBINE_WARPS - 1) / COMBINE_WARPS, COMBINE_WARPS * 32, 0,
-                stream);
+  const int grid = (jobs + COMBINE_WARPS - 1) / COMBINE_WARPS;
+  return launch(combine_kernel, p, grid, COMBINE_WARPS * 32, combine_smem(grid, p.ctas), stream);
 }
 
 }  // namespace kt
