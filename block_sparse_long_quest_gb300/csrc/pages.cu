@@ -57,7 +57,7 @@ __device__ __forceinline__ int ld_cluster(const int* p, uint32_t rank) {
 
 struct Shared {
   int warp_sum[WARPS];
-  int count[2];  // this CTA's counts, read by the cluster
+  int count[1];  // this CTA's count, read by the cluster
 };
 
 // Exclusive prefix of x over the CTA's threads, and the total.
@@ -83,12 +83,12 @@ __device__ __forceinline__ int block_scan(int x, int* total, Shared& sh) {
   return (warp > 0 ? before : 0) + incl - x;
 }
 
-// This CTA's slice of the pages: whole groups of four.
+// CTA r's slice of the pages: whole groups of four.
 struct Slice {
   int lo, hi;
 };
-__device__ __forceinline__ Slice slice_of(int P) {
-  const int groups = (P + 3) / 4, r = cluster_rank();
+__device__ __forceinline__ Slice slice_of(int P, int r) {
+  const int groups = (P + 3) / 4;
   const int lo = (int)((long long)groups * r / CLUSTER) * 4;
   const int hi = (int)((long long)groups * (r + 1) / CLUSTER) * 4;
   return Slice{min(lo, P), min(hi, P)};
@@ -145,7 +145,7 @@ __device__ __forceinline__ void list_pages(const int32_t* refs, Slice s, int bas
 // The `need` lowest free pages into p.list (as many as there are); returns how many there
 // are in the whole pool.  Ends with a cluster barrier.
 __device__ __forceinline__ int find_free(const MapParams& p, int need, Shared& sh) {
-  const Slice s = slice_of(p.P);
+  const Slice s = slice_of(p.P, cluster_rank());
   auto is_free = [](int, int refs) { return refs <= 0 ? 1 : 0; };
   const int mine = count_pages(p.refs, s, is_free, sh);
   if (threadIdx.x == 0) sh.count[0] = mine;
@@ -330,36 +330,36 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, 1)
   griddep_launch_dependents();
   const int tid = threadIdx.x;
   const uint32_t cta = cluster_rank();
-  const Slice s = slice_of(p.P);
+  const Slice s = slice_of(p.P, cluster_rank());
   const int mine = count_pages(p.refs, s, [](int, int r) { return r > 0 ? 1 : 0; }, sh);
   if (tid == 0) sh.count[0] = mine;
   cluster_sync();
-  int used = 0;
-#pragma unroll
-  for (int r = 0; r < CLUSTER; ++r) used += ld_cluster(&sh.count[0], r);
-  // holes: free pages below `used`; movers: pages in use from there on; as many of both
-  auto is_hole = [used](int page, int r) { return page < used && r <= 0 ? 1 : 0; };
-  auto is_mover = [used](int page, int r) { return page >= used && r > 0 ? 1 : 0; };
-  const int holes = count_pages(p.refs, s, is_hole, sh);
-  const int movers = count_pages(p.refs, s, is_mover, sh);
-  cluster_sync();  // count[0] has been read by all
-  if (tid == 0) {
-    sh.count[0] = movers;
-    sh.count[1] = holes;
-  }
-  cluster_sync();
-  int holes_before = 0, movers_before = 0, total = 0;
+  int count[CLUSTER], used = 0, before = 0;
 #pragma unroll
   for (int r = 0; r < CLUSTER; ++r) {
-    const int h = ld_cluster(&sh.count[1], r), m = ld_cluster(&sh.count[0], r);
-    if (r < (int)cta) {
-      holes_before += h;
-      movers_before += m;
-    }
-    total += m;
+    count[r] = ld_cluster(&sh.count[0], r);
+    used += count[r];
+    if (r < (int)cta) before += count[r];
   }
-  list_pages(p.refs, s, holes_before, total, p.list, is_hole, sh);
-  list_pages(p.refs, s, movers_before, total, p.list2, is_mover, sh);
+  // holes: free pages below `used`; movers: pages in use from there on; as many of both.  With
+  // the pages in use below `used` counted too (the slice that `used` cuts is counted by every CTA),
+  // a page's number and the pages in use before it give its rank in either list.
+  int below = 0;
+  Slice cut = {0, 0};
+#pragma unroll
+  for (int r = 0; r < CLUSTER; ++r) {
+    const Slice t = slice_of(p.P, r);
+    if (t.hi <= used) below += count[r];
+    else if (t.lo < used) cut = Slice{t.lo, used};
+  }
+  if (cut.lo < cut.hi) below += count_pages(p.refs, cut, [](int, int r) { return r > 0 ? 1 : 0; }, sh);
+  const int total = used - below;
+  if (s.lo < used)
+    list_pages(p.refs, Slice{s.lo, min(s.hi, used)}, s.lo - before, total, p.list,
+               [](int, int r) { return r <= 0 ? 1 : 0; }, sh);
+  if (s.hi > used)
+    list_pages(p.refs, s, s.lo < used ? 0 : before - below, total, p.list2,
+               [used](int page, int r) { return page >= used && r > 0 ? 1 : 0; }, sh);
   cluster_sync();
   // the moves, and where each page from `used` on goes: list2[page], behind the movers' list
   // (there are at most `used` of them); a page that nobody holds stays

@@ -708,31 +708,40 @@ __device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int x, i
 }
 
 // A tile of codes (128-byte swizzled rows of 128 codes) into a tile of binary16 (two boxes of 64
-// channels) by 128 threads: 8 lanes a row, 16 codes each, rows t / 8 + 16 i.
-constexpr int CODE_ROWS = BS / 16;
-__device__ __forceinline__ void load_codes(const uint8_t* code, int t, uint4 (&v)[CODE_ROWS]) {
-  const int r = t >> 3, c = t & 7;
+// channels) by 128 threads, 16 codes at a time: a warp has one of the boxes, eight rows at a time,
+// four lanes a row.  Eight lanes have rows r and r ^ 5, whose 16-byte words are in different banks
+// both as codes (bit 2) and as binary16 (bit 0).
+constexpr int CODE_WORDS = BS / 16;
+struct CodeLane {
+  int row, from, to;  // first row (the others are 16 apart), bytes into the tiles
+  __device__ __forceinline__ explicit CodeLane(int t) {
+    const int box = t >> 5 & 1, c = t & 3, r = (t >> 3 & 3) ^ (t >> 2 & 1) * 5;
+    row = (t >> 6) * 8 + r;
+    from = row * 128 + (((box * 4 + c) ^ r) << 4);
+    to = box * BOX + row * 128 + (((2 * c) ^ r) << 4);
+  }
+};
+__device__ __forceinline__ void load_codes(const uint8_t* code, CodeLane at, uint4 (&v)[CODE_WORDS]) {
 #pragma unroll
-  for (int i = 0; i < CODE_ROWS; ++i)
-    v[i] = *reinterpret_cast<const uint4*>(code + (r + 16 * i) * 128 + ((c ^ (r & 7)) << 4));
+  for (int i = 0; i < CODE_WORDS; ++i)
+    v[i] = *reinterpret_cast<const uint4*>(code + at.from + i * (16 * 128));
 }
-// Rows from `valid` on become zeros.  The upper four lanes of a row write their second half first,
-// so that the eight are in different banks (the boxes lie a multiple of 128 bytes apart).
-__device__ __forceinline__ void store_codes(uint8_t* tile, int valid, int t, const uint4 (&v)[CODE_ROWS]) {
-  const int r = t >> 3, c = t & 7;
-  const bool up = c >> 2;
-  uint8_t* to = tile + (c >> 2) * BOX + r * 128;
-  const int a = (((c & 3) * 2 + up) ^ (r & 7)) << 4, b = a ^ 16;
+// Rows from `valid` on become zeros.
+__device__ __forceinline__ void store_codes(uint8_t* tile, int valid, CodeLane at,
+                                            uint4 (&v)[CODE_WORDS]) {
+  if (valid < BS) {
 #pragma unroll
-  for (int i = 0; i < CODE_ROWS; ++i) {
-    uint4 w = v[i];
-    if (r + 16 * i >= valid) w = make_uint4(0, 0, 0, 0);
-    const uint2 first = up ? make_uint2(w.z, w.w) : make_uint2(w.x, w.y);
-    const uint2 last = up ? make_uint2(w.x, w.y) : make_uint2(w.z, w.w);
-    *reinterpret_cast<uint4*>(to + i * (16 * 128) + a) =
-        make_uint4(f8x2_lo(first.x), f8x2_hi(first.x), f8x2_lo(first.y), f8x2_hi(first.y));
-    *reinterpret_cast<uint4*>(to + i * (16 * 128) + b) =
-        make_uint4(f8x2_lo(last.x), f8x2_hi(last.x), f8x2_lo(last.y), f8x2_hi(last.y));
+    for (int i = 0; i < CODE_WORDS; ++i)
+      if (at.row + 16 * i >= valid) v[i] = make_uint4(0, 0, 0, 0);
+  }
+  uint8_t* to = tile + at.to;
+  uint8_t* to2 = tile + (at.to ^ 16);
+#pragma unroll
+  for (int i = 0; i < CODE_WORDS; ++i) {
+    *reinterpret_cast<uint4*>(to + i * (16 * 128)) =
+        make_uint4(f8x2_lo(v[i].x), f8x2_hi(v[i].x), f8x2_lo(v[i].y), f8x2_hi(v[i].y));
+    *reinterpret_cast<uint4*>(to2 + i * (16 * 128)) =
+        make_uint4(f8x2_lo(v[i].z), f8x2_hi(v[i].z), f8x2_lo(v[i].w), f8x2_hi(v[i].w));
   }
 }
 
@@ -960,7 +969,7 @@ __global__ void __launch_bounds__(Config<F8>::threads, 1)
     }
   } else if (F8 && warp >= SOFT_WARPS + 4) {
     // ============================ codes to binary16 ============================
-    const int t = tid - (SOFT_WARPS + 4) * 32;
+    const CodeLane at(tid - (SOFT_WARPS + 4) * 32);
     bool ok = true;
 #pragma unroll 1
     for (int e = 0; e < 2 * all_steps && ok; ++e) {
@@ -968,13 +977,13 @@ __global__ void __launch_bounds__(Config<F8>::threads, 1)
       ok = mbar_wait_warp(code_full + 8 * c, ring_parity<CODES>(e), p.status);
       if (!ok) break;
       const int valid = ms.step[(e >> 1) % STEPS_AHEAD].valid, slot = ms.step[(e >> 1) % STEPS_AHEAD].slot;
-      uint4 v[CODE_ROWS];  // (the next load need not wait for the entry's last use)
-      load_codes(codes + c * CODE_TILE, t, v);
+      uint4 v[CODE_WORDS];  // (the next load need not wait for the entry's last use)
+      load_codes(codes + c * CODE_TILE, at, v);
       __syncwarp();
       if (lane == 0) mbar_arrive(code_empty + 8 * c);
       if (use<F8>(e) > 0) ok = mbar_wait_warp(empty + 8 * st, ~use<F8>(e) & 1, p.status);
       if (!ok) break;
-      store_codes(smem + (SLOTS + st) * TILE, valid, t, v);
+      store_codes(smem + (SLOTS + st) * TILE, valid, at, v);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(full + 8 * (ENTRIES * slot + st));
