@@ -11,7 +11,18 @@
 //   plan     one CTA: members of each group (sequences that hold the whole prefix; a group
 //            of one shares nothing), row tiles, and each CTA's first block.
 //   attend   one persistent CTA an SM over equal shares of all blocks.
-//   combine  a warp a row.
+//   combine  a warp for 8 rows and 16 channels.
+// Rows of the tensor-core steps (M = 128) are the queries of a group, as the G <= 8 queries of one
+// sequence fill an eighth of the smallest tile and every sequence would read the prefix anew.
+//
+// What bounds it.  64 sequences of 4 queries a K/V head (8) behind 32K tokens, 270 MB: 89 us, of which
+// plan 3, attend 77, combine 5.  Where two tiles of rows share their blocks the tensor cores do: a
+// block is 24 products of K = 16 a tile (8 for S, 16 for P in two parts), 2100 cycles where they
+// alone would take 1580 (S reads Q and K from shared memory at its full rate, beside which tiles
+// land); behind the prefix it is HBM (6.5 TB/s).  8 groups of 9 behind 16K tokens, 268 MB: 60 us, HBM
+// (5.3 TB/s while attend runs; a slot's chain of S, softmax, P V is about 5000 cycles a block, and
+// CTAs end 20% apart).  4 samples of a prompt of 1K tokens: 18 us, three launches of dependent loads
+// and cold code.
 #include <cstring>
 
 #include "kt_internal.cuh"
@@ -235,7 +246,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constan
   const int pairs = groups.x >> 16, singles = groups.x & 0xffff;
   if (tid == 0)
     *p.head = Head{pairs,         groups.y * p.H_kv,           (groups.y + pairs) * p.H_kv,
-                   singles + p.B, (groups.z + seqs.y) * p.H_kv, (groups.z + singles + seqs.y + seqs.z) * p.H_kv};
+                   singles + p.B, (groups.z + seqs.y) * p.H_kv,
+                   (groups.z + singles + seqs.y + seqs.z) * p.H_kv};
   // items and rows; an item's cost is its blocks and one for its run
 #pragma unroll 1
   for (int i = tid; i < most; i += threads) {
@@ -358,7 +370,7 @@ __device__ __noinline__ Start find_start(const Item* items, const int* cost, int
 // warp 11 fetches the queries of the next run of blocks.  A run of up to 64 rows takes one
 // half of the slot's 128 in turn with the next one, so that its queries come while the other
 // half's are in use.  (Two threads a row have 104 registers each for half an output row and a
-// chunk of scores, and spill: 4400 cycles a softmax instead of TBD.)
+// chunk of scores, and spill: 4400 cycles a softmax instead of 1900.)
 //
 // A slot's block: S (TMEM, 128 columns) = Q K^T; the row threads turn it into P, which goes
 // where the last block's output was; O = P V takes the place of S; the row threads add it to
@@ -370,8 +382,9 @@ __device__ __noinline__ Start find_start(const Item* items, const int* cost, int
 // (alpha then scales what was summed before).  Where there is no maximum yet it is taken first.
 //
 // P is held as two binary16, 2^8 p = hi - lo (22 bits; steps of at least 2^-24), and
-// P V as two products (the tensor cores negate lo): with one alone the output would be good to 11 bits only, and it is
-// binary32.  For 16 tokens, the K of a tensor-core step, columns 0-7 are hi, 8-15 lo.
+// P V as two products (the tensor cores negate lo): with one alone the output would be good to 11
+// bits only, and it is binary32.  For 16 tokens, the K of a tensor-core step, columns 0-7 are hi,
+// 8-15 lo.
 //
 // A items (two tiles of rows over the same blocks) go through both slots at once, each K/V
 // tile read once; with B items the slots are on their own, each with its own share.
@@ -388,13 +401,15 @@ constexpr int UNITS = 4;
 constexpr int STEPS_AHEAD = 8;  // steps described: more than the rings hold
 
 // The 8-bit cache: its codes arrive in a ring of their own, and four more warps (12-15) turn each
-// tile into a binary16 one in the ring that the tensor cores read.  Two tiles of codes are all
-// that the shared memory has room for beside four of binary16 (with three, a slot's next K waits
-// for its V), so the tiles after them are fetched into L2 ahead of their loads.
+// tile into a binary16 one in the ring that the tensor cores read.  Two tiles of codes are all that
+// the shared memory has room for beside four of binary16, so one more waits in those warps'
+// registers for the end of its entry's last use, and the tiles after them are fetched into L2 ahead
+// of their loads (32 sequences behind 128K tokens: 164 us with the codes left in shared memory until
+// then, 142 with one tile in registers, and 142 with three entries and four tiles of codes).
 template <bool F8>
 struct Config {
-  static constexpr int entries = F8 ? 3 : 5;  // K or V tiles that the tensor cores read
-  static constexpr int codes = F8 ? 4 : 0;    // tiles of codes
+  static constexpr int entries = F8 ? 4 : 5;  // K or V tiles that the tensor cores read
+  static constexpr int codes = F8 ? 2 : 0;    // tiles of codes
   static constexpr int threads = (SOFT_WARPS + (F8 ? 8 : 4)) * 32;
   // Registers pass from the other warps to the row threads: three (four) warpgroups are launched
   // with launch_regs a thread (the host checks that), and the shares must not add up to more.
@@ -566,7 +581,7 @@ __device__ __forceinline__ void regs_dec() {
 
 // The softmax runs over chunks of 16 columns, the next one's load in flight, two a turn of the
 // loop: eight in a row are ten kilobytes of code, which every launch fetches anew (3300 cycles
-// for its first block instead of TBD).
+// for its first block instead of 2500).
 //
 // A row's largest score (columns from taddr on).
 template <bool MASK>
@@ -676,17 +691,6 @@ __device__ __forceinline__ void advance(Walk& w, int run, int heads) {
   } while (w.it.blocks == 0);
 }
 
-// Where the n-th tile goes, and how many tiles have gone there before.  (8-bit: one entry for K,
-// two for V, so that no K waits for the end of a P V.)
-template <bool F8>
-__device__ __forceinline__ int place(int n) {
-  return F8 ? (n & 1) + (n & n >> 1 & 1) : n % Config<F8>::entries;
-}
-template <bool F8>
-__device__ __forceinline__ int use(int n) {
-  return F8 ? n >> 1 >> (n & 1) : n / Config<F8>::entries;
-}
-
 // First ring entry of slot s's B step k (K; V is the next one), behind `a` A steps: the
 // slots' steps take turns as long as both have some.
 __device__ __forceinline__ int entry_b(int s, int k, int a, int other) {
@@ -753,7 +757,8 @@ __device__ __forceinline__ void load_queries(const Params& p, const Item& it, in
 #pragma unroll
   for (int j = 0; j < ROWS / 32; ++j) {
     const int i = min(j * 32 + lane, rows - 1);
-    at[j] = (it.member >= 0 ? __ldcg(p.q_rows + it.member + off + i) : it.seq * p.H_kv * p.G + i) + head * p.G;
+    at[j] = (it.member >= 0 ? __ldcg(p.q_rows + it.member + off + i) : it.seq * p.H_kv * p.G + i) +
+            head * p.G;
   }
   const int c = lane & 15, odd = lane >> 4;
   const char* src = reinterpret_cast<const char*>(p.q) + c * 16;
@@ -862,7 +867,7 @@ __global__ void __launch_bounds__(Config<F8>::threads, 1)
         if (bad) set_status(p.status, KT_ERR_DEVICE_CHECK);
         ms.step[(e >> 1) % STEPS_AHEAD] =
             Step{bad, bad ? 0 : min(BS, valid), bad ? 1.0f : ks, bad ? 0.0f : vs, slot,
-                 (slot ? used[1] : used[0]) >> place<F8>(e + 1) & 1u};
+                 (slot ? used[1] : used[0]) >> ((e + 1) % ENTRIES) & 1u};
       }
 #pragma unroll 1
       for (int side = 0; side < 2 && ok; ++side, ++e) {
@@ -872,7 +877,7 @@ __global__ void __launch_bounds__(Config<F8>::threads, 1)
         if (e >= RING)
           ok = mbar_wait_warp((F8 ? code_empty : empty) + 8 * st, ring_parity<RING>(e) ^ 1, p.status);
         if (!ok) break;
-        const uint32_t bit = 1u << place<F8>(e);
+        const uint32_t bit = 1u << (e % ENTRIES);
         if (slot) used[1] ^= bit, last |= bit;
         else used[0] ^= bit, last &= ~bit;
         if (lane == 0) {
@@ -963,7 +968,8 @@ __global__ void __launch_bounds__(Config<F8>::threads, 1)
       if (F8) {
         mbar_wait_warp(code_full + 8 * st, ring_parity<RING>(i), p.status);
       } else {
-        mbar_wait_warp(full + 8 * (ENTRIES * slot + st), ((slot ? used[1] : used[0]) >> st & 1u) ^ 1u, p.status);
+        const uint32_t parity = ((slot ? used[1] : used[0]) >> st & 1u) ^ 1u;
+        mbar_wait_warp(full + 8 * (ENTRIES * slot + st), parity, p.status);
         mbar_wait_warp(empty + 8 * st, ring_parity<RING>(i), p.status);
       }
     }
@@ -973,15 +979,16 @@ __global__ void __launch_bounds__(Config<F8>::threads, 1)
     bool ok = true;
 #pragma unroll 1
     for (int e = 0; e < 2 * all_steps && ok; ++e) {
-      const int c = e % CODES, st = place<F8>(e);
+      const int c = e % CODES, st = e % ENTRIES;
       ok = mbar_wait_warp(code_full + 8 * c, ring_parity<CODES>(e), p.status);
       if (!ok) break;
-      const int valid = ms.step[(e >> 1) % STEPS_AHEAD].valid, slot = ms.step[(e >> 1) % STEPS_AHEAD].slot;
+      const Step& step = ms.step[(e >> 1) % STEPS_AHEAD];
+      const int valid = step.valid, slot = step.slot;
       uint4 v[CODE_WORDS];  // (the next load need not wait for the entry's last use)
       load_codes(codes + c * CODE_TILE, at, v);
       __syncwarp();
       if (lane == 0) mbar_arrive(code_empty + 8 * c);
-      if (use<F8>(e) > 0) ok = mbar_wait_warp(empty + 8 * st, ~use<F8>(e) & 1, p.status);
+      if (e >= ENTRIES) ok = mbar_wait_warp(empty + 8 * st, ring_parity<ENTRIES>(e) ^ 1, p.status);
       if (!ok) break;
       store_codes(smem + (SLOTS + st) * TILE, valid, at, v);
       fence_proxy_async_smem();
@@ -989,9 +996,8 @@ __global__ void __launch_bounds__(Config<F8>::threads, 1)
       if (lane == 0) mbar_arrive(full + 8 * (ENTRIES * slot + st));
     }
 #pragma unroll 1
-    for (int e = max(0, 2 * all_steps - 4); e < 2 * all_steps; ++e)
-      if (e >= 2 * all_steps - 2 || (e & 1)) // the last K, the last two V
-        mbar_wait_warp(empty + 8 * place<F8>(e), use<F8>(e) & 1, p.status);
+    for (int e = max(0, 2 * all_steps - ENTRIES); e < 2 * all_steps; ++e)
+          mbar_wait_warp(empty + 8 * (e % ENTRIES), ring_parity<ENTRIES>(e), p.status);
   } else if (warp == SOFT_WARPS + 3) {
     // ============================ runs and their queries ============================
     Walk w[SLOTS];
@@ -1028,7 +1034,7 @@ __global__ void __launch_bounds__(Config<F8>::threads, 1)
             unit.row0 = row0;
             unit.run = run;
             unit.tokens = it.tokens - w[s].block * BS;
-            unit.part = a ? ((long long)cta + (long long)w[s].item * p.H_kv + w[s].head) * (2 * ROWS) + off
+            unit.part = a ? (cta + (long long)w[s].item * p.H_kv + w[s].head) * (2 * ROWS) + off
                           : p.rows_a + (long long)b_worker(p, s) * p.row_max + it.row_base +
                                 (long long)w[s].head * it.rows;
           }
@@ -1068,7 +1074,7 @@ __global__ void __launch_bounds__(Config<F8>::threads, 1)
     // S = Q K^T of slot s's step k, once K, the run's Q and the end of the last P V are there;
     // n counts the runs begun, left the steps of the one at hand
     auto scores = [&](int s, int k, int e, bool both, int& n, int& left) {
-      const int ek = place<F8>(e);
+      const int ek = e % ENTRIES;
       if (left == 0) {
         ok = ok && mbar_wait_warp(q_full + 8 * (UNITS * s + n % UNITS), (n / UNITS) & 1, p.status);
         left = uniform(ms.unit[s][n % UNITS].run);
@@ -1097,7 +1103,7 @@ __global__ void __launch_bounds__(Config<F8>::threads, 1)
     };
     // O = P V, the high and the low parts of P
     auto values = [&](int s, int k, int e, bool both) {
-      const int ev = place<F8>(e);
+      const int ev = e % ENTRIES;
       ok = ok && mbar_wait_warp(tiles + 8 * ev, used >> ev & 1u, p.status) &&
            mbar_wait_warp(p_full + 8 * s, k & 1, p.status);
       if (!ok) return;
@@ -1195,7 +1201,7 @@ __global__ void __launch_bounds__(Config<F8>::threads, 1)
         tc_fence_after();
         if (!F8 && valid < BS) {
           // V behind the last token may be anything, and 0 * NaN is NaN: zeros there
-          const int ev = place<F8>(e + 1);
+          const int ev = (e + 1) % ENTRIES;
           ok = mbar_wait_warp(full + 8 * ((k < na ? 0 : ENTRIES * s) + ev), step->v_parity, p.status);
           if (!ok) break;
           uint8_t* v = smem + SLOTS * TILE + ev * TILE;
@@ -1308,19 +1314,25 @@ __global__ void __launch_bounds__(Config<F8>::threads, 1)
 
 // ---- combine -----------------------------------------------------------------------------
 // A warp takes 8 rows (consecutive ones of the batch, which mostly are of a tile too) and 16
-// channels: its 8 x 16 bytes of a part's channel group are contiguous.
+// channels: its 8 x 16 bytes of a part's channel group are contiguous.  A row of a long prefix has
+// a part for each CTA that met it (some 20 at 32K tokens): 16 of them in flight at a time (with 8,
+// and the rest one by one, 32 sequences behind 128K tokens took 14 us here instead of 5).  It is
+// bound by two round trips to L2: one behind the plan's data, which are read while attend ends, one
+// for the parts.
 constexpr int COMBINE_WARPS = 8;
 constexpr int COMBINE_ROWS = 8;
 constexpr int COMBINE_BATCH = 16;  // parts in flight
 
-__global__ void __launch_bounds__(COMBINE_WARPS * 32, 2) combine_kernel(const __grid_constant__ Params p) {
-  // What the plan says was there before the kernel ahead let this one start.
+__global__ void __launch_bounds__(COMBINE_WARPS * 32, 2)
+    combine_kernel(const __grid_constant__ Params p) {
+  // What the plan says is read before the kernel ahead has ended: that one waited for the plan to
+  // end before it let this one start.
   const int lane = threadIdx.x & 31, all_rows = p.B * p.G;
   const int chunks = (all_rows + COMBINE_ROWS - 1) / COMBINE_ROWS;
   const int job = blockIdx.x * COMBINE_WARPS + (threadIdx.x >> 5);
   const int h = job / (chunks * 8), col = job % 8 * 4 + (lane >> 3);  // channels 4 col .. + 3
   const int row = job / 8 % chunks * COMBINE_ROWS + (lane & 7);
-  if (h >= p.H_kv || row >= all_rows) return;  // (its share of the grid's dependence ends with it)
+  if (h >= p.H_kv || row >= all_rows) return;
   const int b = row / p.G, g = row % p.G;
   const Head head = load_head(p.head);
   const int4 sp4 = __ldcg(reinterpret_cast<const int4*>(p.seqs + b));
@@ -1341,7 +1353,8 @@ __global__ void __launch_bounds__(COMBINE_WARPS * 32, 2) combine_kernel(const __
   Item it = load_item((a ? p.items_a : p.items_b) + item), own = load_item(p.items_b + sp.item);
   int cost = __ldcg((a ? p.cost_a : p.cost_b) + item);
   const int own_cost = __ldcg(p.cost_b + sp.item);
-  const Shares shares_a(p.ctas, head.steps_a, head.cost_a), shares_b(p.ctas * SLOTS, head.steps_b, head.cost_b);
+  const Shares shares_a(p.ctas, head.steps_a, head.cost_a);
+  const Shares shares_b(p.ctas * SLOTS, head.steps_b, head.cost_b);
   griddep_wait();
   griddep_launch_dependents();
 #pragma unroll 1
@@ -1523,7 +1536,8 @@ cudaError_t launch_prefix(const PrefixLaunch& a, cudaStream_t stream) {
   threads = threads < 64 ? 64 : threads < PLAN_THREADS ? (threads + 31) & ~31 : PLAN_THREADS;
   e = launch(plan_kernel, p, 1, threads, sizeof(PlanShared), stream);
   if (e != cudaSuccess) return e;
-  e = a.k_scale ? launch(attend_kernel<true>, p, p.ctas, Config<true>::threads, smem_bytes<true>(), stream)
+  e = a.k_scale ? launch(attend_kernel<true>, p, p.ctas, Config<true>::threads, smem_bytes<true>(),
+                         stream)
                 : launch(attend_kernel<false>, p, p.ctas, Config<false>::threads, smem_bytes<false>(),
                          stream);
   if (e != cudaSuccess) return e;
