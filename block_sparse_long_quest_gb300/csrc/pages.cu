@@ -7,9 +7,10 @@
 // needs a page takes the r-th free page).  What bounds it is the latency of the passes that
 // wait for one another, so each call is one cluster of CLUSTER CTAs: every CTA counts its
 // slice of the pages, the counts meet in shared memory of the cluster, and the barriers
-// between the passes are the cluster's (under 1 us) instead of launches: a fork is 5 to 6 us for 4
-// samples as for 48 or for 16 of 131K tokens, a compaction 9 us for 300 pages, 11 for 8K.  Ranks
-// follow page and request numbers, so the outcome does not depend on which CTA comes first.
+// between the passes are the cluster's (under 1 us) instead of launches: in a graph a turnover (old
+// samples freed, new ones forked) is 6.5 us for 4 samples, 8.9 for 48 and 12.5 for 16 of 131K tokens,
+// a reservation 3.5, a compaction 8 for 300 pages as for 8K.  Ranks follow page and request
+// numbers, so the outcome does not depend on which CTA comes first.
 #include <cstring>
 
 #include "kt_internal.cuh"
@@ -415,7 +416,7 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, 1)
 // (scales of few heads) in 4-byte words.
 // Bound by HBM: the 2.1 GB that compacting 8K pages of two layers moves take 345 us, 6.1 TB/s of
 // 6.7 that a plain copy reaches; the 0.96 GB of an 8-bit pool 150 us, 6.4.  A few pages (a fork's last
-// blocks) take 4.5 us: a launch and three dependent loads.
+// blocks) take 3 us: a launch and three dependent loads.
 constexpr int COPY_UNIT = 4096;
 constexpr int COPY_THREADS = 512;
 
