@@ -23,6 +23,7 @@
 // (5.3 TB/s while attend runs; a slot's chain of S, softmax, P V is about 5000 cycles a block, and
 // CTAs end 20% apart).  4 samples of a prompt of 1K tokens: 18 us, three launches of dependent loads
 // and cold code.
+#include <cfloat>
 #include <cstring>
 
 #include "kt_internal.cuh"
@@ -278,7 +279,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constan
         sp.single = sh.group_at[g].x & 0xffff;
 #pragma unroll 1
         for (int j = 0; j < p.G; ++j) p.q_rows[at.x * p.G + j] = i * p.H_kv * p.G + j;
-        if (sp.r0 == 0) sh.group[sh.cu[g]] = i;  // its first member, for its items
+        // its first member, for its items (a sequence that is no member does not use its place)
+        if (sp.r0 == 0) sh.group[sh.cu[g]] = i;
       }
       p.seqs[i] = sp;
     }
@@ -1214,7 +1216,7 @@ __global__ void __launch_bounds__(Config<F8>::threads, 1)
         if (step->bad) valid = 0;
         float scale = p.scale_log2, v_scale = 1.0f;
         if (F8) {
-          scale *= step->k_scale;
+          scale = fmaxf(scale * step->k_scale, FLT_MIN);  // (0 times a masked score is no number)
           v_scale = step->v_scale;
         }
         const float2 scale2 = make_float2(scale, scale);

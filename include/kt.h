@@ -471,7 +471,7 @@ typedef struct {
  * tables are read on the device, so a captured call follows their changes.
  * Workspace: KT_OP_PREFIX_ATTN of the same shapes; the call uses its header and its last bytes,
  * so ws_bytes is the size kt_workspace_bytes reported (a workspace of that size also serves the
- * other calls with the parameters it was sized for).  At most 192 CTAs are used.
+ * other calls with the parameters it was sized for).  The attention runs on at most 192 CTAs.
  */
 kt_status kt_prefix_decode_attn(const void* q, const kt_paged_kv* kv,
                                 const kt_prefix_groups* groups, int32_t num_q_heads,

@@ -304,6 +304,14 @@ def test_scales_at_their_ends(kt, k, v):
     run(kt, b)
 
 
+def test_scale_that_leaves_nothing_of_the_scores(kt):
+    """The product of both scales is below binary32: every token weighs the same."""
+    b = Batch([(2, [5, 77, 200])], 2, 4, seed=12, cache="f8")
+    b.ks[:] = 2.0 ** -30
+    b.decode()
+    run(kt, b, scale=1e-42)
+
+
 @pytest.mark.parametrize("value", [float("nan"), float("inf"), -65504.0])
 def test_rows_behind_the_end_may_be_anything(kt, value):
     b = Batch(groups=[(3, [1, 64, 127, 130]), (0, [100])], heads=2, group=4)
