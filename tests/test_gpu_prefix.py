@@ -379,6 +379,49 @@ def test_the_same_every_time_and_on_other_streams(kt, cache):
         assert torch.equal(b.out, first)
 
 
+def test_two_calls_at_once(kt):
+    """On two streams, each with its own workspace, many calls in flight."""
+    batches = [Batch(groups=[(30, [i % 5 for i in range(90)])], heads=2, group=3),
+               Batch(groups=[(40, [20, 300, 129] * 5), (7, [5] * 20)], heads=4, group=4, cache="f8")]
+    firsts = []
+    for b in batches:
+        run(kt, b)
+        firsts.append(b.out.clone())
+    streams = [torch.cuda.Stream() for _ in batches]
+    torch.cuda.synchronize()
+    for b in batches:
+        b.out.fill_(3.0)
+    torch.cuda.synchronize()
+    for _ in range(200):
+        for b, stream in zip(batches, streams):
+            b.call(kt, stream=stream)
+    torch.cuda.synchronize()
+    for b, first in zip(batches, firsts):
+        assert kt.kt_read_device_status(b.ws) == kt.KT_OK
+        assert torch.equal(b.out, first)
+
+
+@CACHES
+def test_calls_in_a_row_share_a_workspace(kt, cache):
+    """Other groups, lengths and outputs from one call to the next, no wait between them."""
+    shapes = [[(12, [20, 300, 129, 5]), (0, [7, 900])], [(1, [2000]), (3, [1, 2, 3, 4, 5])],
+              [(0, [0, 1, 128, 129, 500, 10])]]
+    batches = [Batch(groups=g, heads=2, group=4, seed=i, cache=cache) for i, g in enumerate(shapes)]
+    for b in batches:
+        run(kt, b)
+    firsts = [b.out.clone() for b in batches]
+    ws = max((b.ws for b in batches), key=lambda w: w.numel())
+    for b in batches:
+        b.ws = ws
+    for _ in range(50):
+        for b in batches:
+            b.call(kt)
+    torch.cuda.synchronize()
+    assert kt.kt_read_device_status(ws) == kt.KT_OK
+    for b, first in zip(batches, firsts):
+        assert torch.equal(b.out, first)
+
+
 @CACHES
 def test_captured_call_follows_its_inputs(kt, cache):
     """Lengths, groups and queries change between replays; a second graph shares the workspace."""
