@@ -21,7 +21,7 @@
 // alone would take 1580 (S reads Q and K from shared memory at its full rate, beside which tiles
 // land); behind the prefix it is HBM (6.5 TB/s).  8 groups of 9 behind 16K tokens, 268 MB: 60 us, HBM
 // (5.3 TB/s while attend runs; a slot's chain of S, softmax, P V is about 5000 cycles a block, and
-// CTAs end 20% apart).  4 samples of a prompt of 1K tokens: 18 us, three launches of dependent loads
+// CTAs end 20% apart).  4 samples of a prompt of 1K tokens: 17 us, three launches of dependent loads
 // and cold code.
 #include <cfloat>
 #include <cstring>
@@ -311,10 +311,12 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constan
 
 // Equal shares of the cost of all steps, one a block and one a run (its queries, its part: a run
 // of one block takes about twice the time of a block in the middle of a long one), among up to n
-// workers, but no more than there are steps: the first ones have one more than the others.
+// workers: the first ones have one more than the others.  With more workers than cost each has a
+// block or, for a run's own, nothing (4 samples of 1K tokens: 16.9 us; 18.2 with no more workers
+// than blocks, some of which then had two).
 struct Shares {
   int n, each, more;
-  __device__ __forceinline__ Shares(int workers, int steps, int cost) : n(min(workers, steps)) {
+  __device__ __forceinline__ Shares(int workers, int cost) : n(min(workers, cost)) {
     each = n > 0 ? cost / n : 1;
     more = cost - n * each;
   }
@@ -837,7 +839,7 @@ __global__ void __launch_bounds__(Config<F8>::threads, 1)
     const bool a = warp < 2;
     const int n = a ? p.ctas : p.ctas * SLOTS, steps = a ? h.steps_a : h.steps_b;
     const int w = (a ? cta : b_worker(p, (warp >> 1) - 1)) + (warp & 1);
-    const Shares shares(n, steps, a ? h.cost_a : h.cost_b);
+    const Shares shares(n, a ? h.cost_a : h.cost_b);
     const Start st = find_start(a ? p.items_a : p.items_b, a ? p.cost_a : p.cost_b,
                                 a ? h.items_a : h.items_b, shares, steps, w);
     if (lane == 0) ms.start[warp >> 1][warp & 1] = st;
@@ -1355,8 +1357,8 @@ __global__ void __launch_bounds__(COMBINE_WARPS * 32, 2)
   Item it = load_item((a ? p.items_a : p.items_b) + item), own = load_item(p.items_b + sp.item);
   int cost = __ldcg((a ? p.cost_a : p.cost_b) + item);
   const int own_cost = __ldcg(p.cost_b + sp.item);
-  const Shares shares_a(p.ctas, head.steps_a, head.cost_a);
-  const Shares shares_b(p.ctas * SLOTS, head.steps_b, head.cost_b);
+  const Shares shares_a(p.ctas, head.cost_a);
+  const Shares shares_b(p.ctas * SLOTS, head.cost_b);
   griddep_wait();
   griddep_launch_dependents();
 #pragma unroll 1
