@@ -28,8 +28,8 @@ struct MapParams {
   int32_t* blocks;
   int32_t* refs;
   int* status;
-  int32_t* list;   // workspace [num_pages]: free pages by rank, or where pages move to
-  int32_t* list2;  // workspace [num_pages]
+  int32_t* list;   // workspace [num_pages]: free pages by rank; compact: the movers behind them
+  int32_t* list2;  // workspace [num_pages]; compact: where each page goes
   const int32_t* a;  // fork: sources; free: sequences; reserve: new tokens (nullable)
   const int32_t* b;  // fork: destinations
   int32_t* moves;
@@ -359,30 +359,31 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, 1)
   if (s.lo < used)
     list_pages(p.refs, Slice{s.lo, min(s.hi, used)}, s.lo - before, total, p.list,
                [](int, int r) { return r <= 0 ? 1 : 0; }, sh);
+  int32_t* movers = p.list + (p.P - total);  // behind the holes: both lists are at most P / 2
   if (s.hi > used)
-    list_pages(p.refs, s, s.lo < used ? 0 : before - below, total, p.list2,
+    list_pages(p.refs, s, s.lo < used ? 0 : before - below, total, movers,
                [used](int page, int r) { return page >= used && r > 0 ? 1 : 0; }, sh);
   cluster_sync();
-  // the moves, and where each page from `used` on goes: list2[page], behind the movers' list
-  // (there are at most `used` of them); a page that nobody holds stays
+  // the moves, and where each page goes: list2[page], -1 for a page that nobody holds (a hole
+  // becomes another page, so an entry that names it is found here or not at all)
   if (cta == 0 && tid == 0) *p.num_moves = total;
   for (int i = cta * THREADS + tid; i < total; i += CLUSTER * THREADS) {
-    const int from = p.list2[i], to = p.list[i];
+    const int from = movers[i], to = p.list[i];
     p.moves[2 * (size_t)i] = from;
     p.moves[2 * (size_t)i + 1] = to;
     p.list2[from] = to;
   }
-  for (int i = max(s.lo, used) + tid; i < s.hi; i += THREADS)
-    if (p.refs[i] <= 0) p.list2[i] = i;
-  if (p.new_refs != p.refs)
-    for (int i = s.lo + tid; i < s.hi; i += THREADS) {
-      const int r = p.refs[i];
+  for (int i = s.lo + tid; i < s.hi; i += THREADS) {
+    const int r = p.refs[i];
+    if (r <= 0 || i < used) p.list2[i] = r > 0 ? i : -1;
+    if (p.new_refs != p.refs) {
       if (i >= used) p.new_refs[i] = 0;
       else if (r > 0) p.new_refs[i] = r;
     }
+  }
   cluster_sync();
   for (int i = cta * THREADS + tid; i < total; i += CLUSTER * THREADS) {
-    const int from = p.list2[i];
+    const int from = movers[i];
     p.new_refs[p.list[i]] = p.refs[from];
     if (p.new_refs == p.refs) p.refs[from] = 0;
   }
@@ -398,12 +399,9 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, 1)
     if (j >= n) continue;
     const size_t at = (size_t)b * p.max_blocks + j;
     int page = p.table[at];
-    if (page < 0 || page >= p.P) set_status(p.status, KT_ERR_DEVICE_CHECK);
-    else if (page >= used) {
-      const int to = p.list2[page];
-      if (to == page) set_status(p.status, KT_ERR_DEVICE_CHECK);  // counted as free
-      page = to;
-    }
+    const int to = page >= 0 && page < p.P ? p.list2[page] : -1;
+    if (to < 0) set_status(p.status, KT_ERR_DEVICE_CHECK);  // no page, or counted as free
+    else page = to;
     p.new_table[at] = page;
   }
 }
