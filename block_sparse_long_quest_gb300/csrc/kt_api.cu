@@ -136,6 +136,27 @@ WsLayout layout(kt_op op, const kt_paged_kv* kv, const kt_sparse_params* p, int 
   return L;
 }
 
+// First byte of the region of the attention behind shared prefixes.  That call knows the shapes
+// only, and the selection's regions depend on the selection's parameters too, so it lies behind
+// the most that those can take: the other calls' state is never written over, and a workspace of
+// one of them (a smaller one) is refused.  A unit keeps at most ch candidates for each of its
+// chunks of ch blocks, and SEL_MAX_CAND in all (make_sel_plan).  The scratch of the Dynamic build
+// and the preselection may lie at the same place: it holds nothing from one call to the next.
+size_t prefix_offset(const kt_paged_kv* kv, int G) {
+  const size_t S = (size_t)kv->batch * kv->num_kv_heads, blocks = kv->max_blocks_per_seq;
+  const size_t ch = S * blocks / SEL_TARGET_CTAS + 8;
+  const size_t kept = blocks + ch < SEL_MAX_CAND ? blocks + ch : SEL_MAX_CAND;
+  const size_t slots = (size_t)MAX_ATTN_CTAS * FUSED_KK_CAP;
+  const size_t slot_floats = ((2 * G + G * D) + 3) & ~3;
+  return 256 + align256(S * 4) + align256(2 * (MAX_ATTN_CTAS + S) * slot_floats * 4) +
+         align256(S * 4) + align256(S * kept * 8) + align256(S * kept * 4) +
+         align256(S * MAX_TOPK * 4) + 256 + align256(slots * 8) + align256(slots * 4);
+}
+
+size_t prefix_total(const kt_paged_kv* kv, int G) {
+  return prefix_offset(kv, G) + prefix_ws_bytes(kv->batch, kv->num_kv_heads, G);
+}
+
 // ---- TMA tensor maps over the K / V pools ----------------------------------
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
@@ -399,10 +420,8 @@ kt_status kt_workspace_bytes(kt_op op, const kt_paged_kv* kv, const kt_sparse_pa
   }
   if (s != KT_OK) return s;
   if (op == KT_OP_DYNAMIC_REPS && T < 1) return KT_ERR_INVALID_ARG;
-  *bytes = layout(op, kv, p, T).total;
-  // behind the other calls' regions
-  if (op == KT_OP_PREFIX_ATTN)
-    *bytes += prefix_ws_bytes(kv->batch, kv->num_kv_heads, p->num_q_heads / kv->num_kv_heads);
+  *bytes = op == KT_OP_PREFIX_ATTN ? prefix_total(kv, p->num_q_heads / kv->num_kv_heads)
+                                   : layout(op, kv, p, T).total;
   return KT_OK;
 }
 
@@ -987,9 +1006,7 @@ kt_status prefix_impl(const void* q, const kt_paged_kv* kv, const kt_prefix_grou
     return KT_ERR_INVALID_ARG;
   if (!prefix_units_ok(*kv) || groups->groups > MAX_SEGS) return KT_ERR_UNSUPPORTED;
   const int G = num_q_heads / kv->num_kv_heads;
-  // the last bytes of the workspace: what lies before them keeps the other calls' state
-  const size_t need = prefix_ws_bytes(kv->batch, kv->num_kv_heads, G);
-  if (ws_bytes < 256 + need) return KT_ERR_WORKSPACE_TOO_SMALL;
+  if (ws_bytes < prefix_total(kv, G)) return KT_ERR_WORKSPACE_TOO_SMALL;
   CUtensorMap kmap, vmap;
   const bool codes = k_scale != nullptr;  // the 8-bit cache, whose code pools kv holds
   if (!make_pool_map(&kmap, kv->k_pool, kv, codes) || !make_pool_map(&vmap, kv->v_pool, kv, codes))
@@ -1007,7 +1024,7 @@ kt_status prefix_impl(const void* q, const kt_paged_kv* kv, const kt_prefix_grou
   a.prefix = groups->prefix_blocks;
   a.out = out;
   a.status = at<int>(ws, 0);
-  a.ws = at<uint8_t>(ws, (ws_bytes - need) & ~(size_t)255);
+  a.ws = at<uint8_t>(ws, prefix_offset(kv, G));
   a.B = kv->batch;
   a.H_kv = kv->num_kv_heads;
   a.G = G;

@@ -1454,7 +1454,7 @@ PrefixWs prefix_layout(int B, int H_kv, int G) {
   off = align256(off + total_rows * D * 4);
   L.stats = off;
   off = align256(off + total_rows * 8);
-  L.total = off + 256;  // (its start is aligned down)
+  L.total = off;
   return L;
 }
 

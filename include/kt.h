@@ -469,9 +469,10 @@ typedef struct {
  * parts of either sign, so an infinite V value makes its channel of the rows that attend it
  * infinite or NaN.  Three launches.  The groups, lengths and
  * tables are read on the device, so a captured call follows their changes.
- * Workspace: KT_OP_PREFIX_ATTN of the same shapes; the call uses its header and its last bytes,
- * so ws_bytes is the size kt_workspace_bytes reported (a workspace of that size also serves the
- * other calls with the parameters it was sized for).  The attention runs on at most 192 CTAs.
+ * Workspace: KT_OP_PREFIX_ATTN of the same shapes (its size does not depend on the selection's
+ * parameters); smaller ones, such as KT_OP_SPARSE_STEP's, are refused.  One of that size also
+ * serves the decode step, the selection and the other attention calls of these shapes with one
+ * set of parameters, in any order.  The attention runs on at most 192 CTAs.
  */
 kt_status kt_prefix_decode_attn(const void* q, const kt_paged_kv* kv,
                                 const kt_prefix_groups* groups, int32_t num_q_heads,
