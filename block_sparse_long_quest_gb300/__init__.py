@@ -38,7 +38,7 @@ EXPORTS = (
     "kt_selftest_bounded_wait", "kt_sparse_decode_attn_noalloc", "kt_sparse_decode_step_kernels",
     "kt_preselect_mask_words", "kt_preselect_blocks", "kt_score_select_blocks_presel",
     "kt_sparse_decode_step_presel", "kt_decode_history_slots", "kt_decode_layer_action",
-    "kt_decode_layer", "kt_append_kv", "kt_set_max_ctas", "kt_set_phase_stamps",
+    "kt_decode_layer", "kt_append_kv", "kt_append_kv_lens", "kt_set_max_ctas", "kt_set_phase_stamps",
     "kt_sparse_decode_attn_hostkv", "kt_quantize_kv_q8_0", "kt_sparse_decode_attn_q8_0",
     "kt_noalloc_read_status", "kt_selftest_step_timeout", "kt_sparse_decode_step_q8_0",
     "kt_rope_init", "kt_apply_rope", "kt_workspace_bytes_f8", "kt_reps_pool_bytes_f8",
@@ -186,6 +186,8 @@ def _load():
         "kt_decode_layer": (ctypes.c_int, [P(ReusePolicy), i32, i32, vp, P(PagedKV), vp,
                                            P(SparseParams), vp, vp, vp, vp, sz, vp]),
         "kt_append_kv": (ctypes.c_int, [P(PagedKV), P(SparseParams), vp, vp, vp, vp, sz, vp]),
+        "kt_append_kv_lens": (ctypes.c_int, [P(PagedKV), P(SparseParams), vp, vp, vp, vp, vp, sz,
+                                             vp]),
         "kt_set_max_ctas": (ctypes.c_int, [i32]),
         "kt_set_phase_stamps": (ctypes.c_int, [vp, i32]),
         "kt_sparse_decode_attn_hostkv": (ctypes.c_int, [vp, P(PagedKV), P(SparseParams), vp, vp,
@@ -366,6 +368,17 @@ def kt_append_kv(kv, params, k_new, v_new, reps_pool, ws, stream=None):
     _check(lib.kt_append_kv(ctypes.byref(kv), ctypes.byref(params), _ptr(k_new), _ptr(v_new),
                             _ptr(reps_pool), _ptr(ws), ws.numel(), _stream(stream)),
            "kt_append_kv")
+
+
+def kt_append_kv_lens(kv, params, k_new, v_new, new_lens, reps_pool, ws, stream=None):
+    """new_lens: int32 [batch], receives the new lengths while kv's stay."""
+    if new_lens is None:
+        raise KtError(KT_ERR_INVALID_ARG, "kt_append_kv_lens")
+    _check_int32(new_lens, kv.batch, "kt_append_kv_lens")
+    _check(lib.kt_append_kv_lens(ctypes.byref(kv), ctypes.byref(params), _ptr(k_new), _ptr(v_new),
+                                 _ptr(new_lens), _ptr(reps_pool), _ptr(ws), ws.numel(),
+                                 _stream(stream)),
+           "kt_append_kv_lens")
 
 
 def kt_preselect_mask_words(kv):

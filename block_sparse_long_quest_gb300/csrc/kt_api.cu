@@ -14,6 +14,15 @@ namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+struct Bytes {
+  uintptr_t lo, hi;
+};
+Bytes bytes_of(const void* p, size_t n) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+  return Bytes{a, a + n};
+}
+bool overlap(Bytes a, Bytes b) { return a.lo < b.hi && b.lo < a.hi; }
+
 kt_status check_kv(const kt_paged_kv* kv) {
   if (!kv || !kv->k_pool || !kv->v_pool || !kv->block_table || !kv->seq_lens)
     return KT_ERR_INVALID_ARG;
@@ -1101,15 +1110,19 @@ kt_status kt_decode_layer(const kt_reuse_policy* pol, int32_t token_idx, int32_t
   return kt_sparse_decode_attn(q, kv, p, sel, cnt, out, ws, ws_bytes, stream);
 }
 
-kt_status kt_append_kv(const kt_paged_kv* kv, const kt_sparse_params* p, const void* k_new,
-                       const void* v_new, void* reps_pool, void* ws, size_t ws_bytes,
-                       kt_stream_t stream) {
+kt_status kt_append_kv_lens(const kt_paged_kv* kv, const kt_sparse_params* p, const void* k_new,
+                            const void* v_new, int32_t* new_lens, void* reps_pool, void* ws,
+                            size_t ws_bytes, kt_stream_t stream) {
   kt_status s = check_kv(kv);
   if (s != KT_OK) return s;
   s = check_params(kv, p);
   if (s != KT_OK) return s;
   if (!k_new || !v_new || !ws || ws_bytes < 256 || !aligned16(k_new) || !aligned16(v_new) ||
-      !aligned16(ws) || (reps_pool && !aligned16(reps_pool)))
+      !aligned16(ws) || (reps_pool && !aligned16(reps_pool)) || !new_lens ||
+      !aligned16(new_lens))
+    return KT_ERR_INVALID_ARG;
+  if (new_lens != kv->seq_lens && overlap(bytes_of(new_lens, (size_t)kv->batch * 4),
+                                          bytes_of(kv->seq_lens, (size_t)kv->batch * 4)))
     return KT_ERR_INVALID_ARG;
   AppendLaunch a;
   a.k_new = k_new;
@@ -1117,7 +1130,8 @@ kt_status kt_append_kv(const kt_paged_kv* kv, const kt_sparse_params* p, const v
   a.k_pool = const_cast<void*>(kv->k_pool);
   a.v_pool = const_cast<void*>(kv->v_pool);
   a.table = kv->block_table;
-  a.seq_lens = const_cast<int32_t*>(kv->seq_lens);
+  a.seq_lens = kv->seq_lens;
+  a.new_lens = new_lens;
   a.status = at<int>(ws, 0);
   a.B = kv->batch;
   a.H_kv = kv->num_kv_heads;
@@ -1130,7 +1144,7 @@ kt_status kt_append_kv(const kt_paged_kv* kv, const kt_sparse_params* p, const v
   RepsLaunch r;
   r.k_pool = static_cast<const __half*>(kv->k_pool);
   r.table = kv->block_table;
-  r.seq_lens = kv->seq_lens;
+  r.seq_lens = new_lens;
   r.reps = reps_pool;
   r.B = kv->batch;
   r.H_kv = kv->num_kv_heads;
@@ -1142,6 +1156,13 @@ kt_status kt_append_kv(const kt_paged_kv* kv, const kt_sparse_params* p, const v
   r.first_block = -1;
   r.num_blocks = 1;
   return cuda_status(launch_reps(r, (cudaStream_t)stream));
+}
+
+kt_status kt_append_kv(const kt_paged_kv* kv, const kt_sparse_params* p, const void* k_new,
+                       const void* v_new, void* reps_pool, void* ws, size_t ws_bytes,
+                       kt_stream_t stream) {
+  return kt_append_kv_lens(kv, p, k_new, v_new, kv ? const_cast<int32_t*>(kv->seq_lens) : nullptr,
+                           reps_pool, ws, ws_bytes, stream);
 }
 
 // ---- rotary positions, and the 8-bit cache with a scale per block and head ----
@@ -1229,18 +1250,10 @@ kt_status check_rows(const kt_rows* r, int tokens) {
   return KT_OK;
 }
 
-struct Bytes {
-  uintptr_t lo, hi;
-};
-Bytes bytes_of(const void* p, size_t n) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-  return Bytes{a, a + n};
-}
 Bytes rows_bytes(const kt_rows* r, int tokens) {
   const size_t n = (size_t)(tokens - 1) * r->stride + (size_t)r->heads * D;
   return bytes_of(r->data, n * dtype_bytes(r->dtype));
 }
-bool overlap(Bytes a, Bytes b) { return a.lo < b.hi && b.lo < a.hi; }
 Bytes out_bytes(const kt_rows* r, const void* out, int tokens) {
   return bytes_of(out, (size_t)tokens * r->heads * D * 2);
 }

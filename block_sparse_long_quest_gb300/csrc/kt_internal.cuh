@@ -757,7 +757,8 @@ struct AppendLaunch {
   void* k_pool;
   void* v_pool;
   const int32_t* table;
-  int32_t* seq_lens;
+  const int32_t* seq_lens;
+  int32_t* new_lens;  // may be seq_lens
   int* status;
   int B, H_kv, max_blocks, P;
 };

@@ -142,13 +142,14 @@ struct AppendParams {
   uint4* k_pool;       // [P][H_kv][128][16]
   uint4* v_pool;
   const int32_t* table;
-  int32_t* seq_lens;
+  const int32_t* seq_lens;
+  int32_t* new_lens;   // may be seq_lens
   int* status;
   int H_kv, max_blocks, P;
 };
 
 // One decoded token per sequence (CTA b): the K and V rows of every KV head
-// go to row n % 128 of the page of block n / 128, then n becomes n + 1.
+// go to row n % 128 of the page of block n / 128, then the length is n + 1.
 __global__ void __launch_bounds__(THREADS) append_kernel(const __grid_constant__ AppendParams p) {
   const int b = blockIdx.x;
   const int n = p.seq_lens[b];
@@ -156,7 +157,10 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const __grid_constant__
   int page = -1;
   if (n >= 0 && j < p.max_blocks) page = p.table[(size_t)b * p.max_blocks + j];
   if (page < 0 || page >= p.P) {  // no room in the table, or a page outside the pool
-    if (threadIdx.x == 0) set_status(p.status, KT_ERR_DEVICE_CHECK);
+    if (threadIdx.x == 0) {
+      set_status(p.status, KT_ERR_DEVICE_CHECK);
+      if (p.new_lens != p.seq_lens) p.new_lens[b] = n;
+    }
     return;
   }
   const int per = p.H_kv * (D / 8);  // 16-byte chunks of one token's rows
@@ -168,7 +172,7 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const __grid_constant__
     *dst = *src;
   }
   __syncthreads();  // every thread has read seq_lens[b]
-  if (threadIdx.x == 0) p.seq_lens[b] = n + 1;
+  if (threadIdx.x == 0) p.new_lens[b] = n + 1;
 }
 
 __global__ void selftest_wait_kernel(int* status, int spin_limit) {
@@ -217,6 +221,7 @@ cudaError_t launch_append(const AppendLaunch& a, cudaStream_t stream) {
   p.v_pool = static_cast<uint4*>(a.v_pool);
   p.table = a.table;
   p.seq_lens = a.seq_lens;
+  p.new_lens = a.new_lens;
   p.status = a.status;
   p.H_kv = a.H_kv;
   p.max_blocks = a.max_blocks;

@@ -551,6 +551,16 @@ kt_status kt_append_kv(const kt_paged_kv* kv, const kt_sparse_params* p, const v
                        kt_stream_t stream);
 
 /*
+ * kt_append_kv with the new lengths apart: new_lens (int32 [batch], 16-byte aligned) receives them
+ * (of a sequence that is left unchanged the old one) and kv->seq_lens stays, so that the caches of
+ * several layers can be used with one array of lengths; new_lens == kv->seq_lens: as kt_append_kv.
+ * INVALID_ARG where they overlap otherwise.
+ */
+kt_status kt_append_kv_lens(const kt_paged_kv* kv, const kt_sparse_params* p, const void* k_new,
+                            const void* v_new, int32_t* new_lens, void* reps_pool, void* ws,
+                            size_t ws_bytes, kt_stream_t stream);
+
+/*
  * ---- rotary positions ---------------------------------------------------------
  * The queries and keys that every call here takes carry their positions as
  * rotations: at position pos the pair i (i < rotary_dim/2) of a head's first
@@ -782,9 +792,19 @@ kt_status kt_decode_layer_f8(const kt_reuse_policy* pol, int32_t token_idx, int3
  * sequence has length 0 and num_blocks 0.  Free pages are always taken lowest first,
  * requests in the order of the call, so the outcome is the same every time.  Only
  * whole blocks are ever shared, so appending (kt_append_kv, kt_append_kv_f8) writes
- * into pages of one sequence.  batch is at most 2048 (UNSUPPORTED beyond).  Pointers
- * are 16-byte aligned device pointers; calls that share a map, a pool or a workspace
- * must not overlap on the GPU.
+ * into pages of one sequence, as long as that one holds the page of its next token:
+ * a slot that does not (empty, or left without by kt_reserve_pages) and gets a token
+ * all the same has it written to whatever page its table names there.
+ *
+ * One map serves the caches of several layers, which differ in their pools only.  As
+ * an append advances the lengths, the layers of a step leave the new ones apart
+ * (new_lens of kt_append_kv_lens and kt_append_kv_f8): every layer appends with
+ * seq_lens = the map's and new_lens = another int32 [batch], and attends with
+ * seq_lens = that one; behind the last layer it is copied to the map's (or the last
+ * layer appends in place, and attends with the map's).
+ *
+ * batch is at most 2048 (UNSUPPORTED beyond).  Pointers are 16-byte aligned device
+ * pointers; calls that share a map, a pool or a workspace must not overlap on the GPU.
  */
 typedef struct {
   int32_t* block_table;
