@@ -1321,16 +1321,13 @@ __global__ void __launch_bounds__(Config<F8>::threads, 1)
 // channels: its 8 x 16 bytes of a part's channel group are contiguous.  A row of a long prefix has
 // a part for each CTA that met it (some 20 at 32K tokens): 16 of them in flight at a time (with 8,
 // and the rest one by one, 32 sequences behind 128K tokens took 14 us here instead of 5).  It is
-// bound by two round trips to L2: one behind the plan's data, which are read while attend ends, one
-// for the parts.
+// bound by three round trips to L2: the sequence's place in the plan, its items, the parts.
 constexpr int COMBINE_WARPS = 8;
 constexpr int COMBINE_ROWS = 8;
 constexpr int COMBINE_BATCH = 16;  // parts in flight
 
 __global__ void __launch_bounds__(COMBINE_WARPS * 32, 2)
     combine_kernel(const __grid_constant__ Params p) {
-  // What the plan says is read before the kernel ahead has ended: that one waited for the plan to
-  // end before it let this one start.
   const int lane = threadIdx.x & 31, all_rows = p.B * p.G;
   const int chunks = (all_rows + COMBINE_ROWS - 1) / COMBINE_ROWS;
   const int job = blockIdx.x * COMBINE_WARPS + (threadIdx.x >> 5);
@@ -1338,6 +1335,8 @@ __global__ void __launch_bounds__(COMBINE_WARPS * 32, 2)
   const int row = job / 8 % chunks * COMBINE_ROWS + (lane & 7);
   if (h >= p.H_kv || row >= all_rows) return;
   const int b = row / p.G, g = row % p.G;
+  griddep_wait();  // (also what the plan has written can be read from here on only)
+  griddep_launch_dependents();
   const Head head = load_head(p.head);
   const int4 sp4 = __ldcg(reinterpret_cast<const int4*>(p.seqs + b));
   const SeqPlan sp = {sp4.x, sp4.y, sp4.z, sp4.w, __ldcg(&p.seqs[b].single), {0, 0, 0}};
@@ -1359,8 +1358,6 @@ __global__ void __launch_bounds__(COMBINE_WARPS * 32, 2)
   const int own_cost = __ldcg(p.cost_b + sp.item);
   const Shares shares_a(p.ctas, head.cost_a);
   const Shares shares_b(p.ctas * SLOTS, head.cost_b);
-  griddep_wait();
-  griddep_launch_dependents();
 #pragma unroll 1
   for (int turn = sp.r0 >= 0 ? 0 : 1; turn < 2; ++turn) {
     if (turn == 1) {

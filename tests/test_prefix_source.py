@@ -1,0 +1,42 @@
+"""What the kernels of shared pages and shared prefixes promise in an order that no run can show:
+read from their sources."""
+import os
+import re
+
+import pytest
+
+import block_sparse_long_quest_gb300 as kt
+
+CSRC = os.path.join(os.path.dirname(kt.__file__), "csrc")
+
+
+def source(name):
+    with open(os.path.join(CSRC, name)) as f:
+        return re.sub(r"//[^\n]*", "", f.read())  # without comments
+
+
+def kernels(name):
+    """(name, body) of every kernel of a file."""
+    text = source(name)
+    for m in re.finditer(r"__global__", text):
+        at = text.index("{", m.start())
+        head = text[m.start():at]
+        yield re.findall(r"(\w+)\(const __grid_constant__", head)[0], text[at:text.index("\n}\n", at)]
+
+
+# members of the parameters that point to what an earlier kernel may have written
+POINTERS = r"\bp\.(q|k_scale|v_scale|table|seq_lens|cu|prefix|out|status|head|items_a|items_b|cost_a|" \
+           r"cost_b|q_rows|seqs|parts|stats|lens|blocks|refs|list|list2|a|b|moves|num_moves|new_table|" \
+           r"new_refs|base)\b"
+
+
+@pytest.mark.parametrize("name", ["pages.cu", "prefix.cu"])
+def test_nothing_is_read_before_the_wait(name):
+    """These kernels start before the one ahead of them has ended; what that one and its predecessors
+    have written is visible behind the kernel's own wait only."""
+    found = list(kernels(name))
+    assert len(found) == {"pages.cu": 5, "prefix.cu": 3}[name]
+    for kernel, body in found:
+        before = body[:body.index("griddep_wait();")]
+        assert not re.search(POINTERS, before), kernel
+        assert "load_" not in before and "__ldcg" not in before, kernel
