@@ -1246,6 +1246,7 @@ __global__ void __launch_bounds__(Config<F8>::threads, 1)
             break;
           }
           if (h == INFINITY) shift = 0.0f;  // no token yet: all are masked
+          if (round > 0) tmem_wait_st();  // the stores of P are not ordered among themselves
           if (big) {
             sum = valid < BS ? row_exp<true, true>(ts, tp, valid, scale2, shift, s0)
                              : row_exp<false, true>(ts, tp, valid, scale2, shift, s0);

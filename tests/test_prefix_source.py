@@ -40,3 +40,17 @@ def test_nothing_is_read_before_the_wait(name):
         before = body[:body.index("griddep_wait();")]
         assert not re.search(POINTERS, before), kernel
         assert "load_" not in before and "__ldcg" not in before, kernel
+
+
+def attend_body():
+    return dict(kernels("prefix.cu"))["attend_kernel"]
+
+
+def test_probabilities_are_stored_again_behind_a_wait():
+    """Stores to tensor memory are asynchronous and not ordered among themselves: a row's second pass
+    waits for those of the first one, whose columns it writes again."""
+    loop = attend_body()
+    loop = loop[loop.index("for (int round = 0;; ++round)"):]
+    loop = loop[:loop.index("if (round > 0) break;")]
+    wait = loop.index("if (round > 0) tmem_wait_st();")
+    assert wait < loop.index("row_exp<") and "row_exp<" not in loop[:wait]
