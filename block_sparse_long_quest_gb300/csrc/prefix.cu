@@ -1183,7 +1183,9 @@ __global__ void __launch_bounds__(Config<F8>::threads, 1)
       const int q0 = unit.row0 / 32, warps = (unit.row0 + unit.rows + 31) / 32 - q0;
       const int end = k + unit.run;
       if (quarter < q0 || quarter >= q0 + warps) {
-        // no rows here; the warp keeps in step by arriving for each block
+        // no rows here; the warp keeps in step by arriving for each block (behind its loads from
+        // tensor memory of the run before, whose columns the next products write)
+        tc_fence_before();
         for (; k < end && ok; ++k) {
           ok = mbar_wait_warp(s_full + 8 * s, k & 1, p.status);
           if (ok && lane == 0) mbar_arrive(p_full + 8 * s);

@@ -54,3 +54,15 @@ def test_probabilities_are_stored_again_behind_a_wait():
     loop = loop[:loop.index("if (round > 0) break;")]
     wait = loop.index("if (round > 0) tmem_wait_st();")
     assert wait < loop.index("row_exp<") and "row_exp<" not in loop[:wait]
+
+
+def test_every_arrival_of_the_rows_is_behind_a_fence():
+    """The tensor cores write columns that row warps have read: each path to an arrival on p_full goes
+    through a fence for the warp's own loads and stores of tensor memory."""
+    body = attend_body()
+    arrivals = [m.start() for m in re.finditer(r"mbar_arrive\(p_full", body)]
+    assert len(arrivals) == 2
+    for at, since in zip(arrivals, ("if (quarter < q0", "tmem_wait_st();\n        tc_fence")):
+        begin = body.rindex(since, 0, at)
+        assert "tc_fence_before();" in body[begin:at]
+        assert not re.search(r"tmem_ld|row_exp|row_max", body[begin:at])
