@@ -415,13 +415,25 @@ struct Config {
   static constexpr int entries = F8 ? 4 : 5;  // K or V tiles that the tensor cores read
   static constexpr int codes = F8 ? 2 : 0;    // tiles of codes
   static constexpr int threads = (SOFT_WARPS + (F8 ? 8 : 4)) * 32;
-  // Registers pass from the other warps to the row threads: three (four) warpgroups are launched
-  // with launch_regs a thread (the host checks that), and the shares must not add up to more.
-  static constexpr int launch_regs = F8 ? 128 : 168, row_regs = F8 ? 192 : 216,
-                       control_regs = F8 ? 64 : 72;
-  static_assert(2 * row_regs + (F8 ? 2 : 1) * control_regs <= (F8 ? 4 : 3) * launch_regs,
-                "registers of a CTA");
+  // Registers pass from the other warps to the row threads.  The three (four) warpgroups are
+  // launched with as many a thread as the compiler took (168 and 128), in eights; the shares must
+  // not add up to more than those, or the row threads would wait for registers for ever, and each
+  // must lie on its side of them.  The host checks it before the first launch.
+  static constexpr int row_regs = F8 ? 192 : 216, control_regs = F8 ? 64 : 72;
+  static constexpr bool registers_ok(int taken) {
+    const int launched = (taken + 7) / 8 * 8, others = F8 ? 2 : 1;
+    return control_regs <= launched && launched <= row_regs &&
+           2 * row_regs + others * control_regs <= (2 + others) * launched;
+  }
 };
+static_assert(Config<false>::registers_ok(168) && Config<false>::registers_ok(161) &&
+                  Config<false>::registers_ok(216) && !Config<false>::registers_ok(160) &&
+                  !Config<false>::registers_ok(217),
+              "more registers than needed are no error, fewer are");
+static_assert(Config<true>::registers_ok(128) && Config<true>::registers_ok(121) &&
+                  Config<true>::registers_ok(192) && !Config<true>::registers_ok(120) &&
+                  !Config<true>::registers_ok(193),
+              "more registers than needed are no error, fewer are");
 constexpr int CODE_TILE = BS * D;
 constexpr int FETCH_AHEAD = 4;  // steps of a slot fetched into L2 ahead of their loads
 
@@ -1480,9 +1492,26 @@ cudaError_t prepare_attend() {
   cudaFuncAttributes attr;
   const cudaError_t r = cudaFuncGetAttributes(&attr, attend_kernel<F8>);
   if (r != cudaSuccess) return r;
-  if (attr.numRegs != Config<F8>::launch_regs) return cudaErrorLaunchOutOfResources;
+  if (!Config<F8>::registers_ok(attr.numRegs)) return cudaErrorLaunchOutOfResources;
   return cudaFuncSetAttribute(attend_kernel<F8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               smem_bytes<F8>());
+}
+
+// What the launches of a cache need, once a device: one cache's kernel that cannot run does not
+// turn off the other's.
+template <bool F8>
+cudaError_t prepare() {
+  static std::atomic<int> done[KT_MAX_DEVICES];
+  return (cudaError_t)per_device_cached(done, [] {
+    cudaError_t r = prepare_attend<F8>();
+    if (r == cudaSuccess)
+      r = cudaFuncSetAttribute(combine_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)combine_smem(1, 1));
+    if (r == cudaSuccess)
+      r = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)sizeof(PlanShared));
+    return (int)r;
+  });
 }
 
 }  // namespace
@@ -1524,17 +1553,7 @@ cudaError_t launch_prefix(const PrefixLaunch& a, cudaStream_t stream) {
   p.scale_log2 = a.scale_log2;
   p.k_scale = a.k_scale;
   p.v_scale = a.v_scale;
-  static std::atomic<int> optin[KT_MAX_DEVICES];
-  cudaError_t e = (cudaError_t)per_device_cached(optin, [] {
-    cudaError_t r = prepare_attend<false>();
-    if (r == cudaSuccess) r = prepare_attend<true>();
-    if (r == cudaSuccess)
-      r = cudaFuncSetAttribute(combine_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)combine_smem(1, 1));
-    if (r != cudaSuccess) return (int)r;
-    return (int)cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)sizeof(PlanShared));
-  });
+  cudaError_t e = a.k_scale ? prepare<true>() : prepare<false>();
   if (e != cudaSuccess) return e;
   int threads = a.B > a.groups + 1 ? a.B : a.groups + 1;
   threads = threads < 64 ? 64 : threads < PLAN_THREADS ? (threads + 31) & ~31 : PLAN_THREADS;

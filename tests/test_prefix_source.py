@@ -66,3 +66,12 @@ def test_every_arrival_of_the_rows_is_behind_a_fence():
         begin = body.rindex(since, 0, at)
         assert "tc_fence_before();" in body[begin:at]
         assert not re.search(r"tmem_ld|row_exp|row_max", body[begin:at])
+
+
+def test_a_cache_is_prepared_by_itself():
+    """Whether the registers that the compiler took suffice is asked of the kernel that is launched,
+    as an inequality (its bounds are static assertions beside it)."""
+    text = source("prefix.cu")
+    launch = text[text.index("cudaError_t launch_prefix("):]
+    assert "a.k_scale ? prepare<true>() : prepare<false>()" in launch
+    assert "attr.numRegs !=" not in text and "registers_ok(attr.numRegs)" in text
