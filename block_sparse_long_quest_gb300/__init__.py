@@ -779,9 +779,13 @@ def kt_compact_pages(map, moves, num_moves, ws, *, new_table=None, new_refs=None
 
 def kt_copy_pages(pools, moves, num_moves, ws, stream=None):
     """Copies the pages of moves (as kt_fork_seqs and kt_compact_pages write them) in all pools
-    (a PagePools)."""
+    (a PagePools); nothing where moves has no entries (a pool of one page)."""
+    if moves is None:
+        raise KtError(KT_ERR_INVALID_ARG, "kt_copy_pages")
     n = moves.numel() // 2
     _check_moves(moves, num_moves, n, "kt_copy_pages")
+    if n == 0:
+        return
     _check(lib.kt_copy_pages(pools.array, len(pools.array), pools.num_pages, _ptr(moves),
                              _ptr(num_moves), n, _ptr(ws), ws.numel(), _stream(stream)),
            "kt_copy_pages")

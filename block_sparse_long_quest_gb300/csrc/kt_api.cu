@@ -1695,7 +1695,7 @@ kt_status kt_compact_pages(const kt_page_map* map, int32_t* new_table, int32_t* 
                            kt_stream_t stream) {
   kt_status s = check_map(map);
   if (s != KT_OK) return s;
-  if (!moves || !num_moves || !aligned16(moves) || !aligned16(num_moves) ||
+  if ((!moves && map->num_pages > 1) || !num_moves || !aligned16(moves) || !aligned16(num_moves) ||
       !new_table != !new_refs || !aligned16(new_table) || !aligned16(new_refs))
     return KT_ERR_INVALID_ARG;
   PagesLaunch a;

@@ -862,8 +862,8 @@ kt_status kt_reserve_pages(const kt_page_map* map, const int32_t* new_tokens, vo
 
 /*
  * Moves the pages in use to the front: with n pages in use, those from page n on move,
- * lowest first, to the free pages below n, lowest first.  moves (int32 [num_pages / 2][2])
- * and num_moves as in kt_fork_seqs; kt_copy_pages then copies the pages (of every pool
+ * lowest first, to the free pages below n, lowest first.  moves (int32 [num_pages / 2][2], which
+ * may be NULL for a pool of one page) and num_moves as in kt_fork_seqs; kt_copy_pages then copies the pages (of every pool
  * that goes with the map), before anything else reads or writes them.
  *   new_table, new_refs : int32, as block_table and page_refs, receive the new table (entries
  *                 of held pages; others stay as they were) and counts; both NULL: the map's
@@ -886,7 +886,8 @@ typedef struct {
  * before the call returns; at most 256, UNSUPPORTED beyond) for r < *num_moves, in one launch.
  *   moves, num_moves : device, as kt_fork_seqs and kt_compact_pages write them: no page is
  *                      copied onto twice, nor both copied and copied onto.
- *   max_moves        : entries that moves has room for.
+ *   max_moves        : entries that moves has room for, at least 1 (with none there is nothing
+ *                      to call).
  * A page out of range, or more moves than max_moves, record KT_ERR_DEVICE_CHECK and are
  * skipped.  ws: any zero-initialised workspace of at least 256 bytes (its header is used).
  */
