@@ -278,7 +278,9 @@ __device__ __forceinline__ int pages_needed(const MapParams& p, int b) {
   const int n = p.lens[b], have = p.blocks[b];
   if (more == 0) return 0;
   const long long want = ((long long)n + more + BS - 1) / BS;
-  if (more < 0 || n < 0 || have < 0 || have > p.max_blocks || want > p.max_blocks) return -1;
+  if (more < 0 || n < 0 || have < 0 || have > p.max_blocks || n > (long long)have * BS ||
+      want > p.max_blocks)
+    return -1;
   return want > have ? (int)(want - have) : 0;
 }
 

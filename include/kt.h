@@ -853,9 +853,10 @@ kt_status kt_fork_seqs(const kt_page_map* map, const int32_t* src, const int32_t
  * Gives every sequence b the pages that new_tokens[b] more tokens need (int32 [batch],
  * NULL: one token each, empty slots included), as kt_append_kv and kt_append_kv_f8 expect
  * them.  Pages reserved before are counted, so a call repeated without an append changes
- * nothing.  A sequence whose table has no room, or whose length, num_blocks or count make
- * no sense, records KT_ERR_DEVICE_CHECK and gets none; where the pages run out, that is
- * recorded too and the sequence at which they do and all later ones that need any get none.
+ * nothing.  A sequence that asks for pages (a count other than 0) and whose table has no room,
+ * or whose length, num_blocks or count make no sense (tokens beyond its pages among that),
+ * records KT_ERR_DEVICE_CHECK and gets none; where the pages run out, that is recorded too and
+ * the sequence at which they do and all later ones that need any get none.
  */
 kt_status kt_reserve_pages(const kt_page_map* map, const int32_t* new_tokens, void* ws,
                            size_t ws_bytes, kt_stream_t stream);

@@ -36,3 +36,25 @@ def test_a_pool_of_one_page(kt, held, in_place):
         assert torch.equal(p, w)
     st.check()
     assert pages_ref.Map([[0]], [0], [0], [int(held)]).compact()[0] == []
+
+
+class CheckedMap(pages_ref.Map):
+    """The reference, with lengths beyond the pages that a sequence holds recorded too."""
+
+    def reserve(self, more=None):
+        more = [1] * len(self.lens) if more is None else list(more)
+        for b, (n, have) in enumerate(zip(self.lens, self.blocks)):
+            if more[b] != 0 and not self.check(n <= 128 * have):
+                more[b] = 0
+        super().reserve(more)
+
+
+def test_reserve_for_a_length_beyond_its_pages(kt):
+    """Tokens that no page of the sequence holds (appended without a page) do not get one later."""
+    table = [[0, 9, 9, 9], [1, 2, 9, 9], [9, 9, 9, 9], [3, 9, 9, 9], [9, 9, 9, 9]]
+    st = State(kt, table, [129, 256, 1, 128, 0], [1, 2, 0, 1, 0], [1, 1, 1, 1] + [0] * 8)
+    st.ref.__class__ = CheckedMap
+    st.reserve()
+    assert st.blocks.tolist() == [1, 3, 0, 2, 1]
+    st.reserve([0, 1, 0, 300, 0])  # who asks for none is not looked at
+    st.reserve([-1, 0, 5, 0, 0])
