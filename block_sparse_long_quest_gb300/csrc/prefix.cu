@@ -15,13 +15,13 @@
 // Rows of the tensor-core steps (M = 128) are the queries of a group, as the G <= 8 queries of one
 // sequence fill an eighth of the smallest tile and every sequence would read the prefix anew.
 //
-// What bounds it.  64 sequences of 4 queries a K/V head (8) behind 32K tokens, 270 MB: 89 us, of which
-// plan 3, attend 77, combine 5.  Where two tiles of rows share their blocks the tensor cores do: a
+// What bounds it.  64 sequences of 4 queries a K/V head (8) behind 32K tokens, 270 MB: 90 us, of which
+// plan 3, attend 77, combine 6.  Where two tiles of rows share their blocks the tensor cores do: a
 // block is 24 products of K = 16 a tile (8 for S, 16 for P in two parts), 2100 cycles where they
 // alone would take 1580 (S reads Q and K from shared memory at its full rate, beside which tiles
-// land); behind the prefix it is HBM (6.5 TB/s).  8 groups of 9 behind 16K tokens, 268 MB: 60 us, HBM
+// land); behind the prefix it is HBM (6.5 TB/s).  8 groups of 9 behind 16K tokens, 268 MB: 62 us, HBM
 // (5.3 TB/s while attend runs; a slot's chain of S, softmax, P V is about 5000 cycles a block, and
-// CTAs end 20% apart).  4 samples of a prompt of 1K tokens: 17 us, three launches of dependent loads
+// CTAs end 20% apart).  4 samples of a prompt of 1K tokens: 18 us, three launches of dependent loads
 // and cold code.
 #include <cfloat>
 #include <cstring>
@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constan
 // Equal shares of the cost of all steps, one a block and one a run (its queries, its part: a run
 // of one block takes about twice the time of a block in the middle of a long one), among up to n
 // workers: the first ones have one more than the others.  With more workers than cost each has a
-// block or, for a run's own, nothing (4 samples of 1K tokens: 16.9 us; 18.2 with no more workers
+// block or, for a run's own, nothing (4 samples of 1K tokens: 1.3 us less than with no more workers
 // than blocks, some of which then had two).
 struct Shares {
   int n, each, more;
@@ -1335,8 +1335,9 @@ __global__ void __launch_bounds__(Config<F8>::threads, 1)
 // A warp takes 8 rows (consecutive ones of the batch, which mostly are of a tile too) and 16
 // channels: its 8 x 16 bytes of a part's channel group are contiguous.  A row of a long prefix has
 // a part for each CTA that met it (some 20 at 32K tokens): 16 of them in flight at a time (with 8,
-// and the rest one by one, 32 sequences behind 128K tokens took 14 us here instead of 5).  It is
-// bound by three round trips to L2: the sequence's place in the plan, its items, the parts.
+// and the rest one by one, 32 sequences behind 128K tokens took 14 us here instead of 6).  It is
+// bound by three round trips to L2: the sequence's place in the plan, its items, the parts (5 us
+// with one of them, the plan read while attend still runs, which nothing promises to be there).
 constexpr int COMBINE_WARPS = 8;
 constexpr int COMBINE_ROWS = 8;
 constexpr int COMBINE_BATCH = 16;  // parts in flight

@@ -80,7 +80,7 @@ typedef enum {
   KT_OP_SPARSE_STEP = 3,   /* score/select + sparse attention in one call */
   KT_OP_DYNAMIC_REPS = 4,
   KT_OP_PRESELECT = 5,     /* kt_preselect_blocks (needs T like KT_OP_DYNAMIC_REPS) */
-  KT_OP_PREFIX_ATTN = 6    /* kt_prefix_decode_attn */
+  KT_OP_PREFIX_ATTN = 6    /* kt_prefix_decode_attn (and _f8) */
 } kt_op;
 
 /*
@@ -256,11 +256,12 @@ int32_t kt_sparse_decode_step_kernels(const kt_paged_kv* kv, const kt_sparse_par
 
 /*
  * Caps the CTAs that the attention calls (kt_sparse_decode_attn,
- * kt_sparse_decode_step, kt_decode_layer, kt_dense_decode_attn) launch from
- * the calling host thread: at most max_ctas, and never fewer than one per
- * (sequence, KV head) segment (kt_sparse_decode_attn_f8 and
- * kt_dense_decode_attn_f8 share the segments out over max_ctas even where there
- * are more); 0 restores the default of one per SM.  A
+ * kt_sparse_decode_step, kt_decode_layer, kt_dense_decode_attn,
+ * kt_prefix_decode_attn) launch from the calling host thread: at most max_ctas,
+ * and never fewer than one per (sequence, KV head) segment
+ * (kt_sparse_decode_attn_f8, kt_dense_decode_attn_f8, kt_prefix_decode_attn and
+ * kt_prefix_decode_attn_f8 share the segments out over max_ctas even where there
+ * are more; of the latter two that holds for the launch that reads K and V); 0 restores the default of one per SM.  A
  * caller that runs other work beside the decode step can leave SMs to it.
  * The split-K partition of each segment, and in the one-launch step the
  * scoring slices, follow from the CTA count; outputs agree within rounding
@@ -453,6 +454,13 @@ kt_status kt_dense_decode_attn(const void* q, const kt_paged_kv* kv, int32_t num
  *                   themselves.  The call reads these pages in the table of the group's first
  *                   such sequence only.
  *   groups        : 1 .. 2048; a group may be empty.
+ * It pays where sharing saves reading more than about 0.25 GB, that is where (members - 1) times
+ * the bytes of the prefix in this cache's K and V is more than that; below it kt_dense_decode_attn,
+ * one launch whose repeated reads L2 serves, is the faster one.  With 4 query heads on each of 8
+ * KV heads, this call and the dense one (us, each behind a flush of L2): 4 sequences behind
+ * 1K tokens 26 and 15, 4 behind 16K 39 and 36, 16 behind 4K 36 and 36, 8 behind 16K 41 and 56,
+ * 64 behind 32K 86 and 718; e4m3: 4 behind 32K 51 and 50, 16 behind 4K 35 and 29, 8 behind 16K
+ * 41 and 50, 64 behind 32K 92 and 517 (200 tokens of its own a sequence).
  */
 typedef struct {
   const int32_t* cu_groups;
