@@ -75,3 +75,29 @@ def test_a_cache_is_prepared_by_itself():
     launch = text[text.index("cudaError_t launch_prefix("):]
     assert "a.k_scale ? prepare<true>() : prepare<false>()" in launch
     assert "attr.numRegs !=" not in text and "registers_ok(attr.numRegs)" in text
+
+
+def test_the_simulated_barriers_have_the_kernels_sizes():
+    """test_prefix_barriers models the rings, the runs and who arrives on what: sizes and counts of
+    arrivals are those of the source."""
+    import random
+
+    import test_prefix_barriers as sim
+    text = source("prefix.cu")
+    value = lambda name: int(re.search(r"constexpr int %s = (\d+);" % name, text)[1])  # noqa: E731
+    assert value("UNITS") == sim.UNITS and value("STEPS_AHEAD") == sim.STEPS_AHEAD
+    assert value("SLOTS") == 2 and value("SOFT_WARPS") == 8
+    for f8 in (0, 1):
+        k = sim.Kernel(random.Random(1), [1], (128, 1), [[], []], bool(f8))
+        for name, n in (("entries", k.entries), ("codes", k.codes)):
+            assert int(re.search(r"%s = F8 \? (\d+) : (\d+);" % name, text)[2 - f8]) == n
+        init = dict(re.findall(r"mbar_init\((\w+) \+ 8 \* i, ([^)]+)\);", text))
+        count = {"empty": "2", "full": "F8 ? 4 : 1", "code_full": "1", "code_empty": "4", "s_full": "1",
+                 "p_full": "SOFT_WARPS / SLOTS", "o_full": "1", "q_full": "1", "q_done": "1"}
+        assert init == count
+        bars = dict(empty=k.empty, full=k.full[0], code_full=k.code_full, code_empty=k.code_empty,
+                    s_full=k.s_full, p_full=k.p_full, o_full=k.o_full, q_full=k.q_full[0],
+                    q_done=k.q_done[0])
+        for name, c in count.items():
+            want = {"F8 ? 4 : 1": 4 if f8 else 1, "SOFT_WARPS / SLOTS": 4}.get(c) or int(c)
+            assert all(b.count == want for b in bars[name]), name
