@@ -261,8 +261,9 @@ int32_t kt_sparse_decode_step_kernels(const kt_paged_kv* kv, const kt_sparse_par
  * and never fewer than one per (sequence, KV head) segment
  * (kt_sparse_decode_attn_f8, kt_dense_decode_attn_f8, kt_prefix_decode_attn and
  * kt_prefix_decode_attn_f8 share the segments out over max_ctas even where there
- * are more; of the latter two that holds for the launch that reads K and V); 0 restores the default of one per SM.  A
- * caller that runs other work beside the decode step can leave SMs to it.
+ * are more; of the latter two that holds for the launch that reads K and V);
+ * 0 restores the default of one per SM.  A caller that runs other work beside
+ * the decode step can leave SMs to it.
  * The split-K partition of each segment, and in the one-launch step the
  * scoring slices, follow from the CTA count; outputs agree within rounding
  * and selections outside the near-tie zone whatever the cap.  Host only,
@@ -872,8 +873,8 @@ kt_status kt_reserve_pages(const kt_page_map* map, const int32_t* new_tokens, vo
 /*
  * Moves the pages in use to the front: with n pages in use, those from page n on move,
  * lowest first, to the free pages below n, lowest first.  moves (int32 [num_pages / 2][2], which
- * may be NULL for a pool of one page) and num_moves as in kt_fork_seqs; kt_copy_pages then copies the pages (of every pool
- * that goes with the map), before anything else reads or writes them.
+ * may be NULL for a pool of one page) and num_moves as in kt_fork_seqs; kt_copy_pages then copies
+ * the pages (of every pool that goes with the map), before anything else reads or writes them.
  *   new_table, new_refs : int32, as block_table and page_refs, receive the new table (entries
  *                 of held pages; others stay as they were) and counts; both NULL: the map's
  *                 own are changed.  A table entry that is out of range or counted as free
